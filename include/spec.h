@@ -214,6 +214,60 @@ int spec_kv_create(spec_model* m, int32_t batch, int32_t max_ctx, spec_kv** out)
 int spec_kv_create_paged(spec_model* m, int32_t batch, int32_t max_ctx, int32_t page, int32_t n_pages,
                          spec_kv** out);
 
+/* 8-bit KV cache: rows are quantised as they are written (spec_kv_import,
+ * spec_attend's k and v, and the rows that spec_prefill, the drafts and the
+ * verifications write) and every call that reads the cache works on the values
+ * that it stands for.  Contiguous with page = 0 (n_pages ignored), else paged as
+ * spec_kv_create_paged.  A row x[hd] (one slot of one KV head, K or V) is held as
+ *   e = least integer with max|x| <= 448 * 2^e, kept in [-124, 119]
+ *   y = e4m3(x * 2^-e)      nearest, ties to even, saturating
+ * and stands for y * 2^e, which is always a bf16 number: spec_kv_export returns
+ * it exactly.  Infinities count as no magnitude and saturate, NaN stays NaN.
+ * About half the memory of a bf16 cache (hd + 1 bytes a row instead of 2 hd).
+ * bf16 models only (SPEC_ERR_UNSUPPORTED).  sync. */
+int spec_kv_create_q8(spec_model* m, int32_t batch, int32_t max_ctx, int32_t page, int32_t n_pages,
+                      spec_kv** out);
+
+/* Every sequence of `kv` continues sequence `seq` of `prefix`: a batch of
+ * continuations of one prompt holds the prompt's K and V once.  From this call
+ * on the rows of kv see the prompt's committed slots before their own, their
+ * position ids start at its length, and the attention reads the prompt once for
+ * the whole batch.  The committed lengths, capacities and slots of kv stay its
+ * own (the prompt's slots are not counted); kv_commit, spec_kv_set_lengths and
+ * the page calls leave the prompt alone.  Set it before kv's first rows: rows
+ * that were written earlier keep the position ids they were written with.  The
+ * prompt's length is read when a call runs, so it must not change while kv
+ * depends on it.  prefix NULL detaches.  Either cache may be contiguous, paged,
+ * bf16 or 8-bit; both belong to one bf16 model; a prefix has no prefix of its
+ * own.  spec_kv_destroy(prefix) makes the calls on kv fail with SPEC_ERR_ARG
+ * until kv gets a new prefix or NULL.  Not while a call on kv is being captured
+ * or replayed: a captured call keeps the prompt it was captured with.
+ * Host only. */
+int spec_kv_set_prefix(spec_kv* kv, spec_kv* prefix, int32_t seq);
+
+/* Attention of one layer over the cache for the rows of sequences [0, batch),
+ * as the forward calls run it, for callers with layers of their own.
+ *   n_rows   host int32 [batch]: rows of sequence b, each in [0, 64], sum T <= max_rows
+ *   q        device bf16 [T][H][hd] (position-encoded, not scaled), row stride
+ *            q_stride elements
+ *   k, v     device bf16 [T][Hkv][hd], row strides k_stride / v_stride, both or
+ *            neither: written first, to slots s_b .. s_b + n_rows[b] - 1 of the
+ *            layer (quantised in an 8-bit cache; a paged cache takes the pages).
+ *            NULL: those slots already hold the rows.
+ *   tree_parent  as for spec_verify (host, shared by all sequences; NULL: chains)
+ *   out      device bf16 [T][H][hd], row stride out_stride
+ * Row j of sequence b sees the prompt of the cache's prefix, the slots below
+ * s_b and the rows of its chain or tree path; scores are q.k / sqrt(hd), softmax
+ * statistics and sums are f32.  Head h reads KV head h / (H / Hkv).  A row whose
+ * scores are all -inf, or hold NaN or +inf, gives NaN.  Lengths unchanged;
+ * kv_commit with acc_len n_rows[b] - 1 keeps the rows.  The slots are read on
+ * the device: a captured call may be replayed after the lengths moved.  Slots
+ * beyond the capacity are neither written nor read and set
+ * SPEC_DEVERR_CAPACITY.  bf16 models only.  async. */
+int spec_attend(spec_kv* kv, int32_t layer, int32_t batch, const int32_t* n_rows, const void* q,
+                int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                const int32_t* tree_parent, void* out, int64_t out_stride, void* stream);
+
 /* Pages left in the pool of a paged cache (0 for a contiguous one).  sync. */
 int spec_kv_free_pages(spec_kv* kv, int32_t* host_free, void* stream);
 
@@ -224,7 +278,10 @@ int spec_kv_page_table(spec_kv* kv, int32_t* host_table, void* stream);
 /* Raw contents of one physical page of the pool, read without the page
  * table: host buffer [n_kv_heads][page][head_dim] of the model dtype (bf16
  * or f32) for K (which = 0) or V (which = 1) of `layer`.  A contiguous cache
- * is read as pages of max_ctx slots, page b holding sequence b.  For
+ * is read as pages of max_ctx slots, page b holding sequence b.  An 8-bit cache
+ * gives its e4m3 bytes, and the exponent bytes e + 127 ([n_kv_heads][page]) of K
+ * for which = 2 and of V for which = 3; contiguous, its pages are max_ctx rounded
+ * up to 64 slots.  For
  * inspection (tests, debugging): lets a caller check where the page table
  * put each slot.  SPEC_ERR_ARG for a page, layer or `which` out of range.
  * sync.  Self-speculative decoding page, m.lqnn.cn/news/278124, section 3.3
@@ -420,6 +477,27 @@ int spec_probs(const float* logits, int64_t lg_stride, int32_t rows, int32_t voc
  */
 int spec_sample(const float* probs, int64_t p_stride, int32_t rows, int32_t vocab,
                 const float* u, int32_t* tokens, void* stream);
+
+/* Log probabilities under rows of logits.
+ *   logits   device, `dtype` (SPEC_DTYPE_F32 or SPEC_DTYPE_BF16), row r at
+ *            logits + r * lg_stride elements (lg_stride >= vocab); -inf is a
+ *            masked token
+ *   temperature  > 0, finite: the rows are softmax(logits / temperature)
+ *   tokens   device int32 [rows]; logprob device f32 [rows] out (both or
+ *            neither): log p(tokens[r]), -inf for a masked token, NaN for a
+ *            token outside [0, vocab)
+ *   entropy  device f32 [rows] out, nullable: -sum p log p (nats)
+ *   n_top    0, or up to min(32, vocab) best tokens a row: top_ids device int32
+ *            [rows][n_top] and top_logprobs device f32 [rows][n_top] out, by
+ *            decreasing logit, ties to the lower id (masked tokens, at -inf, after
+ *            the others)
+ * A row without a distribution (NaN or +inf in it, or every token masked) gives
+ * NaN and ids -1.  Sums are f32.  vocab <= 1048576.  async.
+ * Scores the emitted tokens of spec_verify's logits rows, for example to rank
+ * several continuations of one prompt. */
+int spec_logprobs(const void* logits, int32_t dtype, int64_t lg_stride, int32_t rows, int32_t vocab,
+                  float temperature, const int32_t* tokens, float* logprob, float* entropy, int32_t n_top,
+                  int32_t* top_ids, float* top_logprobs, void* stream);
 
 /* Greedy acceptance from target logits (the unfused form of spec_verify's
  * fused acceptance).  logits device f32 [batch][n_rows][vocab]; tokens device

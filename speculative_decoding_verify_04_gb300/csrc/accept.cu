@@ -44,7 +44,7 @@ accept_greedy_kernel(const float* __restrict__ logits, const int* __restrict__ t
 // increasing depth (a move never overwrites a later move's source).  One CTA
 // per (layer, kv head, sequence); lengths are updated by a second launch.
 template <typename KT>
-__global__ void commit_tree_kernel(KT* kc, KT* vc, const int* len, const int* acc_len, const int* path,
+__global__ void commit_tree_kernel(KT* kc, KT* vc, uint8_t* ke, uint8_t* ve, const int* len, const int* acc_len, const int* path,
                                    int path_stride, int n_kv_heads, KVPages kvp, int kv_ctx, int hd, int* err) {
     pdl_wait();
     pdl_trigger();
@@ -59,39 +59,66 @@ __global__ void commit_tree_kernel(KT* kc, KT* vc, const int* len, const int* ac
         KT kv0 = KT(), vv0 = KT();
         const int i = threadIdx.x;
         if (i < hd) { kv0 = kc[(size_t)rs * hd + i]; vv0 = vc[(size_t)rs * hd + i]; }
+        if (ke && i == 0) { ke[rd] = ke[rs]; ve[rd] = ve[rs]; }      // 8-bit caches: the row's exponents
         __syncthreads();
         if (i < hd) { kc[(size_t)rd * hd + i] = kv0; vc[(size_t)rd * hd + i] = vv0; }
         __syncthreads();
     }
 }
 
-// Paged caches.  One thread walks every sequence in order, so which page a
-// block of slots gets is deterministic.
+// Paged caches.  Which page a block of slots gets is deterministic.
 //   ensure: before a call writes slots, every block of slots below end[b]
-//   (len[b] + n[b] when relative, else n[b]) holds a page, popped from the free
-//   stack; an empty stack sets the capacity error.
+//   (len[b] + n[b] when relative, else n[b]) holds a page.  One CTA looks at the
+//   (sequence, block) pairs 1024 at a time; the i-th missing one, in sequence
+//   and block order, takes the i-th page from the top of the free stack, and an
+//   empty stack sets the capacity error.
 //   release (page-granular rollback, "self-speculative decoding" page section
-//   3.3): the blocks past the committed length give their pages back.
+//   3.3): the blocks past the committed length give their pages back; one
+//   thread walks every sequence in order.
 struct PageNeed { int batch; int relative; int n[kMaxPlanBatch]; };
+constexpr int kEnsureThreads = 1024;
 
-__global__ void ensure_pages_kernel(const int* __restrict__ len, PageNeed need, int* table, int page, int max_pages,
-                                    const int* free_pages, int* free_top, int* err) {
+__global__ void __launch_bounds__(kEnsureThreads)
+ensure_pages_kernel(const int* __restrict__ len, PageNeed need, int* table, int page, int max_pages,
+                    const int* free_pages, int* free_top, int* err) {
     pdl_wait();
     pdl_trigger();
-    if (threadIdx.x != 0 || blockIdx.x != 0) return;
-    int top = *free_top;
-    for (int b = 0; b < need.batch; ++b) {
-        const int end = need.relative ? len[b] + need.n[b] : need.n[b];
-        const int blocks = min(max_pages, (end + page - 1) / page);
-        if ((end + page - 1) / page > max_pages) dev_error(err, SPEC_DEVERR_CAPACITY);
-        for (int p = 0; p < blocks; ++p) {
-            int* e = table + (size_t)b * max_pages + p;
-            if (*e >= 0) continue;
-            if (top == 0) { dev_error(err, SPEC_DEVERR_CAPACITY); break; }
-            *e = free_pages[--top];
-        }
+    __shared__ int blocks[kMaxPlanBatch];
+    __shared__ int most, warp_n[kEnsureThreads / 32];
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    if (t == 0) most = 0;
+    __syncthreads();
+    if (t < need.batch) {
+        const int end = need.relative ? len[t] + need.n[t] : need.n[t];
+        const int n = (end + page - 1) / page;
+        if (n > max_pages) dev_error(err, SPEC_DEVERR_CAPACITY);
+        blocks[t] = min(max_pages, n);
+        atomicMax(&most, blocks[t]);
     }
-    *free_top = top;
+    __syncthreads();
+    const int top0 = *free_top, cols = most;
+    int top = top0;
+    for (long long base = 0; base < (long long)need.batch * cols; base += kEnsureThreads) {
+        const long long i = base + t;
+        const int b = cols ? (int)(i / cols) : 0, p = cols ? (int)(i % cols) : 0;
+        int* e = table + (size_t)b * max_pages + p;
+        const bool miss = b < need.batch && p < blocks[min(b, kMaxPlanBatch - 1)] && *e < 0;
+        const unsigned m = __ballot_sync(0xffffffffu, miss);
+        if (lane == 0) warp_n[w] = __popc(m);
+        __syncthreads();
+        int rank = __popc(m & ((1u << lane) - 1u)), total = 0;
+        for (int x = 0; x < kEnsureThreads / 32; ++x) {
+            if (x < w) rank += warp_n[x];
+            total += warp_n[x];
+        }
+        if (miss) {
+            if (rank < top) *e = free_pages[top - 1 - rank];
+            else dev_error(err, SPEC_DEVERR_CAPACITY);
+        }
+        top -= min(total, top);
+        __syncthreads();
+    }
+    if (t == 0 && top != top0) *free_top = top;
 }
 
 __global__ void release_pages_kernel(const int* __restrict__ len, int batch, int* table, int page, int max_pages,
@@ -215,7 +242,7 @@ int kv_ensure_pages(spec_kv* kv, int batch, const int* n, bool relative, cudaStr
     need.relative = relative ? 1 : 0;
     for (int b = 0; b < batch; ++b) need.n[b] = n[b];
     spec_model* m = kv->m;
-    launch_k(m->pdl, ensure_pages_kernel, dim3(1), dim3(32), 0, st, (const int*)kv->len, need, kv->table, kv->page,
+    launch_k(m->pdl, ensure_pages_kernel, dim3(1), dim3(kEnsureThreads), 0, st, (const int*)kv->len, need, kv->table, kv->page,
              kv->max_pages, (const int*)kv->free_pages, kv->free_top, m->err);
     ++m->launches;
     return check_cuda(cudaGetLastError(), "page allocation launch");
@@ -266,13 +293,17 @@ extern "C" int kv_commit(spec_kv* kv, int32_t batch, const int32_t* acc_len, con
         if (path_stride < 1) return set_error(SPEC_ERR_ARG, "kv_commit: bad path stride");
         dim3 grid(m->cfg.n_layers * m->cfg.n_kv_heads, batch);
         const int threads = m->cfg.head_dim;
-        if (m->bf16)
+        if (kv->q8)
+            launch_k(m->pdl, commit_tree_kernel<uint8_t>, grid, dim3(threads), 0, st, (uint8_t*)kv->k, (uint8_t*)kv->v,
+                     kv->ke, kv->ve, kv->len, acc_len, path, path_stride, m->cfg.n_kv_heads, kv->pages(), kv->max_ctx,
+                     m->cfg.head_dim, m->err);
+        else if (m->bf16)
             launch_k(m->pdl, commit_tree_kernel<__nv_bfloat16>, grid, dim3(threads), 0, st,
-                (__nv_bfloat16*)kv->k, (__nv_bfloat16*)kv->v, kv->len, acc_len, path, path_stride,
+                (__nv_bfloat16*)kv->k, (__nv_bfloat16*)kv->v, (uint8_t*)nullptr, (uint8_t*)nullptr, kv->len, acc_len, path, path_stride,
                 m->cfg.n_kv_heads, kv->pages(), kv->max_ctx, m->cfg.head_dim, m->err);
         else
             launch_k(m->pdl, commit_tree_kernel<float>, grid, dim3(threads), 0, st, (float*)kv->k, (float*)kv->v,
-                     kv->len, acc_len, path, path_stride, m->cfg.n_kv_heads, kv->pages(), kv->max_ctx,
+                     (uint8_t*)nullptr, (uint8_t*)nullptr, kv->len, acc_len, path, path_stride, m->cfg.n_kv_heads, kv->pages(), kv->max_ctx,
                      m->cfg.head_dim, m->err);
         cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return check_cuda(e, "kv_commit tree launch");

@@ -1,0 +1,590 @@
+// Attention of a batch's new rows over each sequence's own cache and, where the
+// sequences continue one prompt, over that prompt's cache.
+//
+// Row r of sequence b sees the prompt's slots [0, P), its sequence's slots
+// [0, s_b) and the call's rows that its mask names:
+//     out = sum_j p_j v_j / sum_j p_j,   p_j = 2^(c q.k_j - m),   c = scale log2 e,
+// with m the largest exponent seen.  The prompt is read once for the whole
+// batch: the query vectors of all sequences and of a KV head's group of query
+// heads form one list (vector i of KV head g: row i / G, head g G + i % G), and
+// every tile of prompt keys meets all of them.  Each part of a row's keys (a
+// range of the prompt, a range of the sequence's own slots) leaves a partial
+// state (m, sum p, sum p v) in 32 bits; one warp a (row, head) joins them.
+#include <algorithm>
+#include <cmath>
+
+#include "attend.cuh"
+
+namespace spec {
+
+constexpr int kRowThreads = 128;
+constexpr int kMinKeys = 256;         // least keys of a range: below it the join costs more than the ranges give
+
+struct AttendArgs {
+    const void* q;
+    long long q_stride;
+    float c;                          // scale * log2(e)
+    CacheView own, pre;
+    int pre_seq;                      // sequence of the prompt in its cache
+    int H, Hkv;
+    AttendSpan span;
+    int own_splits, pre_splits;       // pre_splits 0: no prompt part in the row kernel
+    int own_qb, pre_qb;               // query blocks of 16
+    float* part_o;                    // [range][T * H][hd]
+    float* part_ml;                   // [range][T * H][2]: the prompt's ranges, then the sequence's own
+    int own_range0;                   // first range of the own part
+    int* err;
+};
+
+SPEC_DEV float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Eight keys' bytes as bf16 pairs: words of e4m3 -> 2 bf16x2 each
+SPEC_DEV void e4m3x4_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const float2 a = e4m3x2_f32(w), b = e4m3x2_f32(w >> 16);
+    lo = bf16x2(a.x, a.y);
+    hi = bf16x2(b.x, b.y);
+}
+
+// ---------------------------------------------------------------------------
+// The row kernel: 16 query vectors a CTA, the M side of mma.sync m16n8k16, its
+// four warps in turn on 16-key tiles that go from global memory to fragments.
+// Inside a k-step the order of the head dimensions, and inside a tile the order
+// of the keys, is free (both factors use the same), so they are chosen such
+// that every load is a 16-byte piece of a K or V row and that the scores'
+// accumulator fragment is P's operand fragment:
+//   lane (g, c) = (lane / 4, lane % 4);
+//   scores, key half h: column g is tile key 4 (g / 2) + 2 h + g % 2, so lane
+//     (g, c) ends with keys 4c .. 4c+3 of rows g and g + 8;
+//   k-step of dims: bf16 piece p of a K row (8 dims at 32 p + 8 c) serves two
+//     k-steps, an e4m3 piece (16 dims at 64 p + 16 c) four;
+//   values: n-tile nt of column g is dim (hd / 8) g + nt, so lane (g, c) reads
+//     hd / 8 consecutive dims of V rows 4c .. 4c+3.
+// e4m3 tiles become bf16 (exact); a key's exponent multiplies its scores, a
+// value's its probability.  P is split into bf16 hi + lo, so its rounding does
+// not show; f32 queries are split the same way (QF32).
+template <int HD, bool Q8>
+SPEC_DEV void load_tile(const CacheView& cv, long long row, int kt, int k_end, int gq, int cq,
+                        uint32_t (&kb)[2][HD / 16][2], uint32_t (&vb)[4][HD / 16], float (&ks)[4], float (&vs)[4]) {
+    constexpr int VD = HD / 8;
+    if (Q8) {
+        const uint8_t* K = static_cast<const uint8_t*>(cv.k) + row * HD;
+        const uint8_t* V = static_cast<const uint8_t*>(cv.v) + row * HD;
+        uint4 kr[2][HD / 64];
+        uint32_t vr[4][VD / 4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int key = min(4 * (gq >> 1) + 2 * h + (gq & 1), k_end - 1 - kt);
+#pragma unroll
+            for (int p = 0; p < HD / 64; ++p) kr[h][p] = __ldg(reinterpret_cast<const uint4*>(K + key * HD) + 4 * p + cq);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int key = min(4 * cq + r, k_end - 1 - kt);
+            if (HD == 128) {
+                const uint4 w = __ldg(reinterpret_cast<const uint4*>(V + key * HD) + gq);
+                vr[r][0] = w.x; vr[r][1] = w.y; vr[r][VD / 4 - 2] = w.z; vr[r][VD / 4 - 1] = w.w;
+            } else {
+                const uint2 w = __ldg(reinterpret_cast<const uint2*>(V + key * HD) + gq);
+                vr[r][0] = w.x; vr[r][1] = w.y;
+            }
+        }
+        // the pages hold a multiple of 16 slots: four exponents are one aligned word
+        const uint32_t ke = __ldg(reinterpret_cast<const uint32_t*>(cv.ke + row) + cq);
+        const uint32_t ve = __ldg(reinterpret_cast<const uint32_t*>(cv.ve + row) + cq);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            ks[i] = kv8_scale((ke >> (8 * i)) & 0xFF);
+            vs[i] = kv8_scale((ve >> (8 * i)) & 0xFF);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int p = 0; p < HD / 64; ++p) {
+                const uint32_t w[4] = {kr[h][p].x, kr[h][p].y, kr[h][p].z, kr[h][p].w};
+#pragma unroll
+                for (int s = 0; s < 4; ++s) e4m3x4_bf16(w[s], kb[h][4 * p + s][0], kb[h][4 * p + s][1]);
+            }
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < VD / 4; ++i) e4m3x4_bf16(vr[r][i], vb[r][2 * i], vb[r][2 * i + 1]);
+    } else {
+        const __nv_bfloat16* K = static_cast<const __nv_bfloat16*>(cv.k) + row * HD;
+        const __nv_bfloat16* V = static_cast<const __nv_bfloat16*>(cv.v) + row * HD;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int key = min(4 * (gq >> 1) + 2 * h + (gq & 1), k_end - 1 - kt);
+#pragma unroll
+            for (int p = 0; p < HD / 32; ++p) {
+                const uint4 w = __ldg(reinterpret_cast<const uint4*>(K + key * HD) + 4 * p + cq);
+                kb[h][2 * p][0] = w.x; kb[h][2 * p][1] = w.y;
+                kb[h][2 * p + 1][0] = w.z; kb[h][2 * p + 1][1] = w.w;
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int key = min(4 * cq + r, k_end - 1 - kt);
+#pragma unroll
+            for (int p = 0; p < HD / 64; ++p) {
+                const uint4 w = __ldg(reinterpret_cast<const uint4*>(V + key * HD) + (HD / 64) * gq + p);
+                vb[r][4 * p] = w.x; vb[r][4 * p + 1] = w.y; vb[r][4 * p + 2] = w.z; vb[r][4 * p + 3] = w.w;
+            }
+        }
+    }
+    // values of keys past the range: their probability is zero, and zero times what the slot holds must be zero
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (kt + 4 * cq + r >= k_end)
+#pragma unroll
+            for (int i = 0; i < VD / 2; ++i) vb[r][i] = 0u;
+}
+
+// Query fragments of 16 vectors in lane order; dims as the K pieces of the cache's kind order them.
+template <int HD, bool QF32>
+SPEC_DEV void load_queries(const AttendArgs& a, bool q8, int g, int G, int list_row0, int q0, int nq, uint4* sQ) {
+    constexpr int KS = HD / 16;
+    for (int i = threadIdx.x; i < KS * 32; i += kRowThreads) {
+        const int ks = i / 32, ln = i % 32, fg = ln >> 2, fc = ln & 3;
+        const int d0 = q8 ? 64 * (ks >> 2) + 16 * fc + 4 * (ks & 3) : 32 * (ks >> 1) + 8 * fc + 4 * (ks & 1);
+        float x[2][4];
+#pragma unroll
+        for (int rr = 0; rr < 2; ++rr) {
+            const int qi = fg + 8 * rr, qg = q0 + qi;
+            const long long off = (list_row0 + qg / G) * a.q_stride + (g * G + qg % G) * HD + d0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                x[rr][e] = 0.f;
+                if (qi < nq)
+                    x[rr][e] = QF32 ? static_cast<const float*>(a.q)[off + e]
+                                    : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[off + e]);
+            }
+        }
+        sQ[i] = make_uint4(pack_bf16(x[0][0], x[0][1]), pack_bf16(x[1][0], x[1][1]), pack_bf16(x[0][2], x[0][3]),
+                           pack_bf16(x[1][2], x[1][3]));
+        if (QF32)
+            sQ[KS * 32 + i] = make_uint4(pack_bf16_lo(x[0][0], x[0][1]), pack_bf16_lo(x[1][0], x[1][1]),
+                                         pack_bf16_lo(x[0][2], x[0][3]), pack_bf16_lo(x[1][2], x[1][3]));
+    }
+}
+
+// Keys [k_begin, k_end) of one (sequence, KV head) against the CTA's queries.
+// Keys below n_ctx are seen by every row; key n_ctx + x by the rows whose mask has bit x.
+template <int HD, bool Q8, bool QF32>
+SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, int g, int k_begin, int k_end, int n_ctx,
+                           unsigned long long mk0, unsigned long long mk1, const uint4* sQ, float (&o)[HD / 8][4],
+                           float (&m_r)[2], float (&l_r)[2]) {
+    constexpr int KS = HD / 16, VD = HD / 8;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, cq = lane & 3;
+    for (int kt = k_begin + 16 * warp; kt < k_end; kt += 64) {
+        // tiles start at multiples of 16 and pages hold a multiple of 16 slots: no tile crosses a page
+        long long row = kv_row_in_layer(cv.pages, a.Hkv, seq, g, kt);
+        if (row < 0) { dev_error(a.err, SPEC_DEVERR_CAPACITY); row = 0; }
+        uint32_t kb[2][KS][2], vb[4][KS];
+        float ks[4], vs[4];
+        load_tile<HD, Q8>(cv, row, kt, k_end, gq, cq, kb, vb, ks, vs);
+        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const uint4 qh = sQ[s * 32 + lane];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) mma16816(sc[h], qh.x, qh.y, qh.z, qh.w, kb[h][s][0], kb[h][s][1]);
+            if (QF32) {
+                const uint4 ql = sQ[KS * 32 + s * 32 + lane];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) mma16816(sc[h], ql.x, ql.y, ql.z, ql.w, kb[h][s][0], kb[h][s][1]);
+            }
+        }
+        // lane: rows g (sc[h][0..1]) and g + 8 (sc[h][2..3]) at keys 4c + 2h + {0, 1}
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int key = kt + 4 * cq + 2 * h + e;
+                const bool ctx = key < n_ctx, in = key < k_end;
+                const float f = Q8 ? a.c * ks[2 * h + e] : a.c;
+                sc[h][e] = in && (ctx || ((mk0 >> ((key - n_ctx) & 63)) & 1ull)) ? sc[h][e] * f : -INFINITY;
+                sc[h][2 + e] = in && (ctx || ((mk1 >> ((key - n_ctx) & 63)) & 1ull)) ? sc[h][2 + e] * f : -INFINITY;
+            }
+        float alpha[2];
+#pragma unroll
+        for (int rr = 0; rr < 2; ++rr) {
+            float mt = fmaxf(fmaxf(sc[0][2 * rr], sc[0][2 * rr + 1]), fmaxf(sc[1][2 * rr], sc[1][2 * rr + 1]));
+            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+            const float mn = fmaxf(m_r[rr], mt);
+            const float mu = mn == -INFINITY ? 0.f : mn;      // nothing seen yet: every exponent stays -inf, p = 0
+            alpha[rr] = ex2(m_r[rr] - mu);
+            float ps = 0.f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    sc[h][2 * rr + e] = ex2(sc[h][2 * rr + e] - mu);
+                    ps += sc[h][2 * rr + e];
+                }
+            l_r[rr] = l_r[rr] * alpha[rr] + ps;               // this lane's keys; joined over the quad at the end
+            m_r[rr] = mn;
+            if (Q8) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) sc[h][2 * rr + e] *= vs[2 * h + e];
+            }
+        }
+        const uint32_t pa0 = pack_bf16(sc[0][0], sc[0][1]), pa1 = pack_bf16(sc[0][2], sc[0][3]);
+        const uint32_t pa2 = pack_bf16(sc[1][0], sc[1][1]), pa3 = pack_bf16(sc[1][2], sc[1][3]);
+        const uint32_t pl0 = pack_bf16_lo(sc[0][0], sc[0][1]), pl1 = pack_bf16_lo(sc[0][2], sc[0][3]);
+        const uint32_t pl2 = pack_bf16_lo(sc[1][0], sc[1][1]), pl3 = pack_bf16_lo(sc[1][2], sc[1][3]);
+#pragma unroll
+        for (int nt = 0; nt < VD; ++nt) {
+            const int i = nt >> 1;
+            const uint32_t b0 = (nt & 1) ? pair_hi(vb[0][i], vb[1][i]) : pair_lo(vb[0][i], vb[1][i]);
+            const uint32_t b1 = (nt & 1) ? pair_hi(vb[2][i], vb[3][i]) : pair_lo(vb[2][i], vb[3][i]);
+            o[nt][0] *= alpha[0];
+            o[nt][1] *= alpha[0];
+            o[nt][2] *= alpha[1];
+            o[nt][3] *= alpha[1];
+            mma16816(o[nt], pa0, pa1, pa2, pa3, b0, b1);
+            mma16816(o[nt], pl0, pl1, pl2, pl3, b0, b1);
+        }
+    }
+}
+
+SPEC_DEV unsigned long long row_mask(const AttendSpan& s, int b, int j) {
+    if (s.tree == 0) return j >= 63 ? ~0ull : (2ull << j) - 1ull;
+    if (s.tree == 1) return s.mask[j];
+    unsigned long long mk = 0ull;
+    const int* par = s.dev_parent + (size_t)b * kMaxSeqRows;
+    for (int x = j, n = 0; x >= 0 && n < kMaxSeqRows; x = par[x], ++n) mk |= 1ull << x;
+    return mk;
+}
+
+template <int HD, bool QF32>
+__global__ void __launch_bounds__(kRowThreads)
+attend_rows_kernel(const __grid_constant__ AttendArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    constexpr int KS = HD / 16, VD = HD / 8;
+    extern __shared__ float smf[];
+    uint4* sQ = reinterpret_cast<uint4*>(smf);                              // [QF32 ? 2 : 1][KS][32]
+    float* sState = smf + (QF32 ? 2 : 1) * KS * 32 * 4;                     // [4 warps][16][HD + 2]
+    unsigned long long* sMask = reinterpret_cast<unsigned long long*>(sState + 4 * 16 * (HD + 2));   // [16]
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5, gq = lane >> 2, cq = lane & 3;
+    const int G = a.H / a.Hkv;
+    // the prompt's blocks first (the longer ones), then the sequences' own
+    int id = blockIdx.x;
+    const int n_pre = a.pre_splits * a.pre_qb * a.Hkv;
+    const bool is_pre = id < n_pre;
+    int b = 0, list_row0 = 0, rows = a.span.T;
+    if (!is_pre) id -= n_pre;
+    const int g = id % a.Hkv;
+    id /= a.Hkv;
+    const int qb = id % (is_pre ? a.pre_qb : a.own_qb);
+    id /= is_pre ? a.pre_qb : a.own_qb;
+    int split, n_splits, n_ctx, n_keys, range;
+    if (is_pre) {
+        split = id;
+        n_splits = a.pre_splits;
+        n_keys = n_ctx = min(a.pre.len[a.pre_seq], a.pre.cap);
+        range = split;
+    } else {
+        split = id % a.own_splits;
+        b = id / a.own_splits;
+        n_splits = a.own_splits;
+        list_row0 = a.span.row0[b];
+        rows = a.span.row0[b + 1] - list_row0;
+        n_ctx = a.own.len[b] + a.span.extra;
+        n_keys = min(n_ctx + rows, a.own.cap);
+        if (n_ctx + rows > a.own.cap && rows > 0 && t == 0) dev_error(a.err, SPEC_DEVERR_CAPACITY);
+        range = a.own_range0 + split;
+    }
+    const int q0 = qb * 16, nq = min(16, rows * G - q0);
+    if (nq <= 0) return;
+    int chunk = (n_keys + n_splits - 1) / n_splits;
+    chunk = (chunk + 63) / 64 * 64;
+    const int k_begin = min(n_keys, split * chunk), k_end = min(n_keys, k_begin + chunk);
+    const CacheView& cv = is_pre ? a.pre : a.own;
+    const int seq = is_pre ? a.pre_seq : b;
+    load_queries<HD, QF32>(a, cv.q8, g, G, list_row0, q0, nq, sQ);
+    if (t < 16) sMask[t] = !is_pre && t < nq ? row_mask(a.span, b, (q0 + t) / G) : 0ull;
+    __syncthreads();
+    float o[VD][4], m_r[2] = {-INFINITY, -INFINITY}, l_r[2] = {0.f, 0.f};
+#pragma unroll
+    for (int nt = 0; nt < VD; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
+    if (cv.q8) attend_range<HD, true, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, sMask[gq], sMask[gq + 8], sQ, o, m_r, l_r);
+    else attend_range<HD, false, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, sMask[gq], sMask[gq + 8], sQ, o, m_r, l_r);
+    // warp states -> shared: rows g and g + 8, dims VD * 2c + nt and VD * (2c + 1) + nt
+#pragma unroll
+    for (int rr = 0; rr < 2; ++rr) {
+        l_r[rr] += __shfl_xor_sync(0xffffffffu, l_r[rr], 1);
+        l_r[rr] += __shfl_xor_sync(0xffffffffu, l_r[rr], 2);
+        float* st = sState + ((size_t)warp * 16 + gq + 8 * rr) * (HD + 2);
+        if (cq == 0) { st[0] = m_r[rr]; st[1] = l_r[rr]; }
+#pragma unroll
+        for (int nt = 0; nt < VD; ++nt) {
+            st[2 + VD * (2 * cq) + nt] = o[nt][2 * rr];
+            st[2 + VD * (2 * cq + 1) + nt] = o[nt][2 * rr + 1];
+        }
+    }
+    __syncthreads();
+    const size_t TH = (size_t)a.span.T * a.H;
+    for (int i = t; i < nq * HD; i += kRowThreads) {
+        const int r = i / HD, d = i % HD, qg = q0 + r;
+        float M = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) M = fmaxf(M, sState[((size_t)w * 16 + r) * (HD + 2)]);
+        float L = 0.f, O = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float* st = sState + ((size_t)w * 16 + r) * (HD + 2);
+            if (st[0] == -INFINITY) continue;
+            const float wt = ex2(st[0] - M);
+            L += st[1] * wt;
+            O += st[2 + d] * wt;
+        }
+        const size_t vec = range * TH + (size_t)(list_row0 + qg / G) * a.H + g * G + qg % G;
+        a.part_o[vec * HD + d] = O;
+        if (d == 0) { a.part_ml[2 * vec] = M; a.part_ml[2 * vec + 1] = L; }
+    }
+}
+
+// One warp a (row, head): the ranges' states in range order (the prompt's, then the sequence's own).
+struct JoinArgs {
+    const float* part_o; const float* part_ml;
+    int ranges, TH, H;
+    __nv_bfloat16* out;
+    long long stride;
+    size_t lo;                        // 0: one bf16 row; else hi rows and lo rows at this offset
+};
+
+template <int HD>
+__global__ void __launch_bounds__(128)
+attend_join_kernel(const JoinArgs a) {
+    pdl_wait();
+    pdl_trigger();
+    constexpr int E = HD / 32;
+    const int v = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (v >= a.TH) return;
+    float M = -INFINITY;
+    for (int s = lane; s < a.ranges; s += 32) M = fmaxf(M, a.part_ml[2 * ((size_t)s * a.TH + v)]);
+    M = warp_max(M);
+    float L = 0.f, O[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) O[e] = 0.f;
+    if (M != -INFINITY) {
+        for (int s0 = 0; s0 < a.ranges; s0 += 32) {
+            float w = 0.f, l = 0.f;
+            if (s0 + lane < a.ranges) {
+                const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * ((size_t)(s0 + lane) * a.TH + v));
+                w = ex2(ml.x - M);
+                l = ml.y * w;
+            }
+            L += warp_sum(l);
+            const int n = min(32, a.ranges - s0);
+#pragma unroll 4
+            for (int s = 0; s < n; ++s) {
+                const float ws = __shfl_sync(0xffffffffu, w, s);
+                const float* src = a.part_o + ((size_t)(s0 + s) * a.TH + v) * HD + lane * E;
+                float x[E];
+                if (E == 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(src);
+                    x[0] = f.x; x[1] = f.y; x[E - 2] = f.z; x[E - 1] = f.w;
+                } else {
+                    const float2 f = *reinterpret_cast<const float2*>(src);
+                    x[0] = f.x; x[1] = f.y;
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e) O[e] = ws > 0.f ? fmaf(ws, x[e], O[e]) : O[e];
+            }
+        }
+    }
+    const float inv = 1.0f / L;
+    const long long o = (v / a.H) * a.stride + (v % a.H) * HD + lane * E;
+    if (a.lo) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) store_act(a.out, (size_t)(o + e), a.lo, O[e] * inv);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) a.out[o + e] = __float2bfloat16_rn(O[e] * inv);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+
+CacheView cache_view(const spec_kv* kv, int layer) {
+    const size_t off = (size_t)layer * kv->n_pages * kv->m->cfg.n_kv_heads * kv->page;
+    CacheView v{};
+    v.k = (const char*)kv->k + off * kv->m->cfg.head_dim * kv->elem;
+    v.v = (const char*)kv->v + off * kv->m->cfg.head_dim * kv->elem;
+    v.ke = kv->q8 ? kv->ke + off : nullptr;
+    v.ve = kv->q8 ? kv->ve + off : nullptr;
+    v.pages = kv->pages();
+    v.len = kv->len;
+    v.cap = kv->max_ctx;
+    v.q8 = kv->q8;
+    return v;
+}
+
+int make_span(AttendSpan* s, int batch, const int* n_rows, int extra, const int* tree_parent, const int* dev_parent) {
+    s->batch = batch;
+    s->extra = extra;
+    s->tree = dev_parent ? 2 : (tree_parent ? 1 : 0);
+    s->dev_parent = dev_parent;
+    s->max_rows = 0;
+    int r = 0;
+    for (int b = 0; b < batch; ++b) {
+        s->row0[b] = (short)r;
+        r += n_rows[b];
+        s->max_rows = std::max(s->max_rows, n_rows[b]);
+    }
+    s->row0[batch] = (short)r;
+    s->T = r;
+    if (tree_parent && !dev_parent) {
+        for (int j = 0; j < s->max_rows; ++j)
+            s->mask[j] = (1ull << j) | (j > 0 ? s->mask[tree_parent[j]] : 0ull);
+    }
+    return SPEC_OK;
+}
+
+static size_t rows_smem(int hd, bool qf32) {
+    return (qf32 ? 2 : 1) * (hd / 16) * 32 * 16 + 4 * 16 * (hd + 2) * sizeof(float) + 16 * 8;
+}
+
+// Query vectors whose partial states fit: every launch shape below keeps to
+// (ranges) x (T * H) <= 2 x 16 x 512 + 2 T H, and the tile kernel to 2 x 152 tiles of 128 more.
+size_t attend_floats_needed(const spec_model* m) {
+    const size_t th = (size_t)m->cfg.max_rows * m->cfg.n_heads;
+    return (2 * 16 * 512 + 2 * 2 * (size_t)m->num_sms * 128 + 4 * th) * (m->cfg.head_dim + 2);
+}
+
+int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q, int q_f32, long long q_stride,
+                  float scale, const AttendOut& out, cudaStream_t st) {
+    spec_model* m = kv->m;
+    const spec_model_config& c = m->cfg;
+    const int hd = c.head_dim, H = c.n_heads, Hkv = c.n_kv_heads, G = H / Hkv;
+    const spec_kv* pre = kv->prefix;
+    AttendArgs a{};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.c = scale * 1.4426950408889634f;
+    a.own = cache_view(kv, layer);
+    if (pre) a.pre = cache_view(pre, layer);
+    a.pre_seq = kv->prefix_seq;
+    a.H = H;
+    a.Hkv = Hkv;
+    a.span = span;
+    a.err = m->err;
+    const int TH = span.T * H;
+    const size_t fit = m->attend_part_floats / (hd + 2) / TH;      // ranges the workspace holds
+    // key ranges: as many as about three resident CTAs an SM take, by each part's share of the keys
+    a.own_qb = (span.max_rows * G + 15) / 16;
+    a.pre_qb = pre ? (span.T * G + 15) / 16 : 0;
+    const long long own_blocks = (long long)span.batch * Hkv * a.own_qb, pre_blocks = (long long)Hkv * a.pre_qb;
+    const long long keys = own_blocks * kv->max_ctx + pre_blocks * (pre ? pre->max_ctx : 0);
+    const long long per = std::max<long long>(kMinKeys, keys / (3 * m->num_sms) + 1);
+    auto splits = [&](long long blocks, long long ctx) {
+        if (blocks == 0) return 0;
+        return (int)std::max<long long>(1, std::min<long long>({(ctx + per - 1) / per, 64, (16 * 512) / (16 * blocks) + 1}));
+    };
+    a.own_splits = splits(own_blocks, kv->max_ctx);
+    a.pre_splits = splits(pre_blocks, pre ? pre->max_ctx : 0);
+    a.own_range0 = a.pre_splits;
+    const int ranges = a.own_splits + a.pre_splits;
+    if ((size_t)ranges > fit) return set_error(SPEC_ERR_CAPACITY, "attention workspace too small");
+    a.part_o = m->attend_part;
+    a.part_ml = m->attend_part + (size_t)ranges * TH * hd;
+    const dim3 grid((unsigned)(a.pre_splits * pre_blocks + a.own_splits * own_blocks));
+    const size_t smem = rows_smem(hd, q_f32);
+    void (*f)(AttendArgs) = hd == 128 ? (q_f32 ? attend_rows_kernel<128, true> : attend_rows_kernel<128, false>)
+                                      : (q_f32 ? attend_rows_kernel<64, true> : attend_rows_kernel<64, false>);
+    const int slot = prof_start(m, st);
+    cudaError_t e = launch_k(m->pdl, f, grid, dim3(kRowThreads), smem, st, a);
+    SPEC_TRY(check_cuda(e, "attention rows launch"));
+    JoinArgs j{};
+    j.part_o = a.part_o;
+    j.part_ml = a.part_ml;
+    j.ranges = ranges;
+    j.TH = TH;
+    j.H = H;
+    j.out = out.p;
+    j.stride = out.stride;
+    j.lo = out.lo;
+    e = launch_k(m->pdl, hd == 128 ? attend_join_kernel<128> : attend_join_kernel<64>, dim3((TH + 3) / 4), dim3(128), 0, st, j);
+    m->launches += 2;
+    prof_stop(m, slot, st, PROF_ATTN, 0.0);
+    return check_cuda(e, "attention join launch");
+}
+
+}  // namespace spec
+
+using namespace spec;
+
+extern "C" int spec_kv_set_prefix(spec_kv* kv, spec_kv* prefix, int32_t seq) {
+    if (!kv) return set_error(SPEC_ERR_ARG, "spec_kv_set_prefix: null cache");
+    if (prefix) {
+        if (prefix == kv) return set_error(SPEC_ERR_ARG, "spec_kv_set_prefix: a cache cannot be its own prefix");
+        if (prefix->m != kv->m) return set_error(SPEC_ERR_ARG, "spec_kv_set_prefix: cache of another model");
+        if (seq < 0 || seq >= prefix->batch) return set_error(SPEC_ERR_ARG, "spec_kv_set_prefix: seq out of range");
+        if (prefix->prefix || prefix->prefix_lost)
+            return set_error(SPEC_ERR_UNSUPPORTED, "spec_kv_set_prefix: the prefix has a prefix of its own");
+        if (!kv->users.empty()) return set_error(SPEC_ERR_UNSUPPORTED, "spec_kv_set_prefix: the cache is a prefix itself");
+        if (!kv->m->bf16) return set_error(SPEC_ERR_UNSUPPORTED, "spec_kv_set_prefix: bf16 models only");
+    }
+    kv_detach_prefix(kv);
+    if (prefix) {
+        try {
+            prefix->users.push_back(kv);
+        } catch (...) {
+            return set_error(SPEC_ERR_CAPACITY, "spec_kv_set_prefix: out of host memory");
+        }
+        kv->prefix = prefix;
+        kv->prefix_seq = seq;
+    }
+    return SPEC_OK;
+}
+
+extern "C" int spec_attend(spec_kv* kv, int32_t layer, int32_t batch, const int32_t* n_rows, const void* q,
+                           int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           const int32_t* tree_parent, void* out, int64_t out_stride, void* stream) {
+    if (!kv || !n_rows) return set_error(SPEC_ERR_ARG, "spec_attend: null pointer");
+    if ((k == nullptr) != (v == nullptr)) return set_error(SPEC_ERR_ARG, "spec_attend: k and v go together");
+    spec_model* m = kv->m;
+    const spec_model_config& c = m->cfg;
+    if (!m->bf16) return set_error(SPEC_ERR_UNSUPPORTED, "spec_attend: bf16 models only");
+    SPEC_TRY(kv_check_prefix(kv, "spec_attend"));
+    if (layer < 0 || layer >= c.n_layers) return set_error(SPEC_ERR_ARG, "spec_attend: layer out of range");
+    if (batch < 1 || batch > kv->batch) return set_error(SPEC_ERR_ARG, "spec_attend: bad batch");
+    int T = 0, n_max = 0;
+    for (int b = 0; b < batch; ++b) {
+        if (n_rows[b] < 0 || n_rows[b] > kMaxSeqRows) return set_error(SPEC_ERR_ARG, "spec_attend: n_rows[b] must be in [0, 64]");
+        T += n_rows[b];
+        n_max = std::max(n_max, (int)n_rows[b]);
+    }
+    if (T > c.max_rows) return set_error(SPEC_ERR_CAPACITY, "spec_attend: sum of n_rows > max_rows");
+    const int64_t qd = (int64_t)c.n_heads * c.head_dim, kd = (int64_t)c.n_kv_heads * c.head_dim;
+    if (q_stride < qd || out_stride < qd || (k && (k_stride < kd || v_stride < kd)))
+        return set_error(SPEC_ERR_ARG, "spec_attend: a row stride is shorter than its row");
+    if (tree_parent) {
+        if (n_max > 0 && tree_parent[0] != -1) return set_error(SPEC_ERR_ARG, "tree_parent[0] must be -1");
+        for (int i = 1; i < n_max; ++i)
+            if (tree_parent[i] < 0 || tree_parent[i] >= i) return set_error(SPEC_ERR_ARG, "tree_parent[i] must be in [0, i)");
+        for (int b = 0; b < batch; ++b)
+            if (n_rows[b] != n_max) return set_error(SPEC_ERR_ARG, "tree mode: every sequence has the tree's node count");
+    }
+    if (T == 0) return SPEC_OK;
+    if (!q || !out) return set_error(SPEC_ERR_ARG, "spec_attend: null pointer");
+    cudaStream_t st = (cudaStream_t)stream;
+    AttendSpan span{};
+    SPEC_TRY(make_span(&span, batch, n_rows, 0, tree_parent, nullptr));
+    if (k) {
+        SPEC_TRY(kv_ensure_pages(kv, batch, n_rows, true, st));
+        SPEC_TRY(launch_append(kv, layer, span, k, k_stride, v, v_stride, st));
+    }
+    const AttendOut o{(__nv_bfloat16*)out, out_stride, 0};
+    return launch_attend(kv, layer, span, q, 0, q_stride, 1.0f / sqrtf((float)c.head_dim), o, st);
+}

@@ -16,6 +16,7 @@
 #include <string>
 #include <vector>
 
+#include "attend.cuh"
 #include "model.cuh"
 #include "stats.cuh"
 
@@ -68,6 +69,11 @@ __global__ void to_f32_kernel(const T* __restrict__ src, float* __restrict__ dst
     if (i < n) dst[i] = to_f32<T>(src[i]);
 }
 
+__global__ void iota_kernel(int* dst, int n) {
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < n) dst[i] = i;
+}
+
 // Tile-major copy of a bf16 GEMM weight [N][K] (N a multiple of 128, K of 64).
 // Block (tile, k-block) -- 128 rows x 64 columns -- becomes 16 contiguous KB in
 // the order the tensor-core operand takes in shared memory: row r at r * 128
@@ -113,7 +119,10 @@ struct PlanArgs {
 // draft pass j: one row per sequence at slot / position s_b + j, seeing slots
 // [0, s_b + j] (the earlier passes' rows count as context: base s_b + j,
 // local row 0).
-__global__ void plan_kernel(PlanArgs a, RowPlan plan, const int* __restrict__ len, int T, int* err) {
+// Positions of a cache that continues a prompt start at the prompt's length
+// (`before`, null: 0).
+__global__ void plan_kernel(PlanArgs a, RowPlan plan, const int* __restrict__ len, const int* __restrict__ before,
+                            int T, int* err) {
     pdl_wait();
     pdl_trigger();
     const int t = blockIdx.x * blockDim.x + threadIdx.x;
@@ -164,7 +173,7 @@ __global__ void plan_kernel(PlanArgs a, RowPlan plan, const int* __restrict__ le
     } else if (p.mode == 1) {
         dep = p.depth[j];
     }
-    plan.row_pos[t] = s + dep;
+    plan.row_pos[t] = (before ? *before : 0) + s + dep;
 }
 
 // First residual rows of a forward: from the layer-L state (h_in) or the token
@@ -521,15 +530,24 @@ static GemmStep head_step(spec_model* m, spec_kv* kv, const HeadSpec& hs) {
 //   [QKV lo]  attn  [O, gate|up, down, QKV lo+1]  attn  ...  [O, gate|up, down, head]
 // head_follows picks the gain of the last down projection's next-input
 // (the final norm when the LM head reads it).
-static int run_layers(spec_model* m, spec_kv* kv, int T, int batch, int max_rows_per_seq, int lo, int hi,
-                      int tree, bool head_follows, const HeadSpec* head, cudaStream_t st) {
+// `p` is the plan's: caches in 8 bits or with a shared prompt take the attention of attend.cu.
+static int run_layers(spec_model* m, spec_kv* kv, const PlanParams& p, int T, int batch, int max_rows_per_seq, int lo,
+                      int hi, int tree, bool head_follows, const HeadSpec* head, cudaStream_t st) {
     const spec_model_config& c = m->cfg;
     const int qdim = c.n_heads * c.head_dim;
+    const bool by_range = kv->by_range();
+    AttendSpan span{};
+    if (by_range) {
+        int ones[kMaxPlanBatch];
+        for (int b = 0; b < batch; ++b) ones[b] = 1;
+        SPEC_TRY(make_span(&span, batch, p.mode == 2 ? ones : p.n_rows, p.mode == 2 ? p.pass : 0,
+                           tree == 1 ? p.parent : nullptr, tree == 2 ? m->plan.tree_parent : nullptr));
+    }
     // attention as the first phase of the chain that follows it (one launch per layer)
     // (the phase reads one tree for the batch: a tree a sequence takes the separate kernel)
-    const bool fused = tree != 2 && T <= kMaxTPad && attn_phase_ok(m, kv, batch, max_rows_per_seq);
+    const bool fused = !by_range && tree != 2 && T <= kMaxTPad && attn_phase_ok(m, kv, batch, max_rows_per_seq);
     // otherwise, for a few query vectors per (sequence, KV head), the TMA-ring kernel
-    const bool ring = !fused && tree != 2 && m->attn_ring && attn_ring_fits(m, kv, batch, max_rows_per_seq);
+    const bool ring = !by_range && !fused && tree != 2 && m->attn_ring && attn_ring_fits(m, kv, batch, max_rows_per_seq);
     GemmStep pend[5];
     int np = 0;
     for (int l = lo; l < hi; ++l) {
@@ -540,11 +558,26 @@ static int run_layers(spec_model* m, spec_kv* kv, int T, int batch, int max_rows
             EpiParams q = e;
             q.kind = EPI_QKV;
             q.N = m->qkv_n;
+            if (kv->q8) {
+                // the new K and V rows to the staging rows (row r is the one slot of "sequence" r)
+                q.plan.row_seq = m->row_ids;
+                q.plan.row_slot = m->row_zeros;
+                q.kc = m->stage_kv;
+                q.vc = m->stage_kv + (size_t)c.max_rows * c.n_kv_heads * c.head_dim;
+                q.kv_ctx = 1;
+                q.kvp = KVPages{nullptr, 1, 1, 0, -1};
+            }
             pend[np++] = GemmStep{GemmLaunch{&L.tm_qkv, nullptr, L.qkv, m->x_in, c.d_model, m->qkv_n, c.d_model}, q, 0};
             SPEC_TRY(launch_gemm_chain(m, pend, np, st));
             np = 0;
         }
-        if (fused) {   // attention phase of the chain that follows
+        if (by_range) {
+            const int kd = c.n_kv_heads * c.head_dim;
+            if (kv->q8)
+                SPEC_TRY(launch_append(kv, l, span, m->stage_kv, kd, m->stage_kv + (size_t)c.max_rows * kd, kd, st));
+            const AttendOut o{(__nv_bfloat16*)m->x_attn, qdim, (size_t)m->max_rows_pad * qdim};
+            SPEC_TRY(launch_attend(kv, l, span, m->q, 1, qdim, 1.0f, o, st));    // the queries come scaled
+        } else if (fused) {   // attention phase of the chain that follows
             GemmStep at{};
             at.kind = PH_ATTN;
             at.g.tmW = &kv->tm_k;
@@ -621,7 +654,7 @@ static int run_layers(spec_model* m, spec_kv* kv, int T, int batch, int max_rows
     return SPEC_OK;
 }
 
-static int launch_plan(spec_model* m, const PlanParams& p, int T, const int* len, cudaStream_t st,
+static int launch_plan(spec_model* m, const PlanParams& p, int T, const spec_kv* kv, cudaStream_t st,
                        const int* dev_parent = nullptr, int dev_stride = 0) {
     PlanArgs a{};
     a.p = p;
@@ -633,8 +666,9 @@ static int launch_plan(spec_model* m, const PlanParams& p, int T, const int* len
         r += (p.mode == 2) ? 1 : p.n_rows[b];
     }
     const int n = std::max(std::max(T, p.batch), kMaxSeqRows);
-    cudaError_t le = launch_k(m->pdl, plan_kernel, dim3((n + 127) / 128), dim3(128), 0, st, a, m->plan, len, T,
-                              m->err);
+    cudaError_t le = launch_k(m->pdl, plan_kernel, dim3((n + 127) / 128), dim3(128), 0, st, a, m->plan,
+                              (const int*)kv->len, kv->prefix ? (const int*)kv->prefix->len + kv->prefix_seq : nullptr,
+                              T, m->err);
     if (le != cudaSuccess) return check_cuda(le, "plan launch");
     ++m->launches;
     return check_cuda(cudaGetLastError(), "plan launch");
@@ -659,6 +693,20 @@ static int launch_prologue(spec_model* m, int T, const float* h_in, int h_stride
 }
 
 static size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+void kv_detach_prefix(spec_kv* kv) {
+    if (kv->prefix) {
+        std::vector<spec_kv*>& u = kv->prefix->users;
+        u.erase(std::remove(u.begin(), u.end(), kv), u.end());
+    }
+    kv->prefix = nullptr;
+    kv->prefix_lost = false;
+}
+
+int kv_check_prefix(const spec_kv* kv, const char* what) {
+    if (!kv->prefix_lost) return SPEC_OK;
+    return set_error(SPEC_ERR_ARG, std::string(what) + ": the cache's prefix was destroyed (spec_kv_set_prefix)");
+}
 
 }  // namespace spec
 
@@ -842,6 +890,11 @@ extern "C" int spec_model_create(const spec_model_config* cfg, const void* const
     const size_t w_pkv = take(64);
     const size_t w_plan = take((size_t)(4 * R + 3 * c.max_batch + (2 * kMaxSeqRows + kTreeStage) * c.max_batch + 64) * 4);
     const size_t w_dl = take((size_t)c.max_batch * V * 4);
+    m->attend_part_floats = m->bf16 ? attend_floats_needed(m) : 0;
+    const size_t w_at = take(m->attend_part_floats * 4);
+    const size_t stage = m->bf16 ? (size_t)R * c.n_kv_heads * c.head_dim : 0;
+    const size_t w_st = take(2 * stage * 2);
+    const size_t w_id = take((size_t)2 * R * 4);
     m->ws_bytes = off;
     if ((rc = check_cuda(cudaMalloc(&m->ws, off), "cudaMalloc(workspace)"))) return fail(rc);
     if ((rc = check_cuda(cudaMemsetAsync(m->ws, 0, off, st), "workspace clear"))) return fail(rc);
@@ -861,6 +914,12 @@ extern "C" int spec_model_create(const spec_model_config* cfg, const void* const
     m->err = (int*)(S + w_err);
     m->prof_kv = (unsigned long long*)(S + w_pkv);
     m->draft_lg = (float*)(S + w_dl);
+    m->attend_part = (float*)(S + w_at);
+    m->stage_kv = (__nv_bfloat16*)(S + w_st);
+    m->row_ids = (int*)(S + w_id);
+    m->row_zeros = m->row_ids + R;
+    iota_kernel<<<(R + 255) / 256, 256, 0, st>>>(m->row_ids, R);
+    if ((rc = check_cuda(cudaGetLastError(), "row ids"))) return fail(rc);
     int* pl = (int*)(S + w_plan);
     m->plan.row_seq = pl; pl += R;
     m->plan.row_slot = pl; pl += R;
@@ -960,7 +1019,8 @@ extern "C" int spec_set_exit_layer(spec_model* m, int32_t exit_layer) {
 }
 
 // page = 0: contiguous cache (one page of max_ctx slots per sequence)
-static int kv_create(spec_model* m, int32_t batch, int32_t max_ctx, int32_t page, int32_t n_pages, spec_kv** out) {
+static int kv_create(spec_model* m, int32_t batch, int32_t max_ctx, int32_t page, int32_t n_pages, bool q8,
+                     spec_kv** out) {
     *out = nullptr;
     if (batch < 1 || max_ctx < 1) return set_error(SPEC_ERR_ARG, "spec_kv_create: bad sizes");
     if (batch > m->cfg.max_batch) return set_error(SPEC_ERR_CAPACITY, "spec_kv_create: batch > max_batch");
@@ -969,10 +1029,14 @@ static int kv_create(spec_model* m, int32_t batch, int32_t max_ctx, int32_t page
     kv->batch = batch;
     kv->max_ctx = max_ctx;
     kv->paged = page > 0;
-    kv->page = kv->paged ? page : max_ctx;
+    // 8-bit rows are moved in blocks of 64 slots, so a contiguous 8-bit cache is whole blocks long
+    kv->page = kv->paged ? page : (q8 ? (max_ctx + 63) / 64 * 64 : max_ctx);
     kv->max_pages = kv->paged ? (max_ctx + page - 1) / page : 1;
     kv->n_pages = kv->paged ? n_pages : batch;
-    const size_t bytes = (size_t)m->cfg.n_layers * kv->n_pages * m->cfg.n_kv_heads * kv->page * m->cfg.head_dim * m->elem;
+    kv->q8 = q8;
+    kv->elem = q8 ? 1 : m->elem;
+    const size_t rows = (size_t)m->cfg.n_layers * kv->n_pages * m->cfg.n_kv_heads * kv->page;
+    const size_t bytes = rows * m->cfg.head_dim * kv->elem;
     const size_t tab = (size_t)batch * kv->max_pages;
     int rc = check_cuda(cudaMalloc(&kv->k, bytes), "cudaMalloc(K cache)");
     if (!rc) rc = check_cuda(cudaMalloc(&kv->v, bytes), "cudaMalloc(V cache)");
@@ -981,6 +1045,10 @@ static int kv_create(spec_model* m, int32_t batch, int32_t max_ctx, int32_t page
     if (!rc) rc = check_cuda(cudaMemset(kv->k, 0, bytes), "clear K");
     if (!rc) rc = check_cuda(cudaMemset(kv->v, 0, bytes), "clear V");
     if (!rc) rc = check_cuda(cudaMemset(kv->len, 0, (size_t)batch * 4), "clear lengths");
+    if (!rc && q8) rc = check_cuda(cudaMalloc(&kv->ke, rows), "cudaMalloc(K exponents)");
+    if (!rc && q8) rc = check_cuda(cudaMalloc(&kv->ve, rows), "cudaMalloc(V exponents)");
+    if (!rc && q8) rc = check_cuda(cudaMemset(kv->ke, 3, rows), "clear K exponents");     // 2^-124, as a row of zeros
+    if (!rc && q8) rc = check_cuda(cudaMemset(kv->ve, 3, rows), "clear V exponents");
     if (!rc) {
         // contiguous: sequence b is page b; paged: no page held, every page free
         std::vector<int> t(tab, -1);
@@ -997,7 +1065,7 @@ static int kv_create(spec_model* m, int32_t batch, int32_t max_ctx, int32_t page
             kv->free_top = kv->free_pages + n_pages;
         }
     }
-    if (!rc && !make_kv_tmaps(kv)) rc = set_error(SPEC_ERR_CUDA, "spec_kv_create: K/V tensor maps");
+    if (!rc && !q8 && !make_kv_tmaps(kv)) rc = set_error(SPEC_ERR_CUDA, "spec_kv_create: K/V tensor maps");
     if (rc) {
         spec_kv_destroy(kv);
         return rc;
@@ -1008,7 +1076,7 @@ static int kv_create(spec_model* m, int32_t batch, int32_t max_ctx, int32_t page
 
 extern "C" int spec_kv_create(spec_model* m, int32_t batch, int32_t max_ctx, spec_kv** out) {
     if (!m || !out) return set_error(SPEC_ERR_ARG, "spec_kv_create: null pointer");
-    return kv_create(m, batch, max_ctx, 0, 0, out);
+    return kv_create(m, batch, max_ctx, 0, 0, false, out);
 }
 
 extern "C" int spec_kv_create_paged(spec_model* m, int32_t batch, int32_t max_ctx, int32_t page, int32_t n_pages,
@@ -1018,7 +1086,19 @@ extern "C" int spec_kv_create_paged(spec_model* m, int32_t batch, int32_t max_ct
     if (page < 64 || (page & (page - 1)) != 0)
         return set_error(SPEC_ERR_ARG, "spec_kv_create_paged: page must be a power of two, at least 64");
     if (n_pages < 1) return set_error(SPEC_ERR_ARG, "spec_kv_create_paged: n_pages must be positive");
-    return kv_create(m, batch, max_ctx, page, n_pages, out);
+    return kv_create(m, batch, max_ctx, page, n_pages, false, out);
+}
+
+extern "C" int spec_kv_create_q8(spec_model* m, int32_t batch, int32_t max_ctx, int32_t page, int32_t n_pages,
+                                 spec_kv** out) {
+    if (!m || !out) return set_error(SPEC_ERR_ARG, "spec_kv_create_q8: null pointer");
+    *out = nullptr;
+    if (!m->bf16) return set_error(SPEC_ERR_UNSUPPORTED, "spec_kv_create_q8: bf16 models only");
+    if (page != 0 && (page < 64 || (page & (page - 1)) != 0))
+        return set_error(SPEC_ERR_ARG, "spec_kv_create_q8: page must be 0 (contiguous) or a power of two, at least 64");
+    if (page != 0 && n_pages < 1) return set_error(SPEC_ERR_ARG, "spec_kv_create_q8: n_pages must be positive");
+    if (max_ctx > INT_MAX - 63) return set_error(SPEC_ERR_ARG, "spec_kv_create_q8: bad sizes");
+    return kv_create(m, batch, max_ctx, page, n_pages, true, out);
 }
 
 extern "C" int spec_kv_free_pages(spec_kv* kv, int32_t* host_free, void* stream) {
@@ -1041,11 +1121,11 @@ extern "C" int spec_kv_read_page(spec_kv* kv, int32_t which, int32_t layer, int3
                                  void* stream) {
     if (!kv || !host_dst) return set_error(SPEC_ERR_ARG, "spec_kv_read_page: null pointer");
     const spec_model_config& c = kv->m->cfg;
-    if (which < 0 || which > 1 || layer < 0 || layer >= c.n_layers || page < 0 || page >= kv->n_pages)
+    if (which < 0 || which > (kv->q8 ? 3 : 1) || layer < 0 || layer >= c.n_layers || page < 0 || page >= kv->n_pages)
         return set_error(SPEC_ERR_ARG, "spec_kv_read_page: which, layer or page out of range");
-    const size_t page_bytes = (size_t)c.n_kv_heads * kv->page * c.head_dim * kv->m->elem;
-    const char* src = static_cast<const char*>(which ? kv->v : kv->k) +
-                      ((size_t)layer * kv->n_pages + page) * page_bytes;
+    const size_t page_bytes = (size_t)c.n_kv_heads * kv->page * (which < 2 ? c.head_dim * kv->elem : 1);
+    const void* base[4] = {kv->k, kv->v, kv->ke, kv->ve};
+    const char* src = static_cast<const char*>(base[which]) + ((size_t)layer * kv->n_pages + page) * page_bytes;
     SPEC_CUDA(cudaMemcpyAsync(host_dst, src, page_bytes, cudaMemcpyDeviceToHost, (cudaStream_t)stream), "read page");
     SPEC_CUDA(cudaStreamSynchronize((cudaStream_t)stream), "read page sync");
     return SPEC_OK;
@@ -1053,6 +1133,10 @@ extern "C" int spec_kv_read_page(spec_kv* kv, int32_t which, int32_t layer, int3
 
 extern "C" void spec_kv_destroy(spec_kv* kv) {
     if (!kv) return;
+    kv_detach_prefix(kv);
+    for (spec_kv* u : kv->users) { u->prefix = nullptr; u->prefix_lost = true; }
+    cudaFree(kv->ke);
+    cudaFree(kv->ve);
     cudaFree(kv->k);
     cudaFree(kv->v);
     cudaFree(kv->len);
@@ -1097,6 +1181,7 @@ static int kv_copy(spec_kv* kv, int32_t seq, int32_t layer0, int32_t n_layers, i
         need[seq] = slot0 + n_slots;
         SPEC_TRY(kv_ensure_pages(kv, seq + 1, need, false, st));
     }
+    if (kv->q8) return launch_kv8_copy(kv, seq, layer0, n_layers, slot0, n_slots, k, v, to_cache != 0, st);
     for (int which = 0; which < 2; ++which) {
         void* cache = which ? kv->v : kv->k;
         void* buf = which ? v : k;
@@ -1125,6 +1210,7 @@ extern "C" int spec_prefill(spec_model* m, spec_kv* kv, int32_t seq, const int32
                             float* last_logits, int32_t* next_tok, void* stream) {
     if (!m || !kv || !tokens) return set_error(SPEC_ERR_ARG, "spec_prefill: null pointer");
     if (kv->m != m) return set_error(SPEC_ERR_ARG, "spec_prefill: cache of another model");
+    SPEC_TRY(kv_check_prefix(kv, "spec_prefill"));
     if (seq < 0 || seq >= kv->batch || n < 1) return set_error(SPEC_ERR_ARG, "spec_prefill: bad seq or n");
     const spec_model_config& c = m->cfg;
     cudaStream_t st = (cudaStream_t)stream;
@@ -1136,7 +1222,7 @@ extern "C" int spec_prefill(spec_model* m, spec_kv* kv, int32_t seq, const int32
         p.mode = 0;
         p.n_rows[seq] = T;
         SPEC_TRY(kv_ensure_pages(kv, seq + 1, p.n_rows, true, st));
-        SPEC_TRY(launch_plan(m, p, T, kv->len, st));
+        SPEC_TRY(launch_plan(m, p, T, kv, st));
         SPEC_TRY(launch_prologue(m, T, nullptr, 0, tokens + done, 0, 0, 0, st));
         const bool last = done + T >= n;
         const bool head = last && (last_logits || next_tok);
@@ -1151,7 +1237,7 @@ extern "C" int spec_prefill(spec_model* m, spec_kv* kv, int32_t seq, const int32
         hs.cand_stride = 0;
         hs.cand_col = 0;
         hs.batch = seq + 1;
-        SPEC_TRY(run_layers(m, kv, T, seq + 1, T, 0, c.n_layers, 0, head, head ? &hs : nullptr, st));
+        SPEC_TRY(run_layers(m, kv, p, T, seq + 1, T, 0, c.n_layers, 0, head, head ? &hs : nullptr, st));
         launch_k(m->pdl, add_len_kernel, dim3(1), dim3(32), 0, st, kv->len, seq, T, kv->max_ctx, m->err);
         ++m->launches;
         SPEC_CUDA(cudaGetLastError(), "length update");
@@ -1183,7 +1269,7 @@ static int draft_impl(spec_model* m, spec_kv* kv, int32_t batch, const int32_t* 
         p.batch = batch;
         p.mode = 2;
         p.pass = j;
-        SPEC_TRY(launch_plan(m, p, batch, kv->len, st));
+        SPEC_TRY(launch_plan(m, p, batch, kv, st));
         SPEC_TRY(launch_prologue(m, batch, nullptr, 0, cand, k + 1, j, 0, st));
         HeadSpec hs{};
         hs.mode = sampling ? HEAD_STATS : HEAD_DRAFT;
@@ -1202,7 +1288,7 @@ static int draft_impl(spec_model* m, spec_kv* kv, int32_t batch, const int32_t* 
         hs.cand_col = j + 1;
         hs.batch = batch;
         // the LM head leaves the residual stream alone, so the layer-L state is copied after it
-        SPEC_TRY(run_layers(m, kv, batch, batch, 1, 0, c.exit_layer, 0, j < k, j < k ? &hs : nullptr, st));
+        SPEC_TRY(run_layers(m, kv, p, batch, batch, 1, 0, c.exit_layer, 0, j < k, j < k ? &hs : nullptr, st));
         if (sampling && j < k) {
             SampleArgs a{};
             a.in = hs.logits;
@@ -1231,6 +1317,7 @@ extern "C" int spec_draft(spec_model* m, spec_kv* kv, int32_t batch, const int32
                           float* h_L, float* draft_logits, void* stream) {
     if (!m || !kv || !t0 || !cand || !h_L) return set_error(SPEC_ERR_ARG, "spec_draft: null pointer");
     if (kv->m != m) return set_error(SPEC_ERR_ARG, "spec_draft: cache of another model");
+    SPEC_TRY(kv_check_prefix(kv, "spec_draft"));
     return draft_impl(m, kv, batch, t0, k, cand, h_L, draft_logits, 0.f, nullptr, nullptr, (cudaStream_t)stream);
 }
 
@@ -1239,6 +1326,7 @@ extern "C" int spec_draft_sample(spec_model* m, spec_kv* kv, int32_t batch, cons
                                  float* draft_logits, void* stream) {
     if (!m || !kv || !t0 || !cand || !h_L || !u_draft || !q) return set_error(SPEC_ERR_ARG, "spec_draft_sample: null pointer");
     if (kv->m != m) return set_error(SPEC_ERR_ARG, "spec_draft_sample: cache of another model");
+    SPEC_TRY(kv_check_prefix(kv, "spec_draft_sample"));
     if (!(temperature > 0.f) || !(temperature <= 3.402823466e38f))
         return set_error(SPEC_ERR_ARG, "spec_draft_sample: temperature must be positive and finite");
     return draft_impl(m, kv, batch, t0, k, cand, h_L, draft_logits, temperature, u_draft, q, (cudaStream_t)stream);
@@ -1249,6 +1337,7 @@ extern "C" int spec_draft_tree(spec_model* m, spec_kv* kv, int32_t batch, const 
     if (!m || !kv || !t0 || !tree_parent || !tokens || !h_L || !logits)
         return set_error(SPEC_ERR_ARG, "spec_draft_tree: null pointer");
     if (kv->m != m) return set_error(SPEC_ERR_ARG, "spec_draft_tree: cache of another model");
+    SPEC_TRY(kv_check_prefix(kv, "spec_draft_tree"));
     const spec_model_config& c = m->cfg;
     if (c.exit_layer < 1) return set_error(SPEC_ERR_ARG, "spec_draft_tree: exit_layer must be >= 1");
     if (batch < 1 || batch > kv->batch) return set_error(SPEC_ERR_ARG, "spec_draft_tree: bad batch");
@@ -1296,7 +1385,7 @@ extern "C" int spec_draft_tree(spec_model* m, spec_kv* kv, int32_t batch, const 
         // cost is the weight stream, the same for these few rows)
         for (int b = 0; b < batch; ++b) p.n_rows[b] = l1;
         const int T = batch * l1;
-        SPEC_TRY(launch_plan(m, p, T, kv->len, st));
+        SPEC_TRY(launch_plan(m, p, T, kv, st));
         SPEC_TRY(launch_prologue(m, T, nullptr, 0, tokens, n_nodes, 0, 0, st));
         const bool expand = lev < D;
         HeadSpec hs{};
@@ -1307,7 +1396,7 @@ extern "C" int spec_draft_tree(spec_model* m, spec_kv* kv, int32_t batch, const 
         hs.logits_stride = c.vocab;
         hs.logits_row0 = 0;
         hs.batch = batch;
-        SPEC_TRY(run_layers(m, kv, T, batch, l1, 0, c.exit_layer, 1, expand, expand ? &hs : nullptr, st));
+        SPEC_TRY(run_layers(m, kv, p, T, batch, l1, 0, c.exit_layer, 1, expand, expand ? &hs : nullptr, st));
         if (expand) {
             launch_k(m->pdl, tree_expand_kernel, dim3(batch, l1 - l0), dim3(256), 0, st, (const float*)logits,
                      c.vocab, l1, l0, tk, tokens, n_nodes);
@@ -1332,6 +1421,7 @@ extern "C" int spec_draft_tree_dynamic(spec_model* m, spec_kv* kv, int32_t batch
     if (!m || !kv || !t0 || !branching || !tokens || !parents || !n_nodes || !h_L || !logits)
         return set_error(SPEC_ERR_ARG, "spec_draft_tree_dynamic: null pointer");
     if (kv->m != m) return set_error(SPEC_ERR_ARG, "spec_draft_tree_dynamic: cache of another model");
+    SPEC_TRY(kv_check_prefix(kv, "spec_draft_tree_dynamic"));
     const spec_model_config& c = m->cfg;
     if (c.exit_layer < 1) return set_error(SPEC_ERR_ARG, "spec_draft_tree_dynamic: exit_layer must be >= 1");
     if (batch < 1 || batch > kv->batch) return set_error(SPEC_ERR_ARG, "spec_draft_tree_dynamic: bad batch");
@@ -1371,7 +1461,7 @@ extern "C" int spec_draft_tree_dynamic(spec_model* m, spec_kv* kv, int32_t batch
         const int rows = cum[lev];
         for (int b = 0; b < batch; ++b) p.n_rows[b] = rows;
         const int T = batch * rows;
-        SPEC_TRY(launch_plan(m, p, T, kv->len, st, parents, n_max));
+        SPEC_TRY(launch_plan(m, p, T, kv, st, parents, n_max));
         SPEC_TRY(launch_prologue(m, T, nullptr, 0, tokens, n_max, 0, 0, st));
         const bool expand = lev < depth;
         HeadSpec hs{};
@@ -1382,7 +1472,7 @@ extern "C" int spec_draft_tree_dynamic(spec_model* m, spec_kv* kv, int32_t batch
         hs.logits_stride = c.vocab;
         hs.logits_row0 = 0;
         hs.batch = batch;
-        SPEC_TRY(run_layers(m, kv, T, batch, rows, 0, c.exit_layer, 2, expand, expand ? &hs : nullptr, st));
+        SPEC_TRY(run_layers(m, kv, p, T, batch, rows, 0, c.exit_layer, 2, expand, expand ? &hs : nullptr, st));
         if (expand) {
             launch_k(m->pdl, tree_width_kernel, dim3(batch, lw[lev]), dim3(kWidthThreads), 0, st, (const float*)logits, c.vocab,
                      rows, (int)branching[lev], mass, stage);
@@ -1407,6 +1497,7 @@ static int verify_impl(spec_model* m, spec_kv* kv, int32_t batch, const int32_t*
                        int32_t* acc_len, int32_t* next_tok, int32_t* path, cudaStream_t st) {
     if (!m || !kv || !n_rows || !tokens) return set_error(SPEC_ERR_ARG, "spec_verify: null pointer");
     if (kv->m != m) return set_error(SPEC_ERR_ARG, "spec_verify: cache of another model");
+    SPEC_TRY(kv_check_prefix(kv, "spec_verify"));
     const spec_model_config& c = m->cfg;
     if (batch < 1 || batch > kv->batch) return set_error(SPEC_ERR_ARG, "spec_verify: bad batch");
     if ((acc_len == nullptr) != (next_tok == nullptr)) return set_error(SPEC_ERR_ARG, "acc_len and next_tok go together");
@@ -1442,7 +1533,7 @@ static int verify_impl(spec_model* m, spec_kv* kv, int32_t batch, const int32_t*
     }
     const int lo = h_in ? c.exit_layer : 0;
     SPEC_TRY(kv_ensure_pages(kv, batch, p.n_rows, true, st));
-    SPEC_TRY(launch_plan(m, p, T, kv->len, st, dev_parent, par_stride));
+    SPEC_TRY(launch_plan(m, p, T, kv, st, dev_parent, par_stride));
     SPEC_TRY(launch_prologue(m, T, h_in, h_stride, tokens, tok_stride, 0, lo, st));
     HeadSpec hs{};
     // one tree a sequence: summaries in the head, acceptance in its own kernel
@@ -1459,7 +1550,7 @@ static int verify_impl(spec_model* m, spec_kv* kv, int32_t batch, const int32_t*
     hs.next_tok = next_tok;
     hs.path = path;
     hs.batch = batch;
-    SPEC_TRY(run_layers(m, kv, T, batch, max_r, lo, c.n_layers, trees ? 2 : (tree_parent ? 1 : 0), true, &hs, st));
+    SPEC_TRY(run_layers(m, kv, p, T, batch, max_r, lo, c.n_layers, trees ? 2 : (tree_parent ? 1 : 0), true, &hs, st));
     if (trees && acc_len) {
         launch_k(m->pdl, accept_trees_kernel, dim3((batch + 127) / 128), dim3(128), 0, st,
                  (const spec_row_stats*)m->row_stats, m->plan, tokens, tok_stride, batch, acc_len, next_tok, path);

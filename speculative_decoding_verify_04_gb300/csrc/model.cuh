@@ -137,6 +137,11 @@ struct spec_model {
     spec_row_stats* stat_part = nullptr;  // [ceil(V/128)][max_rows]
     spec_row_stats* row_stats = nullptr;  // [max_rows]
     float* draft_lg = nullptr;       // [max_batch][V] draft logits of a sampling pass
+    float* attend_part = nullptr;    // partial states of the attention over 8-bit caches and shared prompts (bf16)
+    size_t attend_part_floats = 0;
+    __nv_bfloat16* stage_kv = nullptr;  // [2][max_rows][Hkv][hd]: a layer's new K and V rows before they are quantised
+    int* row_ids = nullptr;          // [max_rows] 0, 1, ...: the staging rows as a cache of one slot a sequence
+    int* row_zeros = nullptr;        // [max_rows] 0
     float* gemm_part = nullptr;      // split-K partial tiles
     size_t gemm_part_floats = 0;
     int* counters = nullptr;         // tile arrival counters, then chain barrier, chain exits, head tiles
@@ -190,6 +195,17 @@ struct spec_kv {
     int* table = nullptr;            // [batch][max_pages] page of each block of slots, -1 if none
     int* free_pages = nullptr;       // paged: stack of free pages [n_pages], top at free_top[0]
     int* free_top = nullptr;
+    // 8-bit caches: k and v hold e4m3 values, ke and ve the rows' exponents + 127
+    bool q8 = false;
+    size_t elem = 2;                 // bytes a cached value
+    uint8_t* ke = nullptr;           // [layer][page][kvh][slot]
+    uint8_t* ve = nullptr;
+    // the prompt that every sequence of this cache continues (spec_kv_set_prefix)
+    spec_kv* prefix = nullptr;
+    int prefix_seq = 0;
+    bool prefix_lost = false;        // the prompt's cache was destroyed while attached
+    std::vector<spec_kv*> users;     // caches that continue a sequence of this one
+    bool by_range() const { return q8 || prefix != nullptr; }   // attention in ranges (attend.cu)
     spec::KVPages pages() const {
         int sh = -1;
         if (paged) { sh = 0; while ((1 << sh) < page) ++sh; }
@@ -357,6 +373,9 @@ int launch_attention_ring(spec_model* m, const spec_kv* kv, const AttnParams& a,
 // (relative) or n[b] (absolute) of sequences [0, batch); pages past the lengths back
 int kv_ensure_pages(spec_kv* kv, int batch, const int* n, bool relative, cudaStream_t st);
 int kv_release_pages(spec_kv* kv, int batch, cudaStream_t st);
+// shared prompts (capi.cu): leave the prompt; an error where it was destroyed
+void kv_detach_prefix(spec_kv* kv);
+int kv_check_prefix(const spec_kv* kv, const char* what);
 int attn_splits(const spec_model* m, int blocks, int kv_ctx);
 size_t attn_scratch_floats(const spec_model* m, int batch, int max_rows_per_seq, int kv_ctx, int* n_counters);
 size_t attn_partial_floats_needed(const spec_model* m, int batch, int max_rows_per_seq);

@@ -29,7 +29,7 @@ EXPORTS = [
     "spec_verify_noalloc", "spec_draft_sample", "spec_probs", "spec_sample", "spec_schedule_aimd",
     "spec_schedule_decay", "spec_draft_tree", "spec_kv_create_paged", "spec_kv_free_pages", "spec_kv_page_table",
     "spec_draft_tree_dynamic", "spec_verify_trees", "spec_set_exit_layer", "spec_kv_read_page",
-    "spec_test_stall_next_chain",
+    "spec_test_stall_next_chain", "spec_kv_create_q8", "spec_kv_set_prefix", "spec_attend", "spec_logprobs",
 ]
 
 
@@ -64,7 +64,7 @@ def load(path: str = LIB_PATH):
     if not os.path.exists(path):
         raise SpecError(f"{path} is missing: build it with speculative_decoding_verify_04_gb300.build.build()")
     lib = ctypes.CDLL(path)
-    P, I = c_void_p, c_int32
+    P, I, L = c_void_p, c_int32, ctypes.c_int64
     sig = {
         "spec_last_error": ([], ctypes.c_char_p),
         "spec_device_info": ([POINTER(I), POINTER(I), POINTER(I)], I),
@@ -95,6 +95,10 @@ def load(path: str = LIB_PATH):
         "spec_kv_page_table": ([P, POINTER(I), P], I),
         "spec_kv_read_page": ([P, I, I, I, P, P], I),
         "spec_test_stall_next_chain": ([P, I, ctypes.c_int64], I),
+        "spec_kv_create_q8": ([P, I, I, I, I, POINTER(P)], I),
+        "spec_kv_set_prefix": ([P, P, I], I),
+        "spec_attend": ([P, I, I, POINTER(I), P, L, P, L, P, L, POINTER(I), P, L, P], I),
+        "spec_logprobs": ([P, I, L, I, I, c_float, P, P, P, I, P, P, P], I),
         "spec_accept_greedy": ([P, P, POINTER(I), I, I, I, P, P, P, P], I),
         "kv_commit": ([P, I, P, P, I, P], I),
         "spec_row_probs": ([P, I, P, P], I),
@@ -138,6 +142,12 @@ def _need(t, dtype, name, numel=None):
         raise SpecError(f"{name}: need a contiguous CUDA {dtype} tensor")
     if numel is not None and t.numel() < numel:
         raise SpecError(f"{name}: needs at least {numel} elements, has {t.numel()}")
+
+
+def _here(t, name):
+    """The C calls take pointers of the current device only."""
+    if t is not None and t.device.index != torch.cuda.current_device():
+        raise SpecError(f"{name}: on {t.device}, not on the current device")
 
 
 def device_info():
@@ -214,23 +224,35 @@ class Model:
 class KVCache:
     """KV cache of ``batch`` sequences x ``max_ctx`` slots (owns the library handle).
 
-    With ``page`` (a multiple of 64) the cache is paged: a pool of ``n_pages``
-    pages of ``page`` slots shared by the sequences through their page tables.
+    With ``page`` (a power of two, at least 64) the cache is paged: a pool of
+    ``n_pages`` pages of ``page`` slots shared by the sequences through their page
+    tables.  With ``q8`` it holds 8-bit rows, quantised as they are written:
+    e4m3 values under a power of two for every slot and KV head.
     """
 
-    def __init__(self, model: Model, batch, max_ctx, page=None, n_pages=None):
+    def __init__(self, model: Model, batch, max_ctx, page=None, n_pages=None, q8=False):
         self.model = model
         self.batch = batch
         self.max_ctx = max_ctx
         self.page = page
+        self.q8 = bool(q8)
+        self.prefix = None
         h = c_void_p()
-        if page:
-            if n_pages is None:
-                n_pages = batch * ((max_ctx + page - 1) // page)
+        if page and n_pages is None:
+            n_pages = batch * ((max_ctx + page - 1) // page)
+        if q8:
+            _check(load().spec_kv_create_q8(model.handle, batch, max_ctx, page or 0, n_pages or 0, ctypes.byref(h)))
+        elif page:
             _check(load().spec_kv_create_paged(model.handle, batch, max_ctx, page, n_pages, ctypes.byref(h)))
         else:
             _check(load().spec_kv_create(model.handle, batch, max_ctx, ctypes.byref(h)))
         self.handle = h
+
+    def set_prefix(self, prefix, seq=0):
+        """Every sequence continues sequence ``seq`` of the cache ``prefix``, whose
+        slots all of them see (None: no prefix).  The prefix is kept alive."""
+        _check(load().spec_kv_set_prefix(self.handle, None if prefix is None else prefix.handle, int(seq)))
+        self.prefix = prefix
 
     def free_pages(self, stream=None):
         n = c_int32()
@@ -245,10 +267,16 @@ class KVCache:
 
     def read_page(self, which, layer, page, stream=None):
         """Raw physical page ``page`` of the K (which 0) or V (which 1) pool of
-        ``layer``, read without the page table: host tensor [Hkv][page slots][hd]."""
+        ``layer``, read without the page table: host tensor [Hkv][page slots][hd].
+        8-bit caches give uint8: the e4m3 bytes, and for which 2 (K) and 3 (V) the
+        exponents + 127, [Hkv][page slots]."""
         s = self.model.shape
         slots = self.page if self.page else self.max_ctx
-        out = torch.empty((s.n_kv_heads, slots, s.head_dim), dtype=self.model.torch_dtype).pin_memory()
+        dtype = self.model.torch_dtype
+        if self.q8:
+            slots, dtype = (slots + 63) // 64 * 64, torch.uint8
+        shape = (s.n_kv_heads, slots, s.head_dim) if which < 2 else (s.n_kv_heads, slots)
+        out = torch.empty(shape, dtype=dtype).pin_memory()
         _check(load().spec_kv_read_page(self.handle, which, layer, page, c_void_p(out.data_ptr()), _stream(stream)))
         return out
 
@@ -441,6 +469,63 @@ def spec_accept(p, q, draft, u, acc_len, next_tok, stream=None):
     _need(next_tok, torch.int32, "next_tok", B)
     _check(load().spec_accept(_ptr(p), _ptr(q), _ptr(draft), draft.stride(0), _ptr(u), B, k, V, _ptr(acc_len),
                               _ptr(next_tok), _stream(stream)))
+
+
+def _rows3d(t, name, heads, dim, rows, dtype):
+    """[rows][heads][dim] rows with their heads in one piece: (pointer, row stride)."""
+    if (t is None or not t.is_cuda or t.dtype != dtype or t.dim() != 3 or t.shape[0] < rows
+            or tuple(t.shape[1:]) != (heads, dim)
+            or t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+        raise SpecError(f"{name}: need a CUDA {dtype} tensor [{rows}, {heads}, {dim}] with contiguous rows")
+    _here(t, name)
+    return c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def spec_attend(kv, layer, n_rows, q, out, k=None, v=None, tree_parent=None, stream=None):
+    """One layer's attention of the rows ``n_rows`` of each sequence over the cache
+    and its prefix: ``out`` [T, H, hd] from ``q`` [T, H, hd] (bf16, back to back, not
+    scaled).  ``k`` and ``v`` [T, Hkv, hd] are written to the rows' slots first."""
+    s = kv.model.shape
+    T = sum(int(n) for n in n_rows)
+    bf = torch.bfloat16
+    qp, qs = _rows3d(q, "q", s.n_heads, s.head_dim, T, bf)
+    op, os_ = _rows3d(out, "out", s.n_heads, s.head_dim, T, bf)
+    kp, ks = _rows3d(k, "k", s.n_kv_heads, s.head_dim, T, bf) if k is not None else (None, 0)
+    vp, vs = _rows3d(v, "v", s.n_kv_heads, s.head_dim, T, bf) if v is not None else (None, 0)
+    if tree_parent is not None and len(tree_parent) < max(n_rows):
+        raise SpecError("tree_parent: shorter than the sequences' rows")
+    tp = _i32_array(tree_parent) if tree_parent is not None else None
+    _check(load().spec_attend(kv.handle, int(layer), len(n_rows), _i32_array(n_rows), qp, qs, kp, ks, vp, vs, tp, op,
+                              os_, _stream(stream)))
+
+
+def spec_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logprobs=None, temperature=1.0,
+                  stream=None):
+    """log p of ``tokens`` [rows] under softmax(logits / temperature) of ``logits``
+    [rows, V] (f32 or bf16), with the rows' entropy and their ``top_ids`` /
+    ``top_logprobs`` [rows, n] best tokens.  Every output may be None."""
+    if (logits is None or not logits.is_cuda or logits.dtype not in (torch.float32, torch.bfloat16)
+            or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1)):
+        raise SpecError("logits: need a 2-D CUDA float32 or bfloat16 tensor with contiguous rows")
+    rows, V = logits.shape
+    _here(logits, "logits")
+    n = 0
+    if top_ids is not None:
+        if top_ids.dim() != 2 or top_ids.shape[0] < rows:
+            raise SpecError(f"top_ids: need [{rows}, n]")
+        n = top_ids.shape[1]
+    for t, dtype, name, numel in ((tokens, torch.int32, "tokens", rows), (logprob, torch.float32, "logprob", rows),
+                                  (entropy, torch.float32, "entropy", rows),
+                                  (top_ids, torch.int32, "top_ids", rows * n),
+                                  (top_logprobs, torch.float32, "top_logprobs", rows * n)):
+        _need(t, dtype, name, numel)
+        _here(t, name)
+    if rows == 0:
+        return
+    dt = SPEC_DTYPE_BF16 if logits.dtype == torch.bfloat16 else SPEC_DTYPE_F32
+    _check(load().spec_logprobs(_ptr(logits), dt, logits.stride(0) if rows > 1 else V, rows, V, float(temperature),
+                                _ptr(tokens), _ptr(logprob), _ptr(entropy), n, _ptr(top_ids), _ptr(top_logprobs),
+                                _stream(stream)))
 
 
 def spec_accept_greedy(logits, tokens, acc_len, next_tok, tree_parent=None, path=None, stream=None):
