@@ -18,7 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libspec.so")
 SOURCES = ["capi.cu", "gemm.cu", "attention.cu", "attn_ring.cu", "accept.cu", "sample.cu", "noalloc.cu",
-           "attend.cu", "kv8.cu", "logprobs.cu"]
+           "attend.cu", "attend_tile.cu", "kv8.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

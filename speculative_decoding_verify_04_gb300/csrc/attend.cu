@@ -18,29 +18,8 @@
 namespace spec {
 
 constexpr int kRowThreads = 128;
+constexpr int kRowVectors = 16;       // query vectors a KV head up to which the row kernel takes the prompt
 constexpr int kMinKeys = 256;         // least keys of a range: below it the join costs more than the ranges give
-
-struct AttendArgs {
-    const void* q;
-    long long q_stride;
-    float c;                          // scale * log2(e)
-    CacheView own, pre;
-    int pre_seq;                      // sequence of the prompt in its cache
-    int H, Hkv;
-    AttendSpan span;
-    int own_splits, pre_splits;       // pre_splits 0: no prompt part in the row kernel
-    int own_qb, pre_qb;               // query blocks of 16
-    float* part_o;                    // [range][T * H][hd]
-    float* part_ml;                   // [range][T * H][2]: the prompt's ranges, then the sequence's own
-    int own_range0;                   // first range of the own part
-    int* err;
-};
-
-SPEC_DEV float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 
 // Eight keys' bytes as bf16 pairs: words of e4m3 -> 2 bf16x2 each
 SPEC_DEV void e4m3x4_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -470,6 +449,9 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     const spec_kv* pre = kv->prefix;
     AttendArgs a{};
     a.q = q;
+    a.q_f32 = q_f32;
+    a.q_vec = (reinterpret_cast<uintptr_t>(q) & 15) == 0 && q_stride % 8 == 0;
+    a.layer = layer;
     a.q_stride = q_stride;
     a.c = scale * 1.4426950408889634f;
     a.own = cache_view(kv, layer);
@@ -483,7 +465,8 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     const size_t fit = m->attend_part_floats / (hd + 2) / TH;      // ranges the workspace holds
     // key ranges: as many as about three resident CTAs an SM take, by each part's share of the keys
     a.own_qb = (span.max_rows * G + 15) / 16;
-    a.pre_qb = pre ? (span.T * G + 15) / 16 : 0;
+    const bool tile = pre && span.T * G > kRowVectors && attend_tile_ok(pre);
+    a.pre_qb = pre && !tile ? (span.T * G + 15) / 16 : 0;
     const long long own_blocks = (long long)span.batch * Hkv * a.own_qb, pre_blocks = (long long)Hkv * a.pre_qb;
     const long long keys = own_blocks * kv->max_ctx + pre_blocks * (pre ? pre->max_ctx : 0);
     const long long per = std::max<long long>(kMinKeys, keys / (3 * m->num_sms) + 1);
@@ -493,9 +476,13 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     };
     a.own_splits = splits(own_blocks, kv->max_ctx);
     a.pre_splits = splits(pre_blocks, pre ? pre->max_ctx : 0);
-    a.own_range0 = a.pre_splits;
-    const int ranges = a.own_splits + a.pre_splits;
-    if ((size_t)ranges > fit) return set_error(SPEC_ERR_CAPACITY, "attention workspace too small");
+    if (tile) {
+        a.tile_splits = attend_tile_splits(m, span, pre->max_ctx);
+        a.tile_splits = (int)std::min<size_t>(a.tile_splits, fit > (size_t)a.own_splits ? fit - a.own_splits : 0);
+    }
+    a.own_range0 = a.pre_splits + a.tile_splits;
+    const int ranges = a.own_splits + a.own_range0;
+    if ((size_t)ranges > fit || (tile && a.tile_splits == 0)) return set_error(SPEC_ERR_CAPACITY, "attention workspace too small");
     a.part_o = m->attend_part;
     a.part_ml = m->attend_part + (size_t)ranges * TH * hd;
     const dim3 grid((unsigned)(a.pre_splits * pre_blocks + a.own_splits * own_blocks));
@@ -503,6 +490,7 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     void (*f)(AttendArgs) = hd == 128 ? (q_f32 ? attend_rows_kernel<128, true> : attend_rows_kernel<128, false>)
                                       : (q_f32 ? attend_rows_kernel<64, true> : attend_rows_kernel<64, false>);
     const int slot = prof_start(m, st);
+    if (tile) SPEC_TRY(launch_attend_tile(pre, a, st));
     cudaError_t e = launch_k(m->pdl, f, grid, dim3(kRowThreads), smem, st, a);
     SPEC_TRY(check_cuda(e, "attention rows launch"));
     JoinArgs j{};

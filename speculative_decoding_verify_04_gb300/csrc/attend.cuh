@@ -42,6 +42,39 @@ CacheView cache_view(const spec_kv* kv, int layer);
 // span of a call with n_rows[b] rows of sequence b
 int make_span(AttendSpan* s, int batch, const int* n_rows, int extra, const int* tree_parent, const int* dev_parent);
 
+// Parameters of the attention kernels.  Ranges of keys leave partial states:
+// the prompt's ranges first, then each sequence's own.
+struct AttendArgs {
+    const void* q;
+    int q_f32;                        // f32 queries (else bf16)
+    int q_vec;                        // bf16 queries: rows are 16-byte aligned
+    long long q_stride;
+    float c;                          // scale * log2(e)
+    CacheView own, pre;
+    int pre_seq;                      // sequence of the prompt in its cache
+    int layer;
+    int H, Hkv;
+    AttendSpan span;
+    int own_splits, pre_splits;       // key ranges; pre_splits is 0 where the tile kernel takes the prompt
+    int tile_splits;                  // the tile kernel's ranges
+    int own_qb, pre_qb;               // query blocks of 16
+    float* part_o;                    // [range][T * H][hd]
+    float* part_ml;                   // [range][T * H][2]
+    int own_range0;                   // first range of the own part
+    int* err;
+};
+
+SPEC_DEV float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// attend_tile.cu: the prompt's part for lists of many query vectors
+bool attend_tile_ok(const spec_kv* pre);
+int attend_tile_splits(const spec_model* m, const AttendSpan& span, int prompt_cap);
+int launch_attend_tile(const spec_kv* pre, const AttendArgs& a, cudaStream_t st);
+
 // Where the attention's result goes: bf16 rows of the caller, or the model's
 // O-projection input (hi rows, then lo rows at out_lo).
 struct AttendOut { __nv_bfloat16* p; long long stride; size_t lo; };

@@ -1,0 +1,526 @@
+// The shared prompt against many query vectors: tiles of 128 query vectors by
+// 128 keys on the tensor cores (tcgen05), accumulators in tensor memory.
+//
+// A CTA owns one KV head, one range of the prompt's keys and two streams.  With
+// two tiles of query vectors the streams are the tiles, and every K and V tile
+// serves both; with one tile the streams take the key tiles in turn and their
+// states are joined at the end.  Per stream and key tile:
+//     S = Q K^T          tcgen05.mma, both operands in shared memory, S in TMEM
+//     P = 2^(c S - m)    one thread a query vector: S row from TMEM, running max
+//                        and sum in registers, P as bf16 over S in TMEM
+//     O += P V           tcgen05.mma with P as the TMEM operand; V as it lies in
+//                        the cache ([key][dim]: the MN-major form)
+// While one stream's threads do the softmax the tensor cores work for the other.
+// The running maximum used in the exponent moves only when the true one has
+// grown by more than 8 (a factor of 256: sums and O stay far inside f32), so O
+// is rescaled rarely.  Partial states (m, sum p, sum p v) leave in 32 bits.
+//
+// Roles: warps 0-3 and 4-7 the streams' softmax, warp 8 the copies (TMA tensor
+// boxes with the 128-byte swizzle), warp 9 the MMAs; 8-bit caches add four warps
+// that turn raw e4m3 tiles into swizzled bf16 tiles (exact).
+#include <algorithm>
+
+#include "attend.cuh"
+
+namespace spec {
+
+constexpr int kBlkQ = 128;
+constexpr int kBlkK = 128;
+constexpr float kLazy = 8.0f;            // log2 of the growth of the maximum that is let pass
+
+template <int HD, bool Q8>
+struct TileShape {
+    static constexpr int kTileBytes = kBlkK * HD * 2;          // one K or V tile in bf16
+    static constexpr int kQBytes = kBlkQ * HD * 2;
+    static constexpr int kRawBytes = kBlkK * HD;
+    static constexpr int kStages = HD == 128 ? (Q8 ? 4 : 5) : 8;
+    static constexpr int kRaw = Q8 ? (HD == 128 ? 2 : 4) : 0;
+    static constexpr int kThreads = Q8 ? 448 : 320;
+    static constexpr int kTiles = 2 * kQBytes + kStages * kTileBytes + kRaw * kRawBytes;
+    static constexpr int kExpBytes = kRaw * kBlkK;
+    static constexpr int kSmem = kTiles + kExpBytes + 512 + 1024;   // barriers; the tiles start on 1024 bytes
+};
+
+struct TileBars {
+    uint64_t full[8], empty[8];          // K/V ring
+    uint64_t raw_full[4], raw_empty[4];  // raw e4m3 ring
+    uint64_t q_full, s_full[2], p_full[2], pv_done[2], drain;
+    uint32_t tmem;
+    int abort;
+};
+static_assert(sizeof(TileBars) <= 512, "barriers");
+
+// D[tmem] (+)= A[tmem] * B[smem], B MN-major
+SPEC_DEV void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+// [key][64 dims] tiles, 128-byte swizzle, read as the MN-major operand: 64-dim
+// pieces lie `lead` bytes apart, groups of 8 keys 1024 bytes
+SPEC_DEV uint64_t smem_desc_mn(uint32_t saddr, uint32_t lead) {
+    uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(lead >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+SPEC_DEV void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+                 "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+                   "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+}
+SPEC_DEV void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+SPEC_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+SPEC_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                    "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+SPEC_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+                 "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                    "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+                    "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+                    "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+                 : "memory");
+}
+SPEC_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// What a CTA does: its KV head, query tiles and keys.
+struct TileJob {
+    int g, nq, q0;                       // vectors [q0, q0 + nq) of the head's list, nq <= 256
+    int two;                             // two tiles of query vectors (else the streams share one)
+    int k_begin, n_keys, n_kb;           // keys [k_begin, k_begin + n_keys) in n_kb tiles
+    int n_jobs;                          // (stream, key tile) pairs: job n is stream n & 1
+};
+SPEC_DEV int job_kb(const TileJob& J, int n) { return J.two ? n >> 1 : n; }
+
+template <int HD, bool Q8>
+__global__ void __launch_bounds__(TileShape<HD, Q8>::kThreads, 1)
+attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v) {
+    using S = TileShape<HD, Q8>;
+    constexpr int NST = S::kStages, NRAW = S::kRaw > 0 ? S::kRaw : 1;
+    constexpr uint32_t kHalf = kBlkK * 128;                  // bytes of 64 dims of a tile
+    extern __shared__ char smraw[];
+    char* tiles = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
+    char* sQ = tiles;
+    char* ring = sQ + 2 * S::kQBytes;
+    char* raw = ring + NST * S::kTileBytes;
+    uint8_t* rexp = reinterpret_cast<uint8_t*>(raw + S::kRaw * S::kRawBytes);
+    TileBars& B = *reinterpret_cast<TileBars*>(tiles + S::kTiles + S::kExpBytes);
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+
+    if (warp == 9) tmem_alloc(&B.tmem, 512);
+    if (t == 0) {
+        for (int i = 0; i < NST; ++i) { mbar_init(&B.full[i], Q8 ? 4 : 1); mbar_init(&B.empty[i], 1); }
+        for (int i = 0; i < NRAW; ++i) { mbar_init(&B.raw_full[i], 1); mbar_init(&B.raw_empty[i], 4); }
+        mbar_init(&B.q_full, 8);
+        for (int i = 0; i < 2; ++i) { mbar_init(&B.s_full[i], 1); mbar_init(&B.p_full[i], 4); mbar_init(&B.pv_done[i], 1); }
+        mbar_init(&B.drain, 1);
+        B.abort = 0;
+        fence_mbar_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = B.tmem;
+    pdl_trigger();                       // every CTA that can hold TMEM has it: the next kernel's cannot take it first
+    pdl_wait();
+
+    const int G = a.H / a.Hkv, NQ = a.span.T * G, n_pair = (NQ + 2 * kBlkQ - 1) / (2 * kBlkQ);
+    TileJob J;
+    {
+        int id = blockIdx.x;
+        J.g = id % a.Hkv;
+        id /= a.Hkv;
+        J.q0 = (id % n_pair) * 2 * kBlkQ;
+        id /= n_pair;
+        J.nq = min(2 * kBlkQ, NQ - J.q0);
+        J.two = J.nq > kBlkQ;
+        const int P = min(a.pre.len[a.pre_seq], a.pre.cap);
+        const int per = ((P + a.tile_splits - 1) / a.tile_splits + kBlkK - 1) / kBlkK * kBlkK;
+        J.k_begin = min(P, id * per);
+        J.n_keys = min(P - J.k_begin, per);
+        J.n_kb = (J.n_keys + kBlkK - 1) / kBlkK;
+        J.n_jobs = J.two ? 2 * J.n_kb : J.n_kb;
+    }
+    const int split = blockIdx.x / (a.Hkv * n_pair);
+    volatile int* ab = &B.abort;
+
+    if (warp < 8) {
+        // -------- queries into shared memory, then the softmax of stream `warp / 4`
+        const int n_rows = J.two ? 2 * kBlkQ : kBlkQ;
+        for (int i = t; i < n_rows * (HD / 8); i += 256) {
+            const int r = i / (HD / 8), ch = i % (HD / 8);
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (r < J.nq && J.n_kb > 0) {
+                const int qi = J.q0 + r;
+                const long long off = (qi / G) * a.q_stride + (J.g * G + qi % G) * HD + ch * 8;
+                if (a.q_f32) {
+                    const float* p = static_cast<const float*>(a.q) + off;
+                    const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
+                    w = make_uint4(bf16x2(x.x, x.y), bf16x2(x.z, x.w), bf16x2(y.x, y.y), bf16x2(y.z, y.w));
+                } else if (a.q_vec) {
+                    w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + off);
+                } else {
+                    const unsigned short* p = static_cast<const unsigned short*>(a.q) + off;
+                    w = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16,
+                                   p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
+                }
+            }
+            const int rr = r & (kBlkQ - 1);
+            *reinterpret_cast<uint4*>(sQ + (r / kBlkQ) * S::kQBytes + (ch >> 3) * kHalf + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = w;
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.q_full);
+
+        const int st = warp >> 2, row = t & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;                   // TMEM lane 32 * (warp % 4)
+        const uint32_t tS = tmem + st * 128 + lanes, tO = tmem + 256 + st * HD + lanes;
+        float m = -INFINITY, l = 0.f;                                        // m: the maximum that the exponents use
+        int q = 0;                                                           // job of this stream
+        bool ok = true;
+        for (int n = st; n < J.n_jobs; n += 2, ++q) {
+            const int kb = job_kb(J, n), valid = min(kBlkK, J.n_keys - kb * kBlkK);
+            ok = mbar_wait(&B.s_full[st], q & 1, ab, a.err);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            tc_fence_after();
+            float mx = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t r[32];
+                tmem_ld32(tS + 32 * c, r);
+                tmem_wait_ld();
+                if (valid == kBlkK) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(r[i]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, 32 * c + i < valid ? __uint_as_float(r[i]) : -INFINITY);
+                }
+            }
+            mx *= a.c;
+            if (__any_sync(0xffffffffu, mx > m + kLazy || m == -INFINITY)) {
+                const float mn = fmaxf(m, mx);
+                const float f = ex2(m - (mn == -INFINITY ? 0.f : mn));
+                l *= f;
+                m = mn;
+                if (q > 0) {
+                    ok = mbar_wait(&B.pv_done[st], (q - 1) & 1, ab, a.err);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < HD / 32; ++c) {
+                        uint32_t r[32];
+                        tmem_ld32(tO + 32 * c, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+                        tmem_st32(tO + 32 * c, r);
+                    }
+                }
+            }
+            const float mu = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t r[32], p[16];
+                tmem_ld32(tS + 32 * c, r);
+                tmem_wait_ld();
+                float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float x = fmaf(__uint_as_float(r[2 * i]), a.c, -mu), y = fmaf(__uint_as_float(r[2 * i + 1]), a.c, -mu);
+                    if (valid != kBlkK) {
+                        if (32 * c + 2 * i >= valid) x = -INFINITY;
+                        if (32 * c + 2 * i + 1 >= valid) y = -INFINITY;
+                    }
+                    x = ex2(x);
+                    y = ex2(y);
+                    s0 += x;
+                    s1 += y;
+                    p[i] = bf16x2(x, y);
+                }
+                l += s0 + s1;
+                tmem_st16(tS + 16 * c, p);                    // P's columns lie over S columns already read
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.p_full[st]);
+        }
+        // -------- the state: this stream's own rows, or (one tile) joined with the other stream's
+        if (ok && q > 0) ok = mbar_wait(&B.pv_done[st], (q - 1) & 1, ab, a.err);
+        const int n0 = (J.n_jobs + 1) / 2, n1 = J.n_jobs / 2;
+        if (!J.two && ok) {
+            if (n0 > 0) ok = mbar_wait(&B.pv_done[0], (n0 - 1) & 1, ab, a.err);
+            if (ok && n1 > 0) ok = mbar_wait(&B.pv_done[1], (n1 - 1) & 1, ab, a.err);
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+        float* xo = reinterpret_cast<float*>(ring);           // every product has ended: the ring is free
+        float* xml = reinterpret_cast<float*>(sQ + S::kQBytes);
+        if (!J.two) {
+            if (st == 1) {
+                xml[row] = m;
+                xml[kBlkQ + row] = l;
+                if (ok && n1 > 0) {
+#pragma unroll
+                    for (int c = 0; c < HD / 32; ++c) {
+                        uint32_t r[32];
+                        tmem_ld32(tO + 32 * c, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) xo[(32 * c + i) * kBlkQ + row] = __uint_as_float(r[i]);
+                    }
+                }
+            }
+            named_bar(1, 256);
+        }
+        const int qi = st * kBlkQ + row;                     // two tiles: this stream's row; one: stream 0's
+        if (ok && (J.two || st == 0)) {
+            float w0 = 1.f, w1 = 0.f;
+            if (!J.two) {
+                const float m1 = xml[row], l1 = xml[kBlkQ + row], M = fmaxf(m, m1), Mu = M == -INFINITY ? 0.f : M;
+                w0 = ex2(m - Mu);
+                w1 = ex2(m1 - Mu);
+                l = l * w0 + l1 * w1;
+                m = M;
+            }
+            const bool out = qi < J.nq;
+            const int v = J.q0 + qi;
+            const size_t vec = (size_t)split * a.span.T * a.H + (size_t)(v / G) * a.H + J.g * G + v % G;
+            if (out) {
+                a.part_ml[2 * vec] = m;
+                a.part_ml[2 * vec + 1] = l;
+            }
+            if (q > 0) {
+#pragma unroll
+                for (int c = 0; c < HD / 32; ++c) {
+                    uint32_t r[32];
+                    tmem_ld32(tO + 32 * c, r);
+                    tmem_wait_ld();
+                    if (!J.two) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float x1 = n1 > 0 ? xo[(32 * c + i) * kBlkQ + row] * w1 : 0.f;
+                            r[i] = __float_as_uint(fmaf(__uint_as_float(r[i]), w0, x1));
+                        }
+                    }
+                    if (out) {
+                        float4* dst = reinterpret_cast<float4*>(a.part_o + vec * HD + 32 * c);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            dst[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
+                                                 __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
+                    }
+                }
+            }
+        }
+        tc_fence_before();
+    } else if (warp == 8) {
+        // -------- copies: entries K0, V0, K1, V1, ... of the ring
+        constexpr int kBox = 4096 / HD;                       // slots a tensor box
+        const uint64_t keep = l2_policy_evict_last();         // the prompt is read by every query tile
+        int issued = 0;
+        for (int e = 0; e < 2 * J.n_kb; ++e) {
+            const int kt = J.k_begin + (e >> 1) * kBlkK;
+            if (Q8) {
+                const int s = e % NRAW, use = e / NRAW;
+                if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(&B.raw_empty[s], (use - 1) & 1, ab, a.err))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&B.raw_full[s], S::kRawBytes + kBlkK);
+                    const uint8_t* base = static_cast<const uint8_t*>(e & 1 ? a.pre.v : a.pre.k);
+                    const uint8_t* ex = e & 1 ? a.pre.ve : a.pre.ke;
+                    for (int p = 0; p < kBlkK / 64; ++p) {
+                        // 64 slots never cross a page; slots past the keys are read from the first piece again
+                        const int slot = kt + 64 * p < J.k_begin + J.n_keys ? kt + 64 * p : kt;
+                        long long row = kv_row_in_layer(a.pre.pages, a.Hkv, a.pre_seq, J.g, slot);
+                        if (row < 0) { dev_error(a.err, SPEC_DEVERR_CAPACITY); row = 0; }
+                        bulk_load(raw + s * S::kRawBytes + p * 64 * HD, base + row * HD, 64 * HD, &B.raw_full[s], keep);
+                        bulk_load(rexp + s * kBlkK + p * 64, ex + row, 64, &B.raw_full[s], keep);
+                    }
+                }
+            } else {
+                const int s = e % NST, use = e / NST;
+                if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(&B.empty[s], (use - 1) & 1, ab, a.err))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&B.full[s], S::kTileBytes);
+                    for (int p = 0; p < kBlkK / kBox; ++p) {
+                        const int slot = kt + kBox * p < J.k_begin + J.n_keys ? kt + kBox * p : kt;
+                        long long row = kv_row_in_layer(a.pre.pages, a.Hkv, a.pre_seq, J.g, slot);
+                        if (row < 0) { dev_error(a.err, SPEC_DEVERR_CAPACITY); row = 0; }
+                        for (int h = 0; h < HD / 64; ++h)
+                            tma_load_3d(ring + s * S::kTileBytes + h * kHalf + p * kBox * 128, e & 1 ? &tm_v : &tm_k, 64 * h,
+                                        (int)row, a.layer, &B.full[s], keep);
+                    }
+                }
+            }
+            ++issued;
+        }
+        // no copy may be in flight when the CTA ends: after an abort, the last use of each slot lands first
+        if (*ab) {
+            const int ns = Q8 ? NRAW : NST;
+            for (int e = max(0, issued - ns); e < issued; ++e)
+                mbar_wait(Q8 ? &B.raw_full[e % ns] : &B.full[e % ns], (e / ns) & 1, nullptr, a.err);
+        }
+    } else if (warp == 9) {
+        // -------- MMAs
+        constexpr uint32_t kIdS = idesc_bf16_f32(kBlkQ, kBlkK);
+        constexpr uint32_t kIdO = idesc_bf16_f32(kBlkQ, HD) | (1u << 16);    // B is MN-major
+        bool ok = __all_sync(0xffffffffu, mbar_wait(&B.q_full, 0, ab, a.err));
+        auto scores = [&](int n) {
+            const int i = n & 1, e = 2 * job_kb(J, n), s = e % NST;
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&B.full[s], (e / NST) & 1, ab, a.err));
+            if (!ok) return;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t qa = smem_u32(sQ) + (J.two ? i * S::kQBytes : 0), ka = smem_u32(ring) + s * S::kTileBytes;
+#pragma unroll
+                for (int ks = 0; ks < HD / 16; ++ks) {
+                    const uint32_t o = (ks >> 2) * kHalf + (ks & 3) * 32;
+                    tc_mma_f16(tmem + i * 128, smem_desc_sw128(qa + o), smem_desc_sw128(ka + o), kIdS, ks > 0);
+                }
+                tc_commit(&B.s_full[i]);
+                if (!J.two || i == 1) tc_commit(&B.empty[s]);
+            }
+            __syncwarp();
+        };
+        auto values = [&](int n) {
+            const int i = n & 1, kb = job_kb(J, n), e = 2 * kb + 1, s = e % NST;
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&B.full[s], (e / NST) & 1, ab, a.err));
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&B.p_full[i], (n >> 1) & 1, ab, a.err));
+            if (!ok) return;
+            const int valid = min(kBlkK, J.n_keys - kb * kBlkK), steps = (valid + 15) / 16;
+            char* vt = ring + s * S::kTileBytes;
+            if (!Q8 && valid < 16 * steps && (!J.two || i == 0)) {
+                // the last 16 keys' slots past the range: P is zero there, and V must be finite
+                const int n16 = (16 * steps - valid) * 8;
+                for (int x = lane; x < n16 * (HD / 64); x += 32)
+                    *reinterpret_cast<uint4*>(vt + (x / n16) * kHalf + valid * 128 + (x % n16) * 16) = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+                __syncwarp();
+            }
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t va = smem_u32(vt);
+                for (int ks = 0; ks < steps; ++ks)
+                    tc_mma_f16_ts(tmem + 256 + i * HD, tmem + i * 128 + 8 * ks, smem_desc_mn(va + ks * 2048, kHalf), kIdO,
+                                  n > 1 || ks > 0);
+                tc_commit(&B.pv_done[i]);
+                if (!J.two || i == 1) tc_commit(&B.empty[s]);
+            }
+            __syncwarp();
+        };
+        if (J.n_jobs > 0) scores(0);
+        if (J.n_jobs > 1) scores(1);
+        for (int n = 0; n < J.n_jobs && ok; ++n) {
+            values(n);
+            if (n + 2 < J.n_jobs) scores(n + 2);
+        }
+        if (!ok) {                                            // issued MMAs end before the memory goes
+            if (lane == 0) tc_commit(&B.drain);
+            mbar_wait(&B.drain, 0, nullptr, a.err);
+        }
+    } else if (Q8) {
+        // -------- raw e4m3 tiles to swizzled bf16 tiles
+        const int ct = t - 320;
+        for (int e = 0; e < 2 * J.n_kb; ++e) {
+            const int rs = e % NRAW, s = e % NST, use = e / NST;
+            bool ok = mbar_wait(&B.raw_full[rs], (e / NRAW) & 1, ab, a.err);
+            if (ok && use > 0) ok = mbar_wait(&B.empty[s], (use - 1) & 1, ab, a.err);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const int valid = J.n_keys - (e >> 1) * kBlkK;
+            const char* src = raw + rs * S::kRawBytes;
+            char* dst = ring + s * S::kTileBytes;
+            constexpr int CPK = HD / 16;                      // 16-byte pieces of a raw row
+#pragma unroll
+            for (int j = 0; j < CPK; ++j) {
+                const int id = ct + 128 * j, key = id / CPK, ch = id % CPK;
+                const uint4 w = *reinterpret_cast<const uint4*>(src + id * 16);
+                const float sc = key < valid ? kv8_scale(rexp[rs * kBlkK + key]) : 0.f;
+                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                uint32_t o[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 x = e4m3x2_f32(ws[i]), y = e4m3x2_f32(ws[i] >> 16);
+                    o[2 * i] = bf16x2(x.x * sc, x.y * sc);
+                    o[2 * i + 1] = bf16x2(y.x * sc, y.y * sc);
+                }
+                if (key >= valid)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = 0u;    // a NaN there stays out
+                char* d = dst + (ch >> 2) * kHalf + key * 128;
+                const int c0 = (2 * (ch & 3)) ^ (key & 7), c1 = (2 * (ch & 3) + 1) ^ (key & 7);
+                // the upper 64 dims' pieces in the other order: both halves' banks are then distinct
+                const bool flip = (ch >> 2) & 1;
+                const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                *reinterpret_cast<uint4*>(d + ((flip ? c1 : c0) << 4)) = flip ? hi : lo;
+                *reinterpret_cast<uint4*>(d + ((flip ? c0 : c1) << 4)) = flip ? lo : hi;
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&B.full[s]);
+                mbar_arrive(&B.raw_empty[rs]);
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_relinquish();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+bool attend_tile_ok(const spec_kv* pre) { return pre->q8 || pre->tmaps; }
+
+// Key ranges a (KV head, pair of query tiles): one CTA an SM, so the choice that
+// ends soonest counted in key tiles, with what a range costs beyond its keys
+// (queries in, pipeline start, state out) as four.
+int attend_tile_splits(const spec_model* m, const AttendSpan& span, int prompt_cap) {
+    const spec_model_config& c = m->cfg;
+    const int NQ = span.T * (c.n_heads / c.n_kv_heads), units = c.n_kv_heads * ((NQ + 255) / 256);
+    const int kb = std::max(1, (prompt_cap + kBlkK - 1) / kBlkK);
+    int best = 1;
+    long long least = -1;
+    for (int s = 1; s <= std::min(64, kb); ++s) {
+        const long long waves = ((long long)units * s + m->num_sms - 1) / m->num_sms;
+        const long long cost = waves * ((kb + s - 1) / s + 4);
+        if (least < 0 || cost < least) { least = cost; best = s; }
+    }
+    return best;
+}
+
+template <int HD, bool Q8>
+static int launch_tile(const spec_kv* pre, const AttendArgs& a, cudaStream_t st) {
+    using S = TileShape<HD, Q8>;
+    cudaError_t e = cudaFuncSetAttribute(attend_tile_kernel<HD, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess) return check_cuda(e, "attention tile kernel attribute");
+    const int NQ = a.span.T * (a.H / a.Hkv);
+    const dim3 grid((unsigned)(a.Hkv * ((NQ + 2 * kBlkQ - 1) / (2 * kBlkQ)) * a.tile_splits));
+    e = launch_k(pre->m->pdl, attend_tile_kernel<HD, Q8>, grid, dim3(S::kThreads), S::kSmem, st, a, pre->tm_k, pre->tm_v);
+    ++pre->m->launches;
+    return check_cuda(e, "attention tile launch");
+}
+
+int launch_attend_tile(const spec_kv* pre, const AttendArgs& a, cudaStream_t st) {
+    if (pre->m->cfg.head_dim == 128) return pre->q8 ? launch_tile<128, true>(pre, a, st) : launch_tile<128, false>(pre, a, st);
+    return pre->q8 ? launch_tile<64, true>(pre, a, st) : launch_tile<64, false>(pre, a, st);
+}
+
+}  // namespace spec
