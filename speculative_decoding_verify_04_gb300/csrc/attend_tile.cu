@@ -17,7 +17,7 @@
 //
 // Roles: warps 0-3 and 4-7 the streams' softmax, warp 8 the copies (TMA tensor
 // boxes with the 128-byte swizzle), warp 9 the MMAs; 8-bit caches add four warps
-// that turn raw e4m3 tiles into swizzled bf16 tiles (exact).
+// (12-15) that turn raw e4m3 tiles into swizzled bf16 tiles (exact).
 #include <algorithm>
 
 #include "attend.cuh"
@@ -35,7 +35,7 @@ struct TileShape {
     static constexpr int kRawBytes = kBlkK * HD;
     static constexpr int kStages = HD == 128 ? (Q8 ? 4 : 5) : 8;
     static constexpr int kRaw = Q8 ? (HD == 128 ? 2 : 4) : 0;
-    static constexpr int kThreads = Q8 ? 448 : 320;
+    static constexpr int kThreads = Q8 ? 512 : 384;
     static constexpr int kTiles = 2 * kQBytes + kStages * kTileBytes + kRaw * kRawBytes;
     static constexpr int kExpBytes = kRaw * kBlkK;
     static constexpr int kSmem = kTiles + kExpBytes + 512 + 1024;   // barriers; the tiles start on 1024 bytes
@@ -50,11 +50,16 @@ struct TileBars {
 };
 static_assert(sizeof(TileBars) <= 512, "barriers");
 
-// D[tmem] (+)= A[tmem] * B[smem], B MN-major
+// D[tmem] (+)= A[tmem] * B[smem]
 SPEC_DEV void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
                  :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+// a bounded wait of the whole warp
+SPEC_DEV bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* ab, int* err) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, ab, err));
 }
 // [key][64 dims] tiles, 128-byte swizzle, read as the MN-major operand: 64-dim
 // pieces lie `lead` bytes apart, groups of 8 keys 1024 bytes
@@ -94,6 +99,21 @@ SPEC_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
                     "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
                     "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
                  : "memory");
+}
+// two f32 lanes in one instruction
+SPEC_DEV float2 fma2(float2 x, float2 y, float2 z) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 r, a, b, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+    return d;
+}
+SPEC_DEV float2 add2(float2 x, float2 y) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return d;
 }
 SPEC_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -159,6 +179,17 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
     const int split = blockIdx.x / (a.Hkv * n_pair);
     volatile int* ab = &B.abort;
 
+    // the launch's registers, split by role: 512 x 128 = 256 x 200 + 128 x 48 + 128 x 64 and
+    // 384 x 168 = 256 x 216 + 128 x 72
+    if (warp < 8) {
+        if (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    } else if (warp < 12) {
+        if (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    }
     if (warp < 8) {
         // -------- queries into shared memory, then the softmax of stream `warp / 4`
         const int n_rows = J.two ? 2 * kBlkQ : kBlkQ;
@@ -195,23 +226,29 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
         bool ok = true;
         for (int n = st; n < J.n_jobs; n += 2, ++q) {
             const int kb = job_kb(J, n), valid = min(kBlkK, J.n_keys - kb * kBlkK);
-            ok = mbar_wait(&B.s_full[st], q & 1, ab, a.err);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            ok = warp_wait(&B.s_full[st], q & 1, ab, a.err);
+            if (!ok) break;
             tc_fence_after();
-            float mx = -INFINITY;
+            // the whole row at once: 128 scores in registers
+            uint32_t r[4][32];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t r[32];
-                tmem_ld32(tS + 32 * c, r);
-                tmem_wait_ld();
-                if (valid == kBlkK) {
+            for (int c = 0; c < 4; ++c) tmem_ld32(tS + 32 * c, r[c]);
+            tmem_wait_ld();
+            if (valid != kBlkK) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(r[i]));
-                } else {
+                for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = fmaxf(mx, 32 * c + i < valid ? __uint_as_float(r[i]) : -INFINITY);
-                }
+                    for (int i = 0; i < 32; ++i)
+                        if (32 * c + i >= valid) r[c][i] = 0xFF800000u;       // -inf
             }
+            float mx4[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) mx4[c] = __uint_as_float(r[c][0]);
+#pragma unroll
+            for (int i = 1; i < 32; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) mx4[c] = fmaxf(mx4[c], __uint_as_float(r[c][i]));
+            float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
             mx *= a.c;
             if (__any_sync(0xffffffffu, mx > m + kLazy || m == -INFINITY)) {
                 const float mn = fmaxf(m, mx);
@@ -224,38 +261,33 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                     tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < HD / 32; ++c) {
-                        uint32_t r[32];
-                        tmem_ld32(tO + 32 * c, r);
+                        uint32_t o[32];
+                        tmem_ld32(tO + 32 * c, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-                        tmem_st32(tO + 32 * c, r);
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st32(tO + 32 * c, o);
                     }
                 }
             }
             const float mu = m == -INFINITY ? 0.f : m;
+            const float2 cc = make_float2(a.c, a.c), mm = make_float2(-mu, -mu);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                uint32_t r[32], p[16];
-                tmem_ld32(tS + 32 * c, r);
-                tmem_wait_ld();
-                float s0 = 0.f, s1 = 0.f;
+                uint32_t p[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    float x = fmaf(__uint_as_float(r[2 * i]), a.c, -mu), y = fmaf(__uint_as_float(r[2 * i + 1]), a.c, -mu);
-                    if (valid != kBlkK) {
-                        if (32 * c + 2 * i >= valid) x = -INFINITY;
-                        if (32 * c + 2 * i + 1 >= valid) y = -INFINITY;
-                    }
-                    x = ex2(x);
-                    y = ex2(y);
-                    s0 += x;
-                    s1 += y;
-                    p[i] = bf16x2(x, y);
+                    float2 x = fma2(make_float2(__uint_as_float(r[c][2 * i]), __uint_as_float(r[c][2 * i + 1])), cc, mm);
+                    x.x = ex2(x.x);
+                    x.y = ex2(x.y);
+                    sum[i & 1] = add2(sum[i & 1], x);
+                    p[i] = bf16x2(x.x, x.y);
                 }
-                l += s0 + s1;
-                tmem_st16(tS + 16 * c, p);                    // P's columns lie over S columns already read
+                tmem_st16(tS + 16 * c, p);                    // P's columns lie over S columns
             }
+            sum[0] = add2(sum[0], sum[1]);
+            l += sum[0].x + sum[0].y;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -377,66 +409,78 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                 mbar_wait(Q8 ? &B.raw_full[e % ns] : &B.full[e % ns], (e / ns) & 1, nullptr, a.err);
         }
     } else if (warp == 9) {
-        // -------- MMAs
-        constexpr uint32_t kIdS = idesc_bf16_f32(kBlkQ, kBlkK);
-        constexpr uint32_t kIdO = idesc_bf16_f32(kBlkQ, HD) | (1u << 16);    // B is MN-major
-        bool ok = __all_sync(0xffffffffu, mbar_wait(&B.q_full, 0, ab, a.err));
-        auto scores = [&](int n) {
-            const int i = n & 1, e = 2 * job_kb(J, n), s = e % NST;
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&B.full[s], (e / NST) & 1, ab, a.err));
-            if (!ok) return;
-            tc_fence_after();
-            if (lane == 0) {
-                const uint32_t qa = smem_u32(sQ) + (J.two ? i * S::kQBytes : 0), ka = smem_u32(ring) + s * S::kTileBytes;
+        // -------- MMAs, by one thread: an MMA takes the tensor cores 64 cycles (hd 128) and
+        // only about two wait in their queue, so what lies between two groups has to be short
+        if (lane == 0) {
+            constexpr uint32_t kIdS = idesc_bf16_f32(kBlkQ, kBlkK);
+            constexpr uint32_t kIdO = idesc_bf16_f32(kBlkQ, HD) | (1u << 16);    // B is MN-major
+            const uint64_t qd = smem_desc_sw128(smem_u32(sQ)), kd = smem_desc_sw128(smem_u32(ring));
+            const uint64_t vd = smem_desc_mn(smem_u32(ring), kHalf);
+            bool ok = mbar_wait(&B.q_full, 0, ab, a.err);
+            int ks_ = 0, kph = 0, vs_ = 1, vph = 0;           // ring slots and phases of the next K and V tiles
+            auto scores = [&](int i) {
+                if (!J.two || i == 0) ok = ok && mbar_wait(&B.full[ks_], kph, ab, a.err);
+                if (!ok) return;
+                const uint64_t q0 = qd + (J.two && i ? S::kQBytes >> 4 : 0), k0 = kd + ks_ * (S::kTileBytes >> 4);
 #pragma unroll
                 for (int ks = 0; ks < HD / 16; ++ks) {
-                    const uint32_t o = (ks >> 2) * kHalf + (ks & 3) * 32;
-                    tc_mma_f16(tmem + i * 128, smem_desc_sw128(qa + o), smem_desc_sw128(ka + o), kIdS, ks > 0);
+                    const uint32_t o = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+                    tc_mma_f16(tmem + i * 128, q0 + o, k0 + o, kIdS, ks > 0);
                 }
                 tc_commit(&B.s_full[i]);
-                if (!J.two || i == 1) tc_commit(&B.empty[s]);
-            }
-            __syncwarp();
-        };
-        auto values = [&](int n) {
-            const int i = n & 1, kb = job_kb(J, n), e = 2 * kb + 1, s = e % NST;
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&B.full[s], (e / NST) & 1, ab, a.err));
-            ok = ok && __all_sync(0xffffffffu, mbar_wait(&B.p_full[i], (n >> 1) & 1, ab, a.err));
-            if (!ok) return;
-            const int valid = min(kBlkK, J.n_keys - kb * kBlkK), steps = (valid + 15) / 16;
-            char* vt = ring + s * S::kTileBytes;
-            if (!Q8 && valid < 16 * steps && (!J.two || i == 0)) {
-                // the last 16 keys' slots past the range: P is zero there, and V must be finite
-                const int n16 = (16 * steps - valid) * 8;
-                for (int x = lane; x < n16 * (HD / 64); x += 32)
-                    *reinterpret_cast<uint4*>(vt + (x / n16) * kHalf + valid * 128 + (x % n16) * 16) = make_uint4(0, 0, 0, 0);
-                fence_async_smem();
-                __syncwarp();
-            }
-            tc_fence_after();
-            if (lane == 0) {
-                const uint32_t va = smem_u32(vt);
-                for (int ks = 0; ks < steps; ++ks)
-                    tc_mma_f16_ts(tmem + 256 + i * HD, tmem + i * 128 + 8 * ks, smem_desc_mn(va + ks * 2048, kHalf), kIdO,
-                                  n > 1 || ks > 0);
+                if (!J.two || i == 1) {
+                    tc_commit(&B.empty[ks_]);
+                    ks_ += 2;
+                    if (ks_ >= NST) { ks_ -= NST; kph ^= 1; }
+                }
+            };
+            auto values = [&](int n, int i) {
+                if (!J.two || i == 0) ok = ok && mbar_wait(&B.full[vs_], vph, ab, a.err);
+                ok = ok && mbar_wait(&B.p_full[i], (n >> 1) & 1, ab, a.err);
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t v0 = vd + vs_ * (S::kTileBytes >> 4);
+                const uint32_t d = tmem + 256 + i * HD, p = tmem + i * 128;
+                const int valid = J.n_keys - job_kb(J, n) * kBlkK;
+                if (valid >= kBlkK) {
+#pragma unroll
+                    for (int ks = 0; ks < kBlkK / 16; ++ks)
+                        tc_mma_f16_ts(d, p + 8 * ks, v0 + ks * (2048 >> 4), kIdO, n > 1 || ks > 0);
+                } else {
+                    const int steps = (valid + 15) / 16;
+                    if (!Q8 && (!J.two || i == 0)) {
+                        // the last 16 keys' slots past the range: P is zero there, and V must be finite
+                        char* vt = ring + vs_ * S::kTileBytes;
+                        for (int h = 0; h < HD / 64; ++h)
+                            for (int x = valid * 8; x < steps * 128; ++x)
+                                *reinterpret_cast<uint4*>(vt + h * kHalf + x * 16) = make_uint4(0, 0, 0, 0);
+                        fence_async_smem();
+                    }
+                    for (int ks = 0; ks < steps; ++ks)
+                        tc_mma_f16_ts(d, p + 8 * ks, v0 + ks * (2048 >> 4), kIdO, n > 1 || ks > 0);
+                }
                 tc_commit(&B.pv_done[i]);
-                if (!J.two || i == 1) tc_commit(&B.empty[s]);
+                if (!J.two || i == 1) {
+                    tc_commit(&B.empty[vs_]);
+                    vs_ += 2;
+                    if (vs_ >= NST) { vs_ -= NST; vph ^= 1; }
+                }
+            };
+            if (J.n_jobs > 0) scores(0);
+            if (J.n_jobs > 1) scores(1);
+            for (int n = 0; n < J.n_jobs && ok; ++n) {
+                values(n, n & 1);
+                if (n + 2 < J.n_jobs) scores(n & 1);
             }
-            __syncwarp();
-        };
-        if (J.n_jobs > 0) scores(0);
-        if (J.n_jobs > 1) scores(1);
-        for (int n = 0; n < J.n_jobs && ok; ++n) {
-            values(n);
-            if (n + 2 < J.n_jobs) scores(n + 2);
+            if (!ok) {                                        // issued MMAs end before the memory goes
+                tc_commit(&B.drain);
+                mbar_wait(&B.drain, 0, nullptr, a.err);
+            }
         }
-        if (!ok) {                                            // issued MMAs end before the memory goes
-            if (lane == 0) tc_commit(&B.drain);
-            mbar_wait(&B.drain, 0, nullptr, a.err);
-        }
-    } else if (Q8) {
+        __syncwarp();
+    } else if (Q8 && warp >= 12) {
         // -------- raw e4m3 tiles to swizzled bf16 tiles
-        const int ct = t - 320;
+        const int ct = t - 384;
         for (int e = 0; e < 2 * J.n_kb; ++e) {
             const int rs = e % NRAW, s = e % NST, use = e / NST;
             bool ok = mbar_wait(&B.raw_full[rs], (e / NRAW) & 1, ab, a.err);
