@@ -38,13 +38,15 @@ struct TileShape {
     static constexpr int kThreads = Q8 ? 512 : 384;
     static constexpr int kTiles = 2 * kQBytes + kStages * kTileBytes + kRaw * kRawBytes;
     static constexpr int kExpBytes = kRaw * kBlkK;
+    // partial states leave through the ring (and the raw tiles behind it): 256 padded rows, or 128 behind the exchange
+    static_assert(kStages * kTileBytes + kRaw * kRawBytes >= 256 * (HD * 4 + 16), "states");
     static constexpr int kSmem = kTiles + kExpBytes + 512 + 1024;   // barriers; the tiles start on 1024 bytes
 };
 
 struct TileBars {
     uint64_t full[8], empty[8];          // K/V ring
     uint64_t raw_full[4], raw_empty[4];  // raw e4m3 ring
-    uint64_t q_full, s_full[2], p_full[2], pv_done[2], drain;
+    uint64_t q_full, s_full[2], p_full[2], done;
     uint32_t tmem;
     int abort;
 };
@@ -100,6 +102,12 @@ SPEC_DEV void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
                     "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
                  : "memory");
 }
+// the larger of three, the last two as bits
+SPEC_DEV float max3(float x, uint32_t y, uint32_t z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(__uint_as_float(y)), "f"(__uint_as_float(z)));
+    return r;
+}
 // two f32 lanes in one instruction
 SPEC_DEV float2 fma2(float2 x, float2 y, float2 z) {
     float2 d;
@@ -142,13 +150,16 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
     TileBars& B = *reinterpret_cast<TileBars*>(tiles + S::kTiles + S::kExpBytes);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
 
+    const int G = a.H / a.Hkv, NQ = a.span.T * G, n_pair = (NQ + 2 * kBlkQ - 1) / (2 * kBlkQ);
+    const int q0 = (blockIdx.x / a.Hkv) % n_pair * 2 * kBlkQ;
+    const bool two = NQ - q0 > kBlkQ;    // two tiles of query vectors: both streams free each K and V tile
     if (warp == 9) tmem_alloc(&B.tmem, 512);
     if (t == 0) {
-        for (int i = 0; i < NST; ++i) { mbar_init(&B.full[i], Q8 ? 4 : 1); mbar_init(&B.empty[i], 1); }
+        for (int i = 0; i < NST; ++i) { mbar_init(&B.full[i], Q8 ? 4 : 1); mbar_init(&B.empty[i], two ? 2 : 1); }
         for (int i = 0; i < NRAW; ++i) { mbar_init(&B.raw_full[i], 1); mbar_init(&B.raw_empty[i], 4); }
         mbar_init(&B.q_full, 8);
-        for (int i = 0; i < 2; ++i) { mbar_init(&B.s_full[i], 1); mbar_init(&B.p_full[i], 4); mbar_init(&B.pv_done[i], 1); }
-        mbar_init(&B.drain, 1);
+        for (int i = 0; i < 2; ++i) { mbar_init(&B.s_full[i], 1); mbar_init(&B.p_full[i], 5); }
+        mbar_init(&B.done, 1);
         B.abort = 0;
         fence_mbar_init();
     }
@@ -159,16 +170,13 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
     pdl_trigger();                       // every CTA that can hold TMEM has it: the next kernel's cannot take it first
     pdl_wait();
 
-    const int G = a.H / a.Hkv, NQ = a.span.T * G, n_pair = (NQ + 2 * kBlkQ - 1) / (2 * kBlkQ);
     TileJob J;
     {
-        int id = blockIdx.x;
-        J.g = id % a.Hkv;
-        id /= a.Hkv;
-        J.q0 = (id % n_pair) * 2 * kBlkQ;
-        id /= n_pair;
-        J.nq = min(2 * kBlkQ, NQ - J.q0);
-        J.two = J.nq > kBlkQ;
+        const int id = blockIdx.x / (a.Hkv * n_pair);
+        J.g = blockIdx.x % a.Hkv;
+        J.q0 = q0;
+        J.nq = min(2 * kBlkQ, NQ - q0);
+        J.two = two;
         const int P = min(a.pre.len[a.pre_seq], a.pre.cap);
         const int per = ((P + a.tile_splits - 1) / a.tile_splits + kBlkK - 1) / kBlkK * kBlkK;
         J.k_begin = min(P, id * per);
@@ -192,27 +200,34 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
     }
     if (warp < 8) {
         // -------- queries into shared memory, then the softmax of stream `warp / 4`
-        const int n_rows = J.two ? 2 * kBlkQ : kBlkQ;
-        for (int i = t; i < n_rows * (HD / 8); i += 256) {
-            const int r = i / (HD / 8), ch = i % (HD / 8);
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (r < J.nq && J.n_kb > 0) {
-                const int qi = J.q0 + r;
+        // a thread takes one 16-byte piece of every RPP-th row; eight loads go out before the first store
+        constexpr int CPR = HD / 8, RPP = 256 / CPR, NB = HD == 128 ? 8 : 4;
+        const int ch = t % CPR;
+        for (int r0 = t / CPR; r0 < (J.two ? 2 * kBlkQ : kBlkQ); r0 += NB * RPP) {
+            uint4 w[NB];
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                const int r = r0 + k * RPP, qi = J.q0 + r;
+                w[k] = make_uint4(0, 0, 0, 0);
+                if (r >= J.nq) continue;
                 const long long off = (qi / G) * a.q_stride + (J.g * G + qi % G) * HD + ch * 8;
                 if (a.q_f32) {
                     const float* p = static_cast<const float*>(a.q) + off;
-                    const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
-                    w = make_uint4(bf16x2(x.x, x.y), bf16x2(x.z, x.w), bf16x2(y.x, y.y), bf16x2(y.z, y.w));
+                    const float4 x = __ldg(reinterpret_cast<const float4*>(p)), y = __ldg(reinterpret_cast<const float4*>(p + 4));
+                    w[k] = make_uint4(bf16x2(x.x, x.y), bf16x2(x.z, x.w), bf16x2(y.x, y.y), bf16x2(y.z, y.w));
                 } else if (a.q_vec) {
-                    w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + off);
+                    w[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + off));
                 } else {
                     const unsigned short* p = static_cast<const unsigned short*>(a.q) + off;
-                    w = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16,
-                                   p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
+                    w[k] = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16,
+                                      p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
                 }
             }
-            const int rr = r & (kBlkQ - 1);
-            *reinterpret_cast<uint4*>(sQ + (r / kBlkQ) * S::kQBytes + (ch >> 3) * kHalf + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = w;
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                const int r = r0 + k * RPP, rr = r & (kBlkQ - 1);
+                *reinterpret_cast<uint4*>(sQ + (r / kBlkQ) * S::kQBytes + (ch >> 3) * kHalf + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = w[k];
+            }
         }
         fence_async_smem();
         __syncwarp();
@@ -223,12 +238,23 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
         const uint32_t tS = tmem + st * 128 + lanes, tO = tmem + 256 + st * HD + lanes;
         float m = -INFINITY, l = 0.f;                                        // m: the maximum that the exponents use
         int q = 0;                                                           // job of this stream
+        int kslot = J.two ? 0 : 2 * st, vslot = 0;                           // ring slots of its next K and last V tile
+        while (kslot >= NST) kslot -= NST;
         bool ok = true;
         for (int n = st; n < J.n_jobs; n += 2, ++q) {
             const int kb = job_kb(J, n), valid = min(kBlkK, J.n_keys - kb * kBlkK);
             ok = warp_wait(&B.s_full[st], q & 1, ab, a.err);
             if (!ok) break;
             tc_fence_after();
+            if ((warp & 3) == 0 && lane == 0) {
+                // S is there, and with it every product before it: this K tile is free, and the V
+                // tile of the stream's product before
+                mbar_arrive(&B.empty[kslot]);
+                if (q > 0) mbar_arrive(&B.empty[vslot]);
+            }
+            vslot = kslot + 1 == NST ? 0 : kslot + 1;
+            kslot += J.two ? 2 : 4;
+            while (kslot >= NST) kslot -= NST;
             // the whole row at once: 128 scores in registers
             uint32_t r[4][32];
 #pragma unroll
@@ -248,6 +274,7 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
             for (int i = 1; i < 32; ++i)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) mx4[c] = fmaxf(mx4[c], __uint_as_float(r[c][i]));
+
             float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
             mx *= a.c;
             if (__any_sync(0xffffffffu, mx > m + kLazy || m == -INFINITY)) {
@@ -256,9 +283,6 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                 l *= f;
                 m = mn;
                 if (q > 0) {
-                    ok = mbar_wait(&B.pv_done[st], (q - 1) & 1, ab, a.err);
-                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                    tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < HD / 32; ++c) {
                         uint32_t o[32];
@@ -294,13 +318,8 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
             if (lane == 0) mbar_arrive(&B.p_full[st]);
         }
         // -------- the state: this stream's own rows, or (one tile) joined with the other stream's
-        if (ok && q > 0) ok = mbar_wait(&B.pv_done[st], (q - 1) & 1, ab, a.err);
-        const int n0 = (J.n_jobs + 1) / 2, n1 = J.n_jobs / 2;
-        if (!J.two && ok) {
-            if (n0 > 0) ok = mbar_wait(&B.pv_done[0], (n0 - 1) & 1, ab, a.err);
-            if (ok && n1 > 0) ok = mbar_wait(&B.pv_done[1], (n1 - 1) & 1, ab, a.err);
-        }
-        ok = __all_sync(0xffffffffu, ok);
+        const int n1 = J.n_jobs / 2;                          // jobs of stream 1
+        if (ok) ok = warp_wait(&B.done, 0, ab, a.err);
         tc_fence_after();
         float* xo = reinterpret_cast<float*>(ring);           // every product has ended: the ring is free
         float* xml = reinterpret_cast<float*>(sQ + S::kQBytes);
@@ -334,11 +353,12 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
             const bool out = qi < J.nq;
             const int v = J.q0 + qi;
             const size_t vec = (size_t)split * a.span.T * a.H + (size_t)(v / G) * a.H + J.g * G + v % G;
-            if (out) {
-                a.part_ml[2 * vec] = m;
-                a.part_ml[2 * vec + 1] = l;
-            }
+            if (out) *reinterpret_cast<float2*>(a.part_ml + 2 * vec) = make_float2(m, l);
             if (q > 0) {
+                // the row goes out as one bulk copy from shared memory (rows 16 bytes apart in banks):
+                // stored from registers, every instruction of a warp would meet 32 lines
+                constexpr int kRow = HD * 4 + 16;
+                char* so = ring + (J.two ? 0 : HD * kBlkQ * 4) + qi * kRow;
 #pragma unroll
                 for (int c = 0; c < HD / 32; ++c) {
                     uint32_t r[32];
@@ -351,20 +371,24 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                             r[i] = __float_as_uint(fmaf(__uint_as_float(r[i]), w0, x1));
                         }
                     }
-                    if (out) {
-                        float4* dst = reinterpret_cast<float4*>(a.part_o + vec * HD + 32 * c);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            dst[i] = make_float4(__uint_as_float(r[4 * i]), __uint_as_float(r[4 * i + 1]),
-                                                 __uint_as_float(r[4 * i + 2]), __uint_as_float(r[4 * i + 3]));
-                    }
+                    for (int i = 0; i < 8; ++i)
+                        *reinterpret_cast<uint4*>(so + 128 * c + 16 * i) = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                }
+                fence_async_smem();
+                if (out) {
+                    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                                 :: "l"(reinterpret_cast<uint64_t>(a.part_o + vec * HD)), "r"(smem_u32(so)), "r"(HD * 4) : "memory");
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
                 }
             }
         }
         tc_fence_before();
     } else if (warp == 8) {
         // -------- copies: entries K0, V0, K1, V1, ... of the ring
-        constexpr int kBox = 4096 / HD;                       // slots a tensor box
+        constexpr int kBox = 64;                              // slots a tensor box (no page holds fewer)
+        constexpr int kBoxes = kBlkK / kBox * (HD / 64);      // boxes of a tile, one a lane
         const uint64_t keep = l2_policy_evict_last();         // the prompt is read by every query tile
         int issued = 0;
         for (int e = 0; e < 2 * J.n_kb; ++e) {
@@ -388,17 +412,17 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
             } else {
                 const int s = e % NST, use = e / NST;
                 if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(&B.empty[s], (use - 1) & 1, ab, a.err))) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&B.full[s], S::kTileBytes);
-                    for (int p = 0; p < kBlkK / kBox; ++p) {
-                        const int slot = kt + kBox * p < J.k_begin + J.n_keys ? kt + kBox * p : kt;
-                        long long row = kv_row_in_layer(a.pre.pages, a.Hkv, a.pre_seq, J.g, slot);
-                        if (row < 0) { dev_error(a.err, SPEC_DEVERR_CAPACITY); row = 0; }
-                        for (int h = 0; h < HD / 64; ++h)
-                            tma_load_3d(ring + s * S::kTileBytes + h * kHalf + p * kBox * 128, e & 1 ? &tm_v : &tm_k, 64 * h,
-                                        (int)row, a.layer, &B.full[s], keep);
-                    }
+                if (lane == 0) mbar_arrive_expect_tx(&B.full[s], S::kTileBytes);
+                __syncwarp();
+                if (lane < kBoxes) {
+                    const int p = lane / (HD / 64), h = lane % (HD / 64);
+                    const int slot = kt + kBox * p < J.k_begin + J.n_keys ? kt + kBox * p : kt;
+                    long long row = kv_row_in_layer(a.pre.pages, a.Hkv, a.pre_seq, J.g, slot);
+                    if (row < 0) { dev_error(a.err, SPEC_DEVERR_CAPACITY); row = 0; }
+                    tma_load_3d(ring + s * S::kTileBytes + h * kHalf + p * kBox * 128, e & 1 ? &tm_v : &tm_k, 64 * h, (int)row,
+                                a.layer, &B.full[s], keep);
                 }
+                __syncwarp();
             }
             ++issued;
         }
@@ -409,18 +433,23 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                 mbar_wait(Q8 ? &B.raw_full[e % ns] : &B.full[e % ns], (e / ns) & 1, nullptr, a.err);
         }
     } else if (warp == 9) {
-        // -------- MMAs, by one thread: an MMA takes the tensor cores 64 cycles (hd 128) and
-        // only about two wait in their queue, so what lies between two groups has to be short
+        // -------- MMAs, by one thread: the streams' jobs alternate, so that one stream's softmax runs
+        // while the other's products do (two threads let both fall into step: 4190 cycles a pair of
+        // jobs instead of 3300).  An MMA takes the tensor cores 64 cycles (hd 128) and hardly more
+        // than one waits in the thread's queue, so every look at a barrier and every commit lets the
+        // cores run dry (measured, 16 MMAs: 1024 cycles, with one commit and one, two or three waits
+        // 1124, 1221 or 1303).  So a stream's P V and its next S go out together behind one wait: the
+        // gate's arrival on p_full stands for the V tile and the next K tile.  And with one commit: it
+        // covers every MMA before it, and the softmax threads that see S complete free the K tile
+        // and the V tile before it.
         if (lane == 0) {
             constexpr uint32_t kIdS = idesc_bf16_f32(kBlkQ, kBlkK);
             constexpr uint32_t kIdO = idesc_bf16_f32(kBlkQ, HD) | (1u << 16);    // B is MN-major
             const uint64_t qd = smem_desc_sw128(smem_u32(sQ)), kd = smem_desc_sw128(smem_u32(ring));
             const uint64_t vd = smem_desc_mn(smem_u32(ring), kHalf);
             bool ok = mbar_wait(&B.q_full, 0, ab, a.err);
-            int ks_ = 0, kph = 0, vs_ = 1, vph = 0;           // ring slots and phases of the next K and V tiles
+            int ks_ = 0, vs_ = 1;                             // ring slots of the next K and V tiles
             auto scores = [&](int i) {
-                if (!J.two || i == 0) ok = ok && mbar_wait(&B.full[ks_], kph, ab, a.err);
-                if (!ok) return;
                 const uint64_t q0 = qd + (J.two && i ? S::kQBytes >> 4 : 0), k0 = kd + ks_ * (S::kTileBytes >> 4);
 #pragma unroll
                 for (int ks = 0; ks < HD / 16; ++ks) {
@@ -428,56 +457,57 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                     tc_mma_f16(tmem + i * 128, q0 + o, k0 + o, kIdS, ks > 0);
                 }
                 tc_commit(&B.s_full[i]);
-                if (!J.two || i == 1) {
-                    tc_commit(&B.empty[ks_]);
-                    ks_ += 2;
-                    if (ks_ >= NST) { ks_ -= NST; kph ^= 1; }
-                }
+                if (!J.two || i == 1) ks_ = ks_ + 2 >= NST ? ks_ + 2 - NST : ks_ + 2;
             };
-            auto values = [&](int n, int i) {
-                if (!J.two || i == 0) ok = ok && mbar_wait(&B.full[vs_], vph, ab, a.err);
-                ok = ok && mbar_wait(&B.p_full[i], (n >> 1) & 1, ab, a.err);
-                if (!ok) return;
-                tc_fence_after();
+            for (int n = 0; n < 2 && n < J.n_jobs; ++n) {
+                ok = ok && mbar_wait(&B.full[ks_], 0, ab, a.err);
+                if (ok) scores(n);
+            }
+            for (int n = 0; n < J.n_jobs && ok; ++n) {
+                const int i = n & 1;
                 const uint64_t v0 = vd + vs_ * (S::kTileBytes >> 4);
                 const uint32_t d = tmem + 256 + i * HD, p = tmem + i * 128;
-                const int valid = J.n_keys - job_kb(J, n) * kBlkK;
-                if (valid >= kBlkK) {
+                const int steps = min(kBlkK, J.n_keys - job_kb(J, n) * kBlkK + 15) / 16;
+                ok = mbar_wait(&B.p_full[i], (n >> 1) & 1, ab, a.err);
+                if (!ok) break;
+                tc_fence_after();
+                if (steps == kBlkK / 16) {
 #pragma unroll
                     for (int ks = 0; ks < kBlkK / 16; ++ks)
                         tc_mma_f16_ts(d, p + 8 * ks, v0 + ks * (2048 >> 4), kIdO, n > 1 || ks > 0);
                 } else {
-                    const int steps = (valid + 15) / 16;
-                    if (!Q8 && (!J.two || i == 0)) {
-                        // the last 16 keys' slots past the range: P is zero there, and V must be finite
-                        char* vt = ring + vs_ * S::kTileBytes;
-                        for (int h = 0; h < HD / 64; ++h)
-                            for (int x = valid * 8; x < steps * 128; ++x)
-                                *reinterpret_cast<uint4*>(vt + h * kHalf + x * 16) = make_uint4(0, 0, 0, 0);
-                        fence_async_smem();
-                    }
                     for (int ks = 0; ks < steps; ++ks)
                         tc_mma_f16_ts(d, p + 8 * ks, v0 + ks * (2048 >> 4), kIdO, n > 1 || ks > 0);
                 }
-                tc_commit(&B.pv_done[i]);
-                if (!J.two || i == 1) {
-                    tc_commit(&B.empty[vs_]);
-                    vs_ += 2;
-                    if (vs_ >= NST) { vs_ -= NST; vph ^= 1; }
-                }
-            };
-            if (J.n_jobs > 0) scores(0);
-            if (J.n_jobs > 1) scores(1);
-            for (int n = 0; n < J.n_jobs && ok; ++n) {
-                values(n, n & 1);
-                if (n + 2 < J.n_jobs) scores(n & 1);
+                if (!J.two || i == 1) vs_ = vs_ + 2 >= NST ? vs_ + 2 - NST : vs_ + 2;
+                if (n + 2 < J.n_jobs) scores(i);
             }
-            if (!ok) {                                        // issued MMAs end before the memory goes
-                tc_commit(&B.drain);
-                mbar_wait(&B.drain, 0, nullptr, a.err);
-            }
+            tc_commit(&B.done);                               // every MMA; after an abort too, before the memory goes
+            if (!ok) mbar_wait(&B.done, 0, nullptr, a.err);
         }
         __syncwarp();
+    } else if (warp == 10) {
+        // -------- the gate: a job's V tile and the K tile of the stream's next job have come
+        for (int n = 0; n < J.n_jobs; ++n) {
+            const int kb = job_kb(J, n), ev = 2 * kb + 1, ek = 2 * job_kb(J, n + 2), valid = J.n_keys - kb * kBlkK;
+            // (two tiles: stream 1 finds what stream 0 waited for)
+            bool ok = warp_wait(&B.full[ev % NST], (ev / NST) & 1, ab, a.err);
+            if (ok && n + 2 < J.n_jobs) ok = warp_wait(&B.full[ek % NST], (ek / NST) & 1, ab, a.err);
+            if (!ok) break;
+            if (!Q8 && valid < kBlkK && (!J.two || !(n & 1))) {
+                // the last 16 keys' slots past the range: P is zero there, and V must be finite
+                char* vt = ring + (ev % NST) * S::kTileBytes;
+                for (int h = 0; h < HD / 64; ++h)
+                    for (int x = valid * 8 + lane; x < (valid + 15) / 16 * 128; x += 32)
+                        *reinterpret_cast<uint4*>(vt + h * kHalf + x * 16) = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+                __syncwarp();
+            }
+            // p_full takes one gate arrival a phase: not before the stream's last one was used
+            if (n >= 2 && !warp_wait(&B.s_full[n & 1], (n >> 1) & 1, ab, a.err)) break;
+            if (lane == 0) mbar_arrive(&B.p_full[n & 1]);
+            __syncwarp();
+        }
     } else if (Q8 && warp >= 12) {
         // -------- raw e4m3 tiles to swizzled bf16 tiles
         const int ct = t - 384;
@@ -557,7 +587,7 @@ static int launch_tile(const spec_kv* pre, const AttendArgs& a, cudaStream_t st)
     if (e != cudaSuccess) return check_cuda(e, "attention tile kernel attribute");
     const int NQ = a.span.T * (a.H / a.Hkv);
     const dim3 grid((unsigned)(a.Hkv * ((NQ + 2 * kBlkQ - 1) / (2 * kBlkQ)) * a.tile_splits));
-    e = launch_k(pre->m->pdl, attend_tile_kernel<HD, Q8>, grid, dim3(S::kThreads), S::kSmem, st, a, pre->tm_k, pre->tm_v);
+    e = launch_k(pre->m->pdl, attend_tile_kernel<HD, Q8>, grid, dim3(S::kThreads), S::kSmem, st, a, pre->tm_k64, pre->tm_v64);
     ++pre->m->launches;
     return check_cuda(e, "attention tile launch");
 }

@@ -99,12 +99,13 @@ bool make_kv_tmaps(spec_kv* kv) {
     const uint64_t rows = (uint64_t)kv->n_pages * c.n_kv_heads * kv->page;
     if (rows >= (1ull << 31)) return true;            // slot coordinates are 32-bit
     if (!load_encoder()) return false;
-    for (int w = 0; w < 2; ++w) {
+    CUtensorMap* maps[4] = {&kv->tm_k, &kv->tm_v, &kv->tm_k64, &kv->tm_v64};
+    for (int w = 0; w < 4; ++w) {
         cuuint64_t dims[3] = {(cuuint64_t)c.head_dim, rows, (cuuint64_t)c.n_layers};
         cuuint64_t strides[2] = {(cuuint64_t)c.head_dim * 2, rows * c.head_dim * 2};
-        cuuint32_t box[3] = {64, (cuuint32_t)(4096 / c.head_dim), 1};
+        cuuint32_t box[3] = {64, (cuuint32_t)(w < 2 ? 4096 / c.head_dim : 64), 1};
         cuuint32_t estr[3] = {1, 1, 1};
-        CUresult r = g_encode(w ? &kv->tm_v : &kv->tm_k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, w ? kv->v : kv->k, dims,
+        CUresult r = g_encode(maps[w], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, w & 1 ? kv->v : kv->k, dims,
                               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
         if (r != CUDA_SUCCESS) return false;

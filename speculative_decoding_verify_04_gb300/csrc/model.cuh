@@ -216,6 +216,9 @@ struct spec_kv {
     // GEMM chain); tmaps is false where the cache is too large to address
     alignas(64) CUtensorMap tm_k;
     alignas(64) CUtensorMap tm_v;
+    // the same with boxes of 64 dims x 64 slots (tiles of a shared prompt)
+    alignas(64) CUtensorMap tm_k64;
+    alignas(64) CUtensorMap tm_v64;
     bool tmaps = false;
 };
 
