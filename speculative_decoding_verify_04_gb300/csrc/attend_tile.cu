@@ -488,7 +488,9 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
         __syncwarp();
     } else if (warp == 10) {
         // -------- the gate: a job's V tile and the K tile of the stream's next job have come
-        for (int n = 0; n < J.n_jobs; ++n) {
+        bool first = true;                                    // the first K tiles, so that every slot's phases are waited for in turn
+        for (int n = 0; n < 2 && n < J.n_jobs && first; ++n) first = warp_wait(&B.full[2 * job_kb(J, n) % NST], 0, ab, a.err);
+        for (int n = 0; n < J.n_jobs && first; ++n) {
             const int kb = job_kb(J, n), ev = 2 * kb + 1, ek = 2 * job_kb(J, n + 2), valid = J.n_keys - kb * kBlkK;
             // (two tiles: stream 1 finds what stream 0 waited for)
             bool ok = warp_wait(&B.full[ev % NST], (ev / NST) & 1, ab, a.err);
@@ -503,8 +505,10 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                 fence_async_smem();
                 __syncwarp();
             }
-            // p_full takes one gate arrival a phase: not before the stream's last one was used
-            if (n >= 2 && !warp_wait(&B.s_full[n & 1], (n >> 1) & 1, ab, a.err)) break;
+            // p_full takes one gate arrival a phase: this job's S comes after the stream's last P V, so the
+            // last phase is over (every phase of s_full is waited for in turn, the first ones too: a
+            // parity alone does not tell a phase from the one before the last)
+            if (!warp_wait(&B.s_full[n & 1], (n >> 1) & 1, ab, a.err)) break;
             if (lane == 0) mbar_arrive(&B.p_full[n & 1]);
             __syncwarp();
         }

@@ -149,6 +149,54 @@ def test_many_query_vectors(rows, prompt, q8):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("dim,heads,kv_heads,B,rows,prompt", [(128, 32, 8, 64, 8, 6001), (64, 16, 4, 40, 7, 5000),
+                                                              (128, 8, 8, 3, 40, 9000), (64, 32, 1, 64, 4, 3000)])
+def test_long_prompts_and_many_tiles(dim, heads, kv_heads, B, rows, prompt, q8):
+    """Enough key tiles and tiles of query vectors that every SM works through several; ten calls, each against 64
+    bits (computed on the GPU), all of the same bits."""
+    from _attend_util import attend_tol, rows8
+    from speculative_decoding_verify_04_gb300 import spec
+    c = Case(20, heads, kv_heads, dim, [0] * B, [rows] * B, prompt=1, max_rows=B * rows, max_batch=B)
+    g = torch.Generator(device="cuda").manual_seed(21)
+    k, v = (torch.randn(prompt, kv_heads, dim, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    pre = spec.KVCache(c.model, 1, prompt + 3, q8=q8)
+    pre.import_rows(0, 0, k[None], v[None])
+    pre.set_lengths([prompt])
+    c.kv.set_prefix(pre, 0)
+    held = pre.export_rows(0, 0, 1, 0, prompt) if q8 else (k[None], v[None])
+    if q8:                                                  # a stretch of it against the definition
+        assert torch.equal(held[0][0, :50].double().cpu(), torch.from_numpy(rows8(k[:50].double().cpu().numpy())[2]))
+    G, T = heads // kv_heads, B * rows
+    scale = 1.0 / math.sqrt(dim)
+    q = c.q.cuda().double().view(B, rows, kv_heads, G, dim)
+    pk, pv = (x[0].double() for x in held)
+    nk, nv = (x.cuda().double().view(B, rows, kv_heads, dim) for x in (c.k, c.v))
+    hide = ~torch.ones(rows, rows, dtype=torch.bool, device="cuda").tril()
+    ref, mass, big = (torch.empty(T, heads, d, dtype=torch.float64, device="cuda") for d in (dim, dim, 1))
+    for h in range(kv_heads):
+        qh = q[:, :, h]
+        s = torch.cat([torch.einsum("brgd,kd->brgk", qh, pk[:, h]),
+                       torch.einsum("brgd,bkd->brgk", qh, nk[:, :, h]).masked_fill(hide[None, :, None], -math.inf)], -1) * scale
+        p = torch.softmax(s, -1)
+        hs = slice(h * G, (h + 1) * G)
+        for out, vals, new in ((ref, pv[:, h], nv[:, :, h]), (mass, pv[:, h].abs(), nv[:, :, h].abs())):
+            o = torch.einsum("brgk,kd->brgd", p[..., :prompt], vals) + torch.einsum("brgk,bkd->brgd", p[..., prompt:], new)
+            out[:, hs] = o.reshape(T, G, dim)
+        top = torch.maximum(torch.einsum("brgd,kd->brgk", qh.abs(), pk[:, h].abs()).amax(-1),
+                            torch.einsum("brgd,bkd->brgk", qh.abs(), nk[:, :, h].abs()).amax(-1)) * scale
+        big[:, hs, 0] = top.reshape(T, G)
+        del s, p
+    tol = attend_tol(ref, mass, big[..., 0], dim)
+    first = None
+    for _ in range(10):
+        out = c.run()
+        assert ((out.double() - ref).abs() <= tol).all()
+        first = out if first is None else first
+        assert torch.equal(first, out)
+    assert c.model.device_error() == 0
+
+
 @pytest.mark.parametrize("dim", [64, 128])
 @pytest.mark.parametrize("q8", [False, True])
 def test_what_lies_behind_the_lengths_does_not_show(q8, dim):
