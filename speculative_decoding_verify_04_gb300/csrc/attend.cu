@@ -331,54 +331,92 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
     }
 }
 
-// One warp a (row, head): the ranges' states in range order (the prompt's, then the sequence's own).
+// The ranges' states of a (row, head) joined: the prompt's, then the sequence's own, by
+// one warp (eight ranges in flight), or by four that take every fourth range each and
+// whose sums are added in warp order.  Many rows of few ranges are bound by reading the
+// states, few rows of many by the latency of it: more than 12 ranges take four warps
+// (2048 rows of 21 ranges: 12.5 us by one warp, 8.9 by four; 16384 rows of 5: 39 us by
+// four warps).
 struct JoinArgs {
     const float* part_o; const float* part_ml;
-    int ranges, TH, H;
+    int own_range0, own_ranges, pre_ranges;     // pre_ranges: the row kernel's prompt ranges
+    int tile_ctas;                              // > 0: the tile kernel's prompt ranges, counted on the device
+    const int* pre_len; int pre_cap;
+    int TH, H, G, Hkv;
     __nv_bfloat16* out;
     long long stride;
     size_t lo;                        // 0: one bf16 row; else hi rows and lo rows at this offset
 };
 
-template <int HD>
+template <int HD, int NW>
 __global__ void __launch_bounds__(128)
-attend_join_kernel(const JoinArgs a) {
+attend_join_kernel(const __grid_constant__ JoinArgs a) {
     pdl_wait();
     pdl_trigger();
-    constexpr int E = HD / 32;
-    const int v = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (v >= a.TH) return;
+    constexpr int E = HD / 32, U = 8;
+    __shared__ float sO[3][HD], sL[3];
+    const int w = NW == 4 ? threadIdx.x >> 5 : 0, lane = threadIdx.x & 31;
+    const int v = NW == 4 ? blockIdx.x : blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (NW == 1 && v >= a.TH) return;
+    int pre = a.pre_ranges;
+    if (a.tile_ctas) {
+        const int KB = (min(*a.pre_len, a.pre_cap) + 127) / 128;
+        pre = tile_range_count((v % a.H) / a.G, KB, (long long)a.Hkv * KB, a.tile_ctas);
+    }
+    const int n = pre + a.own_ranges;
+    auto slot = [&](int s) { return (size_t)(s < pre ? s : a.own_range0 + s - pre) * a.TH + v; };
     float M = -INFINITY;
-    for (int s = lane; s < a.ranges; s += 32) M = fmaxf(M, a.part_ml[2 * ((size_t)s * a.TH + v)]);
+    for (int s = lane; s < n; s += 32) M = fmaxf(M, a.part_ml[2 * slot(s)]);
     M = warp_max(M);
     float L = 0.f, O[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) O[e] = 0.f;
     if (M != -INFINITY) {
-        for (int s0 = 0; s0 < a.ranges; s0 += 32) {
-            float w = 0.f, l = 0.f;
-            if (s0 + lane < a.ranges) {
-                const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + 2 * ((size_t)(s0 + lane) * a.TH + v));
-                w = ex2(ml.x - M);
-                l = ml.y * w;
-            }
-            L += warp_sum(l);
-            const int n = min(32, a.ranges - s0);
-#pragma unroll 4
-            for (int s = 0; s < n; ++s) {
-                const float ws = __shfl_sync(0xffffffffu, w, s);
-                const float* src = a.part_o + ((size_t)(s0 + s) * a.TH + v) * HD + lane * E;
-                float x[E];
-                if (E == 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(src);
-                    x[0] = f.x; x[1] = f.y; x[E - 2] = f.z; x[E - 1] = f.w;
-                } else {
-                    const float2 f = *reinterpret_cast<const float2*>(src);
-                    x[0] = f.x; x[1] = f.y;
-                }
+        for (int s0 = w; s0 < n; s0 += NW * U) {
+            float2 ml[U];
+            float x[U][E];
 #pragma unroll
-                for (int e = 0; e < E; ++e) O[e] = ws > 0.f ? fmaf(ws, x[e], O[e]) : O[e];
+            for (int u = 0; u < U; ++u) {
+                const int s = s0 + NW * u;
+                ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[u][e] = 0.f;
+                if (s < n) {
+                    const size_t at = slot(s);
+                    ml[u] = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
+                    if (ml[u].x == -INFINITY) continue;       // an empty range: its sums were not written
+                    const float* src = a.part_o + at * HD + lane * E;
+                    if (E == 4) {
+                        const float4 f = *reinterpret_cast<const float4*>(src);
+                        x[u][0] = f.x; x[u][1] = f.y; x[u][E - 2] = f.z; x[u][E - 1] = f.w;
+                    } else {
+                        const float2 f = *reinterpret_cast<const float2*>(src);
+                        x[u][0] = f.x; x[u][1] = f.y;
+                    }
+                }
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float ws = ex2(ml[u].x - M);
+                L = fmaf(ml[u].y, ws, L);
+#pragma unroll
+                for (int e = 0; e < E; ++e) O[e] = fmaf(ws, x[u][e], O[e]);
+            }
+        }
+    }
+    if (NW == 4) {
+        if (w > 0) {
+            if (lane == 0) sL[w - 1] = L;
+#pragma unroll
+            for (int e = 0; e < E; ++e) sO[w - 1][lane * E + e] = O[e];
+        }
+        __syncthreads();
+        if (w > 0) return;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            L += sL[k];
+#pragma unroll
+            for (int e = 0; e < E; ++e) O[e] += sO[k][lane * E + e];
         }
     }
     const float inv = 1.0f / L;
@@ -434,11 +472,12 @@ static size_t rows_smem(int hd, bool qf32) {
     return (qf32 ? 2 : 1) * (hd / 16) * 32 * 16 + 4 * 16 * (hd + 2) * sizeof(float) + 16 * 8;
 }
 
-// Query vectors whose partial states fit: every launch shape below keeps to
-// (ranges) x (T * H) <= 2 x 16 x 512 + 2 T H, and the tile kernel to 2 x 152 tiles of 128 more.
+// Query vectors whose partial states fit.  The row kernel's two parts keep to (ranges) x
+// (T * H) <= 16 x 512 + T H each.  The tile kernel's CTAs are one an SM, so its ranges
+// are (SMs / pairs of query tiles) / Hkv + 2, with T * H <= 256 Hkv (pairs): 256 SMs + 2 T H.
 size_t attend_floats_needed(const spec_model* m) {
     const size_t th = (size_t)m->cfg.max_rows * m->cfg.n_heads;
-    return (2 * 16 * 512 + 2 * 2 * (size_t)m->num_sms * 128 + 4 * th) * (m->cfg.head_dim + 2);
+    return (2 * 16 * 512 + 256 * (size_t)m->num_sms + 4 * th) * (m->cfg.head_dim + 2);
 }
 
 int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q, int q_f32, long long q_stride,
@@ -476,13 +515,15 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     };
     a.own_splits = splits(own_blocks, kv->max_ctx);
     a.pre_splits = splits(pre_blocks, pre ? pre->max_ctx : 0);
+    int tile_ranges = 0;
     if (tile) {
-        a.tile_splits = attend_tile_splits(m, span, pre->max_ctx);
-        a.tile_splits = (int)std::min<size_t>(a.tile_splits, fit > (size_t)a.own_splits ? fit - a.own_splits : 0);
+        a.tile_ctas = attend_tile_ctas(m, span, pre->max_ctx);
+        while (a.tile_ctas > 1 && (size_t)(a.own_splits + attend_tile_ranges(m, a.tile_ctas)) > fit) --a.tile_ctas;
+        tile_ranges = attend_tile_ranges(m, a.tile_ctas);
     }
-    a.own_range0 = a.pre_splits + a.tile_splits;
+    a.own_range0 = a.pre_splits + tile_ranges;
     const int ranges = a.own_splits + a.own_range0;
-    if ((size_t)ranges > fit || (tile && a.tile_splits == 0)) return set_error(SPEC_ERR_CAPACITY, "attention workspace too small");
+    if ((size_t)ranges > fit) return set_error(SPEC_ERR_CAPACITY, "attention workspace too small");
     a.part_o = m->attend_part;
     a.part_ml = m->attend_part + (size_t)ranges * TH * hd;
     const dim3 grid((unsigned)(a.pre_splits * pre_blocks + a.own_splits * own_blocks));
@@ -496,13 +537,22 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     JoinArgs j{};
     j.part_o = a.part_o;
     j.part_ml = a.part_ml;
-    j.ranges = ranges;
+    j.own_range0 = a.own_range0;
+    j.own_ranges = a.own_splits;
+    j.pre_ranges = a.pre_splits;
+    j.tile_ctas = a.tile_ctas;
+    if (pre) j.pre_len = pre->len + kv->prefix_seq;
+    if (pre) j.pre_cap = pre->max_ctx;
     j.TH = TH;
     j.H = H;
+    j.G = G;
+    j.Hkv = Hkv;
     j.out = out.p;
     j.stride = out.stride;
     j.lo = out.lo;
-    e = launch_k(m->pdl, hd == 128 ? attend_join_kernel<128> : attend_join_kernel<64>, dim3((TH + 3) / 4), dim3(128), 0, st, j);
+    void (*jf)(JoinArgs) = ranges > 12 ? (hd == 128 ? attend_join_kernel<128, 4> : attend_join_kernel<64, 4>)
+                                       : (hd == 128 ? attend_join_kernel<128, 1> : attend_join_kernel<64, 1>);
+    e = launch_k(m->pdl, jf, dim3(ranges > 12 ? TH : (TH + 3) / 4), dim3(128), 0, st, j);
     m->launches += 2;
     prof_stop(m, slot, st, PROF_ATTN, 0.0);
     return check_cuda(e, "attention join launch");

@@ -56,7 +56,7 @@ struct AttendArgs {
     int H, Hkv;
     AttendSpan span;
     int own_splits, pre_splits;       // key ranges; pre_splits is 0 where the tile kernel takes the prompt
-    int tile_splits;                  // the tile kernel's ranges
+    int tile_ctas;                    // the tile kernel's CTAs a pair of query tiles
     int own_qb, pre_qb;               // query blocks of 16
     float* part_o;                    // [range][T * H][hd]
     float* part_ml;                   // [range][T * H][2]
@@ -72,7 +72,14 @@ SPEC_DEV float ex2(float x) {
 
 // attend_tile.cu: the prompt's part for lists of many query vectors
 bool attend_tile_ok(const spec_kv* pre);
-int attend_tile_splits(const spec_model* m, const AttendSpan& span, int prompt_cap);
+int attend_tile_ctas(const spec_model* m, const AttendSpan& span, int prompt_cap);
+int attend_tile_ranges(const spec_model* m, int ctas);      // most ranges of one KV head
+// Of n CTAs that share the W = Hkv KB key tiles of all heads evenly (CTA j from j W / n on),
+// the one that holds head g's first.  Its range of the head is range 0, the next one's range 1, ...
+SPEC_DEV int tile_first_cta(int g, int KB, long long W, int n) { return (int)((((long long)g * KB + 1) * n - 1) / W); }
+SPEC_DEV int tile_range_count(int g, int KB, long long W, int n) {
+    return KB == 0 ? 0 : (int)(((long long)(g + 1) * KB * n - 1) / W) - tile_first_cta(g, KB, W, n) + 1;
+}
 int launch_attend_tile(const spec_kv* pre, const AttendArgs& a, cudaStream_t st);
 
 // Where the attention's result goes: bf16 rows of the caller, or the model's

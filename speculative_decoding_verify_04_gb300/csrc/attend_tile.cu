@@ -1,10 +1,11 @@
 // The shared prompt against many query vectors: tiles of 128 query vectors by
 // 128 keys on the tensor cores (tcgen05), accumulators in tensor memory.
 //
-// A CTA owns one KV head, one range of the prompt's keys and two streams.  With
-// two tiles of query vectors the streams are the tiles, and every K and V tile
-// serves both; with one tile the streams take the key tiles in turn and their
-// states are joined at the end.  Per stream and key tile:
+// The (KV head, key tile) list of a pair of query tiles is cut evenly over the
+// pair's CTAs, so all end together whatever the sizes; a CTA takes its part head
+// by head, with two streams.  With two tiles of query vectors the streams are the
+// tiles, and every K and V tile serves both; with one tile the streams take the
+// key tiles in turn and their states are joined at the end.  Per stream and key tile:
 //     S = Q K^T          tcgen05.mma, both operands in shared memory, S in TMEM
 //     P = 2^(c S - m)    one thread a query vector: S row from TMEM, running max
 //                        and sum in registers, P as bf16 over S in TMEM
@@ -43,7 +44,7 @@ struct TileShape {
     static constexpr int kSmem = kTiles + kExpBytes + 512 + 1024;   // barriers; the tiles start on 1024 bytes
 };
 
-struct TileBars {
+struct TileBars {                        // full .. done: every barrier, in one run
     uint64_t full[8], empty[8];          // K/V ring
     uint64_t raw_full[4], raw_empty[4];  // raw e4m3 ring
     uint64_t q_full, s_full[2], p_full[2], done;
@@ -125,7 +126,7 @@ SPEC_DEV float2 add2(float2 x, float2 y) {
 }
 SPEC_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// What a CTA does: its KV head, query tiles and keys.
+// What a CTA does in one turn: a KV head, its query tiles and a run of its keys.
 struct TileJob {
     int g, nq, q0;                       // vectors [q0, q0 + nq) of the head's list, nq <= 256
     int two;                             // two tiles of query vectors (else the streams share one)
@@ -150,18 +151,21 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
     TileBars& B = *reinterpret_cast<TileBars*>(tiles + S::kTiles + S::kExpBytes);
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
 
-    const int G = a.H / a.Hkv, NQ = a.span.T * G, n_pair = (NQ + 2 * kBlkQ - 1) / (2 * kBlkQ);
-    const int q0 = (blockIdx.x / a.Hkv) % n_pair * 2 * kBlkQ;
+    const int G = a.H / a.Hkv, NQ = a.span.T * G;
+    const int q0 = (int)(blockIdx.x / a.tile_ctas) * 2 * kBlkQ;
     const bool two = NQ - q0 > kBlkQ;    // two tiles of query vectors: both streams free each K and V tile
-    if (warp == 9) tmem_alloc(&B.tmem, 512);
-    if (t == 0) {
+    auto init_bars = [&]() {
         for (int i = 0; i < NST; ++i) { mbar_init(&B.full[i], Q8 ? 4 : 1); mbar_init(&B.empty[i], two ? 2 : 1); }
         for (int i = 0; i < NRAW; ++i) { mbar_init(&B.raw_full[i], 1); mbar_init(&B.raw_empty[i], 4); }
         mbar_init(&B.q_full, 8);
         for (int i = 0; i < 2; ++i) { mbar_init(&B.s_full[i], 1); mbar_init(&B.p_full[i], 5); }
         mbar_init(&B.done, 1);
-        B.abort = 0;
         fence_mbar_init();
+    };
+    if (warp == 9) tmem_alloc(&B.tmem, 512);
+    if (t == 0) {
+        init_bars();
+        B.abort = 0;
     }
     tc_fence_before();
     __syncthreads();
@@ -170,35 +174,46 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
     pdl_trigger();                       // every CTA that can hold TMEM has it: the next kernel's cannot take it first
     pdl_wait();
 
-    TileJob J;
-    {
-        const int id = blockIdx.x / (a.Hkv * n_pair);
-        J.g = blockIdx.x % a.Hkv;
+    // the pair's (KV head, key tile) list, cut evenly over its CTAs: this one's part, head by head
+    const int P = min(a.pre.len[a.pre_seq], a.pre.cap), KB = (P + kBlkK - 1) / kBlkK;
+    const long long W = (long long)a.Hkv * KB;
+    const int cta = blockIdx.x % a.tile_ctas;
+    long long at = cta * W / a.tile_ctas;
+    const long long stop = (cta + 1) * W / a.tile_ctas;
+    volatile int* ab = &B.abort;
+
+    // a turn's job; between turns every warp meets twice and the barriers start afresh
+    auto take = [&](TileJob& J) {
+        J.g = (int)(at / KB);
         J.q0 = q0;
         J.nq = min(2 * kBlkQ, NQ - q0);
         J.two = two;
-        const int P = min(a.pre.len[a.pre_seq], a.pre.cap);
-        const int per = ((P + a.tile_splits - 1) / a.tile_splits + kBlkK - 1) / kBlkK * kBlkK;
-        J.k_begin = min(P, id * per);
-        J.n_keys = min(P - J.k_begin, per);
-        J.n_kb = (J.n_keys + kBlkK - 1) / kBlkK;
+        J.k_begin = (int)(at - (long long)J.g * KB) * kBlkK;
+        J.n_kb = (int)min(stop - at, (long long)(J.g + 1) * KB - at);
+        J.n_keys = min(P - J.k_begin, J.n_kb * kBlkK);
         J.n_jobs = J.two ? 2 * J.n_kb : J.n_kb;
-    }
-    const int split = blockIdx.x / (a.Hkv * n_pair);
-    volatile int* ab = &B.abort;
+        at += J.n_kb;
+    };
+    auto turn_over = [&]() {
+        __syncthreads();
+        if (*ab || at >= stop) return true;
+        if (t == 0) {
+            for (uint64_t* b = B.full; b <= &B.done; ++b)
+                asm volatile("mbarrier.inval.shared::cta.b64 [%0];" :: "r"(smem_u32(b)) : "memory");
+            init_bars();
+        }
+        __syncthreads();
+        return false;
+    };
 
     // the launch's registers, split by role: 512 x 128 = 256 x 200 + 128 x 48 + 128 x 64 and
     // 384 x 168 = 256 x 216 + 128 x 72
     if (warp < 8) {
         if (Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-    } else if (warp < 12) {
-        if (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    }
-    if (warp < 8) {
+        for (TileJob J; at < stop;) {
+        take(J);
+        const int range = cta - tile_first_cta(J.g, KB, W, a.tile_ctas);
         // -------- queries into shared memory, then the softmax of stream `warp / 4`
         // a thread takes one 16-byte piece of every RPP-th row; eight loads go out before the first store
         constexpr int CPR = HD / 8, RPP = 256 / CPR, NB = HD == 128 ? 8 : 4;
@@ -352,7 +367,7 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
             }
             const bool out = qi < J.nq;
             const int v = J.q0 + qi;
-            const size_t vec = (size_t)split * a.span.T * a.H + (size_t)(v / G) * a.H + J.g * G + v % G;
+            const size_t vec = (size_t)range * a.span.T * a.H + (size_t)(v / G) * a.H + J.g * G + v % G;
             if (out) *reinterpret_cast<float2*>(a.part_ml + 2 * vec) = make_float2(m, l);
             if (q > 0) {
                 // the row goes out as one bulk copy from shared memory (rows 16 bytes apart in banks):
@@ -384,8 +399,16 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                 }
             }
         }
+        fence_async_smem();                                   // the next copies come over what was written here
         tc_fence_before();
-    } else if (warp == 8) {
+        if (turn_over()) break;
+        }
+    } else if (warp < 12) {
+        if (Q8) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        for (TileJob J; at < stop;) {
+        take(J);
+        if (warp == 8) {
         // -------- copies: entries K0, V0, K1, V1, ... of the ring
         constexpr int kBox = 64;                              // slots a tensor box (no page holds fewer)
         constexpr int kBoxes = kBlkK / kBox * (HD / 64);      // boxes of a tile, one a lane
@@ -432,7 +455,7 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
             for (int e = max(0, issued - ns); e < issued; ++e)
                 mbar_wait(Q8 ? &B.raw_full[e % ns] : &B.full[e % ns], (e / ns) & 1, nullptr, a.err);
         }
-    } else if (warp == 9) {
+        } else if (warp == 9) {
         // -------- MMAs, by one thread: the streams' jobs alternate, so that one stream's softmax runs
         // while the other's products do (two threads let both fall into step: 4190 cycles a pair of
         // jobs instead of 3300).  An MMA takes the tensor cores 64 cycles (hd 128) and hardly more
@@ -448,6 +471,7 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
             const uint64_t qd = smem_desc_sw128(smem_u32(sQ)), kd = smem_desc_sw128(smem_u32(ring));
             const uint64_t vd = smem_desc_mn(smem_u32(ring), kHalf);
             bool ok = mbar_wait(&B.q_full, 0, ab, a.err);
+            tc_fence_after();
             int ks_ = 0, vs_ = 1;                             // ring slots of the next K and V tiles
             auto scores = [&](int i) {
                 const uint64_t q0 = qd + (J.two && i ? S::kQBytes >> 4 : 0), k0 = kd + ks_ * (S::kTileBytes >> 4);
@@ -486,7 +510,7 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
             if (!ok) mbar_wait(&B.done, 0, nullptr, a.err);
         }
         __syncwarp();
-    } else if (warp == 10) {
+        } else if (warp == 10) {
         // -------- the gate: a job's V tile and the K tile of the stream's next job have come
         bool first = true;                                    // the first K tiles, so that every slot's phases are waited for in turn
         for (int n = 0; n < 2 && n < J.n_jobs && first; ++n) first = warp_wait(&B.full[2 * job_kb(J, n) % NST], 0, ab, a.err);
@@ -512,7 +536,13 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
             if (lane == 0) mbar_arrive(&B.p_full[n & 1]);
             __syncwarp();
         }
-    } else if (Q8 && warp >= 12) {
+        }
+        if (turn_over()) break;
+        }
+    } else if (Q8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        for (TileJob J; at < stop;) {
+        take(J);
         // -------- raw e4m3 tiles to swizzled bf16 tiles
         const int ct = t - 384;
         for (int e = 0; e < 2 * J.n_kb; ++e) {
@@ -555,6 +585,8 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                 mbar_arrive(&B.raw_empty[rs]);
             }
         }
+        if (turn_over()) break;
+        }
     }
     __syncthreads();
     if (warp == 9) {
@@ -567,22 +599,28 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
 // ---------------------------------------------------------------------------
 bool attend_tile_ok(const spec_kv* pre) { return pre->q8 || pre->tmaps; }
 
-// Key ranges a (KV head, pair of query tiles): one CTA an SM, so the choice that
-// ends soonest counted in key tiles, with what a range costs beyond its keys
-// (queries in, pipeline start, state out) as four.
-int attend_tile_splits(const spec_model* m, const AttendSpan& span, int prompt_cap) {
+// CTAs a pair of query tiles, one CTA an SM: the choice whose longest CTA ends
+// soonest, counted in key tiles.  A turn costs about 12000 cycles beyond its keys
+// (queries in, pipeline start, state out), a key tile 1500 a tile of query vectors;
+// cuts that fall on heads (a multiple of Hkv CTAs) need one turn, others two.
+// (64 samples x 8 rows over 32768 tokens: 19 CTAs a pair 182 us, the next
+// multiple, 16, 206; 8 chains over 4096 tokens with 32 heads: 152 CTAs 22 us, 128 15 us.)
+int attend_tile_ctas(const spec_model* m, const AttendSpan& span, int prompt_cap) {
     const spec_model_config& c = m->cfg;
-    const int NQ = span.T * (c.n_heads / c.n_kv_heads), units = c.n_kv_heads * ((NQ + 255) / 256);
-    const int kb = std::max(1, (prompt_cap + kBlkK - 1) / kBlkK);
+    const int H = c.n_kv_heads, NQ = span.T * (c.n_heads / H), pairs = (NQ + 2 * kBlkQ - 1) / (2 * kBlkQ);
+    const long long W = (long long)H * std::max(1, (prompt_cap + kBlkK - 1) / kBlkK);
+    const int turn = NQ > kBlkQ ? 4 : 8;
     int best = 1;
     long long least = -1;
-    for (int s = 1; s <= std::min(64, kb); ++s) {
-        const long long waves = ((long long)units * s + m->num_sms - 1) / m->num_sms;
-        const long long cost = waves * ((kb + s - 1) / s + 4);
-        if (least < 0 || cost < least) { least = cost; best = s; }
+    for (int n = 1; n <= m->num_sms && (n == 1 || 2 * n <= W); ++n) {
+        const long long waves = ((long long)pairs * n + m->num_sms - 1) / m->num_sms;
+        const int turns = n % H == 0 ? 1 : (H % n == 0 ? H / n : H / n + 2);
+        const long long cost = waves * ((W + n - 1) / n + turn * turns);
+        if (least < 0 || cost < least) { least = cost; best = n; }
     }
     return best;
 }
+int attend_tile_ranges(const spec_model* m, int ctas) { return ctas / m->cfg.n_kv_heads + 2; }
 
 template <int HD, bool Q8>
 static int launch_tile(const spec_kv* pre, const AttendArgs& a, cudaStream_t st) {
@@ -590,7 +628,7 @@ static int launch_tile(const spec_kv* pre, const AttendArgs& a, cudaStream_t st)
     cudaError_t e = cudaFuncSetAttribute(attend_tile_kernel<HD, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return check_cuda(e, "attention tile kernel attribute");
     const int NQ = a.span.T * (a.H / a.Hkv);
-    const dim3 grid((unsigned)(a.Hkv * ((NQ + 2 * kBlkQ - 1) / (2 * kBlkQ)) * a.tile_splits));
+    const dim3 grid((unsigned)((NQ + 2 * kBlkQ - 1) / (2 * kBlkQ) * a.tile_ctas));
     e = launch_k(pre->m->pdl, attend_tile_kernel<HD, Q8>, grid, dim3(S::kThreads), S::kSmem, st, a, pre->tm_k64, pre->tm_v64);
     ++pre->m->launches;
     return check_cuda(e, "attention tile launch");
