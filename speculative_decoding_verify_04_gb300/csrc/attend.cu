@@ -21,20 +21,38 @@ constexpr int kRowThreads = 128;
 constexpr int kRowVectors = 16;       // query vectors a KV head up to which the row kernel takes the prompt
 constexpr int kMinKeys = 256;         // least keys of a range: below it the join costs more than the ranges give
 
-// Eight keys' bytes as bf16 pairs: words of e4m3 -> 2 bf16x2 each
-SPEC_DEV void e4m3x4_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-    const float2 a = e4m3x2_f32(w), b = e4m3x2_f32(w >> 16);
-    lo = bf16x2(a.x, a.y);
-    hi = bf16x2(b.x, b.y);
+// two e4m3 values as f16 (exact)
+SPEC_DEV uint32_t e4m3x2_f16(uint32_t two) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+    return h;
+}
+SPEC_DEV uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+SPEC_DEV float f16_round(float x) {
+    float r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.rn.f16.f32 h, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(r) : "f"(x));
+    return r;
+}
+SPEC_DEV void mma16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // ---------------------------------------------------------------------------
 // The row kernel: 16 query vectors a CTA, the M side of mma.sync m16n8k16, its
-// four warps in turn on 16-key tiles that go from global memory to fragments.
-// Inside a k-step the order of the head dimensions, and inside a tile the order
-// of the keys, is free (both factors use the same), so they are chosen such
-// that every load is a 16-byte piece of a K or V row and that the scores'
-// accumulator fragment is P's operand fragment:
+// four warps in turn on 16-key tiles that go from global memory to fragments,
+// the next tile's loads ahead of this one's arithmetic in 8-bit caches.  Inside
+// a k-step the order of the head dimensions, and inside a tile the order of the
+// keys, is free (both factors use the same), so they are chosen such that every
+// load is a piece of a K or V row and that the scores' accumulator fragment is
+// P's operand fragment:
 //   lane (g, c) = (lane / 4, lane % 4);
 //   scores, key half h: column g is tile key 4 (g / 2) + 2 h + g % 2, so lane
 //     (g, c) ends with keys 4c .. 4c+3 of rows g and g + 8;
@@ -42,111 +60,174 @@ SPEC_DEV void e4m3x4_bf16(uint32_t w, uint32_t& lo, uint32_t& hi) {
 //     k-steps, an e4m3 piece (16 dims at 64 p + 16 c) four;
 //   values: n-tile nt of column g is dim (hd / 8) g + nt, so lane (g, c) reads
 //     hd / 8 consecutive dims of V rows 4c .. 4c+3.
-// e4m3 tiles become bf16 (exact); a key's exponent multiplies its scores, a
-// value's its probability.  P is split into bf16 hi + lo, so its rounding does
-// not show; f32 queries are split the same way (QF32).
-template <int HD, bool Q8>
-SPEC_DEV void load_tile(const CacheView& cv, long long row, int kt, int k_end, int gq, int cq,
-                        uint32_t (&kb)[2][HD / 16][2], uint32_t (&vb)[4][HD / 16], float (&ks)[4], float (&vs)[4]) {
-    constexpr int VD = HD / 8;
-    if (Q8) {
-        const uint8_t* K = static_cast<const uint8_t*>(cv.k) + row * HD;
-        const uint8_t* V = static_cast<const uint8_t*>(cv.v) + row * HD;
-        uint4 kr[2][HD / 64];
-        uint32_t vr[4][VD / 4];
+//
+// bf16 caches: P is split into bf16 hi + lo, so its rounding does not show.
+// 8-bit caches: products in f16, which holds every e4m3 value (one conversion
+// for two values; to bf16 it takes four).  The queries are scaled by a power of
+// two a row to a magnitude of 2^13 .. 2^14 (bf16 queries stay exact down to
+// 2^-31 of the row's largest); a key's 2^e multiplies its scores; a value's
+// 2^e goes into the exponent of its probability, relative to a maximum of its
+// own (R, over s + e): P' = 2^(s + e - R) is at most 1 and in f16 off by 2^-12
+// of itself, below 2^-14 by 2^-25 of the row's largest.  f32 queries are split
+// into hi + lo (QF32).
+//
+// Bound by instructions (about 250 a 16-key tile and warp at hd 128) and by the
+// latency of the few tiles a warp has.
+template <int HD>
+struct RawTile {                                  // 16 keys of an 8-bit cache as they lie in memory
+    uint4 k[2][HD / 64];
+    uint32_t v[4][HD / 32];
+    uint32_t ke, ve;
+};
+
+template <int HD>
+SPEC_DEV void load_raw(const AttendArgs& a, const CacheView& cv, int seq, int g, int kt, int k_end, int gq, int cq, RawTile<HD>& t) {
+    // tiles start at multiples of 16 and pages hold a multiple of 16 slots: no tile crosses a page
+    long long row = kv_row_in_layer(cv.pages, a.Hkv, seq, g, kt);
+    if (row < 0) { dev_error(a.err, SPEC_DEVERR_CAPACITY); row = 0; }
+    const uint8_t* K = static_cast<const uint8_t*>(cv.k) + row * HD;
+    const uint8_t* V = static_cast<const uint8_t*>(cv.v) + row * HD;
+    const int last = k_end - 1 - kt;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int key = min(4 * (gq >> 1) + 2 * h + (gq & 1), k_end - 1 - kt);
+    for (int h = 0; h < 2; ++h) {
+        const int key = min(4 * (gq >> 1) + 2 * h + (gq & 1), last);
 #pragma unroll
-            for (int p = 0; p < HD / 64; ++p) kr[h][p] = __ldg(reinterpret_cast<const uint4*>(K + key * HD) + 4 * p + cq);
-        }
+        for (int p = 0; p < HD / 64; ++p) t.k[h][p] = __ldg(reinterpret_cast<const uint4*>(K + key * HD) + 4 * p + cq);
+    }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int key = min(4 * cq + r, k_end - 1 - kt);
-            if (HD == 128) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(V + key * HD) + gq);
-                vr[r][0] = w.x; vr[r][1] = w.y; vr[r][VD / 4 - 2] = w.z; vr[r][VD / 4 - 1] = w.w;
-            } else {
-                const uint2 w = __ldg(reinterpret_cast<const uint2*>(V + key * HD) + gq);
-                vr[r][0] = w.x; vr[r][1] = w.y;
-            }
-        }
-        // the pages hold a multiple of 16 slots: four exponents are one aligned word
-        const uint32_t ke = __ldg(reinterpret_cast<const uint32_t*>(cv.ke + row) + cq);
-        const uint32_t ve = __ldg(reinterpret_cast<const uint32_t*>(cv.ve + row) + cq);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            ks[i] = kv8_scale((ke >> (8 * i)) & 0xFF);
-            vs[i] = kv8_scale((ve >> (8 * i)) & 0xFF);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int p = 0; p < HD / 64; ++p) {
-                const uint32_t w[4] = {kr[h][p].x, kr[h][p].y, kr[h][p].z, kr[h][p].w};
-#pragma unroll
-                for (int s = 0; s < 4; ++s) e4m3x4_bf16(w[s], kb[h][4 * p + s][0], kb[h][4 * p + s][1]);
-            }
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-            for (int i = 0; i < VD / 4; ++i) e4m3x4_bf16(vr[r][i], vb[r][2 * i], vb[r][2 * i + 1]);
-    } else {
-        const __nv_bfloat16* K = static_cast<const __nv_bfloat16*>(cv.k) + row * HD;
-        const __nv_bfloat16* V = static_cast<const __nv_bfloat16*>(cv.v) + row * HD;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int key = min(4 * (gq >> 1) + 2 * h + (gq & 1), k_end - 1 - kt);
-#pragma unroll
-            for (int p = 0; p < HD / 32; ++p) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(K + key * HD) + 4 * p + cq);
-                kb[h][2 * p][0] = w.x; kb[h][2 * p][1] = w.y;
-                kb[h][2 * p + 1][0] = w.z; kb[h][2 * p + 1][1] = w.w;
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int key = min(4 * cq + r, k_end - 1 - kt);
-#pragma unroll
-            for (int p = 0; p < HD / 64; ++p) {
-                const uint4 w = __ldg(reinterpret_cast<const uint4*>(V + key * HD) + (HD / 64) * gq + p);
-                vb[r][4 * p] = w.x; vb[r][4 * p + 1] = w.y; vb[r][4 * p + 2] = w.z; vb[r][4 * p + 3] = w.w;
-            }
+    for (int r = 0; r < 4; ++r) {
+        const int key = min(4 * cq + r, last);
+        if (HD == 128) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(V + key * HD) + gq);
+            t.v[r][0] = w.x; t.v[r][1] = w.y; t.v[r][HD / 32 - 2] = w.z; t.v[r][HD / 32 - 1] = w.w;
+        } else {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(V + key * HD) + gq);
+            t.v[r][0] = w.x; t.v[r][1] = w.y;
         }
     }
-    // values of keys past the range: their probability is zero, and zero times what the slot holds must be zero
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-        if (kt + 4 * cq + r >= k_end)
-#pragma unroll
-            for (int i = 0; i < VD / 2; ++i) vb[r][i] = 0u;
+    // the pages hold a multiple of 16 slots: four exponents are one aligned word
+    t.ke = __ldg(reinterpret_cast<const uint32_t*>(cv.ke + row) + cq);
+    t.ve = __ldg(reinterpret_cast<const uint32_t*>(cv.ve + row) + cq);
 }
 
-// Query fragments of 16 vectors in lane order; dims as the K pieces of the cache's kind order them.
+// 16 query vectors: rows to shared memory in 32 bits, then fragments in lane order (dims as
+// the K pieces of the cache's kind order them).  sS: the factor of a row's raw scores.
 template <int HD, bool QF32>
-SPEC_DEV void load_queries(const AttendArgs& a, bool q8, int g, int G, int list_row0, int q0, int nq, uint4* sQ) {
-    constexpr int KS = HD / 16;
-    for (int i = threadIdx.x; i < KS * 32; i += kRowThreads) {
-        const int ks = i / 32, ln = i % 32, fg = ln >> 2, fc = ln & 3;
-        const int d0 = q8 ? 64 * (ks >> 2) + 16 * fc + 4 * (ks & 3) : 32 * (ks >> 1) + 8 * fc + 4 * (ks & 1);
-        float x[2][4];
+SPEC_DEV void load_queries(const AttendArgs& a, bool q8, int g, int G, int list_row0, int q0, int nq, uint4* sQ, float* sS,
+                           float* rows) {
+    constexpr int KS = HD / 16, LD = HD + 4;
+    const int t = threadIdx.x;
+    for (int i = t; i < 16 * (HD / 8); i += kRowThreads) {
+        const int r = i / (HD / 8), ch = i % (HD / 8), qg = q0 + r;
+        float x[8];
 #pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-            const int qi = fg + 8 * rr, qg = q0 + qi;
-            const long long off = (list_row0 + qg / G) * a.q_stride + (g * G + qg % G) * HD + d0;
+        for (int e = 0; e < 8; ++e) x[e] = 0.f;
+        if (r < nq) {
+            const long long off = (list_row0 + qg / G) * a.q_stride + (g * G + qg % G) * HD + ch * 8;
+            if (QF32) {
+                const float* p = static_cast<const float*>(a.q) + off;
+                const float4 u = *reinterpret_cast<const float4*>(p), w = *reinterpret_cast<const float4*>(p + 4);
+                x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w; x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
+            } else {
+                const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.q) + off;
+                if (a.q_vec) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(p);
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[rr][e] = 0.f;
-                if (qi < nq)
-                    x[rr][e] = QF32 ? static_cast<const float*>(a.q)[off + e]
-                                    : __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[off + e]);
+                    for (int e = 0; e < 4; ++e) {
+                        x[2 * e] = __uint_as_float(u[e] << 16);
+                        x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = __bfloat162float(p[e]);
+                }
             }
         }
-        sQ[i] = make_uint4(pack_bf16(x[0][0], x[0][1]), pack_bf16(x[1][0], x[1][1]), pack_bf16(x[0][2], x[0][3]),
-                           pack_bf16(x[1][2], x[1][3]));
-        if (QF32)
-            sQ[KS * 32 + i] = make_uint4(pack_bf16_lo(x[0][0], x[0][1]), pack_bf16_lo(x[1][0], x[1][1]),
-                                         pack_bf16_lo(x[0][2], x[0][3]), pack_bf16_lo(x[1][2], x[1][3]));
+        // the row's largest magnitude, over the HD / 8 lanes that hold it
+        float m = finite_amax(x);
+#pragma unroll
+        for (int o = HD / 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        // 2^13 .. 2^14 after scaling (the factor at most 2^100)
+        const int e = q8 ? min(127 + 13 - (int)(__float_as_uint(m) >> 23), 100) : 0;
+        const float f = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int k = 0; k < 8; k += 4)
+            *reinterpret_cast<float4*>(rows + r * LD + ch * 8 + k) = make_float4(x[k] * f, x[k + 1] * f, x[k + 2] * f, x[k + 3] * f);
+        if (ch == 0) sS[r] = a.c * __uint_as_float((uint32_t)(127 - e) << 23);
+    }
+    __syncthreads();
+    for (int i = t; i < KS * 32; i += kRowThreads) {
+        const int ks = i / 32, ln = i % 32, fg = ln >> 2, fc = ln & 3;
+        const int d0 = q8 ? 64 * (ks >> 2) + 16 * fc + 4 * (ks & 3) : 32 * (ks >> 1) + 8 * fc + 4 * (ks & 1);
+        const float4 u = *reinterpret_cast<const float4*>(rows + fg * LD + d0);
+        const float4 w = *reinterpret_cast<const float4*>(rows + (fg + 8) * LD + d0);
+        if (q8) {
+            sQ[i] = make_uint4(pack_f16(u.x, u.y), pack_f16(w.x, w.y), pack_f16(u.z, u.w), pack_f16(w.z, w.w));
+            if (QF32)
+                sQ[KS * 32 + i] = make_uint4(pack_f16(u.x - f16_round(u.x), u.y - f16_round(u.y)),
+                                             pack_f16(w.x - f16_round(w.x), w.y - f16_round(w.y)),
+                                             pack_f16(u.z - f16_round(u.z), u.w - f16_round(u.w)),
+                                             pack_f16(w.z - f16_round(w.z), w.w - f16_round(w.w)));
+        } else {
+            sQ[i] = make_uint4(pack_bf16(u.x, u.y), pack_bf16(w.x, w.y), pack_bf16(u.z, u.w), pack_bf16(w.z, w.w));
+            if (QF32)
+                sQ[KS * 32 + i] = make_uint4(pack_bf16_lo(u.x, u.y), pack_bf16_lo(w.x, w.y), pack_bf16_lo(u.z, u.w), pack_bf16_lo(w.z, w.w));
+        }
+    }
+}
+
+// running state of a lane's two rows: m and l of the sums of p (l over the lane's keys; joined
+// over the quad at the end), R the reference of O (8-bit caches; else R = m)
+template <int HD>
+struct RowState { float o[HD / 8][4], m[2], l[2], R[2]; };
+
+template <int HD>
+SPEC_DEV void scale_rows(RowState<HD>& s, float f0, float f1) {
+    // most tiles raise no maximum
+    if (__all_sync(0xffffffffu, f0 == 1.f && f1 == 1.f)) return;
+#pragma unroll
+    for (int nt = 0; nt < HD / 8; ++nt) {
+        s.o[nt][0] *= f0;
+        s.o[nt][1] *= f0;
+        s.o[nt][2] *= f1;
+        s.o[nt][3] *= f1;
+    }
+}
+
+// x: the tile's scores of this lane's two rows; y: what the exponents of P are (x, or x + e).
+// Leaves P in y and returns O's factors.
+template <bool Q8>
+SPEC_DEV void softmax_tile(float (&x)[2][4], float (&y)[2][4], float (&m)[2], float (&l)[2], float (&R)[2], float (&f)[2]) {
+#pragma unroll
+    for (int rr = 0; rr < 2; ++rr) {
+        float mt = fmaxf(fmaxf(x[rr][0], x[rr][1]), fmaxf(x[rr][2], x[rr][3]));
+        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
+        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
+        const float mn = fmaxf(m[rr], mt), mu = mn == -INFINITY ? 0.f : mn;   // nothing seen yet: p = 0
+        const float alpha = ex2(m[rr] - mu);
+        float ps = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[rr][e] = ex2(x[rr][e] - mu);
+            ps += x[rr][e];
+        }
+        l[rr] = l[rr] * alpha + ps;
+        m[rr] = mn;
+        if (Q8) {
+            float rt = fmaxf(fmaxf(y[rr][0], y[rr][1]), fmaxf(y[rr][2], y[rr][3]));
+            rt = fmaxf(rt, __shfl_xor_sync(0xffffffffu, rt, 1));
+            rt = fmaxf(rt, __shfl_xor_sync(0xffffffffu, rt, 2));
+            const float rn = fmaxf(R[rr], rt), ru = rn == -INFINITY ? 0.f : rn;
+            f[rr] = R[rr] == rn ? 1.f : ex2(R[rr] - ru);
+            R[rr] = rn;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[rr][e] = ex2(y[rr][e] - ru);
+        } else {
+            f[rr] = alpha;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[rr][e] = x[rr][e];
+        }
     }
 }
 
@@ -154,83 +235,142 @@ SPEC_DEV void load_queries(const AttendArgs& a, bool q8, int g, int G, int list_
 // Keys below n_ctx are seen by every row; key n_ctx + x by the rows whose mask has bit x.
 template <int HD, bool Q8, bool QF32>
 SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, int g, int k_begin, int k_end, int n_ctx,
-                           unsigned long long mk0, unsigned long long mk1, const uint4* sQ, float (&o)[HD / 8][4],
-                           float (&m_r)[2], float (&l_r)[2]) {
+                           unsigned long long mk0, unsigned long long mk1, const uint4* sQ, const float* sS,
+                           RowState<HD>& st) {
     constexpr int KS = HD / 16, VD = HD / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, cq = lane & 3;
-    for (int kt = k_begin + 16 * warp; kt < k_end; kt += 64) {
-        // tiles start at multiples of 16 and pages hold a multiple of 16 slots: no tile crosses a page
-        long long row = kv_row_in_layer(cv.pages, a.Hkv, seq, g, kt);
-        if (row < 0) { dev_error(a.err, SPEC_DEVERR_CAPACITY); row = 0; }
+    const float c0 = sS[gq], c1 = sS[gq + 8];
+    RawTile<HD> nx;
+    int kt = k_begin + 16 * warp;
+    if (Q8 && kt < k_end) load_raw<HD>(a, cv, seq, g, kt, k_end, gq, cq, nx);
+    for (; kt < k_end; kt += 64) {
         uint32_t kb[2][KS][2], vb[4][KS];
-        float ks[4], vs[4];
-        load_tile<HD, Q8>(cv, row, kt, k_end, gq, cq, kb, vb, ks, vs);
+        uint32_t ke = 0, ve = 0;
+        if (Q8) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int p = 0; p < HD / 64; ++p) {
+                    const uint32_t w[4] = {nx.k[h][p].x, nx.k[h][p].y, nx.k[h][p].z, nx.k[h][p].w};
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        kb[h][4 * p + s][0] = e4m3x2_f16(w[s]);
+                        kb[h][4 * p + s][1] = e4m3x2_f16(w[s] >> 16);
+                    }
+                }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int i = 0; i < HD / 32; ++i) {
+                    vb[r][2 * i] = e4m3x2_f16(nx.v[r][i]);
+                    vb[r][2 * i + 1] = e4m3x2_f16(nx.v[r][i] >> 16);
+                }
+            ke = nx.ke;
+            ve = nx.ve;
+            if (kt + 64 < k_end) load_raw<HD>(a, cv, seq, g, kt + 64, k_end, gq, cq, nx);
+        } else {
+            long long row = kv_row_in_layer(cv.pages, a.Hkv, seq, g, kt);
+            if (row < 0) { dev_error(a.err, SPEC_DEVERR_CAPACITY); row = 0; }
+            const __nv_bfloat16* K = static_cast<const __nv_bfloat16*>(cv.k) + row * HD;
+            const __nv_bfloat16* V = static_cast<const __nv_bfloat16*>(cv.v) + row * HD;
+            const int last = k_end - 1 - kt;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int key = min(4 * (gq >> 1) + 2 * h + (gq & 1), last);
+#pragma unroll
+                for (int p = 0; p < HD / 32; ++p) {
+                    const uint4 w = __ldg(reinterpret_cast<const uint4*>(K + key * HD) + 4 * p + cq);
+                    kb[h][2 * p][0] = w.x; kb[h][2 * p][1] = w.y;
+                    kb[h][2 * p + 1][0] = w.z; kb[h][2 * p + 1][1] = w.w;
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int key = min(4 * cq + r, last);
+#pragma unroll
+                for (int p = 0; p < HD / 64; ++p) {
+                    const uint4 w = __ldg(reinterpret_cast<const uint4*>(V + key * HD) + (HD / 64) * gq + p);
+                    vb[r][4 * p] = w.x; vb[r][4 * p + 1] = w.y; vb[r][4 * p + 2] = w.z; vb[r][4 * p + 3] = w.w;
+                }
+            }
+        }
+        if (kt + 16 > k_end) {
+            // values of keys past the range: their probability is zero, and zero times what the slot holds must be zero
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (kt + 4 * cq + r >= k_end)
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) vb[r][i] = 0u;
+        }
         float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const uint4 qh = sQ[s * 32 + lane];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) mma16816(sc[h], qh.x, qh.y, qh.z, qh.w, kb[h][s][0], kb[h][s][1]);
+            for (int h = 0; h < 2; ++h) {
+                if (Q8) mma16816_f16(sc[h], qh.x, qh.y, qh.z, qh.w, kb[h][s][0], kb[h][s][1]);
+                else mma16816(sc[h], qh.x, qh.y, qh.z, qh.w, kb[h][s][0], kb[h][s][1]);
+            }
             if (QF32) {
                 const uint4 ql = sQ[KS * 32 + s * 32 + lane];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) mma16816(sc[h], ql.x, ql.y, ql.z, ql.w, kb[h][s][0], kb[h][s][1]);
+                for (int h = 0; h < 2; ++h) {
+                    if (Q8) mma16816_f16(sc[h], ql.x, ql.y, ql.z, ql.w, kb[h][s][0], kb[h][s][1]);
+                    else mma16816(sc[h], ql.x, ql.y, ql.z, ql.w, kb[h][s][0], kb[h][s][1]);
+                }
             }
         }
         // lane: rows g (sc[h][0..1]) and g + 8 (sc[h][2..3]) at keys 4c + 2h + {0, 1}
+        float x[2][4], y[2][4], f[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int k = 0; k < 4; ++k) {
+            const float kf = Q8 ? kv8_scale((ke >> (8 * k)) & 0xFF) : 1.f;
+            x[0][k] = sc[k >> 1][k & 1] * (Q8 ? c0 * kf : c0);
+            x[1][k] = sc[k >> 1][2 + (k & 1)] * (Q8 ? c1 * kf : c1);
+        }
+        if (kt + 16 > min(n_ctx, k_end)) {                    // a tile that reaches new rows or the end
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int key = kt + 4 * cq + 2 * h + e;
+            for (int k = 0; k < 4; ++k) {
+                const int key = kt + 4 * cq + k;
                 const bool ctx = key < n_ctx, in = key < k_end;
-                const float f = Q8 ? a.c * ks[2 * h + e] : a.c;
-                sc[h][e] = in && (ctx || ((mk0 >> ((key - n_ctx) & 63)) & 1ull)) ? sc[h][e] * f : -INFINITY;
-                sc[h][2 + e] = in && (ctx || ((mk1 >> ((key - n_ctx) & 63)) & 1ull)) ? sc[h][2 + e] * f : -INFINITY;
-            }
-        float alpha[2];
-#pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-            float mt = fmaxf(fmaxf(sc[0][2 * rr], sc[0][2 * rr + 1]), fmaxf(sc[1][2 * rr], sc[1][2 * rr + 1]));
-            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 1));
-            mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, 2));
-            const float mn = fmaxf(m_r[rr], mt);
-            const float mu = mn == -INFINITY ? 0.f : mn;      // nothing seen yet: every exponent stays -inf, p = 0
-            alpha[rr] = ex2(m_r[rr] - mu);
-            float ps = 0.f;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    sc[h][2 * rr + e] = ex2(sc[h][2 * rr + e] - mu);
-                    ps += sc[h][2 * rr + e];
-                }
-            l_r[rr] = l_r[rr] * alpha[rr] + ps;               // this lane's keys; joined over the quad at the end
-            m_r[rr] = mn;
-            if (Q8) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) sc[h][2 * rr + e] *= vs[2 * h + e];
+                if (!(in && (ctx || ((mk0 >> ((key - n_ctx) & 63)) & 1ull)))) x[0][k] = -INFINITY;
+                if (!(in && (ctx || ((mk1 >> ((key - n_ctx) & 63)) & 1ull)))) x[1][k] = -INFINITY;
             }
         }
-        const uint32_t pa0 = pack_bf16(sc[0][0], sc[0][1]), pa1 = pack_bf16(sc[0][2], sc[0][3]);
-        const uint32_t pa2 = pack_bf16(sc[1][0], sc[1][1]), pa3 = pack_bf16(sc[1][2], sc[1][3]);
-        const uint32_t pl0 = pack_bf16_lo(sc[0][0], sc[0][1]), pl1 = pack_bf16_lo(sc[0][2], sc[0][3]);
-        const uint32_t pl2 = pack_bf16_lo(sc[1][0], sc[1][1]), pl3 = pack_bf16_lo(sc[1][2], sc[1][3]);
+        if (Q8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float e = (float)((int)((ve >> (8 * k)) & 0xFF) - 127);
+                y[0][k] = x[0][k] + e;
+                y[1][k] = x[1][k] + e;
+            }
+        }
+        softmax_tile<Q8>(x, y, st.m, st.l, st.R, f);
+        scale_rows<HD>(st, f[0], f[1]);
+        uint32_t pa[4], pl[4];
+        if (Q8) {
+            pa[0] = pack_f16(y[0][0], y[0][1]); pa[1] = pack_f16(y[1][0], y[1][1]);
+            pa[2] = pack_f16(y[0][2], y[0][3]); pa[3] = pack_f16(y[1][2], y[1][3]);
+        } else {
+            pa[0] = pack_bf16(y[0][0], y[0][1]); pa[1] = pack_bf16(y[1][0], y[1][1]);
+            pa[2] = pack_bf16(y[0][2], y[0][3]); pa[3] = pack_bf16(y[1][2], y[1][3]);
+            pl[0] = pack_bf16_lo(y[0][0], y[0][1]); pl[1] = pack_bf16_lo(y[1][0], y[1][1]);
+            pl[2] = pack_bf16_lo(y[0][2], y[0][3]); pl[3] = pack_bf16_lo(y[1][2], y[1][3]);
+        }
 #pragma unroll
         for (int nt = 0; nt < VD; ++nt) {
             const int i = nt >> 1;
             const uint32_t b0 = (nt & 1) ? pair_hi(vb[0][i], vb[1][i]) : pair_lo(vb[0][i], vb[1][i]);
             const uint32_t b1 = (nt & 1) ? pair_hi(vb[2][i], vb[3][i]) : pair_lo(vb[2][i], vb[3][i]);
-            o[nt][0] *= alpha[0];
-            o[nt][1] *= alpha[0];
-            o[nt][2] *= alpha[1];
-            o[nt][3] *= alpha[1];
-            mma16816(o[nt], pa0, pa1, pa2, pa3, b0, b1);
-            mma16816(o[nt], pl0, pl1, pl2, pl3, b0, b1);
+            if (Q8) {
+                mma16816_f16(st.o[nt], pa[0], pa[1], pa[2], pa[3], b0, b1);
+            } else {
+                mma16816(st.o[nt], pa[0], pa[1], pa[2], pa[3], b0, b1);
+                mma16816(st.o[nt], pl[0], pl[1], pl[2], pl[3], b0, b1);
+            }
         }
     }
+    if (!Q8) { st.R[0] = st.m[0]; st.R[1] = st.m[1]; }
 }
 
 SPEC_DEV unsigned long long row_mask(const AttendSpan& s, int b, int j) {
@@ -243,15 +383,17 @@ SPEC_DEV unsigned long long row_mask(const AttendSpan& s, int b, int j) {
 }
 
 template <int HD, bool QF32>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, HD == 128 ? 3 : 4)
 attend_rows_kernel(const __grid_constant__ AttendArgs a) {
     pdl_wait();
     pdl_trigger();
     constexpr int KS = HD / 16, VD = HD / 8;
+    constexpr int LS = HD + 4;                                              // a state row: O, m, l, R
     extern __shared__ float smf[];
     uint4* sQ = reinterpret_cast<uint4*>(smf);                              // [QF32 ? 2 : 1][KS][32]
-    float* sState = smf + (QF32 ? 2 : 1) * KS * 32 * 4;                     // [4 warps][16][HD + 2]
-    unsigned long long* sMask = reinterpret_cast<unsigned long long*>(sState + 4 * 16 * (HD + 2));   // [16]
+    float* sState = smf + (QF32 ? 2 : 1) * KS * 32 * 4;                     // [4 warps][16][LS]; the query rows before
+    float* sS = sState + 4 * 16 * LS;                                       // [16]
+    unsigned long long* sMask = reinterpret_cast<unsigned long long*>(sS + 16);   // [16]
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, gq = lane >> 2, cq = lane & 3;
     const int G = a.H / a.Hkv;
     // the prompt's blocks first (the longer ones), then the sequences' own
@@ -288,46 +430,66 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
     const int k_begin = min(n_keys, split * chunk), k_end = min(n_keys, k_begin + chunk);
     const CacheView& cv = is_pre ? a.pre : a.own;
     const int seq = is_pre ? a.pre_seq : b;
-    load_queries<HD, QF32>(a, cv.q8, g, G, list_row0, q0, nq, sQ);
+    const size_t TH = (size_t)a.span.T * a.H;
+    auto vec_of = [&](int r) { return range * TH + (size_t)(list_row0 + (q0 + r) / G) * a.H + g * G + (q0 + r) % G; };
+    if (k_begin >= k_end) {                                                 // nothing in this range
+        if (t < nq) *reinterpret_cast<float2*>(a.part_ml + 2 * vec_of(t)) = make_float2(-INFINITY, 0.f);
+        return;
+    }
+    load_queries<HD, QF32>(a, cv.q8, g, G, list_row0, q0, nq, sQ, sS, sState);
     if (t < 16) sMask[t] = !is_pre && t < nq ? row_mask(a.span, b, (q0 + t) / G) : 0ull;
     __syncthreads();
-    float o[VD][4], m_r[2] = {-INFINITY, -INFINITY}, l_r[2] = {0.f, 0.f};
+    RowState<HD> rs;
 #pragma unroll
-    for (int nt = 0; nt < VD; ++nt) o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
-    if (cv.q8) attend_range<HD, true, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, sMask[gq], sMask[gq + 8], sQ, o, m_r, l_r);
-    else attend_range<HD, false, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, sMask[gq], sMask[gq + 8], sQ, o, m_r, l_r);
+    for (int rr = 0; rr < 2; ++rr) { rs.m[rr] = rs.R[rr] = -INFINITY; rs.l[rr] = 0.f; }
+#pragma unroll
+    for (int nt = 0; nt < VD; ++nt) rs.o[nt][0] = rs.o[nt][1] = rs.o[nt][2] = rs.o[nt][3] = 0.f;
+    if (cv.q8) attend_range<HD, true, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, sMask[gq], sMask[gq + 8], sQ, sS, rs);
+    else attend_range<HD, false, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, sMask[gq], sMask[gq + 8], sQ, sS, rs);
     // warp states -> shared: rows g and g + 8, dims VD * 2c + nt and VD * (2c + 1) + nt
 #pragma unroll
     for (int rr = 0; rr < 2; ++rr) {
-        l_r[rr] += __shfl_xor_sync(0xffffffffu, l_r[rr], 1);
-        l_r[rr] += __shfl_xor_sync(0xffffffffu, l_r[rr], 2);
-        float* st = sState + ((size_t)warp * 16 + gq + 8 * rr) * (HD + 2);
-        if (cq == 0) { st[0] = m_r[rr]; st[1] = l_r[rr]; }
+        rs.l[rr] += __shfl_xor_sync(0xffffffffu, rs.l[rr], 1);
+        rs.l[rr] += __shfl_xor_sync(0xffffffffu, rs.l[rr], 2);
+        float* st = sState + ((size_t)warp * 16 + gq + 8 * rr) * LS;
+        if (cq == 0) { st[HD] = rs.m[rr]; st[HD + 1] = rs.l[rr]; st[HD + 2] = rs.R[rr]; }
 #pragma unroll
-        for (int nt = 0; nt < VD; ++nt) {
-            st[2 + VD * (2 * cq) + nt] = o[nt][2 * rr];
-            st[2 + VD * (2 * cq + 1) + nt] = o[nt][2 * rr + 1];
+        for (int nt = 0; nt < VD; nt += 4) {
+            *reinterpret_cast<float4*>(st + VD * (2 * cq) + nt) =
+                make_float4(rs.o[nt][2 * rr], rs.o[nt + 1][2 * rr], rs.o[nt + 2][2 * rr], rs.o[nt + 3][2 * rr]);
+            *reinterpret_cast<float4*>(st + VD * (2 * cq + 1) + nt) =
+                make_float4(rs.o[nt][2 * rr + 1], rs.o[nt + 1][2 * rr + 1], rs.o[nt + 2][2 * rr + 1], rs.o[nt + 3][2 * rr + 1]);
         }
     }
     __syncthreads();
-    const size_t TH = (size_t)a.span.T * a.H;
-    for (int i = t; i < nq * HD; i += kRowThreads) {
-        const int r = i / HD, d = i % HD, qg = q0 + r;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) M = fmaxf(M, sState[((size_t)w * 16 + r) * (HD + 2)]);
-        float L = 0.f, O = 0.f;
+    // the warps' states in warp order: sums relative to the largest m, O first to the largest R, then to m
+    for (int i = t; i < nq * (HD / 4); i += kRowThreads) {
+        const int r = i / (HD / 4), d = 4 * (i % (HD / 4));
+        float M = -INFINITY, RR = -INFINITY;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const float* st = sState + ((size_t)w * 16 + r) * (HD + 2);
-            if (st[0] == -INFINITY) continue;
-            const float wt = ex2(st[0] - M);
-            L += st[1] * wt;
-            O += st[2 + d] * wt;
+            const float* st = sState + ((size_t)w * 16 + r) * LS + HD;
+            M = fmaxf(M, st[0]);
+            RR = fmaxf(RR, st[2]);
         }
-        const size_t vec = range * TH + (size_t)(list_row0 + qg / G) * a.H + g * G + qg % G;
-        a.part_o[vec * HD + d] = O;
-        if (d == 0) { a.part_ml[2 * vec] = M; a.part_ml[2 * vec + 1] = L; }
+        float L = 0.f;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const float* st = sState + ((size_t)w * 16 + r) * LS;
+            if (st[HD] == -INFINITY && !(st[HD + 1] != 0.f)) continue;        // this warp saw nothing
+            L += st[HD + 1] * ex2(st[HD] - M);
+            const float wt = ex2(st[HD + 2] - RR);
+            const float4 o = *reinterpret_cast<const float4*>(st + d);
+            O.x = fmaf(o.x, wt, O.x);
+            O.y = fmaf(o.y, wt, O.y);
+            O.z = fmaf(o.z, wt, O.z);
+            O.w = fmaf(o.w, wt, O.w);
+        }
+        const float f = M == -INFINITY ? 1.f : ex2(RR - M);
+        const size_t vec = vec_of(r);
+        *reinterpret_cast<float4*>(a.part_o + vec * HD + d) = make_float4(O.x * f, O.y * f, O.z * f, O.w * f);
+        if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * vec) = make_float2(M, L);
     }
 }
 
@@ -469,7 +631,7 @@ int make_span(AttendSpan* s, int batch, const int* n_rows, int extra, const int*
 }
 
 static size_t rows_smem(int hd, bool qf32) {
-    return (qf32 ? 2 : 1) * (hd / 16) * 32 * 16 + 4 * 16 * (hd + 2) * sizeof(float) + 16 * 8;
+    return (qf32 ? 2 : 1) * (hd / 16) * 32 * 16 + 4 * 16 * (hd + 4) * sizeof(float) + 16 * sizeof(float) + 16 * 8;
 }
 
 // Query vectors whose partial states fit.  The row kernel's two parts keep to (ranges) x
