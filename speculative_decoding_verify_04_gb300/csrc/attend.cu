@@ -302,21 +302,28 @@ SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, in
 #pragma unroll
                     for (int i = 0; i < KS; ++i) vb[r][i] = 0u;
         }
-        float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        // two sums a key half: chains of KS / 2 products
+        float sc[2][4], sd[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[h][e] = sd[h][e] = 0.f;
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const uint4 qh = sQ[s * 32 + lane];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (Q8) mma16816_f16(sc[h], qh.x, qh.y, qh.z, qh.w, kb[h][s][0], kb[h][s][1]);
-                else mma16816(sc[h], qh.x, qh.y, qh.z, qh.w, kb[h][s][0], kb[h][s][1]);
+                float (&acc)[4] = s & 1 ? sd[h] : sc[h];
+                if (Q8) mma16816_f16(acc, qh.x, qh.y, qh.z, qh.w, kb[h][s][0], kb[h][s][1]);
+                else mma16816(acc, qh.x, qh.y, qh.z, qh.w, kb[h][s][0], kb[h][s][1]);
             }
             if (QF32) {
                 const uint4 ql = sQ[KS * 32 + s * 32 + lane];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (Q8) mma16816_f16(sc[h], ql.x, ql.y, ql.z, ql.w, kb[h][s][0], kb[h][s][1]);
-                    else mma16816(sc[h], ql.x, ql.y, ql.z, ql.w, kb[h][s][0], kb[h][s][1]);
+                    float (&acc)[4] = s & 1 ? sd[h] : sc[h];
+                    if (Q8) mma16816_f16(acc, ql.x, ql.y, ql.z, ql.w, kb[h][s][0], kb[h][s][1]);
+                    else mma16816(acc, ql.x, ql.y, ql.z, ql.w, kb[h][s][0], kb[h][s][1]);
                 }
             }
         }
@@ -325,8 +332,8 @@ SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, in
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const float kf = Q8 ? kv8_scale((ke >> (8 * k)) & 0xFF) : 1.f;
-            x[0][k] = sc[k >> 1][k & 1] * (Q8 ? c0 * kf : c0);
-            x[1][k] = sc[k >> 1][2 + (k & 1)] * (Q8 ? c1 * kf : c1);
+            x[0][k] = (sc[k >> 1][k & 1] + sd[k >> 1][k & 1]) * (Q8 ? c0 * kf : c0);
+            x[1][k] = (sc[k >> 1][2 + (k & 1)] + sd[k >> 1][2 + (k & 1)]) * (Q8 ? c1 * kf : c1);
         }
         if (kt + 16 > min(n_ctx, k_end)) {                    // a tile that reaches new rows or the end
 #pragma unroll
@@ -425,7 +432,7 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
     }
     const int q0 = qb * 16, nq = min(16, rows * G - q0);
     if (nq <= 0) return;
-    int chunk = (n_keys + n_splits - 1) / n_splits;
+    int chunk = max(kMinKeys, (n_keys + n_splits - 1) / n_splits);
     chunk = (chunk + 63) / 64 * 64;
     const int k_begin = min(n_keys, split * chunk), k_end = min(n_keys, k_begin + chunk);
     const CacheView& cv = is_pre ? a.pre : a.own;
@@ -664,13 +671,13 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     a.err = m->err;
     const int TH = span.T * H;
     const size_t fit = m->attend_part_floats / (hd + 2) / TH;      // ranges the workspace holds
-    // key ranges: as many as about three resident CTAs an SM take, by each part's share of the keys
+    // key ranges: about six CTAs an SM (three are resident) where the keys allow it, by each part's share of them
     a.own_qb = (span.max_rows * G + 15) / 16;
     const bool tile = pre && span.T * G > kRowVectors && attend_tile_ok(pre);
     a.pre_qb = pre && !tile ? (span.T * G + 15) / 16 : 0;
     const long long own_blocks = (long long)span.batch * Hkv * a.own_qb, pre_blocks = (long long)Hkv * a.pre_qb;
     const long long keys = own_blocks * kv->max_ctx + pre_blocks * (pre ? pre->max_ctx : 0);
-    const long long per = std::max<long long>(kMinKeys, keys / (3 * m->num_sms) + 1);
+    const long long per = std::max<long long>(kMinKeys, keys / (6 * m->num_sms) + 1);
     auto splits = [&](long long blocks, long long ctx) {
         if (blocks == 0) return 0;
         return (int)std::max<long long>(1, std::min<long long>({(ctx + per - 1) / per, 64, (16 * 512) / (16 * blocks) + 1}));

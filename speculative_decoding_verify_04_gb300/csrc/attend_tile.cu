@@ -20,6 +20,7 @@
 // boxes with the 128-byte swizzle), warp 9 the MMAs; 8-bit caches add four warps
 // (12-15) that turn raw e4m3 tiles into swizzled bf16 tiles (exact).
 #include <algorithm>
+#include <atomic>
 
 #include "attend.cuh"
 
@@ -625,8 +626,14 @@ int attend_tile_ranges(const spec_model* m, int ctas) { return ctas / m->cfg.n_k
 template <int HD, bool Q8>
 static int launch_tile(const spec_kv* pre, const AttendArgs& a, cudaStream_t st) {
     using S = TileShape<HD, Q8>;
-    cudaError_t e = cudaFuncSetAttribute(attend_tile_kernel<HD, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-    if (e != cudaSuccess) return check_cuda(e, "attention tile kernel attribute");
+    static std::atomic<unsigned long long> set{0};            // devices whose kernel has its shared memory
+    const unsigned long long bit = 1ull << (pre->m->device & 63);
+    cudaError_t e;
+    if (!(set.load() & bit)) {
+        e = cudaFuncSetAttribute(attend_tile_kernel<HD, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        if (e != cudaSuccess) return check_cuda(e, "attention tile kernel attribute");
+        set.fetch_or(bit);
+    }
     const int NQ = a.span.T * (a.H / a.Hkv);
     const dim3 grid((unsigned)((NQ + 2 * kBlkQ - 1) / (2 * kBlkQ) * a.tile_ctas));
     e = launch_k(pre->m->pdl, attend_tile_kernel<HD, Q8>, grid, dim3(S::kThreads), S::kSmem, st, a, pre->tm_k64, pre->tm_v64);

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from ctypes import POINTER, c_double, c_float, c_int32, c_void_p
 
 import torch
@@ -97,7 +98,7 @@ def load(path: str = LIB_PATH):
         "spec_test_stall_next_chain": ([P, I, ctypes.c_int64], I),
         "spec_kv_create_q8": ([P, I, I, I, I, POINTER(P)], I),
         "spec_kv_set_prefix": ([P, P, I], I),
-        "spec_attend": ([P, I, I, POINTER(I), P, L, P, L, P, L, POINTER(I), P, L, P], I),
+        "spec_attend": ([P, I, I, P, P, L, P, L, P, L, P, P, L, P], I),
         "spec_logprobs": ([P, I, L, I, I, c_float, P, P, P, I, P, P, P], I),
         "spec_accept_greedy": ([P, P, POINTER(I), I, I, I, P, P, P, P], I),
         "kv_commit": ([P, I, P, P, I, P], I),
@@ -125,9 +126,15 @@ def _ptr(t):
     return None if t is None else c_void_p(t.data_ptr())
 
 
+# the current stream's handle without a Stream object around it (3 us a call less)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     s = stream if stream is not None else torch.cuda.current_stream()
-    return c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _i32_array(vals):
@@ -144,9 +151,9 @@ def _need(t, dtype, name, numel=None):
         raise SpecError(f"{name}: needs at least {numel} elements, has {t.numel()}")
 
 
-def _here(t, name):
-    """The C calls take pointers of the current device only."""
-    if t is not None and t.device.index != torch.cuda.current_device():
+def _on(t, dev, name):
+    """The C calls take pointers of the current device, ``dev``, only."""
+    if t.get_device() != dev:
         raise SpecError(f"{name}: on {t.device}, not on the current device")
 
 
@@ -292,14 +299,15 @@ class KVCache:
         """k, v: CUDA tensors [n_layers][n_slots][Hkv][hd] in the model dtype."""
         _need(k, self.model.torch_dtype, "k")
         _need(v, self.model.torch_dtype, "v")
-        _check(load().spec_kv_import(self.handle, seq, layer0, k.shape[0], slot0, k.shape[1], _ptr(k), _ptr(v),
+        n_layers, n_slots = k.shape[:2]
+        _check(load().spec_kv_import(self.handle, seq, layer0, n_layers, slot0, n_slots, k.data_ptr(), v.data_ptr(),
                                      _stream(stream)))
 
     def export_rows(self, seq, layer0, n_layers, slot0, n_slots, stream=None):
         s = self.model.shape
         k = torch.empty((n_layers, n_slots, s.n_kv_heads, s.head_dim), dtype=self.model.torch_dtype, device="cuda")
         v = torch.empty_like(k)
-        _check(load().spec_kv_export(self.handle, seq, layer0, n_layers, slot0, n_slots, _ptr(k), _ptr(v),
+        _check(load().spec_kv_export(self.handle, seq, layer0, n_layers, slot0, n_slots, k.data_ptr(), v.data_ptr(),
                                      _stream(stream)))
         return k, v
 
@@ -471,14 +479,15 @@ def spec_accept(p, q, draft, u, acc_len, next_tok, stream=None):
                               _ptr(next_tok), _stream(stream)))
 
 
-def _rows3d(t, name, heads, dim, rows, dtype):
+def _rows3d(t, name, heads, dim, rows, dtype, dev):
     """[rows][heads][dim] rows with their heads in one piece: (pointer, row stride)."""
-    if (t is None or not t.is_cuda or t.dtype != dtype or t.dim() != 3 or t.shape[0] < rows
-            or tuple(t.shape[1:]) != (heads, dim)
-            or t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim)):
+    sh = t.shape if t is not None else ()
+    st = t.stride() if len(sh) == 3 else ()
+    if (len(sh) != 3 or t.dtype is not dtype or not t.is_cuda or sh[0] < rows or sh[1] != heads or sh[2] != dim
+            or st[2] != 1 or (heads > 1 and st[1] != dim)):
         raise SpecError(f"{name}: need a CUDA {dtype} tensor [{rows}, {heads}, {dim}] with contiguous rows")
-    _here(t, name)
-    return c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else heads * dim
+    _on(t, dev, name)
+    return t.data_ptr(), st[0] if sh[0] > 1 else heads * dim
 
 
 def spec_attend(kv, layer, n_rows, q, out, k=None, v=None, tree_parent=None, stream=None):
@@ -486,17 +495,26 @@ def spec_attend(kv, layer, n_rows, q, out, k=None, v=None, tree_parent=None, str
     and its prefix: ``out`` [T, H, hd] from ``q`` [T, H, hd] (bf16, back to back, not
     scaled).  ``k`` and ``v`` [T, Hkv, hd] are written to the rows' slots first."""
     s = kv.model.shape
-    T = sum(int(n) for n in n_rows)
-    bf = torch.bfloat16
-    qp, qs = _rows3d(q, "q", s.n_heads, s.head_dim, T, bf)
-    op, os_ = _rows3d(out, "out", s.n_heads, s.head_dim, T, bf)
-    kp, ks = _rows3d(k, "k", s.n_kv_heads, s.head_dim, T, bf) if k is not None else (None, 0)
-    vp, vs = _rows3d(v, "v", s.n_kv_heads, s.head_dim, T, bf) if v is not None else (None, 0)
-    if tree_parent is not None and len(tree_parent) < max(n_rows):
-        raise SpecError("tree_parent: shorter than the sequences' rows")
-    tp = _i32_array(tree_parent) if tree_parent is not None else None
-    _check(load().spec_attend(kv.handle, int(layer), len(n_rows), _i32_array(n_rows), qp, qs, kp, ks, vp, vs, tp, op,
-                              os_, _stream(stream)))
+    H, Hkv, hd, bf = s.n_heads, s.n_kv_heads, s.head_dim, torch.bfloat16
+    counts = array("i", n_rows)
+    T, dev = sum(counts), torch.cuda.current_device()
+    qp, qs = _rows3d(q, "q", H, hd, T, bf, dev)
+    op, os_ = _rows3d(out, "out", H, hd, T, bf, dev)
+    kp = vp = tp = None
+    ks = vs = 0
+    if k is not None:
+        kp, ks = _rows3d(k, "k", Hkv, hd, T, bf, dev)
+    if v is not None:
+        vp, vs = _rows3d(v, "v", Hkv, hd, T, bf, dev)
+    if tree_parent is not None:
+        tree = array("i", tree_parent)
+        if counts and len(tree) < max(counts):
+            raise SpecError("tree_parent: shorter than the sequences' rows")
+        tp = tree.buffer_info()[0]
+    rc = load().spec_attend(kv.handle, layer, len(counts), counts.buffer_info()[0], qp, qs, kp, ks, vp, vs, tp, op, os_,
+                            _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def spec_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logprobs=None, temperature=1.0,
@@ -504,28 +522,37 @@ def spec_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logpr
     """log p of ``tokens`` [rows] under softmax(logits / temperature) of ``logits``
     [rows, V] (f32 or bf16), with the rows' entropy and their ``top_ids`` /
     ``top_logprobs`` [rows, n] best tokens.  Every output may be None."""
-    if (logits is None or not logits.is_cuda or logits.dtype not in (torch.float32, torch.bfloat16)
-            or logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1)):
+    sh = logits.shape if logits is not None else ()
+    dt = logits.dtype if len(sh) == 2 else None
+    if dt not in (torch.float32, torch.bfloat16) or not logits.is_cuda or (sh[1] > 1 and logits.stride(1) != 1):
         raise SpecError("logits: need a 2-D CUDA float32 or bfloat16 tensor with contiguous rows")
-    rows, V = logits.shape
-    _here(logits, "logits")
+    rows, V = sh
+    dev = torch.cuda.current_device()
+    _on(logits, dev, "logits")
+    f32, i32 = torch.float32, torch.int32
     n = 0
     if top_ids is not None:
         if top_ids.dim() != 2 or top_ids.shape[0] < rows:
             raise SpecError(f"top_ids: need [{rows}, n]")
         n = top_ids.shape[1]
-    for t, dtype, name, numel in ((tokens, torch.int32, "tokens", rows), (logprob, torch.float32, "logprob", rows),
-                                  (entropy, torch.float32, "entropy", rows),
-                                  (top_ids, torch.int32, "top_ids", rows * n),
-                                  (top_logprobs, torch.float32, "top_logprobs", rows * n)):
+
+    def at(t, dtype, name, numel):
+        if t is None:
+            return None
         _need(t, dtype, name, numel)
-        _here(t, name)
+        _on(t, dev, name)
+        return t.data_ptr()
+
+    tok, lp = at(tokens, i32, "tokens", rows), at(logprob, f32, "logprob", rows)
+    ent = at(entropy, f32, "entropy", rows)
+    ids, tlp = at(top_ids, i32, "top_ids", rows * n), at(top_logprobs, f32, "top_logprobs", rows * n)
     if rows == 0:
         return
-    dt = SPEC_DTYPE_BF16 if logits.dtype == torch.bfloat16 else SPEC_DTYPE_F32
-    _check(load().spec_logprobs(_ptr(logits), dt, logits.stride(0) if rows > 1 else V, rows, V, float(temperature),
-                                _ptr(tokens), _ptr(logprob), _ptr(entropy), n, _ptr(top_ids), _ptr(top_logprobs),
-                                _stream(stream)))
+    rc = load().spec_logprobs(logits.data_ptr(), SPEC_DTYPE_BF16 if dt is torch.bfloat16 else SPEC_DTYPE_F32,
+                              logits.stride(0) if rows > 1 else V, rows, V, temperature, tok, lp, ent, n, ids, tlp,
+                              _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def spec_accept_greedy(logits, tokens, acc_len, next_tok, tree_parent=None, path=None, stream=None):

@@ -38,7 +38,7 @@ def test_logprobs_arguments(lib):
 
 
 def test_attend_and_caches_without_handles(lib):
-    n = (ctypes.c_int32 * 1)(1)
+    n = ctypes.cast((ctypes.c_int32 * 1)(1), P)
     out = P()
     p = P(4096)
     assert lib.spec_attend(None, 0, 1, n, p, 64, None, 0, None, 0, None, p, 64, None) == -1 and "null" in _err(lib)
@@ -51,8 +51,7 @@ def test_binding_refuses_host_tensors(lib):
     from speculative_decoding_verify_04_gb300 import spec
     with pytest.raises(spec.SpecError, match="logits"):
         spec.spec_logprobs(torch.zeros(2, 10), None, torch.zeros(2))
-    from types import SimpleNamespace
-    kv = SimpleNamespace(model=SimpleNamespace(shape=SimpleNamespace(n_heads=2, n_kv_heads=1, head_dim=64)), handle=None)
     q = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
-    with pytest.raises(spec.SpecError, match="q: need a CUDA"):
-        spec.spec_attend(kv, 0, [1], q, q)
+    for bad in (q, q.float(), q[0], None):
+        with pytest.raises(spec.SpecError, match="q: need a CUDA"):
+            spec._rows3d(bad, "q", 2, 64, 1, torch.bfloat16, 0)
