@@ -70,6 +70,29 @@ SPEC_DEV float ex2(float x) {
     return r;
 }
 
+// two f32 lanes in one instruction
+SPEC_DEV float2 fma2(float2 x, float2 y, float2 z) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 r, a, b, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+    return d;
+}
+SPEC_DEV float2 mul2(float2 x, float2 y) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return d;
+}
+SPEC_DEV float2 add2(float2 x, float2 y) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return d;
+}
+
 // attend_tile.cu: the prompt's part for lists of many query vectors
 bool attend_tile_ok(const spec_kv* pre);
 int attend_tile_ctas(const spec_model* m, const AttendSpan& span, int prompt_cap);

@@ -5,7 +5,9 @@
 //     H        = ln 2 (log2 S - U / S)
 // in one pass over the row: a thread keeps a running maximum and the two sums
 // relative to it, rescaled when the maximum grows, and the threads' states join
-// by the same rule.  Bound by reading the logits once.
+// by the same rule.  The difference is taken before the product, so rows masked by
+// the type's lowest value do not overflow.  Bound by reading the logits once;
+// half-precision rows by the instructions too (about six a logit).
 //
 // The n best tokens come from the same pass: every 256 consecutive logits (one
 // step of a warp) leave their maximum in shared memory.  The n best by (value
@@ -15,9 +17,9 @@
 // their logits not below the least of the n maxima are listed, and a listed
 // token's place is the number of listed tokens that rank before it.
 //
-// A row is taken by a cluster of 1 to 8 CTAs, each on a contiguous run of
-// segments; the first CTA gathers the others' states and maxima from their
-// shared memory.
+// A row is taken by a cluster of 1 to 4 CTAs, each on a contiguous run of
+// segments; the others leave their states and maxima in the first one's shared
+// memory and end.
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -29,11 +31,12 @@ namespace cg = cooperative_groups;
 
 namespace spec {
 
-constexpr int kLpThreads = 512;
+constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr int kLpSeg = 256;
 constexpr int kLpMaxTop = 32;
 constexpr int kLpMaxVocab = 1 << 20;
+constexpr int kLpMaxCtas = 4;
 
 struct LogprobArgs {
     const void* x;
@@ -47,16 +50,11 @@ struct LogprobArgs {
 // running state of a set of logits: m = max x, s = sum 2^d, u = sum 2^d d with d = c (x - m)
 struct LpState { float m, s, u; };
 
-SPEC_DEV float lp_ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 // the state relative to a larger (or equal) maximum
 SPEC_DEV void lp_raise(LpState& a, float m, float c) {
     if (a.m == m) return;
-    const float d = (a.m - m) * c, f = lp_ex2(d);
-    // nothing seen yet (m = -inf): the sums are zero
+    const float d = (a.m - m) * c, f = ex2(d);
+    // nothing seen yet (m = -inf): the sums are zero (or NaN)
     a.u = a.m == -INFINITY ? a.u : (f > 0.f ? (a.u + a.s * d) * f : 0.f);
     a.s = a.m == -INFINITY ? a.s : a.s * f;
     a.m = m;
@@ -75,6 +73,21 @@ SPEC_DEV float warp_redux_max(float v) {
     return r;
 }
 
+// a 16-byte piece as floats
+template <typename T>
+SPEC_DEV void lp_unpack(const uint4& w, float* x) {
+    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (sizeof(T) == 4) {
+            x[i] = __uint_as_float(a[i]);
+        } else {
+            x[2 * i] = __uint_as_float(a[i] << 16);
+            x[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
+        }
+    }
+}
+
 // One segment of a row: 8 logits a lane.  Element i of the row sits at position
 // i + mis, mis the elements between a 16-byte boundary and the row's start, so
 // whole pieces are aligned; pieces that the row does not fill are read one by one.
@@ -86,17 +99,7 @@ SPEC_DEV void lp_load(const T* row, int V, int mis, int seg, float (&x)[8]) {
     for (int p = 0; p < NP; ++p) {
         const int i0 = seg * kLpSeg + (p * 32 + lane) * VE - mis;
         if (i0 >= 0 && i0 + VE <= V) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(row + i0));
-            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (sizeof(T) == 4) {
-                    x[p * VE + i] = __uint_as_float(a[i]);
-                } else {
-                    x[p * VE + (2 * i) % VE] = __uint_as_float(a[i] << 16);
-                    x[p * VE + (2 * i + 1) % VE] = __uint_as_float(a[i] & 0xFFFF0000u);
-                }
-            }
+            lp_unpack<T>(__ldg(reinterpret_cast<const uint4*>(row + i0)), &x[p * VE]);
         } else {
 #pragma unroll
             for (int i = 0; i < VE; ++i)
@@ -120,24 +123,35 @@ SPEC_DEV void lp_add(LpState& a, const float (&x)[8], float c, float xm) {
         return;
     }
     lp_raise(a, m, c);
+    const float2 cc = make_float2(c, c), nn = make_float2(-m, -m);
+    float2 s = make_float2(0.f, 0.f), u = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float d = (x[i] - m) * c, e = lp_ex2(d);
-        a.s += e;
-        a.u = fmaf(e, fmaxf(d, -FLT_MAX), a.u);       // a masked logit: 0 * -max, not 0 * -inf
+    for (int i = 0; i < 4; ++i) {
+        float2 d = mul2(add2(make_float2(x[2 * i], x[2 * i + 1]), nn), cc);
+        const float2 e = make_float2(ex2(d.x), ex2(d.y));
+        d.x = fmaxf(d.x, -FLT_MAX);                   // a masked logit: 0 * -max, not 0 * -inf
+        d.y = fmaxf(d.y, -FLT_MAX);
+        s = add2(s, e);
+        u = fma2(e, d, u);
     }
+    a.s += s.x + s.y;
+    a.u += u.x + u.y;
 }
 
 struct LpSmem {
     LpState w[kLpWarps];
-    LpState cta;
+    LpState cta[kLpMaxCtas];          // the first CTA's: every CTA's state
     int sel[kLpMaxTop];
-    float least;
-    int n_cand;
+    float low, least;
+    int n_near, n_cand;
 };
 
+// a cluster barrier in two halves
+SPEC_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+SPEC_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 template <typename T, int TOP>
-__global__ void __launch_bounds__(kLpThreads)
+__global__ void __launch_bounds__(kLpThreads, sizeof(T) == 4 ? 4 : 5)
 logprobs_kernel(const __grid_constant__ LogprobArgs a) {
     pdl_wait();
     pdl_trigger();
@@ -145,29 +159,50 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a) {
     extern __shared__ float dyn[];
     cg::cluster_group cl = cg::this_cluster();
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+    if (C > 1) cluster_arrive();                            // started: its shared memory may be written
     const long long r = blockIdx.x / C;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const T* row = static_cast<const T*>(a.x) + r * a.stride;
     const int mis = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
     const int n_seg = (a.V + mis + kLpSeg - 1) / kLpSeg, per = (n_seg + C - 1) / C;
     const int g0 = min(n_seg, rank * per), g1 = min(n_seg, g0 + per);
-    float* seg_max = dyn;                                   // [per] this CTA's; the first CTA: [n_seg] in the end
+    float* seg_max = dyn;                                   // [n_seg]; each CTA's own part, the first one's all of it
     LpState st{-INFINITY, 0.f, 0.f};
-    for (int g = g0 + w; g < g1; g += 2 * kLpWarps) {
-        float x[2][8];
-        const bool two = g + kLpWarps < g1;
-        lp_load(row, a.V, mis, g, x[0]);
-        if (two) lp_load(row, a.V, mis, g + kLpWarps, x[1]);
+    constexpr int U = 4;                                    // segments in flight a warp
+    constexpr int VE = 16 / sizeof(T), NP = 8 / VE;
+    auto take = [&](const float (&x)[8], int g) {
+        float xm = x[0];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (k == 1 && !two) break;
-            float xm = x[k][0];
+        for (int i = 1; i < 8; ++i) xm = fmaxf(xm, x[i]);
+        lp_add(st, x, a.c, xm);
+        if (TOP) {
+            const float top = warp_redux_max(xm);
+            if (lane == 0) seg_max[g] = top;
+        }
+    };
+    for (int g = g0 + w; g < g1; g += U * kLpWarps) {
+        const int last = g + (U - 1) * kLpWarps;
+        if (last < g1 && g * kLpSeg >= mis && (last + 1) * kLpSeg - mis <= a.V) {
+            // every piece whole: all loads before the first value is looked at
+            uint4 p[U][NP];
+            const T* at = row + (g * kLpSeg - mis + lane * VE);
 #pragma unroll
-            for (int i = 1; i < 8; ++i) xm = fmaxf(xm, x[k][i]);
-            lp_add(st, x[k], a.c, xm);
-            if (TOP) {
-                const float sm_ = warp_redux_max(xm);
-                if (lane == 0) seg_max[g + k * kLpWarps - g0] = sm_;
+            for (int k = 0; k < U; ++k)
+#pragma unroll
+                for (int q = 0; q < NP; ++q)
+                    p[k][q] = __ldg(reinterpret_cast<const uint4*>(at + k * kLpWarps * kLpSeg + q * 32 * VE));
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                float x[8];
+#pragma unroll
+                for (int q = 0; q < NP; ++q) lp_unpack<T>(p[k][q], &x[q * VE]);
+                take(x, g + k * kLpWarps);
+            }
+        } else {
+            for (int k = 0; k < U && g + k * kLpWarps < g1; ++k) {
+                float x[8];
+                lp_load(row, a.V, mis, g + k * kLpWarps, x);
+                take(x, g + k * kLpWarps);
             }
         }
     }
@@ -180,7 +215,7 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a) {
         lp_merge(st, t, a.c);
     }
     if (lane == 0) sm.w[w] = st;
-    if (threadIdx.x == 0) sm.n_cand = 0;
+    if (threadIdx.x == 0) sm.n_near = sm.n_cand = 0;
     __syncthreads();
     if (w == 0) {
         st = lane < kLpWarps ? sm.w[lane] : LpState{-INFINITY, 0.f, 0.f};
@@ -192,21 +227,25 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a) {
             t.u = __shfl_xor_sync(0xffffffffu, st.u, o);
             lp_merge(st, t, a.c);
         }
-        if (lane == 0) sm.cta = st;
+        if (lane == 0 && rank == 0) sm.cta[0] = st;
     }
-    cl.sync();
-    if (rank == 0) {
-        st = sm.cta;
-        for (int k = 1; k < C; ++k) lp_merge(st, *cl.map_shared_rank(&sm.cta, k), a.c);
-        if (TOP)
-            for (int k = 1; k < C; ++k) {
-                const float* far = cl.map_shared_rank(seg_max, k);
-                const int n = min(n_seg, (k + 1) * per) - min(n_seg, k * per);
-                for (int i = threadIdx.x; i < n; i += kLpThreads) seg_max[k * per + i] = far[i];
+    if (C > 1) {
+        cluster_wait();
+        if (rank > 0) {
+            if (threadIdx.x == 0) *cl.map_shared_rank(&sm.cta[rank], 0) = st;
+            if (TOP) {
+                float* first = cl.map_shared_rank(seg_max, 0);
+                for (int i = g0 + threadIdx.x; i < g1; i += kLpThreads) first[i] = seg_max[i];
             }
+        }
+        cluster_arrive();
+        if (rank > 0) return;                                // (a barrier waits for threads that have not ended)
+        cluster_wait();
+    } else {
+        __syncthreads();
     }
-    cl.sync();                                              // the others' shared memory has been read
-    if (rank != 0) return;
+    st = sm.cta[0];
+    for (int k = 1; k < C; ++k) lp_merge(st, sm.cta[k], a.c);
     // a row with NaN, +inf or nothing but -inf has no distribution
     const bool good = st.m > -INFINITY && st.m < INFINITY && st.s < INFINITY;
     const float l2 = log2f(st.s), lse = l2 * 0.6931471805599453f, nan = __int_as_float(0x7fc00000);
@@ -226,51 +265,66 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a) {
         if (threadIdx.x < n) { out_id[threadIdx.x] = -1; out_lp[threadIdx.x] = nan; }
         return;
     }
-    // the n best segments, by one warp: each lane keeps the best of its own (every 32nd)
+    // The n best segments.  Of the best segments of 32 interleaved parts the n-th is a lower bound
+    // of the n-th best of all; the segments not below it are listed (few more than n), and a listed
+    // one's place is the number of listed ones before it.
     const int n_sel = min(n, n_seg);
+    float* nv = dyn + n_seg;                                // [n_seg] listed maxima
+    int* ni = reinterpret_cast<int*>(nv + n_seg);           // [n_seg] and their segments
     if (w == 0) {
         float bv = -INFINITY;
-        int bi = INT_MAX;
-        auto best = [&]() {
-            bv = -INFINITY;
-            bi = INT_MAX;
-            for (int i = lane; i < n_seg; i += 32) {
-                const float v = seg_max[i];
-                // taken segments are marked by NaN
-                if (v > bv || (v == bv && bi == INT_MAX)) { bv = v; bi = i; }
-            }
-        };
-        best();
-        float last = 0.f;
-        for (int k = 0; k < n_sel; ++k) {
-            // -inf segments count too (a mask may leave fewer tokens than n): a lane without any has bi = INT_MAX
-            const float v = warp_redux_max(bv);
-            const unsigned win = __reduce_min_sync(0xffffffffu, (unsigned)(bv == v ? bi : INT_MAX));
-            if (lane == 0) sm.sel[k] = (int)win;
-            last = v;
-            if (bi == (int)win) {
-                seg_max[win] = nan;
-                best();
-            }
+#pragma unroll 4
+        for (int i = lane; i < n_seg; i += 32) bv = fmaxf(bv, seg_max[i]);
+        int before = 0;
+        for (int k = 0; k < 32; ++k) {
+            const float v = __shfl_sync(0xffffffffu, bv, k);
+            before += v > bv || (v == bv && k < lane);
         }
+        // (a part without segments counts as -inf)
+        if (before == n_sel - 1) sm.low = bv;
+    }
+    __syncthreads();
+    const float low = sm.low;
+    for (int i = threadIdx.x; i < n_seg; i += kLpThreads) {
+        const float v = seg_max[i];
+        if (v >= low) {
+            const int at = atomicAdd(&sm.n_near, 1);
+            nv[at] = v;
+            ni[at] = i;
+        }
+    }
+    __syncthreads();
+    const int n_near = sm.n_near;
+    for (int i = threadIdx.x; i < n_near; i += kLpThreads) {
+        const float v = nv[i];
+        const int id = ni[i];
+        int before = 0;
+        for (int k = 0; k < n_near; ++k) before += nv[k] > v || (nv[k] == v && ni[k] < id);
+        if (before < n_sel) sm.sel[before] = id;
         // rows of fewer segments than n: every token is listed
-        if (lane == 0) sm.least = n_sel < n ? -INFINITY : last;
+        if (before == n_sel - 1) sm.least = n_sel < n ? -INFINITY : v;
     }
     __syncthreads();
     const float least = sm.least;
-    float* cv = dyn + n_seg;                                // [n_sel * 256] values
+    float* cv = nv + 2 * n_seg;                             // [n_sel * 256] values
     int* ci = reinterpret_cast<int*>(cv + n_sel * kLpSeg);  // and ids of the listed tokens
-    for (int k = w; k < n_sel; k += kLpWarps) {
-        const int g = sm.sel[k];
-        float x[8];
-        lp_load(row, a.V, mis, g, x);
+    for (int k0 = w; k0 < n_sel; k0 += 4 * kLpWarps) {
+        float x[4][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int id = lp_index<T>(mis, g, e);
-            if (id >= 0 && id < a.V && x[e] >= least) {
-                const int at = atomicAdd(&sm.n_cand, 1);
-                cv[at] = x[e];
-                ci[at] = id;
+        for (int q = 0; q < 4; ++q)
+            if (k0 + q * kLpWarps < n_sel) lp_load(row, a.V, mis, sm.sel[k0 + q * kLpWarps], x[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (k0 + q * kLpWarps >= n_sel) break;
+            const int g = sm.sel[k0 + q * kLpWarps];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int id = lp_index<T>(mis, g, e);
+                if (id >= 0 && id < a.V && x[q][e] >= least) {
+                    const int at = atomicAdd(&sm.n_cand, 1);
+                    cv[at] = x[q][e];
+                    ci[at] = id;
+                }
             }
         }
     }
@@ -313,13 +367,15 @@ extern "C" int spec_logprobs(const void* logits, int32_t dtype, int64_t lg_strid
     SPEC_TRY(check_cuda(cudaGetDevice(&dev), "cudaGetDevice"));
     SPEC_TRY(check_cuda(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev), "attr"));
     LogprobArgs a{logits, lg_stride, vocab, temperature, 1.4426950408889634f / temperature, tokens, logprob, entropy, n_top, top_ids, top_logprobs};
-    // CTAs a row: as many as keep every SM busy, each with 16 segments (one a warp) or more
+    // CTAs a row: until there are three an SM (four or five are resident), 16 segments a CTA or more
+    // (512 rows of 131072: 42 us by one CTA a row, 57 by two; 333 rows of 100003, half
+    // precision: 39 us by one, 26 by two, 29 by four)
     const int n_seg = (vocab + 7 + kLpSeg - 1) / kLpSeg;
     int C = 1;
-    while (C < 8 && (long long)rows * C * 2 <= 2 * sms && n_seg / (2 * C) >= kLpWarps / 2) C *= 2;
+    while (C < kLpMaxCtas && (long long)rows * C < 3 * sms && n_seg / (2 * C) >= 16) C *= 2;
     void (*f)(LogprobArgs) = dtype == SPEC_DTYPE_BF16 ? (n_top ? logprobs_kernel<__nv_bfloat16, 1> : logprobs_kernel<__nv_bfloat16, 0>)
                                                       : (n_top ? logprobs_kernel<float, 1> : logprobs_kernel<float, 0>);
-    const size_t smem = n_top ? (size_t)(n_seg + C + (size_t)std::min(n_top, n_seg) * kLpSeg * 2) * 4 : 0;
+    const size_t smem = n_top ? ((size_t)3 * n_seg + (size_t)std::min(n_top, n_seg) * kLpSeg * 2) * 4 : 0;
     if (smem > 48 * 1024)
         SPEC_TRY(check_cuda(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem), "spec_logprobs attribute"));
     cudaLaunchConfig_t cfg = {};
