@@ -21,17 +21,6 @@ constexpr int kRowThreads = 128;
 constexpr int kRowVectors = 16;       // query vectors a KV head up to which the row kernel takes the prompt
 constexpr int kMinKeys = 256;         // least keys of a range: below it the join costs more than the ranges give
 
-// two e4m3 values as f16 (exact)
-SPEC_DEV uint32_t e4m3x2_f16(uint32_t two) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
-    return h;
-}
-SPEC_DEV uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 SPEC_DEV float f16_round(float x) {
     float r;
     asm("{\n\t.reg .b16 h;\n\tcvt.rn.f16.f32 h, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(r) : "f"(x));

@@ -162,6 +162,22 @@ SPEC_DEV float2 e4m3x2_f32(uint32_t two) {
         : "=f"(f.x), "=f"(f.y) : "r"(h));
     return f;
 }
+// two e4m3 values as f16 (exact)
+SPEC_DEV uint32_t e4m3x2_f16(uint32_t two) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+    return h;
+}
+SPEC_DEV uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+SPEC_DEV uint32_t f16x2_mul(uint32_t x, uint32_t y) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(y));
+    return r;
+}
 // two floats to bf16x2, `lo` in the low half
 SPEC_DEV uint32_t bf16x2(float lo, float hi) {
     uint32_t r;

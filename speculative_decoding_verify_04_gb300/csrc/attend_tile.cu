@@ -18,9 +18,12 @@
 //
 // Roles: warps 0-3 and 4-7 the streams' softmax, warp 8 the copies (TMA tensor
 // boxes with the 128-byte swizzle), warp 9 the MMAs; 8-bit caches add four warps
-// (12-15) that turn raw e4m3 tiles into swizzled bf16 tiles (exact).
+// (12-15) that turn raw e4m3 tiles into swizzled f16 tiles, y 2^e, where every
+// exponent of the turn's keys lies in [-15, 7] (two instructions for two values), else
+// into bf16 tiles (six); both are exact.  f16 queries are scaled by a power of two a row.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "attend.cuh"
 
@@ -42,15 +45,18 @@ struct TileShape {
     static constexpr int kExpBytes = kRaw * kBlkK;
     // partial states leave through the ring (and the raw tiles behind it): 256 padded rows, or 128 behind the exchange
     static_assert(kStages * kTileBytes + kRaw * kRawBytes >= 256 * (HD * 4 + 16), "states");
-    static constexpr int kSmem = kTiles + kExpBytes + 512 + 1024;   // barriers; the tiles start on 1024 bytes
+    static constexpr int kSmem = kTiles + kExpBytes + 512 + (Q8 ? 1024 : 0) + 1024;   // barriers, row factors; the tiles start on 1024 bytes
 };
 
 struct TileBars {                        // full .. done: every barrier, in one run
     uint64_t full[8], empty[8];          // K/V ring
     uint64_t raw_full[4], raw_empty[4];  // raw e4m3 ring
+    uint64_t mode;                       // 8-bit caches: the operands' type is known
     uint64_t q_full, s_full[2], p_full[2], done;
     uint32_t tmem;
     int abort;
+    int half;                            // 8-bit caches: 3 where this turn's products are in f16 (bit 0: no exponent
+                                         // speaks against it, bit 1: not all rows are zeros)
 };
 static_assert(sizeof(TileBars) <= 512, "barriers");
 
@@ -135,6 +141,7 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
     char* raw = ring + NST * S::kTileBytes;
     uint8_t* rexp = reinterpret_cast<uint8_t*>(raw + S::kRaw * S::kRawBytes);
     TileBars& B = *reinterpret_cast<TileBars*>(tiles + S::kTiles + S::kExpBytes);
+    float* row_factor = reinterpret_cast<float*>(tiles + S::kTiles + S::kExpBytes + 512);   // [256], 8-bit caches
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
 
     const int G = a.H / a.Hkv, NQ = a.span.T * G;
@@ -143,7 +150,9 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
     auto init_bars = [&]() {
         for (int i = 0; i < NST; ++i) { mbar_init(&B.full[i], Q8 ? 4 : 1); mbar_init(&B.empty[i], two ? 2 : 1); }
         for (int i = 0; i < NRAW; ++i) { mbar_init(&B.raw_full[i], 1); mbar_init(&B.raw_empty[i], 4); }
+        mbar_init(&B.mode, 4);
         mbar_init(&B.q_full, 8);
+        B.half = 1;
         for (int i = 0; i < 2; ++i) { mbar_init(&B.s_full[i], 1); mbar_init(&B.p_full[i], 5); }
         mbar_init(&B.done, 1);
         fence_mbar_init();
@@ -204,6 +213,7 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
         // a thread takes one 16-byte piece of every RPP-th row; eight loads go out before the first store
         constexpr int CPR = HD / 8, RPP = 256 / CPR, NB = HD == 128 ? 8 : 4;
         const int ch = t % CPR;
+        bool ok = true, half = false;
         for (int r0 = t / CPR; r0 < (J.two ? 2 * kBlkQ : kBlkQ); r0 += NB * RPP) {
             uint4 w[NB];
 #pragma unroll
@@ -224,6 +234,31 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                                       p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
                 }
             }
+            if (Q8 && r0 == t / CPR) {                        // (the first loads are on their way)
+                ok = warp_wait(&B.mode, 0, ab, a.err);
+                half = B.half == 3;
+            }
+            if (half) {
+                // f16: the row's largest magnitude to 2^13 .. 2^14 (CPR lanes hold a row)
+#pragma unroll
+                for (int k = 0; k < NB; ++k) {
+                    const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[2 * i] = __uint_as_float(u[i] << 16);
+                        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+                    }
+                    float m = finite_amax(x);
+#pragma unroll
+                    for (int o = CPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    const int e = min(127 + 13 - (int)(__float_as_uint(m) >> 23), 100);
+                    const float f = __uint_as_float((uint32_t)(127 + e) << 23);
+                    w[k] = make_uint4(pack_f16(x[0] * f, x[1] * f), pack_f16(x[2] * f, x[3] * f), pack_f16(x[4] * f, x[5] * f),
+                                      pack_f16(x[6] * f, x[7] * f));
+                    if (ch == 0) row_factor[r0 + k * RPP] = __uint_as_float((uint32_t)(127 - e) << 23);
+                }
+            }
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
                 const int r = r0 + k * RPP, rr = r & (kBlkQ - 1);
@@ -241,8 +276,8 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
         int q = 0;                                                           // job of this stream
         int kslot = J.two ? 0 : 2 * st, vslot = 0;                           // ring slots of its next K and last V tile
         while (kslot >= NST) kslot -= NST;
-        bool ok = true;
-        for (int n = st; n < J.n_jobs; n += 2, ++q) {
+        float c = a.c;
+        for (int n = st; n < J.n_jobs && ok; n += 2, ++q) {
             const int kb = job_kb(J, n), valid = min(kBlkK, J.n_keys - kb * kBlkK);
             ok = warp_wait(&B.s_full[st], q & 1, ab, a.err);
             if (!ok) break;
@@ -256,6 +291,7 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
             vslot = kslot + 1 == NST ? 0 : kslot + 1;
             kslot += J.two ? 2 : 4;
             while (kslot >= NST) kslot -= NST;
+            if (half && q == 0) c *= row_factor[(J.two ? st * kBlkQ : 0) + row];
             // the whole row at once: 128 scores in registers
             uint32_t r[4][32];
 #pragma unroll
@@ -277,7 +313,7 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                 for (int c = 0; c < 4; ++c) mx4[c] = fmaxf(mx4[c], __uint_as_float(r[c][i]));
 
             float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-            mx *= a.c;
+            mx *= c;
             if (__any_sync(0xffffffffu, mx > m + kLazy || m == -INFINITY)) {
                 const float mn = fmaxf(m, mx);
                 const float f = ex2(m - (mn == -INFINITY ? 0.f : mn));
@@ -296,21 +332,25 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                 }
             }
             const float mu = m == -INFINITY ? 0.f : m;
-            const float2 cc = make_float2(a.c, a.c), mm = make_float2(-mu, -mu);
+            const float2 cc = make_float2(c, c), mm = make_float2(-mu, -mu);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            auto exponentials = [&](auto f16) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t p[16];
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t p[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float2 x = fma2(make_float2(__uint_as_float(r[c][2 * i]), __uint_as_float(r[c][2 * i + 1])), cc, mm);
-                    x.x = ex2(x.x);
-                    x.y = ex2(x.y);
-                    sum[i & 1] = add2(sum[i & 1], x);
-                    p[i] = bf16x2(x.x, x.y);
+                    for (int i = 0; i < 16; ++i) {
+                        float2 x = fma2(make_float2(__uint_as_float(r[c][2 * i]), __uint_as_float(r[c][2 * i + 1])), cc, mm);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        sum[i & 1] = add2(sum[i & 1], x);
+                        p[i] = f16.value ? pack_f16(x.x, x.y) : bf16x2(x.x, x.y);
+                    }
+                    tmem_st16(tS + 16 * c, p);                // P's columns lie over S columns
                 }
-                tmem_st16(tS + 16 * c, p);                    // P's columns lie over S columns
-            }
+            };
+            if (half) exponentials(std::true_type{});
+            else exponentials(std::false_type{});
             sum[0] = add2(sum[0], sum[1]);
             l += sum[0].x + sum[0].y;
             tmem_wait_st();
@@ -452,12 +492,14 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
         // covers every MMA before it, and the softmax threads that see S complete free the K tile
         // and the V tile before it.
         if (lane == 0) {
-            constexpr uint32_t kIdS = idesc_bf16_f32(kBlkQ, kBlkK);
-            constexpr uint32_t kIdO = idesc_bf16_f32(kBlkQ, HD) | (1u << 16);    // B is MN-major
             const uint64_t qd = smem_desc_sw128(smem_u32(sQ)), kd = smem_desc_sw128(smem_u32(ring));
             const uint64_t vd = smem_desc_mn(smem_u32(ring), kHalf);
             bool ok = mbar_wait(&B.q_full, 0, ab, a.err);
             tc_fence_after();
+            // A and B in bf16, or in f16 (both format fields zero)
+            const uint32_t types = Q8 && B.half == 3 ? ~((1u << 7) | (1u << 10)) : ~0u;
+            const uint32_t kIdS = idesc_bf16_f32(kBlkQ, kBlkK) & types;
+            const uint32_t kIdO = (idesc_bf16_f32(kBlkQ, HD) | (1u << 16)) & types;     // B is MN-major
             int ks_ = 0, vs_ = 1;                             // ring slots of the next K and V tiles
             auto scores = [&](int i) {
                 const uint64_t q0 = qd + (J.two && i ? S::kQBytes >> 4 : 0), k0 = kd + ks_ * (S::kTileBytes >> 4);
@@ -531,39 +573,90 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
         take(J);
         // -------- raw e4m3 tiles to swizzled bf16 tiles
         const int ct = t - 384;
+        // f16 holds the turn's rows where every exponent lies in [-15, 7] (values 2^-24 .. 57344)
+        {
+            bool fits = true, seen = false;
+            for (int i = ct; i < (J.n_keys + 15) / 16 * 2 && fits; i += 128) {
+                const int slot = J.k_begin + i / 2 * 16;
+                const long long row = kv_row_in_layer(a.pre.pages, a.Hkv, a.pre_seq, J.g, slot);
+                if (row < 0) continue;                        // (the copies report it)
+                const uint4 w = __ldg(reinterpret_cast<const uint4*>((i & 1 ? a.pre.ve : a.pre.ke) + row));
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int b = 0; b < 16; ++b) {
+                    const int e = (int)((u[b >> 2] >> (8 * (b & 3))) & 0xFF) - 127;
+                    if (slot + b >= J.k_begin + J.n_keys) continue;
+                    // rows of the least exponent (zeros, or nothing above 2^-115) become zeros beside others
+                    if (e != -124) seen = true;
+                    if (e != -124 && (e < -15 || e > 7)) fits = false;
+                }
+            }
+            if (!fits) atomicAnd(&B.half, 2);
+            if (seen) atomicOr(&B.half, 2);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.mode);
+        }
+        const bool mode_ok = warp_wait(&B.mode, 0, ab, a.err);
+        const bool half = B.half == 3;
         for (int e = 0; e < 2 * J.n_kb; ++e) {
             const int rs = e % NRAW, s = e % NST, use = e / NST;
-            bool ok = mbar_wait(&B.raw_full[rs], (e / NRAW) & 1, ab, a.err);
+            bool ok = mode_ok && mbar_wait(&B.raw_full[rs], (e / NRAW) & 1, ab, a.err);
             if (ok && use > 0) ok = mbar_wait(&B.empty[s], (use - 1) & 1, ab, a.err);
             if (!__all_sync(0xffffffffu, ok)) break;
             const int valid = J.n_keys - (e >> 1) * kBlkK;
             const char* src = raw + rs * S::kRawBytes;
             char* dst = ring + s * S::kTileBytes;
             constexpr int CPK = HD / 16;                      // 16-byte pieces of a raw row
+            auto convert = [&](auto f16) {
 #pragma unroll
-            for (int j = 0; j < CPK; ++j) {
-                const int id = ct + 128 * j, key = id / CPK, ch = id % CPK;
-                const uint4 w = *reinterpret_cast<const uint4*>(src + id * 16);
-                const float sc = key < valid ? kv8_scale(rexp[rs * kBlkK + key]) : 0.f;
-                const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-                uint32_t o[8];
+                for (int j0 = 0; j0 < CPK; j0 += 4) {
+                    // four pieces' loads before the first conversion
+                    uint4 w[4];
+                    int eb[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 x = e4m3x2_f32(ws[i]), y = e4m3x2_f32(ws[i] >> 16);
-                    o[2 * i] = bf16x2(x.x * sc, x.y * sc);
-                    o[2 * i + 1] = bf16x2(y.x * sc, y.y * sc);
+                    for (int j = 0; j < 4; ++j) {
+                        const int id = ct + 128 * (j0 + j);
+                        w[j] = *reinterpret_cast<const uint4*>(src + id * 16);
+                        eb[j] = rexp[rs * kBlkK + id / CPK];
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int id = ct + 128 * (j0 + j), key = id / CPK, ch = id % CPK;
+                        const uint32_t ws[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+                        uint32_t o[8];
+                        if (f16.value) {
+                            // 2^e as f16 (2^-15 is a denormal; rows of the least exponent: 0)
+                            const uint32_t h = eb[j] >= 127 - 14 ? (uint32_t)(eb[j] - 127 + 15) << 10 : (eb[j] == 127 - 15 ? 0x0200u : 0u);
+                            const uint32_t hh = h | (h << 16);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                o[2 * i] = f16x2_mul(e4m3x2_f16(ws[i]), hh);
+                                o[2 * i + 1] = f16x2_mul(e4m3x2_f16(ws[i] >> 16), hh);
+                            }
+                        } else {
+                            const float sc = kv8_scale(eb[j]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 x = e4m3x2_f32(ws[i]), y = e4m3x2_f32(ws[i] >> 16);
+                                o[2 * i] = bf16x2(x.x * sc, x.y * sc);
+                                o[2 * i + 1] = bf16x2(y.x * sc, y.y * sc);
+                            }
+                        }
+                        if (key >= valid)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] = 0u;    // a NaN there stays out
+                        char* d = dst + (ch >> 2) * kHalf + key * 128;
+                        const int c0 = (2 * (ch & 3)) ^ (key & 7), c1 = (2 * (ch & 3) + 1) ^ (key & 7);
+                        // the upper 64 dims' pieces in the other order: both halves' banks are then distinct
+                        const bool flip = (ch >> 2) & 1;
+                        const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                        *reinterpret_cast<uint4*>(d + ((flip ? c1 : c0) << 4)) = flip ? hi : lo;
+                        *reinterpret_cast<uint4*>(d + ((flip ? c0 : c1) << 4)) = flip ? lo : hi;
+                    }
                 }
-                if (key >= valid)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = 0u;    // a NaN there stays out
-                char* d = dst + (ch >> 2) * kHalf + key * 128;
-                const int c0 = (2 * (ch & 3)) ^ (key & 7), c1 = (2 * (ch & 3) + 1) ^ (key & 7);
-                // the upper 64 dims' pieces in the other order: both halves' banks are then distinct
-                const bool flip = (ch >> 2) & 1;
-                const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-                *reinterpret_cast<uint4*>(d + ((flip ? c1 : c0) << 4)) = flip ? hi : lo;
-                *reinterpret_cast<uint4*>(d + ((flip ? c0 : c1) << 4)) = flip ? lo : hi;
-            }
+            };
+            if (half) convert(std::true_type{});
+            else convert(std::false_type{});
             fence_async_smem();
             __syncwarp();
             if (lane == 0) {

@@ -73,7 +73,7 @@ class Case:
                          v=self.v.cuda() if v is None else v, tree_parent=self.parents)
         return out
 
-    def check(self, out):
+    def check(self, out, floor=0.0):
         from _attend_util import attend64, attend_tol, chain_mask, tree_mask
         out = out.double().cpu()
         r0 = 0
@@ -92,6 +92,9 @@ class Case:
             ref, mass, big = attend64(self.q[rows].double(), torch.cat(keys), torch.cat(vals),
                                       1.0 / math.sqrt(self.hd), sees)
             tol = attend_tol(ref, mass, big, self.hd)
+            # f32 sums of values far below the largest lose what lies 2^-24 under it; and each of a row's n products
+            # p v (p at most 1 before the division by a sum of at least 1) may be flushed to zero below 2^-126
+            tol = tol + sees.shape[1] * 2.0 ** -126 + floor + 2.0 ** -22 * torch.cat(vals).abs().amax() * (floor > 0)
             off = (out[rows] - ref).abs() - tol
             assert not torch.isnan(out[rows]).any(), f"sequence {b}: NaN"
             assert off.max() <= 0, f"sequence {b}: {off.max()} over the bound"
@@ -203,6 +206,38 @@ def test_what_lies_behind_the_lengths_does_not_show(q8, dim):
     """Slots past the committed lengths hold NaN and infinities; so do the other sequences of the prompt's cache."""
     c = Case(8, 8, 4, dim, [0, 5, 70], [2, 3, 1], prompt=133, q8=q8, prompt_q8=q8, dirty=True, layers=2, layer=1)
     c.check(c.run())
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("scales", ["small", "large", "wide", "zeros", "tiny"])
+@pytest.mark.parametrize("rows", [1, 12])
+def test_8_bit_rows_of_all_magnitudes(dim, scales, rows):
+    """Exponents inside and outside of what half precision holds, rows of zeros among others and alone: the
+    prompt's tiles change their operands' type, the row kernel its references."""
+    from _attend_util import rows8
+    from speculative_decoding_verify_04_gb300 import spec
+    c = Case(30, 8, 2, dim, [9, 40, 100], [rows] * 3, prompt=300, q8=True, prompt_q8=True)
+    g = torch.Generator().manual_seed(31)
+
+    def f(n):
+        e = {"small": lambda: torch.randint(-16, -9, (n, 2, 1), generator=g), "large": lambda: torch.randint(0, 5, (n, 2, 1), generator=g),
+             "wide": lambda: torch.randint(-30, 14, (n, 2, 1), generator=g), "zeros": lambda: torch.randint(-200, 2, (n, 2, 1), generator=g),
+             "tiny": lambda: torch.full((n, 2, 1), -124)}[scales]()
+        x = torch.randn(n, 2, dim, generator=g).double() * torch.exp2(e.double())
+        return x.float().to(torch.bfloat16)
+
+    # keys of ordinary size (the scores must not saturate), values of all sizes
+    k, v = _rows(g, 300, 2, dim), f(300)
+    c.prompt.import_rows(c.pseq, 0, k[None].cuda(), v[None].cuda())
+    c.pk, c.pv = (torch.from_numpy(rows8(x.double().numpy())[2]) for x in (k, v))
+    for b, n in enumerate(c.lens):
+        v = f(n)
+        c.kv.import_rows(b, 0, (c.keys[b].to(torch.bfloat16))[None].cuda(), v[None].cuda())
+        c.keys[b] = torch.from_numpy(rows8(c.keys[b].numpy())[2])
+        c.vals[b] = torch.from_numpy(rows8(v.double().numpy())[2])
+    c.v = f(3 * rows)
+    c.nv = torch.from_numpy(rows8(c.v.double().numpy())[2])
+    c.check(c.run(), floor=2.0 ** -100 if scales in ("zeros", "wide") else 0.0)
 
 
 def test_rows_of_a_fused_projection():
