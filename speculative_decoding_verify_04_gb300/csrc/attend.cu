@@ -99,14 +99,15 @@ SPEC_DEV void load_raw(const AttendArgs& a, const CacheView& cv, int seq, int g,
     t.ve = __ldg(reinterpret_cast<const uint32_t*>(cv.ve + row) + cq);
 }
 
-// 16 query vectors: rows to shared memory in 32 bits, then fragments in lane order (dims as
-// the K pieces of the cache's kind order them).  sS: the factor of a row's raw scores.
-template <int HD, bool QF32>
+// QB (16 or 8) query vectors: rows to shared memory in 32 bits, then fragments in lane order
+// (dims as the K pieces of the cache's kind order them), as the A operand of 16 rows or the B
+// operand of 8 columns.  sS: the factor of a row's raw scores.
+template <int HD, bool QF32, int QB>
 SPEC_DEV void load_queries(const AttendArgs& a, bool q8, int g, int G, int list_row0, int q0, int nq, uint4* sQ, float* sS,
                            float* rows) {
     constexpr int KS = HD / 16, LD = HD + 4;
     const int t = threadIdx.x;
-    for (int i = t; i < 16 * (HD / 8); i += kRowThreads) {
+    for (int i = t; i < QB * (HD / 8); i += kRowThreads) {
         const int r = i / (HD / 8), ch = i % (HD / 8), qg = q0 + r;
         float x[8];
 #pragma unroll
@@ -150,6 +151,15 @@ SPEC_DEV void load_queries(const AttendArgs& a, bool q8, int g, int G, int list_
         const int ks = i / 32, ln = i % 32, fg = ln >> 2, fc = ln & 3;
         const int d0 = q8 ? 64 * (ks >> 2) + 16 * fc + 4 * (ks & 3) : 32 * (ks >> 1) + 8 * fc + 4 * (ks & 1);
         const float4 u = *reinterpret_cast<const float4*>(rows + fg * LD + d0);
+        if (QB == 8) {
+            uint2* s8 = reinterpret_cast<uint2*>(sQ);
+            s8[i] = q8 ? make_uint2(pack_f16(u.x, u.y), pack_f16(u.z, u.w)) : make_uint2(pack_bf16(u.x, u.y), pack_bf16(u.z, u.w));
+            if (QF32)
+                s8[KS * 32 + i] = q8 ? make_uint2(pack_f16(u.x - f16_round(u.x), u.y - f16_round(u.y)),
+                                                  pack_f16(u.z - f16_round(u.z), u.w - f16_round(u.w)))
+                                     : make_uint2(pack_bf16_lo(u.x, u.y), pack_bf16_lo(u.z, u.w));
+            continue;
+        }
         const float4 w = *reinterpret_cast<const float4*>(rows + (fg + 8) * LD + d0);
         if (q8) {
             sQ[i] = make_uint4(pack_f16(u.x, u.y), pack_f16(w.x, w.y), pack_f16(u.z, u.w), pack_f16(w.z, w.w));
@@ -369,6 +379,215 @@ SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, in
     if (!Q8) { st.R[0] = st.m[0]; st.R[1] = st.m[1]; }
 }
 
+// The same for at most 8 query vectors: the keys are the M side (16 keys by 8 queries), so a
+// tile takes half the products and half the accumulators.
+//   scores: lane (g, c) holds keys g and g + 8 of queries 2c and 2c + 1; K pieces as above, of
+//     rows g and g + 8;
+//   values: O is kept transposed, dims by queries: m-tile mt holds dims (hd / 8) g + 2 mt (row g)
+//     and + 1 (row g + 8), so lane (g, c) reads hd / 8 consecutive dims of V rows 2c, 2c + 1,
+//     2c + 8, 2c + 9; P goes from the scores' layout to the operand's by a transposing move.
+template <int HD>
+struct RawFew {
+    uint4 k[2][HD / 64];
+    uint32_t v[4][HD / 32];
+    int ke[2], ve[2];
+};
+template <int HD>
+struct FewState { float o[HD / 16][4], m[2], l[2], R[2]; };
+
+SPEC_DEV uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+SPEC_DEV int few_v_key(int cq, int r) { return 2 * cq + (r & 1) + 8 * (r >> 1); }
+
+template <int HD>
+SPEC_DEV void load_raw_few(const AttendArgs& a, const CacheView& cv, int seq, int g, int kt, int k_end, int gq, int cq, RawFew<HD>& t) {
+    long long row = kv_row_in_layer(cv.pages, a.Hkv, seq, g, kt);
+    if (row < 0) { dev_error(a.err, SPEC_DEVERR_CAPACITY); row = 0; }
+    const uint8_t* K = static_cast<const uint8_t*>(cv.k) + row * HD;
+    const uint8_t* V = static_cast<const uint8_t*>(cv.v) + row * HD;
+    const int last = k_end - 1 - kt;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int key = min(gq + 8 * h, last);
+#pragma unroll
+        for (int p = 0; p < HD / 64; ++p) t.k[h][p] = __ldg(reinterpret_cast<const uint4*>(K + key * HD) + 4 * p + cq);
+        t.ke[h] = __ldg(cv.ke + row + key);
+        t.ve[h] = __ldg(cv.ve + row + key);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int key = min(few_v_key(cq, r), last);
+        if (HD == 128) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(V + key * HD) + gq);
+            t.v[r][0] = w.x; t.v[r][1] = w.y; t.v[r][HD / 32 - 2] = w.z; t.v[r][HD / 32 - 1] = w.w;
+        } else {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>(V + key * HD) + gq);
+            t.v[r][0] = w.x; t.v[r][1] = w.y;
+        }
+    }
+}
+
+template <int HD, bool Q8, bool QF32>
+SPEC_DEV void attend_range_few(const AttendArgs& a, const CacheView& cv, int seq, int g, int k_begin, int k_end, int n_ctx,
+                               const unsigned long long* sMask, const uint2* sQ, const float* sS, FewState<HD>& st) {
+    constexpr int KS = HD / 16, MT = HD / 16;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, cq = lane & 3;
+    const float cf[2] = {sS[2 * cq], sS[2 * cq + 1]};
+    RawFew<HD> nx;
+    int kt = k_begin + 16 * warp;
+    if (Q8 && kt < k_end) load_raw_few<HD>(a, cv, seq, g, kt, k_end, gq, cq, nx);
+    for (; kt < k_end; kt += 64) {
+        uint32_t ka[KS][4], vb[4][MT];
+        float kf[2] = {1.f, 1.f}, vf[2] = {0.f, 0.f};
+        if (Q8) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int p = 0; p < HD / 64; ++p) {
+                    const uint32_t w[4] = {nx.k[h][p].x, nx.k[h][p].y, nx.k[h][p].z, nx.k[h][p].w};
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        ka[4 * p + s][h] = e4m3x2_f16(w[s]);
+                        ka[4 * p + s][2 + h] = e4m3x2_f16(w[s] >> 16);
+                    }
+                }
+                kf[h] = kv8_scale(nx.ke[h]);
+                vf[h] = (float)(nx.ve[h] - 127);
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int i = 0; i < HD / 32; ++i) {
+                    vb[r][2 * i] = e4m3x2_f16(nx.v[r][i]);
+                    vb[r][2 * i + 1] = e4m3x2_f16(nx.v[r][i] >> 16);
+                }
+            if (kt + 64 < k_end) load_raw_few<HD>(a, cv, seq, g, kt + 64, k_end, gq, cq, nx);
+        } else {
+            long long row = kv_row_in_layer(cv.pages, a.Hkv, seq, g, kt);
+            if (row < 0) { dev_error(a.err, SPEC_DEVERR_CAPACITY); row = 0; }
+            const __nv_bfloat16* K = static_cast<const __nv_bfloat16*>(cv.k) + row * HD;
+            const __nv_bfloat16* V = static_cast<const __nv_bfloat16*>(cv.v) + row * HD;
+            const int last = k_end - 1 - kt;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int key = min(gq + 8 * h, last);
+#pragma unroll
+                for (int p = 0; p < HD / 32; ++p) {
+                    const uint4 w = __ldg(reinterpret_cast<const uint4*>(K + key * HD) + 4 * p + cq);
+                    ka[2 * p][h] = w.x; ka[2 * p][2 + h] = w.y;
+                    ka[2 * p + 1][h] = w.z; ka[2 * p + 1][2 + h] = w.w;
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int key = min(few_v_key(cq, r), last);
+#pragma unroll
+                for (int p = 0; p < HD / 64; ++p) {
+                    const uint4 w = __ldg(reinterpret_cast<const uint4*>(V + key * HD) + (HD / 64) * gq + p);
+                    vb[r][4 * p] = w.x; vb[r][4 * p + 1] = w.y; vb[r][4 * p + 2] = w.z; vb[r][4 * p + 3] = w.w;
+                }
+            }
+        }
+        if (kt + 16 > k_end) {
+            // values of keys past the range: their probability is zero, and zero times what the slot holds must be zero
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (kt + few_v_key(cq, r) >= k_end)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) vb[r][i] = 0u;
+        }
+        float sc[2][4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[0][e] = sc[1][e] = 0.f;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            const uint2 qh = sQ[s * 32 + lane];
+            if (Q8) mma16816_f16(sc[s & 1], ka[s][0], ka[s][1], ka[s][2], ka[s][3], qh.x, qh.y);
+            else mma16816(sc[s & 1], ka[s][0], ka[s][1], ka[s][2], ka[s][3], qh.x, qh.y);
+            if (QF32) {
+                const uint2 ql = sQ[KS * 32 + s * 32 + lane];
+                if (Q8) mma16816_f16(sc[s & 1], ka[s][0], ka[s][1], ka[s][2], ka[s][3], ql.x, ql.y);
+                else mma16816(sc[s & 1], ka[s][0], ka[s][1], ka[s][2], ka[s][3], ql.x, ql.y);
+            }
+        }
+        // x[j][h]: query 2c + j, key g + 8 h; y: what the exponent of P is
+        float x[2][2], y[2][2], f[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) x[j][h] = (sc[0][2 * h + j] + sc[1][2 * h + j]) * (Q8 ? cf[j] * kf[h] : cf[j]);
+        if (kt + 16 > min(n_ctx, k_end)) {                    // a tile that reaches new rows or the end
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const unsigned long long mk = sMask[2 * cq + j];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int key = kt + gq + 8 * h;
+                    if (!(key < k_end && (key < n_ctx || ((mk >> ((key - n_ctx) & 63)) & 1ull)))) x[j][h] = -INFINITY;
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float mt = fmaxf(x[j][0], x[j][1]);
+            y[j][0] = x[j][0] + vf[0];
+            y[j][1] = x[j][1] + vf[1];
+            float rt = fmaxf(y[j][0], y[j][1]);
+#pragma unroll
+            for (int o = 4; o <= 16; o <<= 1) {
+                mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
+                if (Q8) rt = fmaxf(rt, __shfl_xor_sync(0xffffffffu, rt, o));
+            }
+            const float mn = fmaxf(st.m[j], mt), mu = mn == -INFINITY ? 0.f : mn;   // nothing seen yet: p = 0
+            const float alpha = st.m[j] == mn ? 1.f : ex2(st.m[j] - mu);
+            const float p0 = ex2(x[j][0] - mu), p1 = ex2(x[j][1] - mu);
+            st.l[j] = st.l[j] * alpha + (p0 + p1);            // this lane's keys; joined at the end
+            st.m[j] = mn;
+            if (Q8) {
+                const float rn = fmaxf(st.R[j], rt), ru = rn == -INFINITY ? 0.f : rn;
+                f[j] = st.R[j] == rn ? 1.f : ex2(st.R[j] - ru);
+                st.R[j] = rn;
+                y[j][0] = ex2(y[j][0] - ru);
+                y[j][1] = ex2(y[j][1] - ru);
+            } else {
+                f[j] = alpha;
+                y[j][0] = p0;
+                y[j][1] = p1;
+            }
+        }
+        if (!__all_sync(0xffffffffu, f[0] == 1.f && f[1] == 1.f)) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                st.o[mt][0] *= f[0];
+                st.o[mt][1] *= f[1];
+                st.o[mt][2] *= f[0];
+                st.o[mt][3] *= f[1];
+            }
+        }
+        uint32_t b[2], bl[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            b[h] = transpose8(Q8 ? pack_f16(y[0][h], y[1][h]) : pack_bf16(y[0][h], y[1][h]));
+            if (!Q8) bl[h] = transpose8(pack_bf16_lo(y[0][h], y[1][h]));
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+            const uint32_t a0 = pair_lo(vb[0][mt], vb[1][mt]), a1 = pair_hi(vb[0][mt], vb[1][mt]);
+            const uint32_t a2 = pair_lo(vb[2][mt], vb[3][mt]), a3 = pair_hi(vb[2][mt], vb[3][mt]);
+            if (Q8) {
+                mma16816_f16(st.o[mt], a0, a1, a2, a3, b[0], b[1]);
+            } else {
+                mma16816(st.o[mt], a0, a1, a2, a3, b[0], b[1]);
+                mma16816(st.o[mt], a0, a1, a2, a3, bl[0], bl[1]);
+            }
+        }
+    }
+    if (!Q8) { st.R[0] = st.m[0]; st.R[1] = st.m[1]; }
+}
+
 SPEC_DEV unsigned long long row_mask(const AttendSpan& s, int b, int j) {
     if (s.tree == 0) return j >= 63 ? ~0ull : (2ull << j) - 1ull;
     if (s.tree == 1) return s.mask[j];
@@ -378,18 +597,18 @@ SPEC_DEV unsigned long long row_mask(const AttendSpan& s, int b, int j) {
     return mk;
 }
 
-template <int HD, bool QF32>
-__global__ void __launch_bounds__(kRowThreads, HD == 128 ? 3 : 4)
+template <int HD, bool QF32, int QB>
+__global__ void __launch_bounds__(kRowThreads, QB == 8 ? (HD == 128 ? 4 : 5) : (HD == 128 ? 3 : 4))
 attend_rows_kernel(const __grid_constant__ AttendArgs a) {
     pdl_wait();
     pdl_trigger();
     constexpr int KS = HD / 16, VD = HD / 8;
     constexpr int LS = HD + 4;                                              // a state row: O, m, l, R
     extern __shared__ float smf[];
-    uint4* sQ = reinterpret_cast<uint4*>(smf);                              // [QF32 ? 2 : 1][KS][32]
-    float* sState = smf + (QF32 ? 2 : 1) * KS * 32 * 4;                     // [4 warps][16][LS]; the query rows before
-    float* sS = sState + 4 * 16 * LS;                                       // [16]
-    unsigned long long* sMask = reinterpret_cast<unsigned long long*>(sS + 16);   // [16]
+    uint4* sQ = reinterpret_cast<uint4*>(smf);                              // [QF32 ? 2 : 1][KS][32] (8 queries: uint2)
+    float* sState = smf + (QF32 ? 2 : 1) * KS * 32 * (QB / 4);              // [4 warps][QB][LS]; the query rows before
+    float* sS = sState + 4 * QB * LS;                                       // [QB]
+    unsigned long long* sMask = reinterpret_cast<unsigned long long*>(sS + QB);   // [QB]
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, gq = lane >> 2, cq = lane & 3;
     const int G = a.H / a.Hkv;
     // the prompt's blocks first (the longer ones), then the sequences' own
@@ -419,7 +638,7 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
         if (n_ctx + rows > a.own.cap && rows > 0 && t == 0) dev_error(a.err, SPEC_DEVERR_CAPACITY);
         range = a.own_range0 + split;
     }
-    const int q0 = qb * 16, nq = min(16, rows * G - q0);
+    const int q0 = qb * QB, nq = min(QB, rows * G - q0);
     if (nq <= 0) return;
     int chunk = max(kMinKeys, (n_keys + n_splits - 1) / n_splits);
     chunk = (chunk + 63) / 64 * 64;
@@ -432,29 +651,51 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
         if (t < nq) *reinterpret_cast<float2*>(a.part_ml + 2 * vec_of(t)) = make_float2(-INFINITY, 0.f);
         return;
     }
-    load_queries<HD, QF32>(a, cv.q8, g, G, list_row0, q0, nq, sQ, sS, sState);
-    if (t < 16) sMask[t] = !is_pre && t < nq ? row_mask(a.span, b, (q0 + t) / G) : 0ull;
+    load_queries<HD, QF32, QB>(a, cv.q8, g, G, list_row0, q0, nq, sQ, sS, sState);
+    if (t < QB) sMask[t] = !is_pre && t < nq ? row_mask(a.span, b, (q0 + t) / G) : 0ull;
     __syncthreads();
-    RowState<HD> rs;
+    if (QB == 8) {
+        FewState<HD> rs;
 #pragma unroll
-    for (int rr = 0; rr < 2; ++rr) { rs.m[rr] = rs.R[rr] = -INFINITY; rs.l[rr] = 0.f; }
+        for (int j = 0; j < 2; ++j) { rs.m[j] = rs.R[j] = -INFINITY; rs.l[j] = 0.f; }
 #pragma unroll
-    for (int nt = 0; nt < VD; ++nt) rs.o[nt][0] = rs.o[nt][1] = rs.o[nt][2] = rs.o[nt][3] = 0.f;
-    if (cv.q8) attend_range<HD, true, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, sMask[gq], sMask[gq + 8], sQ, sS, rs);
-    else attend_range<HD, false, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, sMask[gq], sMask[gq + 8], sQ, sS, rs);
-    // warp states -> shared: rows g and g + 8, dims VD * 2c + nt and VD * (2c + 1) + nt
+        for (int mt = 0; mt < HD / 16; ++mt) rs.o[mt][0] = rs.o[mt][1] = rs.o[mt][2] = rs.o[mt][3] = 0.f;
+        const uint2* s8 = reinterpret_cast<const uint2*>(sQ);
+        if (cv.q8) attend_range_few<HD, true, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, sMask, s8, sS, rs);
+        else attend_range_few<HD, false, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, sMask, s8, sS, rs);
+        // warp states -> shared: queries 2c and 2c + 1, dims VD * g ..
 #pragma unroll
-    for (int rr = 0; rr < 2; ++rr) {
-        rs.l[rr] += __shfl_xor_sync(0xffffffffu, rs.l[rr], 1);
-        rs.l[rr] += __shfl_xor_sync(0xffffffffu, rs.l[rr], 2);
-        float* st = sState + ((size_t)warp * 16 + gq + 8 * rr) * LS;
-        if (cq == 0) { st[HD] = rs.m[rr]; st[HD + 1] = rs.l[rr]; st[HD + 2] = rs.R[rr]; }
+        for (int j = 0; j < 2; ++j) {
 #pragma unroll
-        for (int nt = 0; nt < VD; nt += 4) {
-            *reinterpret_cast<float4*>(st + VD * (2 * cq) + nt) =
-                make_float4(rs.o[nt][2 * rr], rs.o[nt + 1][2 * rr], rs.o[nt + 2][2 * rr], rs.o[nt + 3][2 * rr]);
-            *reinterpret_cast<float4*>(st + VD * (2 * cq + 1) + nt) =
-                make_float4(rs.o[nt][2 * rr + 1], rs.o[nt + 1][2 * rr + 1], rs.o[nt + 2][2 * rr + 1], rs.o[nt + 3][2 * rr + 1]);
+            for (int o = 4; o <= 16; o <<= 1) rs.l[j] += __shfl_xor_sync(0xffffffffu, rs.l[j], o);
+            float* st = sState + ((size_t)warp * QB + 2 * cq + j) * LS;
+            if (gq == 0) { st[HD] = rs.m[j]; st[HD + 1] = rs.l[j]; st[HD + 2] = rs.R[j]; }
+#pragma unroll
+            for (int mt = 0; mt < HD / 16; ++mt)
+                *reinterpret_cast<float2*>(st + VD * gq + 2 * mt) = make_float2(rs.o[mt][j], rs.o[mt][2 + j]);
+        }
+    } else {
+        RowState<HD> rs;
+#pragma unroll
+        for (int rr = 0; rr < 2; ++rr) { rs.m[rr] = rs.R[rr] = -INFINITY; rs.l[rr] = 0.f; }
+#pragma unroll
+        for (int nt = 0; nt < VD; ++nt) rs.o[nt][0] = rs.o[nt][1] = rs.o[nt][2] = rs.o[nt][3] = 0.f;
+        if (cv.q8) attend_range<HD, true, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, sMask[gq], sMask[gq + 8], sQ, sS, rs);
+        else attend_range<HD, false, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, sMask[gq], sMask[gq + 8], sQ, sS, rs);
+        // warp states -> shared: rows g and g + 8, dims VD * 2c + nt and VD * (2c + 1) + nt
+#pragma unroll
+        for (int rr = 0; rr < 2; ++rr) {
+            rs.l[rr] += __shfl_xor_sync(0xffffffffu, rs.l[rr], 1);
+            rs.l[rr] += __shfl_xor_sync(0xffffffffu, rs.l[rr], 2);
+            float* st = sState + ((size_t)warp * QB + gq + 8 * rr) * LS;
+            if (cq == 0) { st[HD] = rs.m[rr]; st[HD + 1] = rs.l[rr]; st[HD + 2] = rs.R[rr]; }
+#pragma unroll
+            for (int nt = 0; nt < VD; nt += 4) {
+                *reinterpret_cast<float4*>(st + VD * (2 * cq) + nt) =
+                    make_float4(rs.o[nt][2 * rr], rs.o[nt + 1][2 * rr], rs.o[nt + 2][2 * rr], rs.o[nt + 3][2 * rr]);
+                *reinterpret_cast<float4*>(st + VD * (2 * cq + 1) + nt) =
+                    make_float4(rs.o[nt][2 * rr + 1], rs.o[nt + 1][2 * rr + 1], rs.o[nt + 2][2 * rr + 1], rs.o[nt + 3][2 * rr + 1]);
+            }
         }
     }
     __syncthreads();
@@ -464,7 +705,7 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
         float M = -INFINITY, RR = -INFINITY;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const float* st = sState + ((size_t)w * 16 + r) * LS + HD;
+            const float* st = sState + ((size_t)w * QB + r) * LS + HD;
             M = fmaxf(M, st[0]);
             RR = fmaxf(RR, st[2]);
         }
@@ -472,7 +713,7 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
         float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-            const float* st = sState + ((size_t)w * 16 + r) * LS;
+            const float* st = sState + ((size_t)w * QB + r) * LS;
             if (st[HD] == -INFINITY && !(st[HD + 1] != 0.f)) continue;        // this warp saw nothing
             L += st[HD + 1] * ex2(st[HD] - M);
             const float wt = ex2(st[HD + 2] - RR);
@@ -626,8 +867,8 @@ int make_span(AttendSpan* s, int batch, const int* n_rows, int extra, const int*
     return SPEC_OK;
 }
 
-static size_t rows_smem(int hd, bool qf32) {
-    return (qf32 ? 2 : 1) * (hd / 16) * 32 * 16 + 4 * 16 * (hd + 4) * sizeof(float) + 16 * sizeof(float) + 16 * 8;
+static size_t rows_smem(int hd, bool qf32, int qb) {
+    return (qf32 ? 2 : 1) * (hd / 16) * 32 * qb + 4 * qb * (hd + 4) * sizeof(float) + qb * sizeof(float) + qb * 8;
 }
 
 // Query vectors whose partial states fit.  The row kernel's two parts keep to (ranges) x
@@ -661,9 +902,11 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     const int TH = span.T * H;
     const size_t fit = m->attend_part_floats / (hd + 2) / TH;      // ranges the workspace holds
     // key ranges: about six CTAs an SM (three are resident) where the keys allow it, by each part's share of them
-    a.own_qb = (span.max_rows * G + 15) / 16;
     const bool tile = pre && span.T * G > kRowVectors && attend_tile_ok(pre);
-    a.pre_qb = pre && !tile ? (span.T * G + 15) / 16 : 0;
+    // blocks of 8 query vectors where one holds all of a part's, else of 16
+    const int QB = span.max_rows * G <= 8 && (!pre || tile || span.T * G <= 8) ? 8 : 16;
+    a.own_qb = (span.max_rows * G + QB - 1) / QB;
+    a.pre_qb = pre && !tile ? (span.T * G + QB - 1) / QB : 0;
     const long long own_blocks = (long long)span.batch * Hkv * a.own_qb, pre_blocks = (long long)Hkv * a.pre_qb;
     const long long keys = own_blocks * kv->max_ctx + pre_blocks * (pre ? pre->max_ctx : 0);
     const long long per = std::max<long long>(kMinKeys, keys / (6 * m->num_sms) + 1);
@@ -685,9 +928,11 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     a.part_o = m->attend_part;
     a.part_ml = m->attend_part + (size_t)ranges * TH * hd;
     const dim3 grid((unsigned)(a.pre_splits * pre_blocks + a.own_splits * own_blocks));
-    const size_t smem = rows_smem(hd, q_f32);
-    void (*f)(AttendArgs) = hd == 128 ? (q_f32 ? attend_rows_kernel<128, true> : attend_rows_kernel<128, false>)
-                                      : (q_f32 ? attend_rows_kernel<64, true> : attend_rows_kernel<64, false>);
+    const size_t smem = rows_smem(hd, q_f32, QB);
+    void (*const kernels[8])(AttendArgs) = {
+        attend_rows_kernel<64, false, 8>, attend_rows_kernel<64, false, 16>, attend_rows_kernel<64, true, 8>, attend_rows_kernel<64, true, 16>,
+        attend_rows_kernel<128, false, 8>, attend_rows_kernel<128, false, 16>, attend_rows_kernel<128, true, 8>, attend_rows_kernel<128, true, 16>};
+    void (*f)(AttendArgs) = kernels[(hd == 128 ? 4 : 0) + (q_f32 ? 2 : 0) + (QB == 16 ? 1 : 0)];
     const int slot = prof_start(m, st);
     if (tile) SPEC_TRY(launch_attend_tile(pre, a, st));
     cudaError_t e = launch_k(m->pdl, f, grid, dim3(kRowThreads), smem, st, a);
