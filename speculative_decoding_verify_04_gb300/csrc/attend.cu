@@ -935,7 +935,9 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     void (*f)(AttendArgs) = kernels[(hd == 128 ? 4 : 0) + (q_f32 ? 2 : 0) + (QB == 16 ? 1 : 0)];
     const int slot = prof_start(m, st);
     if (tile) SPEC_TRY(launch_attend_tile(pre, a, st));
-    cudaError_t e = launch_k(m->pdl, f, grid, dim3(kRowThreads), smem, st, a);
+    // behind the tile kernel without early launch: row CTAs that wait on its SMs cost more than their
+    // start does (8 chains over 4096 tokens 45 -> 37 us a call, 64 decodes over 16384 90 -> 81 us)
+    cudaError_t e = launch_k(m->pdl && !tile, f, grid, dim3(kRowThreads), smem, st, a);
     SPEC_TRY(check_cuda(e, "attention rows launch"));
     JoinArgs j{};
     j.part_o = a.part_o;

@@ -98,6 +98,8 @@ struct Kv8CopyArgs {
 template <int HD, bool IN>
 __global__ void __launch_bounds__(256)
 kv8_copy_kernel(const __grid_constant__ Kv8CopyArgs a) {
+    pdl_wait();
+    pdl_trigger();
     constexpr int L = HD / 8, RPS = 32 / L, STEPS = kCopySlots / RPS;
     const int which = blockIdx.y, lane = threadIdx.x & 31, grp = lane / L, l = lane % L;
     const long long n_items = (long long)a.n_layers * a.n_blk * a.Hkv;
@@ -184,9 +186,9 @@ int launch_kv8_copy(spec_kv* kv, int seq, int layer0, int n_layers, int slot0, i
     const dim3 grid((unsigned)std::min<long long>((items + 7) / 8, 1 << 16), 2);
     void (*f)(Kv8CopyArgs) = c.head_dim == 128 ? (to_cache ? kv8_copy_kernel<128, true> : kv8_copy_kernel<128, false>)
                                                : (to_cache ? kv8_copy_kernel<64, true> : kv8_copy_kernel<64, false>);
-    f<<<grid, 256, 0, st>>>(a);
+    const cudaError_t e = launch_k(m->pdl, f, grid, dim3(256), 0, st, a);
     ++m->launches;
-    return check_cuda(cudaGetLastError(), "8-bit cache copy launch");
+    return check_cuda(e, "8-bit cache copy launch");
 }
 
 int launch_append(spec_kv* kv, int layer, const AttendSpan& span, const void* k, long long k_stride, const void* v,
