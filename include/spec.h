@@ -259,7 +259,10 @@ int spec_kv_set_prefix(spec_kv* kv, spec_kv* prefix, int32_t seq);
  * Row j of sequence b sees the prompt of the cache's prefix, the slots below
  * s_b and the rows of its chain or tree path; scores are q.k / sqrt(hd), softmax
  * statistics and sums are f32.  Head h reads KV head h / (H / Hkv).  A row whose
- * scores are all -inf, or hold NaN or +inf, gives NaN.  Lengths unchanged;
+ * scores are all -inf, or hold NaN or +inf, gives NaN, as one that sees a new row
+ * with a NaN or an infinity in v; what a row does not see has no influence on it.
+ * The model's workspace is used: one stream at a time, as every call on a model.
+ * Lengths unchanged;
  * kv_commit with acc_len n_rows[b] - 1 keeps the rows.  The slots are read on
  * the device: a captured call may be replayed after the lengths moved.  Slots
  * beyond the capacity are neither written nor read and set

@@ -176,6 +176,13 @@ SPEC_DEV void load_queries(const AttendArgs& a, bool q8, int g, int G, int list_
     }
 }
 
+// two values of which one is NaN or an infinity (f16: as bits of an exponent of ones)
+template <bool Q8>
+SPEC_DEV bool not_finite2(uint32_t w) {
+    constexpr uint32_t E = Q8 ? 0x7C00u : 0x7F80u;
+    return (w & E) == E || (w & (E << 16)) == (E << 16);
+}
+
 // running state of a lane's two rows: m and l of the sums of p (l over the lane's keys; joined
 // over the quad at the end), R the reference of O (8-bit caches; else R = m)
 template <int HD>
@@ -301,6 +308,23 @@ SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, in
 #pragma unroll
                     for (int i = 0; i < KS; ++i) vb[r][i] = 0u;
         }
+        // a new row's NaN or infinity must not reach the rows that do not see it (0 * NaN): it leaves the
+        // product, and the rows that see it become NaN
+        uint32_t bad = 0;
+        if (kt + 16 > n_ctx) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                bool b = false;
+#pragma unroll
+                for (int i = 0; i < KS; ++i) b |= not_finite2<Q8>(vb[r][i]);
+                if (kt + 4 * cq + r < n_ctx) b = false;
+                if (b)
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) vb[r][i] = 0u;
+                // any of the eight lanes that hold the key's values
+                if (__ballot_sync(0xffffffffu, b) & (0x11111111u << cq)) bad |= 1u << r;
+            }
+        }
         // two sums a key half: chains of KS / 2 products
         float sc[2][4], sd[2][4];
 #pragma unroll
@@ -341,6 +365,10 @@ SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, in
                 const bool ctx = key < n_ctx, in = key < k_end;
                 if (!(in && (ctx || ((mk0 >> ((key - n_ctx) & 63)) & 1ull)))) x[0][k] = -INFINITY;
                 if (!(in && (ctx || ((mk1 >> ((key - n_ctx) & 63)) & 1ull)))) x[1][k] = -INFINITY;
+                if ((bad >> k) & 1u) {
+                    if (x[0][k] != -INFINITY) x[0][k] = __int_as_float(0x7fc00000);
+                    if (x[1][k] != -INFINITY) x[1][k] = __int_as_float(0x7fc00000);
+                }
             }
         }
         if (Q8) {
@@ -499,6 +527,25 @@ SPEC_DEV void attend_range_few(const AttendArgs& a, const CacheView& cv, int seq
 #pragma unroll
                     for (int i = 0; i < MT; ++i) vb[r][i] = 0u;
         }
+        // a new row's NaN or infinity must not reach the rows that do not see it (0 * NaN): it leaves the
+        // product, and the rows that see it become NaN
+        uint32_t bad = 0;                                     // bit k: tile key k
+        if (kt + 16 > n_ctx) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                bool b = false;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) b |= not_finite2<Q8>(vb[r][i]);
+                if (kt + few_v_key(cq, r) < n_ctx) b = false;
+                if (b)
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) vb[r][i] = 0u;
+                const uint32_t any = __ballot_sync(0xffffffffu, b);
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (any & (0x11111111u << c)) bad |= 1u << few_v_key(c, r);
+            }
+        }
         float sc[2][4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[0][e] = sc[1][e] = 0.f;
@@ -527,6 +574,7 @@ SPEC_DEV void attend_range_few(const AttendArgs& a, const CacheView& cv, int seq
                 for (int h = 0; h < 2; ++h) {
                     const int key = kt + gq + 8 * h;
                     if (!(key < k_end && (key < n_ctx || ((mk >> ((key - n_ctx) & 63)) & 1ull)))) x[j][h] = -INFINITY;
+                    else if ((bad >> (gq + 8 * h)) & 1u) x[j][h] = __int_as_float(0x7fc00000);
                 }
             }
         }
@@ -999,6 +1047,9 @@ extern "C" int spec_attend(spec_kv* kv, int32_t layer, int32_t batch, const int3
     spec_model* m = kv->m;
     const spec_model_config& c = m->cfg;
     if (!m->bf16) return set_error(SPEC_ERR_UNSUPPORTED, "spec_attend: bf16 models only");
+    int dev = -1;
+    SPEC_TRY(check_cuda(cudaGetDevice(&dev), "spec_attend: cudaGetDevice"));
+    if (dev != m->device) return set_error(SPEC_ERR_ARG, "spec_attend: the model is on another device than the current one");
     SPEC_TRY(kv_check_prefix(kv, "spec_attend"));
     if (layer < 0 || layer >= c.n_layers) return set_error(SPEC_ERR_ARG, "spec_attend: layer out of range");
     if (batch < 1 || batch > kv->batch) return set_error(SPEC_ERR_ARG, "spec_attend: bad batch");

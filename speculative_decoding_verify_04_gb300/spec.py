@@ -157,6 +157,16 @@ def _on(t, dev, name):
         raise SpecError(f"{name}: on {t.device}, not on the current device")
 
 
+def _at(t, dtype, name, numel, dev):
+    """Pointer of a contiguous tensor of the current device (None: None)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() < numel or not t.is_contiguous():
+        _need(t, dtype, name, numel)
+        _on(t, dev, name)
+    return t.data_ptr()
+
+
 def device_info():
     lib = load()
     a, b, c = c_int32(), c_int32(), c_int32()
@@ -529,23 +539,16 @@ def spec_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logpr
     rows, V = sh
     dev = torch.cuda.current_device()
     _on(logits, dev, "logits")
-    f32, i32 = torch.float32, torch.int32
     n = 0
     if top_ids is not None:
         if top_ids.dim() != 2 or top_ids.shape[0] < rows:
             raise SpecError(f"top_ids: need [{rows}, n]")
         n = top_ids.shape[1]
-
-    def at(t, dtype, name, numel):
-        if t is None:
-            return None
-        _need(t, dtype, name, numel)
-        _on(t, dev, name)
-        return t.data_ptr()
-
-    tok, lp = at(tokens, i32, "tokens", rows), at(logprob, f32, "logprob", rows)
-    ent = at(entropy, f32, "entropy", rows)
-    ids, tlp = at(top_ids, i32, "top_ids", rows * n), at(top_logprobs, f32, "top_logprobs", rows * n)
+    tok = _at(tokens, torch.int32, "tokens", rows, dev)
+    lp = _at(logprob, torch.float32, "logprob", rows, dev)
+    ent = _at(entropy, torch.float32, "entropy", rows, dev)
+    ids = _at(top_ids, torch.int32, "top_ids", rows * n, dev)
+    tlp = _at(top_logprobs, torch.float32, "top_logprobs", rows * n, dev)
     if rows == 0:
         return
     rc = load().spec_logprobs(logits.data_ptr(), SPEC_DTYPE_BF16 if dt is torch.bfloat16 else SPEC_DTYPE_F32,

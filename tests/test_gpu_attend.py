@@ -348,6 +348,44 @@ def test_minus_infinity_keys_and_nan_rows():
     assert torch.isnan(out[0]).all() and (out[1] == 2).all() and torch.isnan(out[2]).all()
 
 
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("heads,dim", [(2, 64), (8, 64), (2, 128), (8, 128)])
+def test_a_new_rows_nan_stays_with_the_rows_that_see_it(q8, heads, dim):
+    """A tree whose nodes 2 and 5 hold NaN and infinities in k and v: their descendants are NaN, the others are as
+    if those rows were zeros (one and several query heads a KV head: both forms of the row kernel)."""
+    from speculative_decoding_verify_04_gb300 import spec
+    c = Case(40, heads, 2, dim, [21], [7], prompt=30, q8=q8, parents=TREE)
+    clean_k, clean_v = c.k.clone(), c.v.clone()
+    clean_k[[2, 5]] = 0
+    clean_v[[2, 5]] = 0
+    want = c.run(k=clean_k.cuda(), v=clean_v.cuda())
+    k, v = c.k.clone(), c.v.clone()
+    k[2], v[2], v[5, 0, 3], v[5, 1, 7] = math.nan, math.nan, math.nan, math.nan
+    if not q8:
+        v[2, :, ::2] = math.inf
+    got = c.run(k=k.cuda(), v=v.cuda())
+    assert torch.isnan(got[[2, 5]].float()).all()
+    assert torch.equal(got[[0, 1, 3, 4, 6]], want[[0, 1, 3, 4, 6]])
+    assert c.model.device_error() == 0
+
+
+@pytest.mark.parametrize("own_page,prompt_page", [(None, 64), (128, None), (64, 256)])
+@pytest.mark.parametrize("q8,prompt_q8", [(False, True), (True, False)])
+def test_caches_of_different_kinds(own_page, prompt_page, q8, prompt_q8):
+    from _attend_util import rows8
+    from speculative_decoding_verify_04_gb300 import spec
+    c = Case(41, 8, 2, 64, [70, 3], [6, 5], prompt=300, q8=q8, page=own_page)
+    pre = spec.KVCache(c.model, 1, 320, page=prompt_page, q8=prompt_q8)
+    g = torch.Generator().manual_seed(42)
+    k, v = _rows(g, 300, 2, 64), _rows(g, 300, 2, 64)
+    pre.import_rows(0, 0, k[None].cuda(), v[None].cuda())
+    pre.set_lengths([300])
+    c.kv.set_prefix(pre)
+    f = (lambda x: torch.from_numpy(rows8(x.double().numpy())[2])) if prompt_q8 else (lambda x: x.double())
+    c.pk, c.pv = f(k), f(v)
+    c.check(c.run())
+
+
 def test_refusals():
     from _attend_util import head_model
     from speculative_decoding_verify_04_gb300 import spec

@@ -217,6 +217,41 @@ def test_best_of_n():
     assert model.device_error() == 0
 
 
+def test_tree_drafts_and_the_call_without_allocations():
+    """The tree drafts propose over a shared prompt what they propose over the whole context; spec_verify_noalloc gives
+    the bits of spec_verify over 8-bit and shared caches."""
+    from speculative_decoding_verify_04_gb300 import spec
+    lib()
+    model, _, shape = model_pair(SHAPES["hd64"], seed=23, max_rows=64, max_batch=2, max_position=512)
+    prompt = make_tokens(90, shape.vocab, seed=24)
+    suffixes = [make_tokens(5, shape.vocab, seed=25), make_tokens(17, shape.vocab, seed=26)]
+    par = [int(p) for p in tree_parents([2, 2])]
+    n = len(par)
+    whole = spec.KVCache(model, 2, 160)
+    t1 = _i32(2)
+    for b, s in enumerate(suffixes):
+        spec.spec_prefill(model, whole, b, cuda_i32(np.concatenate([prompt, s])), next_tok=t1[b:b + 1])
+    scratch = torch.empty(2 * n, shape.vocab, device="cuda")
+    ref, refL = _i32(2, n), torch.empty(2, n, shape.d_model, device="cuda")
+    spec.spec_draft_tree(model, whole, t1, par, ref, refL, scratch)
+    for q8 in (False, True):
+        kv, t0 = _continuations(model, prompt, suffixes, q8=q8, prompt_q8=q8)
+        tok, hL = _i32(2, n), torch.empty(2, n, shape.d_model, device="cuda")
+        spec.spec_draft_tree(model, kv, t1, par, tok, hL, scratch)
+        par_d, n_d, tok_d = _i32(2, n), _i32(2), _i32(2, n)
+        spec.spec_draft_tree_dynamic(model, kv, t1, [2, 2], 1.5, tok_d, par_d, n_d, hL.clone(), scratch)
+        assert n_d.tolist() == [n, n] and torch.equal(tok_d, tok)
+        if not q8:
+            # the states differ by the queries' rounding only
+            assert torch.equal(t0, t1) and torch.equal(tok, ref)
+            assert (hL - refL).abs().max() < TOL
+        a, b = (torch.empty(2 * n, shape.vocab, device="cuda") for _ in range(2))
+        spec.spec_verify(model, kv, [n, n], tok, n, h_in=hL, h_stride=n, tree_parent=par, logits=a)
+        spec.spec_verify_noalloc(model, kv, [n, n], tok, n, h_in=hL, h_stride=n, tree_parent=par, logits=b)
+        assert torch.equal(a, b)
+    assert model.device_error() == 0
+
+
 def test_without_a_prefix_nothing_changes():
     """A cache that had a prefix and lost it gives the bits of one that never had; a cache that serves as prefix too."""
     from speculative_decoding_verify_04_gb300 import spec
