@@ -67,6 +67,64 @@ SPEC_DEV void lp_merge(LpState& a, LpState b, float c) {
     a.u += b.u;
 }
 
+// (value, id) as a number that is larger for what ranks before: by value down (both zeros alike), id up
+SPEC_DEV unsigned long long lp_key(float v, int id) {
+    const uint32_t u = __float_as_uint(v + 0.f);
+    return (unsigned long long)(u >> 31 ? ~u : u | 0x80000000u) << 32 | (uint32_t)~id;
+}
+SPEC_DEV int lp_key_id(unsigned long long k) { return (int)~(uint32_t)k; }
+SPEC_DEV float lp_key_value(unsigned long long k) {
+    const uint32_t u = (uint32_t)(k >> 32);
+    return __uint_as_float(u >> 31 ? u & 0x7FFFFFFFu : ~u);
+}
+// appends `key` of the lanes with `in` to a list, in lane order behind one addition a warp
+SPEC_DEV void lp_list(unsigned long long* list, int* count, unsigned long long key, bool in) {
+    const uint32_t m = __ballot_sync(0xffffffffu, in);
+    if (m == 0) return;
+    const int lane = threadIdx.x & 31;
+    int at = 0;
+    if (lane == 0) at = atomicAdd(count, __popc(m));
+    at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1u));
+    if (in) list[at] = key;
+}
+// Of a segment's elements that equal the least listed value (bits eq of in) only the n of the lowest
+// ids stay: a row of equal logits would else list whole segments (512 rows of 131072 with one token
+// left by a mask and 20 alternatives: 330 us).
+template <typename T>
+SPEC_DEV uint32_t lp_first_equal(uint32_t in, uint32_t eq, int n) {
+    constexpr int VE = 16 / sizeof(T);                      // ids rise over a piece's VE elements, lanes, pieces
+    const int lane = threadIdx.x & 31;
+    int seen = 0;
+#pragma unroll
+    for (int p = 0; p < 8 / VE; ++p) {
+        const uint32_t mine = (eq >> (p * VE)) & ((1u << VE) - 1u);
+        int upto = __popc(mine);                            // of the lanes up to this one
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        int at = seen + upto - __popc(mine);
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+            if ((mine >> e) & 1u)
+                if (at++ >= n) in &= ~(1u << (p * VE + e));
+        seen += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return in;
+}
+// How many of nc listed keys are larger than `key`, counted until there are n.
+SPEC_DEV int lp_place(const unsigned long long* list, int nc, int n, unsigned long long key) {
+    int before = 0, j = 0;
+    for (; j + 8 <= nc && before < n; j += 8) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) before += list[j + q] > key ? 1 : 0;
+    }
+    if (before < n)
+        for (; j < nc; ++j) before += list[j] > key ? 1 : 0;
+    return before;
+}
+
 SPEC_DEV float warp_redux_max(float v) {
     float r;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -156,7 +214,7 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a) {
     pdl_wait();
     pdl_trigger();
     __shared__ LpSmem sm;
-    extern __shared__ float dyn[];
+    extern __shared__ __align__(16) float dyn[];
     cg::cluster_group cl = cg::this_cluster();
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     if (C > 1) cluster_arrive();                            // started: its shared memory may be written
@@ -269,8 +327,7 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a) {
     // of the n-th best of all; the segments not below it are listed (few more than n), and a listed
     // one's place is the number of listed ones before it.
     const int n_sel = min(n, n_seg);
-    float* nv = dyn + n_seg;                                // [n_seg] listed maxima
-    int* ni = reinterpret_cast<int*>(nv + n_seg);           // [n_seg] and their segments
+    unsigned long long* near = reinterpret_cast<unsigned long long*>(dyn + (n_seg + 1) / 2 * 2);   // [n_seg] listed maxima, segments
     if (w == 0) {
         float bv = -INFINITY;
 #pragma unroll 4
@@ -285,29 +342,23 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a) {
     }
     __syncthreads();
     const float low = sm.low;
-    for (int i = threadIdx.x; i < n_seg; i += kLpThreads) {
-        const float v = seg_max[i];
-        if (v >= low) {
-            const int at = atomicAdd(&sm.n_near, 1);
-            nv[at] = v;
-            ni[at] = i;
-        }
+    for (int i0 = 0; i0 < n_seg; i0 += kLpThreads) {
+        const int i = i0 + threadIdx.x;
+        const float v = i < n_seg ? seg_max[i] : 0.f;
+        lp_list(near, &sm.n_near, lp_key(v, i), i < n_seg && v >= low);
     }
     __syncthreads();
     const int n_near = sm.n_near;
     for (int i = threadIdx.x; i < n_near; i += kLpThreads) {
-        const float v = nv[i];
-        const int id = ni[i];
-        int before = 0;
-        for (int k = 0; k < n_near; ++k) before += nv[k] > v || (nv[k] == v && ni[k] < id);
-        if (before < n_sel) sm.sel[before] = id;
+        const unsigned long long key = near[i];
+        const int before = lp_place(near, n_near, n_sel, key);
+        if (before < n_sel) sm.sel[before] = lp_key_id(key);
         // rows of fewer segments than n: every token is listed
-        if (before == n_sel - 1) sm.least = n_sel < n ? -INFINITY : v;
+        if (before == n_sel - 1) sm.least = n_sel < n ? -INFINITY : lp_key_value(key);
     }
     __syncthreads();
     const float least = sm.least;
-    float* cv = nv + 2 * n_seg;                             // [n_sel * 256] values
-    int* ci = reinterpret_cast<int*>(cv + n_sel * kLpSeg);  // and ids of the listed tokens
+    unsigned long long* cand = near + n_seg;                // [n_sel * 256] listed tokens
     for (int k0 = w; k0 < n_sel; k0 += 4 * kLpWarps) {
         float x[4][8];
 #pragma unroll
@@ -317,27 +368,29 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a) {
         for (int q = 0; q < 4; ++q) {
             if (k0 + q * kLpWarps >= n_sel) break;
             const int g = sm.sel[k0 + q * kLpWarps];
+            uint32_t in = 0, eq = 0;                        // bit e: listed, equal to the least
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int id = lp_index<T>(mis, g, e);
-                if (id >= 0 && id < a.V && x[q][e] >= least) {
-                    const int at = atomicAdd(&sm.n_cand, 1);
-                    cv[at] = x[q][e];
-                    ci[at] = id;
-                }
+                if (id >= 0 && id < a.V && x[q][e] >= least) in |= 1u << e;
+                if (x[q][e] == least) eq |= in & (1u << e);
+            }
+            if (__reduce_add_sync(0xffffffffu, __popc(eq)) > n) in = lp_first_equal<T>(in, eq, n);
+            if (in) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if ((in >> e) & 1u) cand[atomicAdd(&sm.n_cand, 1)] = lp_key(x[q][e], lp_index<T>(mis, g, e));
             }
         }
     }
     __syncthreads();
     const int nc = sm.n_cand;
     for (int i = threadIdx.x; i < nc; i += kLpThreads) {
-        const float v = cv[i];
-        const int id = ci[i];
-        int before = 0;
-        for (int j = 0; j < nc; ++j) before += cv[j] > v || (cv[j] == v && ci[j] < id);
+        const unsigned long long key = cand[i];
+        const int before = lp_place(cand, nc, n, key);
         if (before < n) {
-            out_id[before] = id;
-            out_lp[before] = (v - st.m) / a.T - lse;
+            out_id[before] = lp_key_id(key);
+            out_lp[before] = (lp_key_value(key) - st.m) / a.T - lse;
         }
     }
 }
@@ -375,7 +428,7 @@ extern "C" int spec_logprobs(const void* logits, int32_t dtype, int64_t lg_strid
     while (C < kLpMaxCtas && (long long)rows * C < 3 * sms && n_seg / (2 * C) >= 16) C *= 2;
     void (*f)(LogprobArgs) = dtype == SPEC_DTYPE_BF16 ? (n_top ? logprobs_kernel<__nv_bfloat16, 1> : logprobs_kernel<__nv_bfloat16, 0>)
                                                       : (n_top ? logprobs_kernel<float, 1> : logprobs_kernel<float, 0>);
-    const size_t smem = n_top ? ((size_t)3 * n_seg + (size_t)std::min(n_top, n_seg) * kLpSeg * 2) * 4 : 0;
+    const size_t smem = n_top ? (size_t)(n_seg + 1) / 2 * 8 + ((size_t)n_seg + (size_t)std::min(n_top, n_seg) * kLpSeg) * 8 : 0;
     if (smem > 48 * 1024)
         SPEC_TRY(check_cuda(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem), "spec_logprobs attribute"));
     cudaLaunchConfig_t cfg = {};

@@ -105,6 +105,25 @@ def test_ties_go_to_the_lower_id(dtype):
     _check(big, torch.tensor([69999, 0], dtype=torch.int32).cuda(), 32)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [1, 20, 32])
+@pytest.mark.parametrize("V", [9001, 131072])
+def test_long_runs_of_equal_logits(dtype, n, V):
+    """A mask that leaves fewer tokens than asked for, equal rows, zeros of both signs, ties at the last place."""
+    x = torch.full((6, V), -math.inf, dtype=dtype)
+    x[0, V - 3] = 1.0
+    x[1, [5, 600, V - 1]] = torch.tensor([0.5, -2.0, 0.5], dtype=dtype)
+    x[2] = 0.25
+    x[3] = 0.0
+    x[3, 1::2] = -0.0
+    x[4] = -1.0
+    x[4, 300:300 + n - 1] = 2.0                             # one place is left to the equal ones
+    x[5] = -1.0
+    x[5, V // 2:V // 2 + 700] = 3.0
+    t = torch.tensor([V - 3, 600, V - 1, 1, 300, V - 1], dtype=torch.int32)
+    _check(x.cuda(), t.cuda(), n)
+
+
 def test_one_segment_holds_every_best_token():
     x = torch.linspace(0, 1, 5000).repeat(2, 1)
     x[0, 512:768] = torch.linspace(5, 9, 256)
