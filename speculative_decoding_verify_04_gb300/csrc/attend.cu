@@ -11,6 +11,7 @@
 // range of the prompt, a range of the sequence's own slots) leaves a partial
 // state (m, sum p, sum p v) in 32 bits; one warp a (row, head) joins them.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "attend.cuh"
@@ -18,8 +19,14 @@
 namespace spec {
 
 constexpr int kRowThreads = 128;
-constexpr int kRowVectors = 16;       // query vectors a KV head up to which the row kernel takes the prompt
-constexpr int kMinKeys = 256;         // least keys of a range: below it the join costs more than the ranges give
+// Query vectors a KV head up to which the row kernel takes the prompt: 16, and 64 where (blocks of 16)
+// x KV heads x slots are few.  Measured per call (us, row kernel / tile kernel; 8 KV heads, 8 bits):
+// 16 vectors over 32768 slots 35 / 56; 32 over 32768 56 / 57 (bf16 73 / 52); 32 over 4096 19 / 25;
+// 64 over 4096 29 / 26; 64 over 512 17 / 25; 128 over 512 19 / 24.
+constexpr int kRowVectors = 16, kRowVectorsShort = 64, kRowKeysShort = 65536;
+// least keys of a range: one sequence of 256 slots takes 12.8 us a call at 256, 10.8 at 128, 14.5 at 512; 16 of
+// 10 rows over 671 slots 33 at 256, 35 at 128, 37 at 512
+constexpr int kMinKeys = 256;
 
 SPEC_DEV float f16_round(float x) {
     float r;
@@ -60,80 +67,122 @@ SPEC_DEV void mma16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
 // of itself, below 2^-14 by 2^-25 of the row's largest.  f32 queries are split
 // into hi + lo (QF32).
 //
-// Bound by instructions (about 250 a 16-key tile and warp at hd 128) and by the
-// latency of the few tiles a warp has.
-template <int HD>
-struct RawTile {                                  // 16 keys of an 8-bit cache as they lie in memory
-    uint4 k[2][HD / 64];
-    uint32_t v[4][HD / 32];
-    uint32_t ke, ve;
+// Bound by latency: 64 sequences of 512 slots on average (hd 128, 8 KV heads, 8 bits, 4
+// vectors) take 28 us, 2.4 TB/s, of which half a CTA's life is its start (lengths, pages,
+// queries, first tiles) and end (the warps' states joined); a warp has five tiles of 2500
+// cycles, 600 instructions a tile with the starts shared out, and the issue slots are 34 %
+// used.  One long cache does better: 8 vectors over 32768 slots of 32 KV heads take 72 us a
+// call in 8 bits (3.7 TB/s) and 89 in bf16 (6.0 TB/s, 89 % of the measured copy rate).
+//
+// 8-bit caches: a lane's pieces of the next two tiles are copied ahead into shared memory, in slots of
+// the lane's own: no other lane reads them, so a lane waits for its own copies only (8 vectors over
+// 32768 keys and 32 KV heads: 82 us; one tile ahead in registers: 95).  bf16 tiles go straight to
+// registers: the tile as it is loaded is its fragments (94 us; through shared memory: 127).
+SPEC_DEV int few_v_key(int cq, int r) { return 2 * cq + (r & 1) + 8 * (r >> 1); }
+
+template <int HD, bool FEW>
+struct TileSlot {
+    static constexpr int kStages = 2;                  // tiles ahead
+    static constexpr int kK = HD / 32;                 // 16-byte pieces of K a lane
+    static constexpr int kVBytes = HD / 8;             // bytes of each of its four V rows
+    static constexpr int kWords = FEW ? 4 : 2;         // words of exponents a lane
+    static constexpr int kVAt = 32 * 16 * kK, kWordsAt = kVAt + 32 * kVBytes * 4;
+    static constexpr int kBytes = kWordsAt + 32 * 4 * kWords;
+    static constexpr int kRing = 4 * kStages * kBytes;
 };
 
-template <int HD>
-SPEC_DEV void load_raw(const AttendArgs& a, const CacheView& cv, int seq, int g, int kt, int k_end, int gq, int cq, RawTile<HD>& t) {
-    // tiles start at multiples of 16 and pages hold a multiple of 16 slots: no tile crosses a page
-    long long row = kv_row_in_layer(cv.pages, a.Hkv, seq, g, kt);
+template <int BYTES>
+SPEC_DEV void copy_ahead(uint32_t dst, const void* src) {
+    if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+SPEC_DEV void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+SPEC_DEV void copies_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
+// first row of the 16-key tile at kt (0 past the range's end): tiles start at multiples of 16 and pages
+// hold a multiple of 16 slots, so no tile crosses a page
+SPEC_DEV long long tile_row(const AttendArgs& a, const CacheView& cv, int seq, int g, int kt, int k_end) {
+    return kt < k_end ? kv_row_in_layer(cv.pages, a.Hkv, seq, g, kt) : 0;
+}
+
+// this lane's pieces of the tile at kt, whose first row is `row`, into its slots
+template <int HD, bool FEW>
+SPEC_DEV void copy_tile(const AttendArgs& a, const CacheView& cv, long long row, int kt, int k_end, uint32_t slot) {
+    using S = TileSlot<HD, FEW>;
+    const int lane = threadIdx.x & 31, gq = lane >> 2, cq = lane & 3, last = k_end - 1 - kt;
     if (row < 0) { dev_error(a.err, SPEC_DEVERR_CAPACITY); row = 0; }
-    const uint8_t* K = static_cast<const uint8_t*>(cv.k) + row * HD;
-    const uint8_t* V = static_cast<const uint8_t*>(cv.v) + row * HD;
-    const int last = k_end - 1 - kt;
+    const char* K = static_cast<const char*>(cv.k) + row * HD;
+    const char* V = static_cast<const char*>(cv.v) + row * HD;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        const int key = min(4 * (gq >> 1) + 2 * h + (gq & 1), last);
+        const int key = min(FEW ? gq + 8 * h : 4 * (gq >> 1) + 2 * h + (gq & 1), last);
 #pragma unroll
-        for (int p = 0; p < HD / 64; ++p) t.k[h][p] = __ldg(reinterpret_cast<const uint4*>(K + key * HD) + 4 * p + cq);
+        for (int p = 0; p < S::kK / 2; ++p)
+            copy_ahead<16>(slot + 512 * (h * (S::kK / 2) + p) + 16 * lane, K + key * HD + 16 * (4 * p + cq));
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        const int key = min(4 * cq + r, last);
-        if (HD == 128) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(V + key * HD) + gq);
-            t.v[r][0] = w.x; t.v[r][1] = w.y; t.v[r][HD / 32 - 2] = w.z; t.v[r][HD / 32 - 1] = w.w;
-        } else {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(V + key * HD) + gq);
-            t.v[r][0] = w.x; t.v[r][1] = w.y;
-        }
+        const int key = min(FEW ? few_v_key(cq, r) : 4 * cq + r, last);
+        copy_ahead<S::kVBytes>(slot + S::kVAt + S::kVBytes * (32 * r + lane), V + key * HD + S::kVBytes * gq);
     }
     // the pages hold a multiple of 16 slots: four exponents are one aligned word
-    t.ke = __ldg(reinterpret_cast<const uint32_t*>(cv.ke + row) + cq);
-    t.ve = __ldg(reinterpret_cast<const uint32_t*>(cv.ve + row) + cq);
+#pragma unroll
+    for (int w = 0; w < S::kWords; ++w) {
+        const uint8_t* e = (w >= S::kWords / 2 ? cv.ve : cv.ke) + row;
+        copy_ahead<4>(slot + S::kWordsAt + 4 * (32 * w + lane), e + 4 * (FEW ? 2 * (w & 1) + (gq >> 2) : cq));
+    }
 }
 
 // QB (16 or 8) query vectors: rows to shared memory in 32 bits, then fragments in lane order
 // (dims as the K pieces of the cache's kind order them), as the A operand of 16 rows or the B
 // operand of 8 columns.  sS: the factor of a row's raw scores.
+template <int HD, int QB>
+struct QueryPieces { float x[(QB * HD / 8 + kRowThreads - 1) / kRowThreads][8]; };
+
+// this thread's pieces of the query rows from memory
 template <int HD, bool QF32, int QB>
-SPEC_DEV void load_queries(const AttendArgs& a, bool q8, int g, int G, int list_row0, int q0, int nq, uint4* sQ, float* sS,
-                           float* rows) {
-    constexpr int KS = HD / 16, LD = HD + 4;
-    const int t = threadIdx.x;
-    for (int i = t; i < QB * (HD / 8); i += kRowThreads) {
-        const int r = i / (HD / 8), ch = i % (HD / 8), qg = q0 + r;
-        float x[8];
+SPEC_DEV void fetch_queries(const AttendArgs& a, int g, int G, int list_row0, int q0, int nq, QueryPieces<HD, QB>& qp) {
+    constexpr int N = sizeof(qp.x) / sizeof(qp.x[0]);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int i = threadIdx.x + n * kRowThreads, r = i / (HD / 8), ch = i % (HD / 8), qg = q0 + r;
+        float (&x)[8] = qp.x[n];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = 0.f;
-        if (r < nq) {
-            const long long off = (list_row0 + qg / G) * a.q_stride + (g * G + qg % G) * HD + ch * 8;
-            if (QF32) {
-                const float* p = static_cast<const float*>(a.q) + off;
-                const float4 u = *reinterpret_cast<const float4*>(p), w = *reinterpret_cast<const float4*>(p + 4);
-                x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w; x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
-            } else {
-                const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.q) + off;
-                if (a.q_vec) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(p);
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        if (r >= nq) continue;
+        const long long off = (list_row0 + qg / G) * a.q_stride + (g * G + qg % G) * HD + ch * 8;
+        if (QF32) {
+            const float* p = static_cast<const float*>(a.q) + off;
+            const float4 u = *reinterpret_cast<const float4*>(p), w = *reinterpret_cast<const float4*>(p + 4);
+            x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w; x[4] = w.x; x[5] = w.y; x[6] = w.z; x[7] = w.w;
+        } else {
+            const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.q) + off;
+            if (a.q_vec) {
+                const uint4 w = *reinterpret_cast<const uint4*>(p);
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x[2 * e] = __uint_as_float(u[e] << 16);
-                        x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = __bfloat162float(p[e]);
+                for (int e = 0; e < 4; ++e) {
+                    x[2 * e] = __uint_as_float(u[e] << 16);
+                    x[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
                 }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = __bfloat162float(p[e]);
             }
         }
+    }
+}
+
+template <int HD, bool QF32, int QB>
+SPEC_DEV void load_queries(const AttendArgs& a, bool q8, const QueryPieces<HD, QB>& qp, uint4* sQ, float* sS, float* rows) {
+    constexpr int KS = HD / 16, LD = HD + 4, N = sizeof(qp.x) / sizeof(qp.x[0]);
+    const int t = threadIdx.x;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        const int i = t + n * kRowThreads, r = i / (HD / 8), ch = i % (HD / 8);
+        if (i >= QB * (HD / 8)) break;                      // whole warps
+        const float (&x)[8] = qp.x[n];
         // the row's largest magnitude, over the HD / 8 lanes that hold it
         float m = finite_amax(x);
 #pragma unroll
@@ -241,15 +290,32 @@ SPEC_DEV void softmax_tile(float (&x)[2][4], float (&y)[2][4], float (&m)[2], fl
 // Keys below n_ctx are seen by every row; key n_ctx + x by the rows whose mask has bit x.
 template <int HD, bool Q8, bool QF32>
 SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, int g, int k_begin, int k_end, int n_ctx,
-                           unsigned long long mk0, unsigned long long mk1, const uint4* sQ, const float* sS,
-                           RowState<HD>& st) {
+                           const QueryPieces<HD, 16>& qp, const unsigned long long* sMask, uint4* sQ, float* sS,
+                           float* rows, char* ring, RowState<HD>& st) {
     constexpr int KS = HD / 16, VD = HD / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, cq = lane & 3;
-    const float c0 = sS[gq], c1 = sS[gq + 8];
-    RawTile<HD> nx;
+    using S = TileSlot<HD, false>;
+    const uint32_t slot0 = smem_u32(ring) + warp * S::kStages * S::kBytes;
+    const char* slots = ring + warp * S::kStages * S::kBytes;
     int kt = k_begin + 16 * warp;
-    if (Q8 && kt < k_end) load_raw<HD>(a, cv, seq, g, kt, k_end, gq, cq, nx);
-    for (; kt < k_end; kt += 64) {
+    // the first tiles' copies go out before the queries are taken; rows are looked up a tile before their use
+    long long row = tile_row(a, cv, seq, g, kt, k_end), row_nx = tile_row(a, cv, seq, g, kt + 64, k_end);
+    if (Q8) {
+        const long long row_2 = tile_row(a, cv, seq, g, kt + 64 * S::kStages, k_end);
+        if (kt < k_end) copy_tile<HD, false>(a, cv, row, kt, k_end, slot0);
+        copies_commit();
+        if (kt + 64 < k_end) copy_tile<HD, false>(a, cv, row_nx, kt + 64, k_end, slot0 + S::kBytes);
+        copies_commit();
+        row_nx = row_2;
+    }
+    load_queries<HD, QF32, 16>(a, Q8, qp, sQ, sS, rows);
+    __syncthreads();
+    const float c0 = sS[gq], c1 = sS[gq + 8];
+    const unsigned long long mk0 = sMask[gq], mk1 = sMask[gq + 8];
+    for (int stage = 0; kt < k_end; kt += 64, stage = stage + 1 < S::kStages ? stage + 1 : 0) {
+        const char* slot = slots + stage * S::kBytes;
+        auto k_piece = [&](int h, int p) { return *reinterpret_cast<const uint4*>(slot + 512 * (h * (S::kK / 2) + p) + 16 * lane); };
+        if (Q8) copies_wait<S::kStages - 1>();
         uint32_t kb[2][KS][2], vb[4][KS];
         uint32_t ke = 0, ve = 0;
         if (Q8) {
@@ -257,7 +323,8 @@ SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, in
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int p = 0; p < HD / 64; ++p) {
-                    const uint32_t w[4] = {nx.k[h][p].x, nx.k[h][p].y, nx.k[h][p].z, nx.k[h][p].w};
+                    const uint4 u = k_piece(h, p);
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
                         kb[h][4 * p + s][0] = e4m3x2_f16(w[s]);
@@ -265,17 +332,26 @@ SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, in
                     }
                 }
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < 4; ++r) {
+                if (S::kVBytes == 16) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(slot + S::kVAt + 16 * (32 * r + lane));
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int i = 0; i < HD / 32; ++i) {
-                    vb[r][2 * i] = e4m3x2_f16(nx.v[r][i]);
-                    vb[r][2 * i + 1] = e4m3x2_f16(nx.v[r][i] >> 16);
+                    for (int i = 0; i < HD / 32; ++i) { vb[r][2 * i] = e4m3x2_f16(u[i]); vb[r][2 * i + 1] = e4m3x2_f16(u[i] >> 16); }
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2*>(slot + S::kVAt + 8 * (32 * r + lane));
+                    vb[r][0] = e4m3x2_f16(w.x); vb[r][1] = e4m3x2_f16(w.x >> 16);
+                    vb[r][2] = e4m3x2_f16(w.y); vb[r][3] = e4m3x2_f16(w.y >> 16);
                 }
-            ke = nx.ke;
-            ve = nx.ve;
-            if (kt + 64 < k_end) load_raw<HD>(a, cv, seq, g, kt + 64, k_end, gq, cq, nx);
+            }
+            ke = *reinterpret_cast<const uint32_t*>(slot + S::kWordsAt + 4 * lane);
+            ve = *reinterpret_cast<const uint32_t*>(slot + S::kWordsAt + 4 * (32 + lane));
+            // the slot is read: the tile after the next one into it
+            __syncwarp();
+            if (kt + 64 * S::kStages < k_end)
+                copy_tile<HD, false>(a, cv, row_nx, kt + 64 * S::kStages, k_end, slot0 + stage * S::kBytes);
+            copies_commit();
         } else {
-            long long row = kv_row_in_layer(cv.pages, a.Hkv, seq, g, kt);
             if (row < 0) { dev_error(a.err, SPEC_DEVERR_CAPACITY); row = 0; }
             const __nv_bfloat16* K = static_cast<const __nv_bfloat16*>(cv.k) + row * HD;
             const __nv_bfloat16* V = static_cast<const __nv_bfloat16*>(cv.v) + row * HD;
@@ -299,7 +375,9 @@ SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, in
                     vb[r][4 * p] = w.x; vb[r][4 * p + 1] = w.y; vb[r][4 * p + 2] = w.z; vb[r][4 * p + 3] = w.w;
                 }
             }
+            row = row_nx;
         }
+        row_nx = tile_row(a, cv, seq, g, kt + 64 * (Q8 ? S::kStages + 1 : 2), k_end);
         if (kt + 16 > k_end) {
             // values of keys past the range: their probability is zero, and zero times what the slot holds must be zero
 #pragma unroll
@@ -415,12 +493,6 @@ SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, in
 //     and + 1 (row g + 8), so lane (g, c) reads hd / 8 consecutive dims of V rows 2c, 2c + 1,
 //     2c + 8, 2c + 9; P goes from the scores' layout to the operand's by a transposing move.
 template <int HD>
-struct RawFew {
-    uint4 k[2][HD / 64];
-    uint32_t v[4][HD / 32];
-    int ke[2], ve[2];
-};
-template <int HD>
 struct FewState { float o[HD / 16][4], m[2], l[2], R[2]; };
 
 SPEC_DEV uint32_t transpose8(uint32_t x) {
@@ -428,46 +500,34 @@ SPEC_DEV uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
-SPEC_DEV int few_v_key(int cq, int r) { return 2 * cq + (r & 1) + 8 * (r >> 1); }
-
-template <int HD>
-SPEC_DEV void load_raw_few(const AttendArgs& a, const CacheView& cv, int seq, int g, int kt, int k_end, int gq, int cq, RawFew<HD>& t) {
-    long long row = kv_row_in_layer(cv.pages, a.Hkv, seq, g, kt);
-    if (row < 0) { dev_error(a.err, SPEC_DEVERR_CAPACITY); row = 0; }
-    const uint8_t* K = static_cast<const uint8_t*>(cv.k) + row * HD;
-    const uint8_t* V = static_cast<const uint8_t*>(cv.v) + row * HD;
-    const int last = k_end - 1 - kt;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int key = min(gq + 8 * h, last);
-#pragma unroll
-        for (int p = 0; p < HD / 64; ++p) t.k[h][p] = __ldg(reinterpret_cast<const uint4*>(K + key * HD) + 4 * p + cq);
-        t.ke[h] = __ldg(cv.ke + row + key);
-        t.ve[h] = __ldg(cv.ve + row + key);
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const int key = min(few_v_key(cq, r), last);
-        if (HD == 128) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4*>(V + key * HD) + gq);
-            t.v[r][0] = w.x; t.v[r][1] = w.y; t.v[r][HD / 32 - 2] = w.z; t.v[r][HD / 32 - 1] = w.w;
-        } else {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>(V + key * HD) + gq);
-            t.v[r][0] = w.x; t.v[r][1] = w.y;
-        }
-    }
-}
-
 template <int HD, bool Q8, bool QF32>
 SPEC_DEV void attend_range_few(const AttendArgs& a, const CacheView& cv, int seq, int g, int k_begin, int k_end, int n_ctx,
-                               const unsigned long long* sMask, const uint2* sQ, const float* sS, FewState<HD>& st) {
+                               const QueryPieces<HD, 8>& qp, const unsigned long long* sMask, uint4* sQ4, float* sS,
+                               float* rows, char* ring, FewState<HD>& st) {
     constexpr int KS = HD / 16, MT = HD / 16;
+    const uint2* sQ = reinterpret_cast<const uint2*>(sQ4);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, cq = lane & 3;
-    const float cf[2] = {sS[2 * cq], sS[2 * cq + 1]};
-    RawFew<HD> nx;
+    using S = TileSlot<HD, true>;
+    const uint32_t slot0 = smem_u32(ring) + warp * S::kStages * S::kBytes;
+    const char* slots = ring + warp * S::kStages * S::kBytes;
     int kt = k_begin + 16 * warp;
-    if (Q8 && kt < k_end) load_raw_few<HD>(a, cv, seq, g, kt, k_end, gq, cq, nx);
-    for (; kt < k_end; kt += 64) {
+    // the first tiles' copies go out before the queries are taken; rows are looked up a tile before their use
+    long long row = tile_row(a, cv, seq, g, kt, k_end), row_nx = tile_row(a, cv, seq, g, kt + 64, k_end);
+    if (Q8) {
+        const long long row_2 = tile_row(a, cv, seq, g, kt + 64 * S::kStages, k_end);
+        if (kt < k_end) copy_tile<HD, true>(a, cv, row, kt, k_end, slot0);
+        copies_commit();
+        if (kt + 64 < k_end) copy_tile<HD, true>(a, cv, row_nx, kt + 64, k_end, slot0 + S::kBytes);
+        copies_commit();
+        row_nx = row_2;
+    }
+    load_queries<HD, QF32, 8>(a, Q8, qp, sQ4, sS, rows);
+    __syncthreads();
+    const float cf[2] = {sS[2 * cq], sS[2 * cq + 1]};
+    for (int stage = 0; kt < k_end; kt += 64, stage = stage + 1 < S::kStages ? stage + 1 : 0) {
+        const char* slot = slots + stage * S::kBytes;
+        auto k_piece = [&](int h, int p) { return *reinterpret_cast<const uint4*>(slot + 512 * (h * (S::kK / 2) + p) + 16 * lane); };
+        if (Q8) copies_wait<S::kStages - 1>();
         uint32_t ka[KS][4], vb[4][MT];
         float kf[2] = {1.f, 1.f}, vf[2] = {0.f, 0.f};
         if (Q8) {
@@ -475,26 +535,39 @@ SPEC_DEV void attend_range_few(const AttendArgs& a, const CacheView& cv, int seq
             for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int p = 0; p < HD / 64; ++p) {
-                    const uint32_t w[4] = {nx.k[h][p].x, nx.k[h][p].y, nx.k[h][p].z, nx.k[h][p].w};
+                    const uint4 u = k_piece(h, p);
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
                         ka[4 * p + s][h] = e4m3x2_f16(w[s]);
                         ka[4 * p + s][2 + h] = e4m3x2_f16(w[s] >> 16);
                     }
                 }
-                kf[h] = kv8_scale(nx.ke[h]);
-                vf[h] = (float)(nx.ve[h] - 127);
+                // the words of keys g and g + 8
+                const uint32_t ew = *reinterpret_cast<const uint32_t*>(slot + S::kWordsAt + 4 * (32 * h + lane));
+                const uint32_t vw = *reinterpret_cast<const uint32_t*>(slot + S::kWordsAt + 4 * (32 * (2 + h) + lane));
+                kf[h] = kv8_scale((ew >> (8 * (gq & 3))) & 0xFF);
+                vf[h] = (float)((int)((vw >> (8 * (gq & 3))) & 0xFF) - 127);
             }
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
+            for (int r = 0; r < 4; ++r) {
+                if (S::kVBytes == 16) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(slot + S::kVAt + 16 * (32 * r + lane));
+                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int i = 0; i < HD / 32; ++i) {
-                    vb[r][2 * i] = e4m3x2_f16(nx.v[r][i]);
-                    vb[r][2 * i + 1] = e4m3x2_f16(nx.v[r][i] >> 16);
+                    for (int i = 0; i < HD / 32; ++i) { vb[r][2 * i] = e4m3x2_f16(u[i]); vb[r][2 * i + 1] = e4m3x2_f16(u[i] >> 16); }
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2*>(slot + S::kVAt + 8 * (32 * r + lane));
+                    vb[r][0] = e4m3x2_f16(w.x); vb[r][1] = e4m3x2_f16(w.x >> 16);
+                    vb[r][2] = e4m3x2_f16(w.y); vb[r][3] = e4m3x2_f16(w.y >> 16);
                 }
-            if (kt + 64 < k_end) load_raw_few<HD>(a, cv, seq, g, kt + 64, k_end, gq, cq, nx);
+            }
+            // the slot is read: the tile after the next one into it
+            __syncwarp();
+            if (kt + 64 * S::kStages < k_end)
+                copy_tile<HD, true>(a, cv, row_nx, kt + 64 * S::kStages, k_end, slot0 + stage * S::kBytes);
+            copies_commit();
         } else {
-            long long row = kv_row_in_layer(cv.pages, a.Hkv, seq, g, kt);
             if (row < 0) { dev_error(a.err, SPEC_DEVERR_CAPACITY); row = 0; }
             const __nv_bfloat16* K = static_cast<const __nv_bfloat16*>(cv.k) + row * HD;
             const __nv_bfloat16* V = static_cast<const __nv_bfloat16*>(cv.v) + row * HD;
@@ -518,7 +591,9 @@ SPEC_DEV void attend_range_few(const AttendArgs& a, const CacheView& cv, int seq
                     vb[r][4 * p] = w.x; vb[r][4 * p + 1] = w.y; vb[r][4 * p + 2] = w.z; vb[r][4 * p + 3] = w.w;
                 }
             }
+            row = row_nx;
         }
+        row_nx = tile_row(a, cv, seq, g, kt + 64 * (Q8 ? S::kStages + 1 : 2), k_end);
         if (kt + 16 > k_end) {
             // values of keys past the range: their probability is zero, and zero times what the slot holds must be zero
 #pragma unroll
@@ -645,8 +720,10 @@ SPEC_DEV unsigned long long row_mask(const AttendSpan& s, int b, int j) {
     return mk;
 }
 
+constexpr int row_ctas_per_sm(int hd, int qb) { return hd == 128 ? 3 : (qb == 8 ? 5 : 4); }
+
 template <int HD, bool QF32, int QB>
-__global__ void __launch_bounds__(kRowThreads, QB == 8 ? (HD == 128 ? 4 : 5) : (HD == 128 ? 3 : 4))
+__global__ void __launch_bounds__(kRowThreads, row_ctas_per_sm(HD, QB))
 attend_rows_kernel(const __grid_constant__ AttendArgs a) {
     pdl_wait();
     pdl_trigger();
@@ -654,9 +731,11 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
     constexpr int LS = HD + 4;                                              // a state row: O, m, l, R
     extern __shared__ float smf[];
     uint4* sQ = reinterpret_cast<uint4*>(smf);                              // [QF32 ? 2 : 1][KS][32] (8 queries: uint2)
-    float* sState = smf + (QF32 ? 2 : 1) * KS * 32 * (QB / 4);              // [4 warps][QB][LS]; the query rows before
-    float* sS = sState + 4 * QB * LS;                                       // [QB]
-    unsigned long long* sMask = reinterpret_cast<unsigned long long*>(sS + QB);   // [QB]
+    float* sRows = smf + (QF32 ? 2 : 1) * KS * 32 * (QB / 4);               // [QB][LS] the queries before
+    unsigned long long* sMask = reinterpret_cast<unsigned long long*>(sRows + QB * LS);   // [QB]
+    float* sS = reinterpret_cast<float*>(sMask + QB);                       // [QB]
+    float* sState = sS + QB;                                                // [4 warps][QB][LS]
+    char* ring = reinterpret_cast<char*>(sState);                           // the tiles, before the states
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, gq = lane >> 2, cq = lane & 3;
     const int G = a.H / a.Hkv;
     // the prompt's blocks first (the longer ones), then the sequences' own
@@ -688,6 +767,8 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
     }
     const int q0 = qb * QB, nq = min(QB, rows * G - q0);
     if (nq <= 0) return;
+    QueryPieces<HD, QB> qp;                                                 // on their way while the lengths are read
+    fetch_queries<HD, QF32, QB>(a, g, G, list_row0, q0, nq, qp);
     int chunk = max(kMinKeys, (n_keys + n_splits - 1) / n_splits);
     chunk = (chunk + 63) / 64 * 64;
     const int k_begin = min(n_keys, split * chunk), k_end = min(n_keys, k_begin + chunk);
@@ -699,18 +780,16 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
         if (t < nq) *reinterpret_cast<float2*>(a.part_ml + 2 * vec_of(t)) = make_float2(-INFINITY, 0.f);
         return;
     }
-    load_queries<HD, QF32, QB>(a, cv.q8, g, G, list_row0, q0, nq, sQ, sS, sState);
     if (t < QB) sMask[t] = !is_pre && t < nq ? row_mask(a.span, b, (q0 + t) / G) : 0ull;
-    __syncthreads();
-    if (QB == 8) {
+    if constexpr (QB == 8) {
         FewState<HD> rs;
 #pragma unroll
         for (int j = 0; j < 2; ++j) { rs.m[j] = rs.R[j] = -INFINITY; rs.l[j] = 0.f; }
 #pragma unroll
         for (int mt = 0; mt < HD / 16; ++mt) rs.o[mt][0] = rs.o[mt][1] = rs.o[mt][2] = rs.o[mt][3] = 0.f;
-        const uint2* s8 = reinterpret_cast<const uint2*>(sQ);
-        if (cv.q8) attend_range_few<HD, true, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, sMask, s8, sS, rs);
-        else attend_range_few<HD, false, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, sMask, s8, sS, rs);
+        if (cv.q8) attend_range_few<HD, true, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, qp, sMask, sQ, sS, sRows, ring, rs);
+        else attend_range_few<HD, false, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, qp, sMask, sQ, sS, sRows, ring, rs);
+        __syncthreads();                     // the states lie where the tiles were
         // warp states -> shared: queries 2c and 2c + 1, dims VD * g ..
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -728,8 +807,9 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
         for (int rr = 0; rr < 2; ++rr) { rs.m[rr] = rs.R[rr] = -INFINITY; rs.l[rr] = 0.f; }
 #pragma unroll
         for (int nt = 0; nt < VD; ++nt) rs.o[nt][0] = rs.o[nt][1] = rs.o[nt][2] = rs.o[nt][3] = 0.f;
-        if (cv.q8) attend_range<HD, true, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, sMask[gq], sMask[gq + 8], sQ, sS, rs);
-        else attend_range<HD, false, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, sMask[gq], sMask[gq + 8], sQ, sS, rs);
+        if (cv.q8) attend_range<HD, true, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, qp, sMask, sQ, sS, sRows, ring, rs);
+        else attend_range<HD, false, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, qp, sMask, sQ, sS, sRows, ring, rs);
+        __syncthreads();
         // warp states -> shared: rows g and g + 8, dims VD * 2c + nt and VD * (2c + 1) + nt
 #pragma unroll
         for (int rr = 0; rr < 2; ++rr) {
@@ -915,8 +995,16 @@ int make_span(AttendSpan* s, int batch, const int* n_rows, int extra, const int*
     return SPEC_OK;
 }
 
-static size_t rows_smem(int hd, bool qf32, int qb) {
-    return (qf32 ? 2 : 1) * (hd / 16) * 32 * qb + 4 * qb * (hd + 4) * sizeof(float) + qb * sizeof(float) + qb * 8;
+template <int HD, bool FEW>
+static size_t ring_bytes(bool q8) {
+    return q8 ? TileSlot<HD, FEW>::kRing : 0;
+}
+// shared memory of the row kernel; q8: one of its caches is in 8 bits
+static size_t rows_smem(int hd, bool qf32, int qb, bool q8) {
+    const size_t ring = hd == 128 ? (qb == 8 ? ring_bytes<128, true>(q8) : ring_bytes<128, false>(q8))
+                                  : (qb == 8 ? ring_bytes<64, true>(q8) : ring_bytes<64, false>(q8));
+    const size_t row = (size_t)(hd + 4) * sizeof(float);
+    return (qf32 ? 2 : 1) * (hd / 16) * 32 * qb + qb * (row + 12) + std::max(ring, 4 * qb * row);
 }
 
 // Query vectors whose partial states fit.  The row kernel's two parts keep to (ranges) x
@@ -949,18 +1037,23 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     a.err = m->err;
     const int TH = span.T * H;
     const size_t fit = m->attend_part_floats / (hd + 2) / TH;      // ranges the workspace holds
-    // key ranges: about six CTAs an SM (three are resident) where the keys allow it, by each part's share of them
-    const bool tile = pre && span.T * G > kRowVectors && attend_tile_ok(pre);
+    const long long pre_work = pre ? (long long)((span.T * G + 15) / 16) * Hkv * pre->max_ctx : 0;
+    const bool rows_do = span.T * G <= kRowVectors || (span.T * G <= kRowVectorsShort && pre_work <= kRowKeysShort);
+    const bool tile = pre && !rows_do && attend_tile_ok(pre);
     // blocks of 8 query vectors where one holds all of a part's, else of 16
     const int QB = span.max_rows * G <= 8 && (!pre || tile || span.T * G <= 8) ? 8 : 16;
     a.own_qb = (span.max_rows * G + QB - 1) / QB;
     a.pre_qb = pre && !tile ? (span.T * G + QB - 1) / QB : 0;
     const long long own_blocks = (long long)span.batch * Hkv * a.own_qb, pre_blocks = (long long)Hkv * a.pre_qb;
     const long long keys = own_blocks * kv->max_ctx + pre_blocks * (pre ? pre->max_ctx : 0);
-    const long long per = std::max<long long>(kMinKeys, keys / (6 * m->num_sms) + 1);
+    // ranges: as many CTAs as run at a time, by each part's share of the keys; more only add starts and
+    // partial states (8 vectors, 32 KV heads, 32768 slots: one wave 72 us in 8 bits and 89 in bf16, two 86
+    // and 117)
+    const long long wave = (long long)row_ctas_per_sm(hd, QB) * m->num_sms;
+    const long long per = std::max<long long>(kMinKeys, keys / wave + 1), round = per > kMinKeys ? per / 2 : per - 1;
     auto splits = [&](long long blocks, long long ctx) {
         if (blocks == 0) return 0;
-        return (int)std::max<long long>(1, std::min<long long>({(ctx + per - 1) / per, 64, (16 * 512) / (16 * blocks) + 1}));
+        return (int)std::max<long long>(1, std::min<long long>({(ctx + round) / per, 64, (16 * 512) / (16 * blocks) + 1}));
     };
     a.own_splits = splits(own_blocks, kv->max_ctx);
     a.pre_splits = splits(pre_blocks, pre ? pre->max_ctx : 0);
@@ -976,11 +1069,19 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     a.part_o = m->attend_part;
     a.part_ml = m->attend_part + (size_t)ranges * TH * hd;
     const dim3 grid((unsigned)(a.pre_splits * pre_blocks + a.own_splits * own_blocks));
-    const size_t smem = rows_smem(hd, q_f32, QB);
+    const size_t smem = rows_smem(hd, q_f32, QB, a.own.q8 || (a.pre_qb > 0 && a.pre.q8));
     void (*const kernels[8])(AttendArgs) = {
         attend_rows_kernel<64, false, 8>, attend_rows_kernel<64, false, 16>, attend_rows_kernel<64, true, 8>, attend_rows_kernel<64, true, 16>,
         attend_rows_kernel<128, false, 8>, attend_rows_kernel<128, false, 16>, attend_rows_kernel<128, true, 8>, attend_rows_kernel<128, true, 16>};
-    void (*f)(AttendArgs) = kernels[(hd == 128 ? 4 : 0) + (q_f32 ? 2 : 0) + (QB == 16 ? 1 : 0)];
+    const int which = (hd == 128 ? 4 : 0) + (q_f32 ? 2 : 0) + (QB == 16 ? 1 : 0);
+    void (*f)(AttendArgs) = kernels[which];
+    static std::atomic<unsigned long long> set[8] = {};        // devices where a kernel may take more than 48 KB
+    const unsigned long long bit = 1ull << (m->device & 63);
+    if (smem > 48 * 1024 && !(set[which].load() & bit)) {
+        SPEC_TRY(check_cuda(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rows_smem(hd, true, QB, true)),
+                            "attention rows attribute"));
+        set[which].fetch_or(bit);
+    }
     const int slot = prof_start(m, st);
     if (tile) SPEC_TRY(launch_attend_tile(pre, a, st));
     // behind the tile kernel without early launch: row CTAs that wait on its SMs cost more than their

@@ -115,6 +115,22 @@ def test_prompt_lengths(prompt, q8):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("prompt", [0, 1, 15, 63, 64, 65, 127, 128, 129, 255, 257, 700])
+@pytest.mark.parametrize("q8,dim,page", [(False, 64, None), (True, 128, None), (False, 128, 64), (True, 64, 128)])
+def test_prompt_lengths_under_many_vectors(prompt, q8, dim, page):
+    """More than 64 query vectors a KV head; what lies behind the lengths is NaN or an infinity."""
+    c = Case(9, 16, 2, dim, [3, 70, 0], [6, 5, 1], prompt=prompt, q8=q8, prompt_q8=q8, page=page, dirty=True)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("T,prompt", [(4, 300), (5, 300), (8, 1000), (15, 1000), (16, 1000), (17, 300)])
+@pytest.mark.parametrize("q8,prompt_q8", [(False, True), (True, False), (True, True)])
+def test_prompts_under_up_to_68_vectors(T, prompt, q8, prompt_q8):
+    """One to five blocks of 16 query vectors over a short prompt, and the first size past them."""
+    c = Case(10, 8, 2, 128, [20, 300], [T - 1, 1], prompt=prompt, q8=q8, prompt_q8=prompt_q8)
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("n", [0, 1, 15, 16, 17, 63, 64, 65, 255, 256, 700])
 @pytest.mark.parametrize("q8", [False, True])
 def test_own_lengths_without_a_prompt(n, q8):
