@@ -725,8 +725,13 @@ constexpr int row_ctas_per_sm(int hd, int qb) { return hd == 128 ? 3 : (qb == 8 
 template <int HD, bool QF32, int QB>
 __global__ void __launch_bounds__(kRowThreads, row_ctas_per_sm(HD, QB))
 attend_rows_kernel(const __grid_constant__ AttendArgs a) {
-    pdl_wait();
+    // Behind the tile kernel this one works beside it: neither reads what the other writes, and the tile
+    // kernel lets it start after its own wait, so everything before is done.  Its last CTA waits for the
+    // tile kernel, so the join, which waits for this kernel, has both (64 samples over 32768 tokens 238 ->
+    // 229 us a call, 8 chains over 4096 37 -> 33).
+    if (a.tile_ctas == 0) pdl_wait();
     pdl_trigger();
+    if (a.tile_ctas > 0 && blockIdx.x == gridDim.x - 1) { pdl_wait(); return; }
     constexpr int KS = HD / 16, VD = HD / 8;
     constexpr int LS = HD + 4;                                              // a state row: O, m, l, R
     extern __shared__ float smf[];
@@ -1053,7 +1058,10 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     const long long per = std::max<long long>(kMinKeys, keys / wave + 1), round = per > kMinKeys ? per / 2 : per - 1;
     auto splits = [&](long long blocks, long long ctx) {
         if (blocks == 0) return 0;
-        return (int)std::max<long long>(1, std::min<long long>({(ctx + round) / per, 64, (16 * 512) / (16 * blocks) + 1}));
+        long long n = (ctx + round) / per;
+        // whole caches that would be among the longest CTAs are halved: sequences differ in length
+        if (n == 1 && 2 * ctx > per && ctx > 2 * kMinKeys) n = 2;
+        return (int)std::max<long long>(1, std::min<long long>({n, 64, (16 * 512) / (16 * blocks) + 1}));
     };
     a.own_splits = splits(own_blocks, kv->max_ctx);
     a.pre_splits = splits(pre_blocks, pre ? pre->max_ctx : 0);
@@ -1068,7 +1076,7 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     if ((size_t)ranges > fit) return set_error(SPEC_ERR_CAPACITY, "attention workspace too small");
     a.part_o = m->attend_part;
     a.part_ml = m->attend_part + (size_t)ranges * TH * hd;
-    const dim3 grid((unsigned)(a.pre_splits * pre_blocks + a.own_splits * own_blocks));
+    const dim3 grid((unsigned)(a.pre_splits * pre_blocks + a.own_splits * own_blocks + (tile ? 1 : 0)));
     const size_t smem = rows_smem(hd, q_f32, QB, a.own.q8 || (a.pre_qb > 0 && a.pre.q8));
     void (*const kernels[8])(AttendArgs) = {
         attend_rows_kernel<64, false, 8>, attend_rows_kernel<64, false, 16>, attend_rows_kernel<64, true, 8>, attend_rows_kernel<64, true, 16>,
@@ -1084,9 +1092,7 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     }
     const int slot = prof_start(m, st);
     if (tile) SPEC_TRY(launch_attend_tile(pre, a, st));
-    // behind the tile kernel without early launch: row CTAs that wait on its SMs cost more than their
-    // start does (8 chains over 4096 tokens 45 -> 37 us a call, 64 decodes over 16384 90 -> 81 us)
-    cudaError_t e = launch_k(m->pdl && !tile, f, grid, dim3(kRowThreads), smem, st, a);
+    cudaError_t e = launch_k(m->pdl, f, grid, dim3(kRowThreads), smem, st, a);
     SPEC_TRY(check_cuda(e, "attention rows launch"));
     JoinArgs j{};
     j.part_o = a.part_o;

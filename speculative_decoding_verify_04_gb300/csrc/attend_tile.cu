@@ -166,8 +166,8 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = B.tmem;
-    pdl_trigger();                       // every CTA that can hold TMEM has it: the next kernel's cannot take it first
     pdl_wait();
+    pdl_trigger();                       // after the wait: the row kernel takes it that what this one waited for is done
 
     // the pair's (KV head, key tile) list, cut evenly over its CTAs: this one's part, head by head
     const int P = min(a.pre.len[a.pre_seq], a.pre.cap), KB = (P + kBlkK - 1) / kBlkK;

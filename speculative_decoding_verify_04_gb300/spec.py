@@ -130,9 +130,9 @@ def _ptr(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream=None):
+def _stream(stream=None, dev=None):
     if stream is None and _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device() if dev is None else dev)
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
 
@@ -522,7 +522,7 @@ def spec_attend(kv, layer, n_rows, q, out, k=None, v=None, tree_parent=None, str
             raise SpecError("tree_parent: shorter than the sequences' rows")
         tp = tree.buffer_info()[0]
     rc = load().spec_attend(kv.handle, layer, len(counts), counts.buffer_info()[0], qp, qs, kp, ks, vp, vs, tp, op, os_,
-                            _stream(stream))
+                            _stream(stream, dev))
     if rc:
         _check(rc)
 
@@ -553,7 +553,7 @@ def spec_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logpr
         return
     rc = load().spec_logprobs(logits.data_ptr(), SPEC_DTYPE_BF16 if dt is torch.bfloat16 else SPEC_DTYPE_F32,
                               logits.stride(0) if rows > 1 else V, rows, V, temperature, tok, lp, ent, n, ids, tlp,
-                              _stream(stream))
+                              _stream(stream, dev))
     if rc:
         _check(rc)
 
