@@ -21,6 +21,14 @@
 // (12-15) that turn raw e4m3 tiles into swizzled f16 tiles, y 2^e, where every
 // exponent of the turn's keys lies in [-15, 7] (two instructions for two values), else
 // into bf16 tiles (six); both are exact.  f16 queries are scaled by a power of two a row.
+//
+// 128 query vectors a stream is what one MMA takes and what one thread a vector serves;
+// two streams are what the 512 columns of tensor memory hold (S and O of 128 each).  Keys
+// come in tiles of 128: at 64 the hand-overs between MMAs and softmax would double.
+// Bound by that hand-over: 64 x 8 rows of 32 heads over 8 KV heads, hd 128, 32768 tokens
+// in bf16 take 182 us, 1.51 PFLOP/s (79 % of the measured peak, tensor pipe 67 %): 3060
+// cycles a key tile against 2048 of products.  Short lists are bound by their starts:
+// 6.7 key tiles a CTA (64 vectors x 4 heads, 16384 tokens in 8 bits) take 32 us.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
