@@ -71,8 +71,9 @@ __global__ void commit_tree_kernel(KT* kc, KT* vc, uint8_t* ke, uint8_t* ve, con
 //   (len[b] + n[b] when relative, else n[b]) holds a page.  One CTA looks at the
 //   (sequence, block) pairs 1024 at a time; the i-th missing one, in sequence
 //   and block order, takes the i-th page from the top of the free stack, and an
-//   empty stack sets the capacity error.  Bound by the latency of its three dependent
-//   reads: 16 sequences of 4 blocks 3.2 us, 64 of 17 5.5 us.
+//   empty stack sets the capacity error.  Where all are held, as in most calls, one
+//   look at the table says so.  Bound by the latency of dependent reads: 16 sequences of
+//   4 blocks 2.3 us, 64 of 17 3.7 us (3.3 and 5.5 with the places counted).
 //   release (page-granular rollback, "self-speculative decoding" page section
 //   3.3): the blocks past the committed length give their pages back; one
 //   thread walks every sequence in order.
@@ -98,12 +99,25 @@ ensure_pages_kernel(const int* __restrict__ len, PageNeed need, int* table, int 
     }
     __syncthreads();
     const int top0 = *free_top, cols = most;
+    const long long pairs = (long long)need.batch * cols;
+    auto entry = [&](long long i, int*& e) {                  // pair i's entry; whether its page is missing
+        const int b = (pairs >> 31) ? (int)(i / cols) : (int)((unsigned)i / (unsigned)cols);
+        const int p = (int)(i - (long long)b * cols);
+        e = table + (size_t)b * max_pages + p;
+        return i < pairs && p < blocks[min(b, kMaxPlanBatch - 1)] && *e < 0;
+    };
+    // most calls find every page held: all entries at once, without places
+    bool any = false;
+#pragma unroll 4
+    for (long long i = t; i < pairs; i += kEnsureThreads) {
+        int* e;
+        any |= entry(i, e);
+    }
+    if (!__syncthreads_or(any)) return;
     int top = top0;
-    for (long long base = 0; base < (long long)need.batch * cols; base += kEnsureThreads) {
-        const long long i = base + t;
-        const int b = cols ? (int)(i / cols) : 0, p = cols ? (int)(i % cols) : 0;
-        int* e = table + (size_t)b * max_pages + p;
-        const bool miss = b < need.batch && p < blocks[min(b, kMaxPlanBatch - 1)] && *e < 0;
+    for (long long base = 0; base < pairs; base += kEnsureThreads) {
+        int* e;
+        const bool miss = base + t < pairs && entry(base + t, e);
         const unsigned m = __ballot_sync(0xffffffffu, miss);
         if (lane == 0) warp_n[w] = __popc(m);
         __syncthreads();

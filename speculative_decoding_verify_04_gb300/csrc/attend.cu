@@ -868,8 +868,8 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
 // whose sums are added in warp order.  Many rows of few ranges are bound by reading the
 // states, few rows of many by the latency of it: more than 12 ranges take four warps
 // (2048 rows of 21 ranges: 12.5 us by one warp, 8.9 by four; 16384 rows of 5: 39 us by
-// four warps).  16384 rows of 5 ranges take 13.2 us, 36 MB at half the issue slots; 2048
-// rows of 21 ranges 8.9 us.
+// four warps).  With the sums fetched beside the maxima 16384 rows of 5 ranges take 12.5 us,
+// 2.9 TB/s at half the issue slots, and 2048 rows of 21 ranges 8.4 us, 2.6 TB/s.
 struct JoinArgs {
     const float* part_o; const float* part_ml;
     int own_range0, own_ranges, pre_ranges;     // pre_ranges: the row kernel's prompt ranges
@@ -898,6 +898,32 @@ attend_join_kernel(const __grid_constant__ JoinArgs a) {
     }
     const int n = pre + a.own_ranges;
     auto slot = [&](int s) { return (size_t)(s < pre ? s : a.own_range0 + s - pre) * a.TH + v; };
+    // U ranges' sums are on their way while the maxima are looked at (those of an empty range, whatever
+    // they hold, are dropped)
+    float2 ml[U];
+    float x[U][E];
+    auto fetch = [&](int s0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + NW * u;
+            ml[u] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[u][e] = 0.f;
+            if (s < n) {
+                const size_t at = slot(s);
+                ml[u] = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
+                const float* src = a.part_o + at * HD + lane * E;
+                if (E == 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(src);
+                    x[u][0] = f.x; x[u][1] = f.y; x[u][E - 2] = f.z; x[u][E - 1] = f.w;
+                } else {
+                    const float2 f = *reinterpret_cast<const float2*>(src);
+                    x[u][0] = f.x; x[u][1] = f.y;
+                }
+            }
+        }
+    };
+    fetch(w);
     float M = -INFINITY;
     for (int s = lane; s < n; s += 32) M = fmaxf(M, a.part_ml[2 * slot(s)]);
     M = warp_max(M);
@@ -905,36 +931,17 @@ attend_join_kernel(const __grid_constant__ JoinArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) O[e] = 0.f;
     if (M != -INFINITY) {
-        for (int s0 = w; s0 < n; s0 += NW * U) {
-            float2 ml[U];
-            float x[U][E];
+        for (int s0 = w; s0 < n;) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int s = s0 + NW * u;
-                ml[u] = make_float2(-INFINITY, 0.f);
-#pragma unroll
-                for (int e = 0; e < E; ++e) x[u][e] = 0.f;
-                if (s < n) {
-                    const size_t at = slot(s);
-                    ml[u] = *reinterpret_cast<const float2*>(a.part_ml + 2 * at);
-                    if (ml[u].x == -INFINITY) continue;       // an empty range: its sums were not written
-                    const float* src = a.part_o + at * HD + lane * E;
-                    if (E == 4) {
-                        const float4 f = *reinterpret_cast<const float4*>(src);
-                        x[u][0] = f.x; x[u][1] = f.y; x[u][E - 2] = f.z; x[u][E - 1] = f.w;
-                    } else {
-                        const float2 f = *reinterpret_cast<const float2*>(src);
-                        x[u][0] = f.x; x[u][1] = f.y;
-                    }
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
+                const bool none = ml[u].x == -INFINITY;
                 const float ws = ex2(ml[u].x - M);
                 L = fmaf(ml[u].y, ws, L);
 #pragma unroll
-                for (int e = 0; e < E; ++e) O[e] = fmaf(ws, x[u][e], O[e]);
+                for (int e = 0; e < E; ++e) O[e] = fmaf(ws, none ? 0.f : x[u][e], O[e]);
             }
+            s0 += NW * U;
+            if (s0 < n) fetch(s0);
         }
     }
     if (NW == 4) {

@@ -97,11 +97,15 @@ SPEC_DEV float2 add2(float2 x, float2 y) {
 bool attend_tile_ok(const spec_kv* pre);
 int attend_tile_ctas(const spec_model* m, const AttendSpan& span, int prompt_cap);
 int attend_tile_ranges(const spec_model* m, int ctas);      // most ranges of one KV head
+// a / b of numbers >= 0; nearly always a division of 32 bits, a third of the other's instructions
+SPEC_DEV long long quotient(long long a, long long b) {
+    return ((a | b) >> 32) ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
 // Of n CTAs that share the W = Hkv KB key tiles of all heads evenly (CTA j from j W / n on),
 // the one that holds head g's first.  Its range of the head is range 0, the next one's range 1, ...
-SPEC_DEV int tile_first_cta(int g, int KB, long long W, int n) { return (int)((((long long)g * KB + 1) * n - 1) / W); }
+SPEC_DEV int tile_first_cta(int g, int KB, long long W, int n) { return (int)quotient(((long long)g * KB + 1) * n - 1, W); }
 SPEC_DEV int tile_range_count(int g, int KB, long long W, int n) {
-    return KB == 0 ? 0 : (int)(((long long)(g + 1) * KB * n - 1) / W) - tile_first_cta(g, KB, W, n) + 1;
+    return KB == 0 ? 0 : (int)quotient((long long)(g + 1) * KB * n - 1, W) - tile_first_cta(g, KB, W, n) + 1;
 }
 int launch_attend_tile(const spec_kv* pre, const AttendArgs& a, cudaStream_t st);
 

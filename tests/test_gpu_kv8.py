@@ -165,6 +165,16 @@ def test_many_sequences_take_pages_in_order():
         at += need
     assert kv.page_table() == want and m.device_error() == 0
     assert kv.free_pages() == B * blocks - at
+    # nothing missing, then a few more blocks here and there: the next pages, in the sequences' order
+    kv.set_lengths(lens)
+    assert kv.page_table() == want
+    more = [min(blocks * 64, n + 64) if b % 3 == 0 else n for b, n in enumerate(lens)]
+    kv.set_lengths(more)
+    for row, n in zip(want, more):
+        for p in range(-(-n // 64)):
+            if row[p] < 0:
+                row[p], at = at, at + 1
+    assert kv.page_table() == want and m.device_error() == 0
 
 
 def test_refusals():
