@@ -325,6 +325,55 @@ def test_captured_and_replayed_after_the_lengths_moved():
     c.check(out)
 
 
+@pytest.mark.parametrize("prompt_q8", [False, True])
+def test_calls_in_a_row_over_two_caches(prompt_q8):
+    """Two caches of one model behind one prompt, called in turn without a wait, eagerly and in a graph: the kernels
+    of neighbouring calls overlap and share the workspace, and every output has the bits of a call on its own."""
+    from speculative_decoding_verify_04_gb300 import spec
+    B, rows = 12, 6
+    c = Case(41, 16, 2, 128, [37 * b for b in range(B)], [rows] * B, prompt=3001, q8=True, prompt_q8=prompt_q8)
+    g = torch.Generator(device="cuda").manual_seed(42)
+
+    def r(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").to(torch.bfloat16)
+
+    other = spec.KVCache(c.model, B, 700)
+    for b in range(B):
+        other.import_rows(b, 0, r(1, 600 - 50 * b, 2, 128), r(1, 600 - 50 * b, 2, 128))
+    other.set_lengths([600 - 50 * b for b in range(B)])
+    other.set_prefix(c.prompt, c.pseq)
+    T = B * rows
+    calls = [(c.kv, c.q.cuda(), c.k.cuda(), c.v.cuda()), (other, r(T, 16, 128), r(T, 2, 128), r(T, 2, 128))]
+
+    def run(i):
+        kv, q, k, v = calls[i]
+        out = torch.full_like(q, 7.0)
+        spec.spec_attend(kv, 0, [rows] * B, q, out, k=k, v=v)
+        return out
+
+    want = []
+    for i in range(2):
+        want.append(run(i))
+        torch.cuda.synchronize()
+    c.check(want[0])
+    outs = [(i & 1, run(i & 1)) for i in range(40)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(want[i], o) for i, o in outs)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            outs = [(i & 1, run(i & 1)) for i in range(5)]
+        for _ in range(10):
+            for _, o in outs:
+                o.fill_(3.0)
+            graph.replay()
+            assert all(torch.equal(want[i], o) for i, o in outs)
+    torch.cuda.synchronize()
+    assert c.model.device_error() == 0
+
+
 def test_on_another_stream():
     from speculative_decoding_verify_04_gb300 import spec
     c = Case(13, 8, 2, 64, [10, 40], [2, 2], prompt=90, q8=True)
