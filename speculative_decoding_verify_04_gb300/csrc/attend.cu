@@ -725,13 +725,10 @@ constexpr int row_ctas_per_sm(int hd, int qb) { return hd == 128 ? 3 : (qb == 8 
 template <int HD, bool QF32, int QB>
 __global__ void __launch_bounds__(kRowThreads, row_ctas_per_sm(HD, QB))
 attend_rows_kernel(const __grid_constant__ AttendArgs a) {
-    // Behind the tile kernel this one works beside it: neither reads what the other writes, and the tile
-    // kernel lets it start after its own wait, so everything before is done.  Its last CTA waits for the
-    // tile kernel, so the join, which waits for this kernel, has both (64 samples over 32768 tokens 238 ->
-    // 229 us a call, 8 chains over 4096 37 -> 33).
-    if (a.tile_ctas == 0) pdl_wait();
+    // Behind the tile kernel too: what the launches before that one wrote (the new rows) is visible to a grid
+    // that waits, not to one that was only let start.  Working beside the tile kernel took 3 to 9 us less a call.
+    pdl_wait();
     pdl_trigger();
-    if (a.tile_ctas > 0 && blockIdx.x == gridDim.x - 1) { pdl_wait(); return; }
     constexpr int KS = HD / 16, VD = HD / 8;
     constexpr int LS = HD + 4;                                              // a state row: O, m, l, R
     extern __shared__ float smf[];
@@ -1084,7 +1081,7 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     if ((size_t)ranges > fit) return set_error(SPEC_ERR_CAPACITY, "attention workspace too small");
     a.part_o = m->attend_part;
     a.part_ml = m->attend_part + (size_t)ranges * TH * hd;
-    const dim3 grid((unsigned)(a.pre_splits * pre_blocks + a.own_splits * own_blocks + (tile ? 1 : 0)));
+    const dim3 grid((unsigned)(a.pre_splits * pre_blocks + a.own_splits * own_blocks));
     const size_t smem = rows_smem(hd, q_f32, QB, a.own.q8 || (a.pre_qb > 0 && a.pre.q8));
     void (*const kernels[8])(AttendArgs) = {
         attend_rows_kernel<64, false, 8>, attend_rows_kernel<64, false, 16>, attend_rows_kernel<64, true, 8>, attend_rows_kernel<64, true, 16>,

@@ -175,7 +175,7 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
     tc_fence_after();
     const uint32_t tmem = B.tmem;
     pdl_wait();
-    pdl_trigger();                       // after the wait: the row kernel takes it that what this one waited for is done
+    pdl_trigger();
 
     // the pair's (KV head, key tile) list, cut evenly over its CTAs: this one's part, head by head
     const int P = min(a.pre.len[a.pre_seq], a.pre.cap), KB = (P + kBlkK - 1) / kBlkK;

@@ -257,9 +257,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N) {
 
 // Programmatic dependent launch: a kernel launched with the PDL attribute may
 // start while the previous kernel on the stream is still running.  It must call
-// pdl_wait() before touching memory the previous kernel reads or writes;
-// pdl_trigger() lets the next kernel launch early.  Both are no-ops when the
-// kernel was launched without the attribute.
+// pdl_wait() before touching memory the previous kernel reads or writes, in
+// every CTA: what earlier kernels wrote is visible to a grid that waits.
+// pdl_trigger() lets the next kernel launch early, and comes after the wait, so
+// that every kernel two launches back has completed when a kernel starts.  Both
+// are no-ops when the kernel was launched without the attribute.
 SPEC_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 SPEC_DEV void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
