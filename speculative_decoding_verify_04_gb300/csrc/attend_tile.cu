@@ -56,7 +56,7 @@ struct TileShape {
     static constexpr int kSmem = kTiles + kExpBytes + 512 + (Q8 ? 1024 : 0) + 1024;   // barriers, row factors; the tiles start on 1024 bytes
 };
 
-struct TileBars {                        // full .. done: every barrier, in one run
+struct TileBars {                        // (a form with fewer stages leaves the last of full .. raw_empty unused)
     uint64_t full[8], empty[8];          // K/V ring
     uint64_t raw_full[4], raw_empty[4];  // raw e4m3 ring
     uint64_t mode;                       // 8-bit caches: the operands' type is known
@@ -155,14 +155,18 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
     const int G = a.H / a.Hkv, NQ = a.span.T * G;
     const int q0 = (int)(blockIdx.x / a.tile_ctas) * 2 * kBlkQ;
     const bool two = NQ - q0 > kBlkQ;    // two tiles of query vectors: both streams free each K and V tile
+    // every barrier of this kernel form, with its arrivals: what is taken down between turns is what was set up
+    auto each_bar = [&](auto f) {
+        for (int i = 0; i < NST; ++i) { f(&B.full[i], Q8 ? 4 : 1); f(&B.empty[i], two ? 2 : 1); }
+        for (int i = 0; i < NRAW; ++i) { f(&B.raw_full[i], 1); f(&B.raw_empty[i], 4); }
+        f(&B.mode, 4);
+        f(&B.q_full, 8);
+        for (int i = 0; i < 2; ++i) { f(&B.s_full[i], 1); f(&B.p_full[i], 5); }
+        f(&B.done, 1);
+    };
     auto init_bars = [&]() {
-        for (int i = 0; i < NST; ++i) { mbar_init(&B.full[i], Q8 ? 4 : 1); mbar_init(&B.empty[i], two ? 2 : 1); }
-        for (int i = 0; i < NRAW; ++i) { mbar_init(&B.raw_full[i], 1); mbar_init(&B.raw_empty[i], 4); }
-        mbar_init(&B.mode, 4);
-        mbar_init(&B.q_full, 8);
+        each_bar([](uint64_t* b, int arrivals) { mbar_init(b, arrivals); });
         B.half = 1;
-        for (int i = 0; i < 2; ++i) { mbar_init(&B.s_full[i], 1); mbar_init(&B.p_full[i], 5); }
-        mbar_init(&B.done, 1);
         fence_mbar_init();
     };
     if (warp == 9) tmem_alloc(&B.tmem, 512);
@@ -201,8 +205,9 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
         __syncthreads();
         if (*ab || at >= stop) return true;
         if (t == 0) {
-            for (uint64_t* b = B.full; b <= &B.done; ++b)
+            each_bar([](uint64_t* b, int) {
                 asm volatile("mbarrier.inval.shared::cta.b64 [%0];" :: "r"(smem_u32(b)) : "memory");
+            });
             init_bars();
         }
         __syncthreads();
