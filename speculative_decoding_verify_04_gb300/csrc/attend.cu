@@ -891,7 +891,8 @@ attend_join_kernel(const __grid_constant__ JoinArgs a) {
     int pre = a.pre_ranges;
     if (a.tile_ctas) {
         const int KB = (min(*a.pre_len, a.pre_cap) + 127) / 128;
-        pre = tile_range_count((v % a.H) / a.G, KB, (long long)a.Hkv * KB, a.tile_ctas);
+        const long long W = (long long)a.Hkv * KB;
+        pre = tile_range_count((v % a.H) / a.G, KB, W, tile_ctas_at_work(a.tile_ctas, W));
     }
     const int n = pre + a.own_ranges;
     auto slot = [&](int s) { return (size_t)(s < pre ? s : a.own_range0 + s - pre) * a.TH + v; };

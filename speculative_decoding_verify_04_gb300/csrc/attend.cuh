@@ -56,7 +56,7 @@ struct AttendArgs {
     int H, Hkv;
     AttendSpan span;
     int own_splits, pre_splits;       // key ranges; pre_splits is 0 where the tile kernel takes the prompt
-    int tile_ctas;                    // the tile kernel's CTAs a pair of query tiles
+    int tile_ctas;                    // the tile kernel's CTAs a pair of query tiles (at most: tile_ctas_at_work)
     int own_qb, pre_qb;               // query blocks of 16
     float* part_o;                    // [range][T * H][hd]
     float* part_ml;                   // [range][T * H][2]
@@ -101,7 +101,10 @@ int attend_tile_ranges(const spec_model* m, int ctas);      // most ranges of on
 SPEC_DEV long long quotient(long long a, long long b) {
     return ((a | b) >> 32) ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
-// Of n CTAs that share the W = Hkv KB key tiles of all heads evenly (CTA j from j W / n on),
+// CTAs that share W key tiles: the host's count, chosen for a full cache, or one a tile where the prompt
+// has fewer tiles, so that none is without keys and every range that the join counts is written.
+SPEC_DEV int tile_ctas_at_work(int ctas, long long W) { return W < ctas ? (int)W : ctas; }
+// Of n <= W CTAs that share the W = Hkv KB key tiles of all heads evenly (CTA j from j W / n on),
 // the one that holds head g's first.  Its range of the head is range 0, the next one's range 1, ...
 SPEC_DEV int tile_first_cta(int g, int KB, long long W, int n) { return (int)quotient(((long long)g * KB + 1) * n - 1, W); }
 SPEC_DEV int tile_range_count(int g, int KB, long long W, int n) {

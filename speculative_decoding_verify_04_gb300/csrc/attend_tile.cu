@@ -184,9 +184,9 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
     // the pair's (KV head, key tile) list, cut evenly over its CTAs: this one's part, head by head
     const int P = min(a.pre.len[a.pre_seq], a.pre.cap), KB = (P + kBlkK - 1) / kBlkK;
     const long long W = (long long)a.Hkv * KB;
-    const int cta = blockIdx.x % a.tile_ctas;
-    long long at = cta * W / a.tile_ctas;
-    const long long stop = (cta + 1) * W / a.tile_ctas;
+    const int cta = blockIdx.x % a.tile_ctas, ctas = tile_ctas_at_work(a.tile_ctas, W);
+    long long at = cta < ctas ? cta * W / ctas : 0;
+    const long long stop = cta < ctas ? (cta + 1) * W / ctas : 0;
     volatile int* ab = &B.abort;
 
     // a turn's job; between turns every warp meets twice and the barriers start afresh
@@ -221,7 +221,7 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
         else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         for (TileJob J; at < stop;) {
         take(J);
-        const int range = cta - tile_first_cta(J.g, KB, W, a.tile_ctas);
+        const int range = cta - tile_first_cta(J.g, KB, W, ctas);
         // -------- queries into shared memory, then the softmax of stream `warp / 4`
         // a thread takes one 16-byte piece of every RPP-th row; eight loads go out before the first store
         constexpr int CPR = HD / 8, RPP = 256 / CPR, NB = HD == 128 ? 8 : 4;
