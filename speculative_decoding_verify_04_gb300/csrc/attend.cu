@@ -63,9 +63,10 @@ SPEC_DEV void mma16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
 // two a row to a magnitude of 2^13 .. 2^14 (bf16 queries stay exact down to
 // 2^-31 of the row's largest); a key's 2^e multiplies its scores; a value's
 // 2^e goes into the exponent of its probability, relative to a maximum of its
-// own (R, over s + e): P' = 2^(s + e - R) is at most 1 and in f16 off by 2^-12
-// of itself, below 2^-14 by 2^-25 of the row's largest.  f32 queries are split
-// into hi + lo (QF32).
+// own (R, over s + e): P' = 2^(15 + s + e - R) is at most 2^15 and in f16 off by
+// 2^-11 of itself (the cache's own values are off by 2^-4 of what was written),
+// below 2^-29 of the row's largest by 2^-40 of it; the sum of p takes p in 32 bits.
+// f32 queries are split into hi + lo (QF32).
 //
 // Bound by latency: 64 sequences of 512 slots on average (hd 128, 8 KV heads, 8 bits, 4
 // vectors) take 28 us, 2.4 TB/s, of which half a CTA's life is its start (lengths, pages,
@@ -232,6 +233,9 @@ SPEC_DEV bool not_finite2(uint32_t w) {
     return (w & E) == E || (w & (E << 16)) == (E << 16);
 }
 
+// P' of 8-bit caches: up to the top of f16's range, so that its smallest numbers lie far below any weight that counts
+constexpr float kF16Top = 32768.f;
+
 // running state of a lane's two rows: m and l of the sums of p (l over the lane's keys; joined
 // over the quad at the end), R the reference of O (8-bit caches; else R = m)
 template <int HD>
@@ -277,7 +281,7 @@ SPEC_DEV void softmax_tile(float (&x)[2][4], float (&y)[2][4], float (&m)[2], fl
             f[rr] = R[rr] == rn ? 1.f : ex2(R[rr] - ru);
             R[rr] = rn;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[rr][e] = ex2(y[rr][e] - ru);
+            for (int e = 0; e < 4; ++e) y[rr][e] = ex2(y[rr][e] - ru) * kF16Top;
         } else {
             f[rr] = alpha;
 #pragma unroll
@@ -673,8 +677,8 @@ SPEC_DEV void attend_range_few(const AttendArgs& a, const CacheView& cv, int seq
                 const float rn = fmaxf(st.R[j], rt), ru = rn == -INFINITY ? 0.f : rn;
                 f[j] = st.R[j] == rn ? 1.f : ex2(st.R[j] - ru);
                 st.R[j] = rn;
-                y[j][0] = ex2(y[j][0] - ru);
-                y[j][1] = ex2(y[j][1] - ru);
+                y[j][0] = ex2(y[j][0] - ru) * kF16Top;
+                y[j][1] = ex2(y[j][1] - ru) * kF16Top;
             } else {
                 f[j] = alpha;
                 y[j][0] = p0;
@@ -853,7 +857,7 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
             O.z = fmaf(o.z, wt, O.z);
             O.w = fmaf(o.w, wt, O.w);
         }
-        const float f = M == -INFINITY ? 1.f : ex2(RR - M);
+        const float f = (M == -INFINITY ? 1.f : ex2(RR - M)) * (cv.q8 ? 1.f / kF16Top : 1.f);
         const size_t vec = vec_of(r);
         *reinterpret_cast<float4*>(a.part_o + vec * HD + d) = make_float4(O.x * f, O.y * f, O.z * f, O.w * f);
         if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * vec) = make_float2(M, L);

@@ -22,6 +22,9 @@
 // exponent of the turn's keys lies in [-15, 7] (two instructions for two values), else
 // into bf16 tiles (six); both are exact.  f16 queries are scaled by a power of two a row.
 //
+// P is rounded to the product's type, by 2^-8 of itself in bf16 and by 2^-11 in f16 (there,
+// below 2^-21 of the row's largest, by 2^-32 of it); the sum of p takes p in 32 bits.
+//
 // 128 query vectors a stream is what one MMA takes and what one thread a vector serves;
 // two streams are what the 512 columns of tensor memory hold (S and O of 128 each).  Keys
 // come in tiles of 128: at 64 the hand-overs between MMAs and softmax would double.
@@ -40,6 +43,7 @@ namespace spec {
 constexpr int kBlkQ = 128;
 constexpr int kBlkK = 128;
 constexpr float kLazy = 8.0f;            // log2 of the growth of the maximum that is let pass
+constexpr float kF16Log2 = 7.0f;         // P in f16 is 2^7 times what it is in bf16: 2^15 at most with kLazy
 
 template <int HD, bool Q8>
 struct TileShape {
@@ -344,7 +348,7 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                     }
                 }
             }
-            const float mu = m == -INFINITY ? 0.f : m;
+            const float mu = (m == -INFINITY ? 0.f : m) - (half ? kF16Log2 : 0.f);
             const float2 cc = make_float2(c, c), mm = make_float2(-mu, -mu);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             auto exponentials = [&](auto f16) {
@@ -375,6 +379,7 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
         const int n1 = J.n_jobs / 2;                          // jobs of stream 1
         if (ok) ok = warp_wait(&B.done, 0, ab, a.err);
         tc_fence_after();
+        if (half) m -= kF16Log2;                              // what the state's sums are relative to
         float* xo = reinterpret_cast<float*>(ring);           // every product has ended: the ring is free
         float* xml = reinterpret_cast<float*>(sQ + S::kQBytes);
         if (!J.two) {
