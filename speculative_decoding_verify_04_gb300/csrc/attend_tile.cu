@@ -19,7 +19,7 @@
 // Roles: warps 0-3 and 4-7 the streams' softmax, warp 8 the copies (TMA tensor
 // boxes with the 128-byte swizzle), warp 9 the MMAs; 8-bit caches add four warps
 // (12-15) that turn raw e4m3 tiles into swizzled f16 tiles, y 2^e, where every
-// exponent of the turn's keys lies in [-15, 7] (two instructions for two values), else
+// exponent of the turn's keys lies in [-15, 7] or its row is zeros (two instructions for two values), else
 // into bf16 tiles (six); both are exact.  f16 queries are scaled by a power of two a row.
 //
 // P is rounded to the product's type, by 2^-8 of itself in bf16 and by 2^-11 in f16 (there,
@@ -600,13 +600,23 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                 if (row < 0) continue;                        // (the copies report it)
                 const uint4 w = __ldg(reinterpret_cast<const uint4*>((i & 1 ? a.pre.ve : a.pre.ke) + row));
                 const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+                uint32_t least = 0;                           // rows of the least exponent
 #pragma unroll
                 for (int b = 0; b < 16; ++b) {
                     const int e = (int)((u[b >> 2] >> (8 * (b & 3))) & 0xFF) - 127;
                     if (slot + b >= J.k_begin + J.n_keys) continue;
-                    // rows of the least exponent (zeros, or nothing above 2^-115) become zeros beside others
-                    if (e != -124) seen = true;
+                    if (e == -124) least |= 1u << b;
+                    else seen = true;
                     if (e != -124 && (e < -15 || e > 7)) fits = false;
+                }
+                // they fit where they are zeros; what they hold else lies below f16's range
+                const uint4* y = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(i & 1 ? a.pre.v : a.pre.k) + row * HD);
+                for (; least && fits; least &= least - 1) {
+                    const uint4* at_b = y + (__ffs(least) - 1) * (HD / 16);
+                    for (int p = 0; p < HD / 16; ++p) {
+                        const uint4 x = __ldg(at_b + p);
+                        if ((x.x | x.y | x.z | x.w) & 0x7F7F7F7Fu) fits = false;
+                    }
                 }
             }
             if (!fits) atomicAnd(&B.half, 2);
@@ -643,7 +653,7 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                         const uint32_t ws[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
                         uint32_t o[8];
                         if (f16.value) {
-                            // 2^e as f16 (2^-15 is a denormal; rows of the least exponent: 0)
+                            // 2^e as f16 (2^-15 is a denormal; rows of the least exponent are zeros: 0)
                             const uint32_t h = eb[j] >= 127 - 14 ? (uint32_t)(eb[j] - 127 + 15) << 10 : (eb[j] == 127 - 15 ? 0x0200u : 0u);
                             const uint32_t hh = h | (h << 16);
 #pragma unroll

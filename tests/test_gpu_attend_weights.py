@@ -1,4 +1,5 @@
-"""Weights far below a row's largest one: what the attention's operands of 16 bits must not lose."""
+"""Weights far below a row's largest one and values far below the others: what the attention's operands of 16 bits must
+not lose."""
 import math
 
 import numpy as np
@@ -73,3 +74,23 @@ def test_many_weights_far_below_the_largest(dim, rows, prompt):
     tol = tol + n * (2.0 ** -32 if prompt and rows > 16 else 2.0 ** -40) / 80
     assert 10 * tol[0, 0, 1] < ref[0, 0, 1]
     assert ((out - ref).abs() <= tol).all(), ((out - ref).abs() / tol).amax()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("rows", [1, 12, 32])
+def test_a_value_far_below_the_others(dim, rows):
+    """One key has all of the weight, its value is far below the smallest that half precision holds; the others'
+    values are ordinary."""
+    n = 40
+    g = torch.Generator().manual_seed(3)
+    scores = torch.full((n,), -240.0)                    # weights below 2^-170
+    scores[17] = 0.0
+    values = torch.randn(n, dim, generator=g)
+    values[17] = values[17].sign() * torch.linspace(1.0, 1.75, dim) * 2.0 ** -116
+    c = Keys(dim, rows, scores, values, True, True)
+    from _attend_util import rows8
+    c.v = torch.from_numpy(rows8(c.v.double().numpy())[2])
+    out, (ref, tol) = c.run(), c.want()
+    # weights below 2^-126 may be flushed to zero; the reference's are below 2^-170
+    assert (ref.abs() > 2.0 ** -117).all()
+    assert ((out - ref).abs() <= tol).all()
