@@ -28,11 +28,6 @@ constexpr int kRowVectors = 16, kRowVectorsShort = 64, kRowKeysShort = 65536;
 // 10 rows over 671 slots 33 at 256, 35 at 128, 37 at 512
 constexpr int kMinKeys = 256;
 
-SPEC_DEV float f16_round(float x) {
-    float r;
-    asm("{\n\t.reg .b16 h;\n\tcvt.rn.f16.f32 h, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(r) : "f"(x));
-    return r;
-}
 SPEC_DEV void mma16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
@@ -1077,7 +1072,7 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     a.pre_splits = splits(pre_blocks, pre ? pre->max_ctx : 0);
     int tile_ranges = 0;
     if (tile) {
-        a.tile_ctas = attend_tile_ctas(m, span, pre->max_ctx);
+        a.tile_ctas = attend_tile_ctas(m, span, q_f32, pre->max_ctx);
         while (a.tile_ctas > 1 && (size_t)(a.own_splits + attend_tile_ranges(m, a.tile_ctas)) > fit) --a.tile_ctas;
         tile_ranges = attend_tile_ranges(m, a.tile_ctas);
     }

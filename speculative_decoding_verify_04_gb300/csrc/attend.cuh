@@ -95,7 +95,7 @@ SPEC_DEV float2 add2(float2 x, float2 y) {
 
 // attend_tile.cu: the prompt's part for lists of many query vectors
 bool attend_tile_ok(const spec_kv* pre);
-int attend_tile_ctas(const spec_model* m, const AttendSpan& span, int prompt_cap);
+int attend_tile_ctas(const spec_model* m, const AttendSpan& span, bool q_f32, int prompt_cap);
 int attend_tile_ranges(const spec_model* m, int ctas);      // most ranges of one KV head
 // a / b of numbers >= 0; nearly always a division of 32 bits, a third of the other's instructions
 SPEC_DEV long long quotient(long long a, long long b) {
@@ -178,6 +178,11 @@ SPEC_DEV uint32_t e4m3x2_f16(uint32_t two) {
 SPEC_DEV uint32_t pack_f16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+SPEC_DEV float f16_round(float x) {
+    float r;
+    asm("{\n\t.reg .b16 h;\n\tcvt.rn.f16.f32 h, %1;\n\tcvt.f32.f16 %0, h;\n\t}" : "=f"(r) : "f"(x));
     return r;
 }
 SPEC_DEV uint32_t f16x2_mul(uint32_t x, uint32_t y) {

@@ -23,7 +23,12 @@
 // into bf16 tiles (six); both are exact.  f16 queries are scaled by a power of two a row.
 //
 // P is rounded to the product's type, by 2^-8 of itself in bf16 and by 2^-11 in f16 (there,
-// below 2^-21 of the row's largest, by 2^-32 of it); the sum of p takes p in 32 bits.
+// below 2^-21 of the row's largest, by 2^-32 of it); the sum of p takes p in 32 bits.  With bf16
+// queries, whose results leave in bf16, that is all.  f32 queries (the forward calls, whose
+// attention splits Q and P wherever it runs: P in one bf16 alone is past their bound in 32 layers)
+// take two operands, hi + lo, each with products of its own: Q in either type, P in bf16, the lo
+// part in the half of S's columns that P leaves; f16 keeps one P.  Q's lo part lies where the
+// second tile of query vectors would, so a CTA has one tile.
 //
 // 128 query vectors a stream is what one MMA takes and what one thread a vector serves;
 // two streams are what the 512 columns of tensor memory hold (S and O of 128 each).  Keys
@@ -139,7 +144,10 @@ struct TileJob {
 };
 SPEC_DEV int job_kb(const TileJob& J, int n) { return J.two ? n >> 1 : n; }
 
-template <int HD, bool Q8>
+// query vectors of a CTA
+constexpr int tile_vectors(bool q_f32) { return q_f32 ? kBlkQ : 2 * kBlkQ; }
+
+template <int HD, bool Q8, bool QF32>
 __global__ void __launch_bounds__(TileShape<HD, Q8>::kThreads, 1)
 attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v) {
@@ -157,8 +165,8 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
 
     const int G = a.H / a.Hkv, NQ = a.span.T * G;
-    const int q0 = (int)(blockIdx.x / a.tile_ctas) * 2 * kBlkQ;
-    const bool two = NQ - q0 > kBlkQ;    // two tiles of query vectors: both streams free each K and V tile
+    const int q0 = (int)(blockIdx.x / a.tile_ctas) * tile_vectors(QF32);
+    const bool two = !QF32 && NQ - q0 > kBlkQ;    // two tiles of query vectors: both streams free each K and V tile
     // every barrier of this kernel form, with its arrivals: what is taken down between turns is what was set up
     auto each_bar = [&](auto f) {
         for (int i = 0; i < NST; ++i) { f(&B.full[i], Q8 ? 4 : 1); f(&B.empty[i], two ? 2 : 1); }
@@ -197,7 +205,7 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
     auto take = [&](TileJob& J) {
         J.g = (int)(at / KB);
         J.q0 = q0;
-        J.nq = min(2 * kBlkQ, NQ - q0);
+        J.nq = min(tile_vectors(QF32), NQ - q0);
         J.two = two;
         J.k_begin = (int)(at - (long long)J.g * KB) * kBlkK;
         J.n_kb = (int)min(stop - at, (long long)(J.g + 1) * KB - at);
@@ -228,58 +236,99 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
         const int range = cta - tile_first_cta(J.g, KB, W, ctas);
         // -------- queries into shared memory, then the softmax of stream `warp / 4`
         // a thread takes one 16-byte piece of every RPP-th row; eight loads go out before the first store
-        constexpr int CPR = HD / 8, RPP = 256 / CPR, NB = HD == 128 ? 8 : 4;
+        constexpr int CPR = HD / 8, RPP = 256 / CPR, NB = HD == 128 && !QF32 ? 8 : 4;
         const int ch = t % CPR;
         bool ok = true, half = false;
-        for (int r0 = t / CPR; r0 < (J.two ? 2 * kBlkQ : kBlkQ); r0 += NB * RPP) {
-            uint4 w[NB];
+        // f16: the row's largest magnitude to 2^13 .. 2^14 (CPR lanes hold a row); the power of two, its inverse kept
+        auto half_factor = [&](const float (&x)[8], int r) {
+            float m = finite_amax(x);
 #pragma unroll
-            for (int k = 0; k < NB; ++k) {
-                const int r = r0 + k * RPP, qi = J.q0 + r;
-                w[k] = make_uint4(0, 0, 0, 0);
-                if (r >= J.nq) continue;
-                const long long off = (qi / G) * a.q_stride + (J.g * G + qi % G) * HD + ch * 8;
-                if (a.q_f32) {
-                    const float* p = static_cast<const float*>(a.q) + off;
-                    const float4 x = __ldg(reinterpret_cast<const float4*>(p)), y = __ldg(reinterpret_cast<const float4*>(p + 4));
-                    w[k] = make_uint4(bf16x2(x.x, x.y), bf16x2(x.z, x.w), bf16x2(y.x, y.y), bf16x2(y.z, y.w));
-                } else if (a.q_vec) {
-                    w[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + off));
-                } else {
-                    const unsigned short* p = static_cast<const unsigned short*>(a.q) + off;
-                    w[k] = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16,
-                                      p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
-                }
-            }
-            if (Q8 && r0 == t / CPR) {                        // (the first loads are on their way)
-                ok = warp_wait(&B.mode, 0, ab, a.err);
-                half = B.half == 3;
-            }
-            if (half) {
-                // f16: the row's largest magnitude to 2^13 .. 2^14 (CPR lanes hold a row)
+            for (int o = CPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const int e = min(127 + 13 - (int)(__float_as_uint(m) >> 23), 100);
+            if (ch == 0) row_factor[r] = __uint_as_float((uint32_t)(127 - e) << 23);
+            return __uint_as_float((uint32_t)(127 + e) << 23);
+        };
+        auto q_piece = [&](int r) {                           // where the thread's piece of row r goes
+            const int rr = r & (kBlkQ - 1);
+            return reinterpret_cast<uint4*>(sQ + (r / kBlkQ) * S::kQBytes + (ch >> 3) * kHalf + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4));
+        };
+        for (int r0 = t / CPR; r0 < (J.two ? 2 * kBlkQ : kBlkQ); r0 += NB * RPP) {
+            if constexpr (QF32) {
+                float x[NB][8];
 #pragma unroll
                 for (int k = 0; k < NB; ++k) {
-                    const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-                    float x[8];
+                    const int r = r0 + k * RPP, qi = J.q0 + r;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[2 * i] = __uint_as_float(u[i] << 16);
-                        x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-                    }
-                    float m = finite_amax(x);
-#pragma unroll
-                    for (int o = CPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                    const int e = min(127 + 13 - (int)(__float_as_uint(m) >> 23), 100);
-                    const float f = __uint_as_float((uint32_t)(127 + e) << 23);
-                    w[k] = make_uint4(pack_f16(x[0] * f, x[1] * f), pack_f16(x[2] * f, x[3] * f), pack_f16(x[4] * f, x[5] * f),
-                                      pack_f16(x[6] * f, x[7] * f));
-                    if (ch == 0) row_factor[r0 + k * RPP] = __uint_as_float((uint32_t)(127 - e) << 23);
+                    for (int e = 0; e < 8; ++e) x[k][e] = 0.f;
+                    if (r >= J.nq) continue;
+                    const float* p = static_cast<const float*>(a.q) + (qi / G) * a.q_stride + (J.g * G + qi % G) * HD + ch * 8;
+                    const float4 u = __ldg(reinterpret_cast<const float4*>(p)), w = __ldg(reinterpret_cast<const float4*>(p + 4));
+                    x[k][0] = u.x; x[k][1] = u.y; x[k][2] = u.z; x[k][3] = u.w;
+                    x[k][4] = w.x; x[k][5] = w.y; x[k][6] = w.z; x[k][7] = w.w;
                 }
-            }
+                if (Q8 && r0 == t / CPR) {                    // (the first loads are on their way)
+                    ok = warp_wait(&B.mode, 0, ab, a.err);
+                    half = B.half == 3;
+                }
 #pragma unroll
-            for (int k = 0; k < NB; ++k) {
-                const int r = r0 + k * RPP, rr = r & (kBlkQ - 1);
-                *reinterpret_cast<uint4*>(sQ + (r / kBlkQ) * S::kQBytes + (ch >> 3) * kHalf + rr * 128 + (((ch & 7) ^ (rr & 7)) << 4)) = w[k];
+                for (int k = 0; k < NB; ++k) {
+                    const int r = r0 + k * RPP;
+                    uint32_t hi[4], lo[4];
+                    if (half) {
+                        const float f = half_factor(x[k], r);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float y = x[k][2 * i] * f, z = x[k][2 * i + 1] * f;
+                            hi[i] = pack_f16(y, z);
+                            lo[i] = pack_f16(y - f16_round(y), z - f16_round(z));
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            hi[i] = pack_bf16(x[k][2 * i], x[k][2 * i + 1]);
+                            lo[i] = pack_bf16_lo(x[k][2 * i], x[k][2 * i + 1]);
+                        }
+                    }
+                    *q_piece(r) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *q_piece(r + kBlkQ) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+            } else {
+                uint4 w[NB];
+#pragma unroll
+                for (int k = 0; k < NB; ++k) {
+                    const int r = r0 + k * RPP, qi = J.q0 + r;
+                    w[k] = make_uint4(0, 0, 0, 0);
+                    if (r >= J.nq) continue;
+                    const long long off = (qi / G) * a.q_stride + (J.g * G + qi % G) * HD + ch * 8;
+                    if (a.q_vec) {
+                        w[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + off));
+                    } else {
+                        const unsigned short* p = static_cast<const unsigned short*>(a.q) + off;
+                        w[k] = make_uint4(p[0] | (uint32_t)p[1] << 16, p[2] | (uint32_t)p[3] << 16,
+                                          p[4] | (uint32_t)p[5] << 16, p[6] | (uint32_t)p[7] << 16);
+                    }
+                }
+                if (Q8 && r0 == t / CPR) {                    // (the first loads are on their way)
+                    ok = warp_wait(&B.mode, 0, ab, a.err);
+                    half = B.half == 3;
+                }
+                if (half) {
+#pragma unroll
+                    for (int k = 0; k < NB; ++k) {
+                        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                        float x[8];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            x[2 * i] = __uint_as_float(u[i] << 16);
+                            x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+                        }
+                        const float f = half_factor(x, r0 + k * RPP);
+                        w[k] = make_uint4(pack_f16(x[0] * f, x[1] * f), pack_f16(x[2] * f, x[3] * f), pack_f16(x[4] * f, x[5] * f),
+                                          pack_f16(x[6] * f, x[7] * f));
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < NB; ++k) *q_piece(r0 + k * RPP) = w[k];
             }
         }
         fence_async_smem();
@@ -352,9 +401,10 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
             const float2 cc = make_float2(c, c), mm = make_float2(-mu, -mu);
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             auto exponentials = [&](auto f16) {
+                constexpr bool kSplit = QF32 && !decltype(f16)::value;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t p[16];
+                    uint32_t p[16], pl[kSplit ? 16 : 1];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float2 x = fma2(make_float2(__uint_as_float(r[c][2 * i]), __uint_as_float(r[c][2 * i + 1])), cc, mm);
@@ -362,8 +412,10 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                         x.y = ex2(x.y);
                         sum[i & 1] = add2(sum[i & 1], x);
                         p[i] = f16.value ? pack_f16(x.x, x.y) : bf16x2(x.x, x.y);
+                        if constexpr (kSplit) pl[i] = bf16x2(x.x - __uint_as_float(p[i] << 16), x.y - __uint_as_float(p[i] & 0xFFFF0000u));
                     }
                     tmem_st16(tS + 16 * c, p);                // P's columns lie over S columns
+                    if constexpr (kSplit) tmem_st16(tS + 64 + 16 * c, pl);
                 }
             };
             if (half) exponentials(std::true_type{});
@@ -516,6 +568,7 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
             tc_fence_after();
             // A and B in bf16, or in f16 (both format fields zero)
             const uint32_t types = Q8 && B.half == 3 ? ~((1u << 7) | (1u << 10)) : ~0u;
+            const bool split_p = QF32 && types == ~0u;
             const uint32_t kIdS = idesc_bf16_f32(kBlkQ, kBlkK) & types;
             const uint32_t kIdO = (idesc_bf16_f32(kBlkQ, HD) | (1u << 16)) & types;     // B is MN-major
             int ks_ = 0, vs_ = 1;                             // ring slots of the next K and V tiles
@@ -525,6 +578,14 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                 for (int ks = 0; ks < HD / 16; ++ks) {
                     const uint32_t o = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
                     tc_mma_f16(tmem + i * 128, q0 + o, k0 + o, kIdS, ks > 0);
+                }
+                if constexpr (QF32) {
+                    const uint64_t ql = q0 + (S::kQBytes >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < HD / 16; ++ks) {
+                        const uint32_t o = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+                        tc_mma_f16(tmem + i * 128, ql + o, k0 + o, kIdS, 1);
+                    }
                 }
                 tc_commit(&B.s_full[i]);
                 if (!J.two || i == 1) ks_ = ks_ + 2 >= NST ? ks_ + 2 - NST : ks_ + 2;
@@ -549,6 +610,8 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                     for (int ks = 0; ks < steps; ++ks)
                         tc_mma_f16_ts(d, p + 8 * ks, v0 + ks * (2048 >> 4), kIdO, n > 1 || ks > 0);
                 }
+                if (split_p)
+                    for (int ks = 0; ks < steps; ++ks) tc_mma_f16_ts(d, p + 64 + 8 * ks, v0 + ks * (2048 >> 4), kIdO, 1);
                 if (!J.two || i == 1) vs_ = vs_ + 2 >= NST ? vs_ + 2 - NST : vs_ + 2;
                 if (n + 2 < J.n_jobs) scores(i);
             }
@@ -708,15 +771,15 @@ bool attend_tile_ok(const spec_kv* pre) { return pre->q8 || pre->tmaps; }
 
 // CTAs a pair of query tiles, one CTA an SM: the choice whose longest CTA ends
 // soonest, counted in key tiles.  A turn costs about 12000 cycles beyond its keys
-// (queries in, pipeline start, state out), a key tile 1500 a tile of query vectors;
+// (queries in, pipeline start, state out), a key tile 1500 a tile of query vectors (f32: 3000);
 // cuts that fall on heads (a multiple of Hkv CTAs) need one turn, others two.
 // (64 samples x 8 rows over 32768 tokens: 19 CTAs a pair 182 us, the next
 // multiple, 16, 206; 8 chains over 4096 tokens with 32 heads: 152 CTAs 22 us, 128 15 us.)
-int attend_tile_ctas(const spec_model* m, const AttendSpan& span, int prompt_cap) {
+int attend_tile_ctas(const spec_model* m, const AttendSpan& span, bool q_f32, int prompt_cap) {
     const spec_model_config& c = m->cfg;
-    const int H = c.n_kv_heads, NQ = span.T * (c.n_heads / H), pairs = (NQ + 2 * kBlkQ - 1) / (2 * kBlkQ);
+    const int H = c.n_kv_heads, NQ = span.T * (c.n_heads / H), QV = tile_vectors(q_f32), pairs = (NQ + QV - 1) / QV;
     const long long W = (long long)H * std::max(1, (prompt_cap + kBlkK - 1) / kBlkK);
-    const int turn = NQ > kBlkQ ? 4 : 8;
+    const int turn = NQ > kBlkQ || q_f32 ? 4 : 8;
     int best = 1;
     long long least = -1;
     for (int n = 1; n <= m->num_sms && (n == 1 || 2 * n <= W); ++n) {
@@ -729,27 +792,29 @@ int attend_tile_ctas(const spec_model* m, const AttendSpan& span, int prompt_cap
 }
 int attend_tile_ranges(const spec_model* m, int ctas) { return ctas / m->cfg.n_kv_heads + 2; }
 
-template <int HD, bool Q8>
+template <int HD, bool Q8, bool QF32>
 static int launch_tile(const spec_kv* pre, const AttendArgs& a, cudaStream_t st) {
     using S = TileShape<HD, Q8>;
     static std::atomic<unsigned long long> set{0};            // devices whose kernel has its shared memory
     const unsigned long long bit = 1ull << (pre->m->device & 63);
     cudaError_t e;
     if (!(set.load() & bit)) {
-        e = cudaFuncSetAttribute(attend_tile_kernel<HD, Q8>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        e = cudaFuncSetAttribute(attend_tile_kernel<HD, Q8, QF32>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
         if (e != cudaSuccess) return check_cuda(e, "attention tile kernel attribute");
         set.fetch_or(bit);
     }
-    const int NQ = a.span.T * (a.H / a.Hkv);
-    const dim3 grid((unsigned)((NQ + 2 * kBlkQ - 1) / (2 * kBlkQ) * a.tile_ctas));
-    e = launch_k(pre->m->pdl, attend_tile_kernel<HD, Q8>, grid, dim3(S::kThreads), S::kSmem, st, a, pre->tm_k64, pre->tm_v64);
+    const int NQ = a.span.T * (a.H / a.Hkv), QV = tile_vectors(QF32);
+    const dim3 grid((unsigned)((NQ + QV - 1) / QV * a.tile_ctas));
+    e = launch_k(pre->m->pdl, attend_tile_kernel<HD, Q8, QF32>, grid, dim3(S::kThreads), S::kSmem, st, a, pre->tm_k64, pre->tm_v64);
     ++pre->m->launches;
     return check_cuda(e, "attention tile launch");
 }
 
 int launch_attend_tile(const spec_kv* pre, const AttendArgs& a, cudaStream_t st) {
-    if (pre->m->cfg.head_dim == 128) return pre->q8 ? launch_tile<128, true>(pre, a, st) : launch_tile<128, false>(pre, a, st);
-    return pre->q8 ? launch_tile<64, true>(pre, a, st) : launch_tile<64, false>(pre, a, st);
+    int (*const launch[8])(const spec_kv*, const AttendArgs&, cudaStream_t) = {
+        launch_tile<64, false, false>, launch_tile<64, false, true>, launch_tile<64, true, false>, launch_tile<64, true, true>,
+        launch_tile<128, false, false>, launch_tile<128, false, true>, launch_tile<128, true, false>, launch_tile<128, true, true>};
+    return launch[(pre->m->cfg.head_dim == 128 ? 4 : 0) + (pre->q8 ? 2 : 0) + (a.q_f32 ? 1 : 0)](pre, a, st);
 }
 
 }  // namespace spec

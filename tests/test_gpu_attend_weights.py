@@ -1,5 +1,5 @@
-"""Weights far below a row's largest one and values far below the others: what the attention's operands of 16 bits must
-not lose."""
+"""Weights far below a row's largest one, values far below the others, and queries in 32 bits: what the attention's
+operands of 16 bits must not lose."""
 import math
 
 import numpy as np
@@ -94,3 +94,102 @@ def test_a_value_far_below_the_others(dim, rows):
     # weights below 2^-126 may be flushed to zero; the reference's are below 2^-170
     assert (ref.abs() > 2.0 ** -117).all()
     assert ((out - ref).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_forward_calls_keep_queries_of_32_bits_under_any_dispatch(dim, q8):
+    """A verification over a prompt held in a short and in a long cache: one goes to the row kernel, one to the tile
+    kernel, everything else is the same.  One layer with an identity O projection, no MLP and an identity LM head, so
+    that a logit is an element of (embedding + attention) / rms."""
+    from _attend_util import attend64
+    from _gpu_util import cuda_i32, lib, to_cuda
+    from oracle.decoder import linear, rms_norm, rope
+    from speculative_decoding_verify_04_gb300 import spec
+    from synthetic import ModelShape, make_tokens, make_weights, weights_to_numpy
+    lib()
+    H, Hkv, n, B, R = 512 // dim, 128 // dim, 300, 4, 4
+    shape = ModelShape(1, 512, H, Hkv, dim, 512, 512, 0, "bf16")
+    w = make_weights(shape, 70)
+    lw = w["layers"][0]
+    for name, std in (("wq", 5.0), ("wk", 1.0), ("wv", 1.0)):
+        lw[name] = (lw[name].float() * (std / 0.02 / math.sqrt(512))).to(torch.bfloat16)
+    lw["wo"], w["lm_head"] = torch.eye(512).to(torch.bfloat16), torch.eye(512).to(torch.bfloat16)
+    lw["w_down"].zero_()
+    wn = weights_to_numpy(w)
+    model = spec.Model(shape, to_cuda(w), max_rows=64, max_batch=B, max_position=512)
+    g = torch.Generator(device="cuda").manual_seed(71)
+    k, v = (torch.randn(1, n, Hkv, dim, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    toks = np.stack([make_tokens(R, 512, seed=72 + b) for b in range(B)])
+    got = []
+    # 16 rows of 4 heads a KV head are 64 vectors: the tile kernel takes them where the cache is long
+    for cap in (n, 40000):
+        pre, kv = spec.KVCache(model, 1, cap, q8=q8), spec.KVCache(model, B, 64, q8=q8)
+        pre.import_rows(0, 0, k, v)
+        pre.set_lengths([n])
+        kv.set_prefix(pre)
+        logits = torch.empty(B, R, 512, device="cuda")
+        launches = model.launch_count()
+        spec.spec_verify(model, kv, [R] * B, cuda_i32(toks), R, logits=logits)
+        got.append((logits.double().cpu(), model.launch_count() - launches))
+    (a, la), (b, lb) = got
+    assert lb == la + 1                                  # the tile kernel is one launch more
+    pk, pv = (x[0].double().cpu() for x in pre.export_rows(0, 0, 1, 0, n))
+    for s in range(B):
+        h = np.asarray(wn["embed"][toks[s]], dtype=np.float64)
+        q = linear(rms_norm(h, wn["layers"][0]["attn_norm"], shape.rms_eps), wn["layers"][0]["wq"]).reshape(R, H, dim)
+        q = torch.from_numpy(np.stack([rope(q[t], n + t, shape.rope_theta) for t in range(R)]))
+        nk, nv = (x[0].double().cpu() for x in kv.export_rows(s, 0, 1, 0, R))
+        sees = np.concatenate([np.ones((R, n), dtype=bool), np.tril(np.ones((R, R), dtype=bool))], 1)
+        out, mass, big = attend64(q, torch.cat([pk, nk]), torch.cat([pv, nv]), 1.0 / math.sqrt(dim), sees)
+        # a path's error: queries in two bf16 parts, each off by 2^-8 of what it holds (together 2^-16), and f32 sums of
+        # two products a dim; weights off by d move the mean by 2 d mass; a weight's operand is off by 2^-16 (bf16 pair)
+        # or 2^-11 (f16, 8-bit caches; 2^-32 of the row's largest below 2^-24 of it); f32 sums over the keys
+        d = (2.0 ** -16 + 2 * dim * 2.0 ** -24) * big[..., None] + 2.0 ** -21
+        e = (2 * d + (2.0 ** -11 if q8 else 2.0 ** -16) + (n + R) * 2.0 ** -24) * mass
+        if q8:
+            e = e + (n + R) * 2.0 ** -32 * torch.cat([pv, nv]).abs().amax()
+        e = (2 * e + 2 * 2.0 ** -16 * out.abs()).reshape(R, 512)       # two paths, each output as a bf16 pair
+        y = torch.from_numpy(h) + out.reshape(R, 512)
+        rms = (y.square().mean(-1, keepdim=True) + shape.rms_eps).sqrt()
+        y = y / rms
+        # the logits: the same norm of both, its input a bf16 pair
+        tol = e / rms + y.abs() * (e.amax(-1, keepdim=True) / rms + 2.0 ** -14)
+        off = (a[s] - b[s]).abs()
+        assert ((a[s] - y).abs() < 0.05).all()           # (the formula is the model's)
+        assert (off <= tol).all(), (off / tol).amax()
+    assert model.device_error() == 0
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_32_layers_over_a_shared_prompt(q8):
+    """A deep model's verification over a prompt in the tile kernel: against the oracle within the bound of the bf16
+    path, and (8-bit prompts, whose values the oracle does not round) against the row kernel's."""
+    from _gpu_util import cuda_i32, lib, model_pair
+    from oracle import spec as OS
+    from speculative_decoding_verify_04_gb300 import spec
+    from synthetic import ModelShape, make_tokens
+    from test_gpu_shared_prompt import TOL
+    lib()
+    B, R, n = 6, 4, 150
+    model, dec, shape = model_pair(ModelShape(32, 256, 8, 2, 64, 512, 2048, 1, "bf16"), seed=75, max_rows=64, max_batch=B,
+                                   max_position=512)
+    prompt = make_tokens(n, shape.vocab, seed=76)
+    toks = np.stack([make_tokens(R, shape.vocab, seed=77 + b) for b in range(B)])
+    pre, kv = spec.KVCache(model, 1, n, q8=q8), spec.KVCache(model, B, 64, q8=q8)
+    spec.spec_prefill(model, pre, 0, cuda_i32(prompt))
+    kv.set_prefix(pre)
+    got = torch.empty(B, R, shape.vocab, device="cuda")
+    spec.spec_verify(model, kv, [R] * B, cuda_i32(toks), R, logits=got)     # 96 vectors a KV head
+    for b in range(B):
+        if q8:
+            # one sequence's 16 vectors
+            want = torch.empty(R, shape.vocab, device="cuda")
+            spec.spec_verify(model, kv, [R], cuda_i32(toks[b]), R, logits=want)
+            want = want.cpu().numpy()
+        else:
+            cache = dec.new_cache(n + R)
+            dec.prefill(cache, prompt)
+            want = OS.verify(dec, cache, n, dec.embed(toks[b]), 0)
+        assert np.abs(got[b].cpu().numpy() - want).max() < TOL, b
+    assert model.device_error() == 0
