@@ -397,6 +397,11 @@ logprobs_kernel(const __grid_constant__ LogprobArgs a) {
     }
 }
 
+// segments' maxima and keys, and the listed tokens
+constexpr size_t lp_smem(int n_seg, int n_top) {
+    return n_top ? (size_t)(n_seg + 1) / 2 * 8 + ((size_t)n_seg + (size_t)(n_top < n_seg ? n_top : n_seg) * kLpSeg) * 8 : 0;
+}
+
 }  // namespace spec
 
 using namespace spec;
@@ -430,9 +435,12 @@ extern "C" int spec_logprobs(const void* logits, int32_t dtype, int64_t lg_strid
     while (C < kLpMaxCtas && (long long)rows * C < 3 * sms && n_seg / (2 * C) >= 16) C *= 2;
     void (*f)(LogprobArgs) = dtype == SPEC_DTYPE_BF16 ? (n_top ? logprobs_kernel<__nv_bfloat16, 1> : logprobs_kernel<__nv_bfloat16, 0>)
                                                       : (n_top ? logprobs_kernel<float, 1> : logprobs_kernel<float, 0>);
-    const size_t smem = n_top ? (size_t)(n_seg + 1) / 2 * 8 + ((size_t)n_seg + (size_t)std::min(n_top, n_seg) * kLpSeg) * 8 : 0;
-    if (smem > 48 * 1024)
-        SPEC_TRY(check_cuda(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem), "spec_logprobs attribute"));
+    const size_t smem = lp_smem(n_seg, n_top);
+    if (smem > 48 * 1024) {
+        // the most that any call takes: another thread's call may come between this one's two steps
+        constexpr int most = (int)lp_smem((kLpMaxVocab + 7 + kLpSeg - 1) / kLpSeg, kLpMaxTop);
+        SPEC_TRY(check_cuda(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, most), "spec_logprobs attribute"));
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * C));
     cfg.blockDim = dim3(kLpThreads);
