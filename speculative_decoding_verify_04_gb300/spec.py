@@ -268,6 +268,8 @@ class KVCache:
     def set_prefix(self, prefix, seq=0):
         """Every sequence continues sequence ``seq`` of the cache ``prefix``, whose
         slots all of them see (None: no prefix).  The prefix is kept alive."""
+        if prefix is not None and not prefix.handle:
+            raise SpecError("set_prefix: the prefix is closed")
         _check(load().spec_kv_set_prefix(self.handle, None if prefix is None else prefix.handle, int(seq)))
         self.prefix = prefix
 
