@@ -581,7 +581,11 @@ int spec_schedule_decay(const int32_t* generated, const int32_t* total, int32_t 
  * cudaFree may imply.  The call's scratch -- the GEMM split-K partial tiles
  * and arrival counters and the attention split partials and counters -- comes
  * from a 32 MiB static __device__ array that every GPU loading the library
- * keeps until the process exits.  The first call on a device looks up the
+ * keeps until the process exits.  Over an 8-bit cache or one with a prefix the
+ * attention's partial states and the rows to be quantised lie in the model's
+ * workspace instead (allocated by spec_model_create, so nothing is allocated
+ * here either): such a call must not overlap any other call on the model.  The
+ * first call on a device looks up the
  * array's device address (cudaGetSymbolAddress) and caches it; make that
  * first call before any stream capture.  The array is shared by every call
  * and keeps the last call's contents, so each call clears the counters it

@@ -8,7 +8,9 @@
 // point takes the GEMM split-K partial tiles and arrival counters, and the
 // attention split partials and counters, from `g_verify_scratch` below.  Every
 // GPU that loads the library holds this array (kScratchBytes) until the
-// process exits.
+// process exits.  8-bit caches and caches with a prefix leave their partial
+// states, and their new rows before they are quantised, in the model's
+// workspace, which was allocated with the model.
 #include <mutex>
 
 #include "model.cuh"
@@ -68,6 +70,7 @@ extern "C" int spec_verify_noalloc(spec_model* m, spec_kv* kv, int32_t batch, co
     if (!m || !kv || !n_rows || !tokens) return set_error(SPEC_ERR_ARG, "spec_verify_noalloc: null pointer");
     if (kv->m != m) return set_error(SPEC_ERR_ARG, "spec_verify_noalloc: cache of another model");
     if (batch < 1 || batch > kv->batch) return set_error(SPEC_ERR_ARG, "spec_verify_noalloc: bad batch");
+    SPEC_TRY(kv_check_prefix(kv, "spec_verify_noalloc"));
     const spec_model_config& c = m->cfg;
     int T = 0, max_r = 1;
     for (int b = 0; b < batch; ++b) {
