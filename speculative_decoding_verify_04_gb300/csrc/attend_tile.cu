@@ -674,8 +674,10 @@ attend_tile_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__
                 }
                 // they fit where they are zeros; what they hold else lies below f16's range
                 const uint4* y = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(i & 1 ? a.pre.v : a.pre.k) + row * HD);
+#pragma unroll 1
                 for (; least && fits; least &= least - 1) {
                     const uint4* at_b = y + (__ffs(least) - 1) * (HD / 16);
+#pragma unroll 1
                     for (int p = 0; p < HD / 16; ++p) {
                         const uint4 x = __ldg(at_b + p);
                         if ((x.x | x.y | x.z | x.w) & 0x7F7F7F7Fu) fits = false;
