@@ -223,6 +223,9 @@ int spec_kv_create_paged(spec_model* m, int32_t batch, int32_t max_ctx, int32_t 
  *   y = e4m3(x * 2^-e)      nearest, ties to even, saturating
  * and stands for y * 2^e, which is always a bf16 number: spec_kv_export returns
  * it exactly.  Infinities count as no magnitude and saturate, NaN stays NaN.
+ * The forward calls' attention over such rows takes queries in two parts, as
+ * over bf16 rows, and probabilities as one f16 number: off by 2^-11 of
+ * themselves, or by 2^-32 of the row's largest where that is more.
  * About half the memory of a bf16 cache (hd + 1 bytes a row instead of 2 hd).
  * bf16 models only (SPEC_ERR_UNSUPPORTED).  sync. */
 int spec_kv_create_q8(spec_model* m, int32_t batch, int32_t max_ctx, int32_t page, int32_t n_pages,
@@ -237,7 +240,10 @@ int spec_kv_create_q8(spec_model* m, int32_t batch, int32_t max_ctx, int32_t pag
  * the page calls leave the prompt alone.  Set it before kv's first rows: rows
  * that were written earlier keep the position ids they were written with.  The
  * prompt's length is read when a call runs, so it must not change while kv
- * depends on it.  prefix NULL detaches.  Either cache may be contiguous, paged,
+ * depends on it.  The forward calls' queries and probabilities enter the
+ * products over the prompt as pairs of bf16 numbers (off by 2^-16 of
+ * themselves), as they do without one; 8-bit prompts as spec_kv_create_q8
+ * says.  prefix NULL detaches.  Either cache may be contiguous, paged,
  * bf16 or 8-bit; both belong to one bf16 model; a prefix has no prefix of its
  * own.  spec_kv_destroy(prefix) makes the calls on kv fail with SPEC_ERR_ARG
  * until kv gets a new prefix or NULL.  Not while a call on kv is being captured
@@ -258,7 +264,8 @@ int spec_kv_set_prefix(spec_kv* kv, spec_kv* prefix, int32_t seq);
  *   out      device bf16 [T][H][hd], row stride out_stride
  * Row j of sequence b sees the prompt of the cache's prefix, the slots below
  * s_b and the rows of its chain or tree path; scores are q.k / sqrt(hd), softmax
- * statistics and sums are f32.  Head h reads KV head h / (H / Hkv).  A row whose
+ * statistics and sums are f32, and a probability is off by at most 2^-8 of
+ * itself (one bf16 number) in its product with v.  Head h reads KV head h / (H / Hkv).  A row whose
  * scores are all -inf, or hold NaN or +inf, gives NaN, as one that sees a new row
  * with a NaN or an infinity in v; what a row does not see has no influence on it.
  * The model's workspace is used: one stream at a time, as every call on a model.

@@ -20,9 +20,9 @@ namespace spec {
 
 constexpr int kRowThreads = 128;
 // Query vectors a KV head up to which the row kernel takes the prompt: 16, and 64 where (blocks of 16)
-// x KV heads x slots are few.  Measured per call (us, row kernel / tile kernel; 8 KV heads, 8 bits):
-// 16 vectors over 32768 slots 35 / 56; 32 over 32768 56 / 57 (bf16 73 / 52); 32 over 4096 19 / 25;
-// 64 over 4096 29 / 26; 64 over 512 17 / 25; 128 over 512 19 / 24.
+// x KV heads x slots are few.  Measured per call (us, row kernel / tile kernel; 8 KV heads, 8 bits, sequences of
+// one row behind 32 slots of their own): 16 vectors over 32768 slots 31 / 51; 32 over 32768 44 / 53 (bf16
+// 50 / 48); 32 over 4096 19 / 24; 64 over 4096 27 / 28; 64 over 512 17 / 25; 128 over 512 24 / 30.
 constexpr int kRowVectors = 16, kRowVectorsShort = 64, kRowKeysShort = 65536;
 // least keys of a range: one sequence of 256 slots takes 12.8 us a call at 256, 10.8 at 128, 14.5 at 512; 16 of
 // 10 rows over 671 slots 33 at 256, 35 at 128, 37 at 512

@@ -28,7 +28,8 @@
 // attention splits Q and P wherever it runs: P in one bf16 alone is past their bound in 32 layers)
 // take two operands, hi + lo, each with products of its own: Q in either type, P in bf16, the lo
 // part in the half of S's columns that P leaves; f16 keeps one P.  Q's lo part lies where the
-// second tile of query vectors would, so a CTA has one tile.
+// second tile of query vectors would, so a CTA has one tile and a K or V tile serves half as many:
+// 64 x 8 rows of 32 heads over 8, 32768 tokens, take about 510 us instead of 182 (8 bits 606 instead of 280).
 //
 // 128 query vectors a stream is what one MMA takes and what one thread a vector serves;
 // two streams are what the 512 columns of tensor memory hold (S and O of 128 each).  Keys

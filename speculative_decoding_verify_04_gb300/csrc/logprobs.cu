@@ -8,8 +8,8 @@
 // by the same rule.  The difference is taken before the product, so rows masked by
 // the type's lowest value do not overflow.  Bound by reading the logits once (512 f32
 // rows of 131072: 42 us, 6.3 TB/s, 94 % of the measured copy rate; with 20
-// alternatives 54); half-precision rows by the instructions, about six a logit (333
-// rows of 100003: 21 us, 3.2 TB/s; with one alternative 27).
+// alternatives 54); half-precision rows by the instructions, about twenty a logit: 60 %
+// of the issue slots (333 rows of 100003: 21 us, 3.2 TB/s; with one alternative 27).
 //
 // The n best tokens come from the same pass: every 256 consecutive logits (one
 // step of a warp) leave their maximum in shared memory.  The n best by (value
