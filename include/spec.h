@@ -141,6 +141,32 @@ typedef struct spec_aimd_schedule {
     int32_t down_num, down_den;  /* e.g. 7 / 10                                   */
 } spec_aimd_schedule;
 
+/* Rotary positions of rows (spec_rope). */
+#define SPEC_ROPE_AXES 4
+typedef struct spec_rope_config {
+    int32_t n_heads, n_kv_heads;   /* heads of q's and k's rows; 0: no such rows        */
+    int32_t head_dim;              /* 2 .. 256                                           */
+    int32_t dtype;                 /* of all four: SPEC_DTYPE_F32 or SPEC_DTYPE_BF16      */
+    int32_t axes;                  /* position axes, 1 .. 4 (for example time, height, width) */
+    int32_t sections[SPEC_ROPE_AXES];  /* frequency pairs of each axis, n in all         */
+    int32_t interleaved;           /* 0: the sections one after another; else the axes
+                              take the pairs in turn while their sections last           */
+    double  theta;                 /* base, 1 .. 1e30                                    */
+} spec_rope_config;
+
+/* How spec_sample_logits draws: one setting for all rows, or a device array [rows]
+ * where the pointer is not NULL. */
+typedef struct spec_sample_config {
+    float   temperature;   /* 0: the best token; else 1e-30 .. 1e30               */
+    float   top_p;         /* >= 1: no nucleus; else 0 .. 1                       */
+    float   min_p;         /* 0 .. 1, 0: none                                     */
+    int32_t top_k;         /* 0 (or vocab and more): no top-k                     */
+    const float* temperatures;
+    const float* top_ps;
+    const float* min_ps;
+    const int32_t* top_ks;
+} spec_sample_config;
+
 /* Last error message of the calling thread ("" if none).  The string stays
  * valid until the next failing call on the same thread. */
 const char* spec_last_error(void);
@@ -251,6 +277,26 @@ int spec_kv_create_q8(spec_model* m, int32_t batch, int32_t max_ctx, int32_t pag
  * Host only. */
 int spec_kv_set_prefix(spec_kv* kv, spec_kv* prefix, int32_t seq);
 
+/* Attention over a window, for layers [layer0, layer0 + n_layers) of `kv`: from
+ * this call on a row of index i of its sequence sees the key of index t (of what it
+ * would see without a window) only where
+ *   i - t < window   or   t < sinks:
+ * the last `window` tokens, itself among them, and the sequence's first `sinks`.  The
+ * index counts the slots of the cache's prefix, if it has one, and then the
+ * sequence's own; a candidate row's index is that of its position (its depth behind
+ * the committed slots), so a tree's node sees the last of its own path.  Position
+ * ids stay what they are.  window 0 takes the windows of these layers away.  Layers may
+ * differ (window layers between layers that see everything).  It holds for every call
+ * that reads the cache (spec_attend, spec_prefill, the drafts and verifications)
+ * and is read when a call is enqueued: a captured call keeps the window that it was
+ * captured with.  Keys that no row sees are not read (but for the rest of a tile of
+ * 16), and what a row does not see has no influence on it; the cache keeps the rows
+ * all the same.  The window is kv's own: of a cache that continues another one, the
+ * other's window does not count.  In the forward calls, queries and probabilities
+ * enter the products as over an 8-bit or prompted cache (spec_kv_create_q8,
+ * spec_kv_set_prefix).  bf16 models only.  Host only. */
+int spec_kv_set_window(spec_kv* kv, int32_t layer0, int32_t n_layers, int32_t window, int32_t sinks);
+
 /* Attention of one layer over the cache for the rows of sequences [0, batch),
  * as the forward calls run it, for callers with layers of their own.
  *   n_rows   host int32 [batch]: rows of sequence b, each in [0, 64], sum T <= max_rows
@@ -263,7 +309,8 @@ int spec_kv_set_prefix(spec_kv* kv, spec_kv* prefix, int32_t seq);
  *   tree_parent  as for spec_verify (host, shared by all sequences; NULL: chains)
  *   out      device bf16 [T][H][hd], row stride out_stride
  * Row j of sequence b sees the prompt of the cache's prefix, the slots below
- * s_b and the rows of its chain or tree path; scores are q.k / sqrt(hd), softmax
+ * s_b and the rows of its chain or tree path, of all these what the layer's window
+ * leaves (spec_kv_set_window); scores are q.k / sqrt(hd), softmax
  * statistics and sums are f32, and a probability is off by at most 2^-8 of
  * itself (one bf16 number) in its product with v.  Head h reads KV head h / (H / Hkv).  A row whose
  * scores are all -inf, or hold NaN or +inf, gives NaN, as one that sees a new row
@@ -277,6 +324,28 @@ int spec_kv_set_prefix(spec_kv* kv, spec_kv* prefix, int32_t seq);
 int spec_attend(spec_kv* kv, int32_t layer, int32_t batch, const int32_t* n_rows, const void* q,
                 int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                 const int32_t* tree_parent, void* out, int64_t out_stride, void* stream);
+
+/* Query and key rows with their positions encoded, for callers with layers of
+ * their own: what spec_attend takes.  A head's first 2 n dims (n = the sum of the
+ * sections, 2 n <= head_dim) are the pairs (x_i, x_{i+n}); pair i is turned by
+ *   a_i = p theta^(-i / n),  p the row's position on the axis of pair i:
+ *   y_i = x_i cos a_i - x_{i+n} sin a_i,  y_{i+n} = x_{i+n} cos a_i + x_i sin a_i
+ * and the other dims are copied (with theta = the model's and one section of
+ * head_dim / 2 as the forward calls do it).  Angles are exact to 2^-28 however far
+ * the position, the arithmetic is f32, rounded once.
+ *   rows       rows of q [rows][n_heads][head_dim] and k [rows][n_kv_heads][head_dim]
+ *              (device, row strides in elements) and of their results q_out and k_out,
+ *              which may be q and k themselves (same stride) but not overlap them else
+ *   positions  device int32 [axes][rows], axis stride pos_stride (any value, negative
+ *              ones too); or NULL, and the rows are those of a call on `kv` (batch,
+ *              n_rows, tree_parent as for spec_attend, n_rows adding up to rows): row j
+ *              of sequence b at s_b + j, in a tree at s_b + depth, behind the cache's
+ *              prefix if it has one.  The lengths are read on the device.
+ * No model is needed with positions.  async. */
+int spec_rope(const spec_rope_config* cfg, int32_t rows, const void* q, int64_t q_stride, void* q_out,
+              int64_t q_out_stride, const void* k, int64_t k_stride, void* k_out, int64_t k_out_stride,
+              const int32_t* positions, int64_t pos_stride, spec_kv* kv, int32_t batch, const int32_t* n_rows,
+              const int32_t* tree_parent, void* stream);
 
 /* Pages left in the pool of a paged cache (0 for a contiguous one).  sync. */
 int spec_kv_free_pages(spec_kv* kv, int32_t* host_free, void* stream);
@@ -509,6 +578,32 @@ int spec_logprobs(const void* logits, int32_t dtype, int64_t lg_stride, int32_t 
                   float temperature, const int32_t* tokens, float* logprob, float* entropy, int32_t n_top,
                   int32_t* top_ids, float* top_logprobs, void* stream);
 
+/* One token a row of logits from given random numbers, after temperature, top-k,
+ * top-p and min-p, in this order.  With w_i = exp((x_i - max x) / temperature):
+ *   top_k   the k largest logits stay, ties to the lower id
+ *   top_p   of those the shortest run, by decreasing logit (ties to the lower id),
+ *           whose w add up to at least top_p of theirs (one token at least)
+ *   min_p   of those the w_i >= min_p (the best token's w is 1)
+ * and the token is the first by id at which the sum of the w that stay is more than u
+ * times their sum; temperature 0 takes the best token (ties to the lower id).
+ *   logits   device, `dtype` (SPEC_DTYPE_F32 or SPEC_DTYPE_BF16), row r at
+ *            logits + r * lg_stride elements (lg_stride >= vocab); -inf is a
+ *            masked token
+ *   u        device f32 [rows], each in [0, 1)
+ *   tokens   device int32 [rows] out
+ *   logprob  device f32 [rows] out, nullable: log of the token's probability among
+ *            those that stay
+ *   probs    device f32 out, nullable, row r at probs + r * p_stride: that
+ *            distribution, zeros elsewhere (the p or q of spec_accept)
+ * A weight is exact to 2^-38 of itself and to half of 2^-q of the best token's
+ * (q = 62 - ceil log2 vocab, 45 for 131072 tokens), and sums are exact: the token is that
+ * of the exact weights unless u or a cut lies that close to a border.  Calls of any number of rows give the same bits.  A row without
+ * a distribution (NaN or +inf in it, or every token masked), and one whose settings
+ * by row or u are out of range, gets token -1 and NaN.  vocab <= 1048576.  async. */
+int spec_sample_logits(const void* logits, int32_t dtype, int64_t lg_stride, int32_t rows, int32_t vocab,
+                       const float* u, const spec_sample_config* cfg, int32_t* tokens, float* logprob,
+                       float* probs, int64_t p_stride, void* stream);
+
 /* Greedy acceptance from target logits (the unfused form of spec_verify's
  * fused acceptance).  logits device f32 [batch][n_rows][vocab]; tokens device
  * int32 [batch][n_rows]; tree_parent host int32 [n_rows] or NULL (chain);
@@ -588,7 +683,7 @@ int spec_schedule_decay(const int32_t* generated, const int32_t* total, int32_t 
  * cudaFree may imply.  The call's scratch -- the GEMM split-K partial tiles
  * and arrival counters and the attention split partials and counters -- comes
  * from a 32 MiB static __device__ array that every GPU loading the library
- * keeps until the process exits.  Over an 8-bit cache or one with a prefix the
+ * keeps until the process exits.  Over an 8-bit cache or one with a prefix or a window the
  * attention's partial states and the rows to be quantised lie in the model's
  * workspace instead (allocated by spec_model_create, so nothing is allocated
  * here either): such a call must not overlap any other call on the model.  The

@@ -98,8 +98,9 @@ SPEC_DEV void copies_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) :
 
 // first row of the 16-key tile at kt (0 past the range's end): tiles start at multiples of 16 and pages
 // hold a multiple of 16 slots, so no tile crosses a page
-SPEC_DEV long long tile_row(const AttendArgs& a, const CacheView& cv, int seq, int g, int kt, int k_end) {
-    return kt < k_end ? kv_row_in_layer(cv.pages, a.Hkv, seq, g, kt) : 0;
+template <bool WIN>
+SPEC_DEV long long tile_row(const AttendArgs& a, const CacheView& cv, const KeyMap& km, int seq, int g, int kt, int k_end) {
+    return kt < k_end ? kv_row_in_layer(cv.pages, a.Hkv, seq, g, key_slot<WIN>(km, kt)) : 0;
 }
 
 // this lane's pieces of the tile at kt, whose first row is `row`, into its slots
@@ -287,9 +288,9 @@ SPEC_DEV void softmax_tile(float (&x)[2][4], float (&y)[2][4], float (&m)[2], fl
 
 // Keys [k_begin, k_end) of one (sequence, KV head) against the CTA's queries.
 // Keys below n_ctx are seen by every row; key n_ctx + x by the rows whose mask has bit x.
-template <int HD, bool Q8, bool QF32>
-SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, int g, int k_begin, int k_end, int n_ctx,
-                           const QueryPieces<HD, 16>& qp, const unsigned long long* sMask, uint4* sQ, float* sS,
+template <int HD, bool Q8, bool QF32, bool WIN>
+SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, const KeyMap& km, int seq, int g, int k_begin, int k_end,
+                           int n_ctx, const QueryPieces<HD, 16>& qp, const RowSight* sSight, uint4* sQ, float* sS,
                            float* rows, char* ring, RowState<HD>& st) {
     constexpr int KS = HD / 16, VD = HD / 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gq = lane >> 2, cq = lane & 3;
@@ -298,9 +299,9 @@ SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, in
     const char* slots = ring + warp * S::kStages * S::kBytes;
     int kt = k_begin + 16 * warp;
     // the first tiles' copies go out before the queries are taken; rows are looked up a tile before their use
-    long long row = tile_row(a, cv, seq, g, kt, k_end), row_nx = tile_row(a, cv, seq, g, kt + 64, k_end);
+    long long row = tile_row<WIN>(a, cv, km, seq, g, kt, k_end), row_nx = tile_row<WIN>(a, cv, km, seq, g, kt + 64, k_end);
     if (Q8) {
-        const long long row_2 = tile_row(a, cv, seq, g, kt + 64 * S::kStages, k_end);
+        const long long row_2 = tile_row<WIN>(a, cv, km, seq, g, kt + 64 * S::kStages, k_end);
         if (kt < k_end) copy_tile<HD, false>(a, cv, row, kt, k_end, slot0);
         copies_commit();
         if (kt + 64 < k_end) copy_tile<HD, false>(a, cv, row_nx, kt + 64, k_end, slot0 + S::kBytes);
@@ -310,7 +311,7 @@ SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, in
     load_queries<HD, QF32, 16>(a, Q8, qp, sQ, sS, rows);
     __syncthreads();
     const float c0 = sS[gq], c1 = sS[gq + 8];
-    const unsigned long long mk0 = sMask[gq], mk1 = sMask[gq + 8];
+    const RowSight see0 = sSight[gq], see1 = sSight[gq + 8];
     for (int stage = 0; kt < k_end; kt += 64, stage = stage + 1 < S::kStages ? stage + 1 : 0) {
         const char* slot = slots + stage * S::kBytes;
         auto k_piece = [&](int h, int p) { return *reinterpret_cast<const uint4*>(slot + 512 * (h * (S::kK / 2) + p) + 16 * lane); };
@@ -376,7 +377,7 @@ SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, in
             }
             row = row_nx;
         }
-        row_nx = tile_row(a, cv, seq, g, kt + 64 * (Q8 ? S::kStages + 1 : 2), k_end);
+        row_nx = tile_row<WIN>(a, cv, km, seq, g, kt + 64 * (Q8 ? S::kStages + 1 : 2), k_end);
         if (kt + 16 > k_end) {
             // values of keys past the range: their probability is zero, and zero times what the slot holds must be zero
 #pragma unroll
@@ -388,13 +389,15 @@ SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, in
         // a new row's NaN or infinity must not reach the rows that do not see it (0 * NaN): it leaves the
         // product, and the rows that see it become NaN
         uint32_t bad = 0;
-        if (kt + 16 > n_ctx) {
+        const int at_slot = key_slot<WIN>(km, kt);
+        const bool edge = at_slot + 16 > n_ctx || (WIN && at_slot < km.low_max);   // not every row sees every key
+        if (edge) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 bool b = false;
 #pragma unroll
                 for (int i = 0; i < KS; ++i) b |= not_finite2<Q8>(vb[r][i]);
-                if (kt + 4 * cq + r < n_ctx) b = false;
+                if (!WIN && kt + 4 * cq + r < n_ctx) b = false;
                 if (b)
 #pragma unroll
                     for (int i = 0; i < KS; ++i) vb[r][i] = 0u;
@@ -435,13 +438,13 @@ SPEC_DEV void attend_range(const AttendArgs& a, const CacheView& cv, int seq, in
             x[0][k] = (sc[k >> 1][k & 1] + sd[k >> 1][k & 1]) * (Q8 ? c0 * kf : c0);
             x[1][k] = (sc[k >> 1][2 + (k & 1)] + sd[k >> 1][2 + (k & 1)]) * (Q8 ? c1 * kf : c1);
         }
-        if (kt + 16 > min(n_ctx, k_end)) {                    // a tile that reaches new rows or the end
+        if (edge || kt + 16 > k_end) {                        // ... or a tile that reaches the end
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int key = kt + 4 * cq + k;
-                const bool ctx = key < n_ctx, in = key < k_end;
-                if (!(in && (ctx || ((mk0 >> ((key - n_ctx) & 63)) & 1ull)))) x[0][k] = -INFINITY;
-                if (!(in && (ctx || ((mk1 >> ((key - n_ctx) & 63)) & 1ull)))) x[1][k] = -INFINITY;
+                const int slot_k = at_slot + 4 * cq + k;
+                const bool in = kt + 4 * cq + k < k_end;
+                if (!(in && row_sees<WIN>(km, see0, slot_k, n_ctx))) x[0][k] = -INFINITY;
+                if (!(in && row_sees<WIN>(km, see1, slot_k, n_ctx))) x[1][k] = -INFINITY;
                 if ((bad >> k) & 1u) {
                     if (x[0][k] != -INFINITY) x[0][k] = __int_as_float(0x7fc00000);
                     if (x[1][k] != -INFINITY) x[1][k] = __int_as_float(0x7fc00000);
@@ -499,9 +502,9 @@ SPEC_DEV uint32_t transpose8(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
-template <int HD, bool Q8, bool QF32>
-SPEC_DEV void attend_range_few(const AttendArgs& a, const CacheView& cv, int seq, int g, int k_begin, int k_end, int n_ctx,
-                               const QueryPieces<HD, 8>& qp, const unsigned long long* sMask, uint4* sQ4, float* sS,
+template <int HD, bool Q8, bool QF32, bool WIN>
+SPEC_DEV void attend_range_few(const AttendArgs& a, const CacheView& cv, const KeyMap& km, int seq, int g, int k_begin, int k_end,
+                               int n_ctx, const QueryPieces<HD, 8>& qp, const RowSight* sSight, uint4* sQ4, float* sS,
                                float* rows, char* ring, FewState<HD>& st) {
     constexpr int KS = HD / 16, MT = HD / 16;
     const uint2* sQ = reinterpret_cast<const uint2*>(sQ4);
@@ -511,9 +514,9 @@ SPEC_DEV void attend_range_few(const AttendArgs& a, const CacheView& cv, int seq
     const char* slots = ring + warp * S::kStages * S::kBytes;
     int kt = k_begin + 16 * warp;
     // the first tiles' copies go out before the queries are taken; rows are looked up a tile before their use
-    long long row = tile_row(a, cv, seq, g, kt, k_end), row_nx = tile_row(a, cv, seq, g, kt + 64, k_end);
+    long long row = tile_row<WIN>(a, cv, km, seq, g, kt, k_end), row_nx = tile_row<WIN>(a, cv, km, seq, g, kt + 64, k_end);
     if (Q8) {
-        const long long row_2 = tile_row(a, cv, seq, g, kt + 64 * S::kStages, k_end);
+        const long long row_2 = tile_row<WIN>(a, cv, km, seq, g, kt + 64 * S::kStages, k_end);
         if (kt < k_end) copy_tile<HD, true>(a, cv, row, kt, k_end, slot0);
         copies_commit();
         if (kt + 64 < k_end) copy_tile<HD, true>(a, cv, row_nx, kt + 64, k_end, slot0 + S::kBytes);
@@ -592,7 +595,7 @@ SPEC_DEV void attend_range_few(const AttendArgs& a, const CacheView& cv, int seq
             }
             row = row_nx;
         }
-        row_nx = tile_row(a, cv, seq, g, kt + 64 * (Q8 ? S::kStages + 1 : 2), k_end);
+        row_nx = tile_row<WIN>(a, cv, km, seq, g, kt + 64 * (Q8 ? S::kStages + 1 : 2), k_end);
         if (kt + 16 > k_end) {
             // values of keys past the range: their probability is zero, and zero times what the slot holds must be zero
 #pragma unroll
@@ -604,13 +607,15 @@ SPEC_DEV void attend_range_few(const AttendArgs& a, const CacheView& cv, int seq
         // a new row's NaN or infinity must not reach the rows that do not see it (0 * NaN): it leaves the
         // product, and the rows that see it become NaN
         uint32_t bad = 0;                                     // bit k: tile key k
-        if (kt + 16 > n_ctx) {
+        const int at_slot = key_slot<WIN>(km, kt);
+        const bool edge = at_slot + 16 > n_ctx || (WIN && at_slot < km.low_max);   // not every row sees every key
+        if (edge) {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 bool b = false;
 #pragma unroll
                 for (int i = 0; i < MT; ++i) b |= not_finite2<Q8>(vb[r][i]);
-                if (kt + few_v_key(cq, r) < n_ctx) b = false;
+                if (!WIN && kt + few_v_key(cq, r) < n_ctx) b = false;
                 if (b)
 #pragma unroll
                     for (int i = 0; i < MT; ++i) vb[r][i] = 0u;
@@ -640,14 +645,13 @@ SPEC_DEV void attend_range_few(const AttendArgs& a, const CacheView& cv, int seq
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int h = 0; h < 2; ++h) x[j][h] = (sc[0][2 * h + j] + sc[1][2 * h + j]) * (Q8 ? cf[j] * kf[h] : cf[j]);
-        if (kt + 16 > min(n_ctx, k_end)) {                    // a tile that reaches new rows or the end
+        if (edge || kt + 16 > k_end) {                        // ... or a tile that reaches the end
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const unsigned long long mk = sMask[2 * cq + j];
+                const RowSight see = sSight[2 * cq + j];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int key = kt + gq + 8 * h;
-                    if (!(key < k_end && (key < n_ctx || ((mk >> ((key - n_ctx) & 63)) & 1ull)))) x[j][h] = -INFINITY;
+                    if (!(kt + gq + 8 * h < k_end && row_sees<WIN>(km, see, at_slot + gq + 8 * h, n_ctx))) x[j][h] = -INFINITY;
                     else if ((bad >> (gq + 8 * h)) & 1u) x[j][h] = __int_as_float(0x7fc00000);
                 }
             }
@@ -710,18 +714,9 @@ SPEC_DEV void attend_range_few(const AttendArgs& a, const CacheView& cv, int seq
     if (!Q8) { st.R[0] = st.m[0]; st.R[1] = st.m[1]; }
 }
 
-SPEC_DEV unsigned long long row_mask(const AttendSpan& s, int b, int j) {
-    if (s.tree == 0) return j >= 63 ? ~0ull : (2ull << j) - 1ull;
-    if (s.tree == 1) return s.mask[j];
-    unsigned long long mk = 0ull;
-    const int* par = s.dev_parent + (size_t)b * kMaxSeqRows;
-    for (int x = j, n = 0; x >= 0 && n < kMaxSeqRows; x = par[x], ++n) mk |= 1ull << x;
-    return mk;
-}
-
 constexpr int row_ctas_per_sm(int hd, int qb) { return hd == 128 ? 3 : (qb == 8 ? 5 : 4); }
 
-template <int HD, bool QF32, int QB>
+template <int HD, bool QF32, int QB, bool WIN>
 __global__ void __launch_bounds__(kRowThreads, row_ctas_per_sm(HD, QB))
 attend_rows_kernel(const __grid_constant__ AttendArgs a) {
     // Behind the tile kernel too: what the launches before that one wrote (the new rows) is visible to a grid
@@ -733,15 +728,16 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
     extern __shared__ float smf[];
     uint4* sQ = reinterpret_cast<uint4*>(smf);                              // [QF32 ? 2 : 1][KS][32] (8 queries: uint2)
     float* sRows = smf + (QF32 ? 2 : 1) * KS * 32 * (QB / 4);               // [QB][LS] the queries before
-    unsigned long long* sMask = reinterpret_cast<unsigned long long*>(sRows + QB * LS);   // [QB]
-    float* sS = reinterpret_cast<float*>(sMask + QB);                       // [QB]
+    RowSight* sSight = reinterpret_cast<RowSight*>(sRows + QB * LS);        // [QB]
+    float* sS = reinterpret_cast<float*>(sSight + QB);                      // [QB]
     float* sState = sS + QB;                                                // [4 warps][QB][LS]
     char* ring = reinterpret_cast<char*>(sState);                           // the tiles, before the states
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, gq = lane >> 2, cq = lane & 3;
     const int G = a.H / a.Hkv;
     // the prompt's blocks first (the longer ones), then the sequences' own
     int id = blockIdx.x;
-    const int n_pre = a.pre_splits * a.pre_qb * a.Hkv;
+    // (with a window the sequences see different parts of it, so each has blocks of its own there too)
+    const int n_pre = a.pre_splits * a.pre_qb * a.Hkv * (WIN ? a.span.batch : 1);
     const bool is_pre = id < n_pre;
     int b = 0, list_row0 = 0, rows = a.span.T;
     if (!is_pre) id -= n_pre;
@@ -750,10 +746,18 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
     const int qb = id % (is_pre ? a.pre_qb : a.own_qb);
     id /= is_pre ? a.pre_qb : a.own_qb;
     int split, n_splits, n_ctx, n_keys, range;
+    int base = 0, prompt = 0;                                               // WIN: index of the first row, length of the prompt
     if (is_pre) {
         split = id;
         n_splits = a.pre_splits;
         n_keys = n_ctx = min(a.pre.len[a.pre_seq], a.pre.cap);
+        if (WIN) {
+            split = id % a.pre_splits;
+            b = id / a.pre_splits;
+            list_row0 = a.span.row0[b];
+            rows = a.span.row0[b + 1] - list_row0;
+            base = n_keys + a.own.len[b] + a.span.extra;
+        }
         range = split;
     } else {
         split = id % a.own_splits;
@@ -765,11 +769,25 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
         n_keys = min(n_ctx + rows, a.own.cap);
         if (n_ctx + rows > a.own.cap && rows > 0 && t == 0) dev_error(a.err, SPEC_DEVERR_CAPACITY);
         range = a.own_range0 + split;
+        if (WIN) {
+            if (a.pre.len) prompt = min(a.pre.len[a.pre_seq], a.pre.cap);
+            base = prompt + n_ctx;
+        }
     }
     const int q0 = qb * QB, nq = min(QB, rows * G - q0);
     if (nq <= 0) return;
     QueryPieces<HD, QB> qp;                                                 // on their way while the lengths are read
     fetch_queries<HD, QF32, QB>(a, g, G, list_row0, q0, nq, qp);
+    KeyMap km{0, 0, 0, 0};
+    if (WIN) {
+        // slots that the sequence's first row sees: the later ones see none before them but the sinks
+        const int lo = max(0, base - prompt - a.window + 1) & ~15;
+        km.sinks = min(max(a.sinks - prompt, 0), n_ctx);
+        km.sink_keys = (km.sinks + 15) & ~15;
+        km.lo = lo;
+        if (km.sink_keys >= lo) km.sink_keys = km.lo = 0;                   // one run of keys
+        n_keys = km.lo < n_keys ? km.sink_keys + n_keys - km.lo : min(km.sink_keys, n_keys);
+    }
     int chunk = max(kMinKeys, (n_keys + n_splits - 1) / n_splits);
     chunk = (chunk + 63) / 64 * 64;
     const int k_begin = min(n_keys, split * chunk), k_end = min(n_keys, k_begin + chunk);
@@ -778,18 +796,35 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
     const size_t TH = (size_t)a.span.T * a.H;
     auto vec_of = [&](int r) { return range * TH + (size_t)(list_row0 + (q0 + r) / G) * a.H + g * G + (q0 + r) % G; };
     if (k_begin >= k_end) {                                                 // nothing in this range
+        if (WIN && a.direct) {
+            for (int i = t; i < nq * HD; i += kRowThreads)
+                put_out(a.out, (list_row0 + (q0 + i / HD) / G) * a.out.stride + (g * G + (q0 + i / HD) % G) * HD + i % HD, __int_as_float(0x7fc00000));
+            return;
+        }
         if (t < nq) *reinterpret_cast<float2*>(a.part_ml + 2 * vec_of(t)) = make_float2(-INFINITY, 0.f);
         return;
     }
-    if (t < QB) sMask[t] = !is_pre && t < nq ? row_mask(a.span, b, (q0 + t) / G) : 0ull;
+    if (t < QB) {
+        RowSight rs{0ull, 0};
+        const int j = (q0 + t) / G;
+        if ((WIN || !is_pre) && t < nq) rs.mask = row_mask(a.span, b, j);
+        if (WIN) {
+            const int d = t < nq ? __popcll(rs.mask) - 1 : 0;
+            rs.low = base - prompt + d - a.window + 1;
+            rs.mask = is_pre ? 0ull : window_mask(a.span, b, rs.mask, d, a.window, a.sinks - base);
+        }
+        sSight[t] = rs;
+    }
+    // depths are at most the row's index, so no row's bound lies past the last row's
+    if (WIN) km.low_max = base - prompt + (q0 + nq - 1) / G - a.window + 1;
     if constexpr (QB == 8) {
         FewState<HD> rs;
 #pragma unroll
         for (int j = 0; j < 2; ++j) { rs.m[j] = rs.R[j] = -INFINITY; rs.l[j] = 0.f; }
 #pragma unroll
         for (int mt = 0; mt < HD / 16; ++mt) rs.o[mt][0] = rs.o[mt][1] = rs.o[mt][2] = rs.o[mt][3] = 0.f;
-        if (cv.q8) attend_range_few<HD, true, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, qp, sMask, sQ, sS, sRows, ring, rs);
-        else attend_range_few<HD, false, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, qp, sMask, sQ, sS, sRows, ring, rs);
+        if (cv.q8) attend_range_few<HD, true, QF32, WIN>(a, cv, km, seq, g, k_begin, k_end, n_ctx, qp, sSight, sQ, sS, sRows, ring, rs);
+        else attend_range_few<HD, false, QF32, WIN>(a, cv, km, seq, g, k_begin, k_end, n_ctx, qp, sSight, sQ, sS, sRows, ring, rs);
         __syncthreads();                     // the states lie where the tiles were
         // warp states -> shared: queries 2c and 2c + 1, dims VD * g ..
 #pragma unroll
@@ -808,8 +843,8 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
         for (int rr = 0; rr < 2; ++rr) { rs.m[rr] = rs.R[rr] = -INFINITY; rs.l[rr] = 0.f; }
 #pragma unroll
         for (int nt = 0; nt < VD; ++nt) rs.o[nt][0] = rs.o[nt][1] = rs.o[nt][2] = rs.o[nt][3] = 0.f;
-        if (cv.q8) attend_range<HD, true, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, qp, sMask, sQ, sS, sRows, ring, rs);
-        else attend_range<HD, false, QF32>(a, cv, seq, g, k_begin, k_end, n_ctx, qp, sMask, sQ, sS, sRows, ring, rs);
+        if (cv.q8) attend_range<HD, true, QF32, WIN>(a, cv, km, seq, g, k_begin, k_end, n_ctx, qp, sSight, sQ, sS, sRows, ring, rs);
+        else attend_range<HD, false, QF32, WIN>(a, cv, km, seq, g, k_begin, k_end, n_ctx, qp, sSight, sQ, sS, sRows, ring, rs);
         __syncthreads();
         // warp states -> shared: rows g and g + 8, dims VD * 2c + nt and VD * (2c + 1) + nt
 #pragma unroll
@@ -853,6 +888,15 @@ attend_rows_kernel(const __grid_constant__ AttendArgs a) {
             O.w = fmaf(o.w, wt, O.w);
         }
         const float f = (M == -INFINITY ? 1.f : ex2(RR - M)) * (cv.q8 ? 1.f / kF16Top : 1.f);
+        if (WIN && a.direct) {
+            const float inv = f / L;
+            const long long at = (list_row0 + (q0 + r) / G) * a.out.stride + (g * G + (q0 + r) % G) * HD + d;
+            put_out(a.out, at, O.x * inv);
+            put_out(a.out, at + 1, O.y * inv);
+            put_out(a.out, at + 2, O.z * inv);
+            put_out(a.out, at + 3, O.w * inv);
+            continue;
+        }
         const size_t vec = vec_of(r);
         *reinterpret_cast<float4*>(a.part_o + vec * HD + d) = make_float4(O.x * f, O.y * f, O.z * f, O.w * f);
         if (d == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * vec) = make_float2(M, L);
@@ -1014,7 +1058,7 @@ static size_t rows_smem(int hd, bool qf32, int qb, bool q8) {
     const size_t ring = hd == 128 ? (qb == 8 ? ring_bytes<128, true>(q8) : ring_bytes<128, false>(q8))
                                   : (qb == 8 ? ring_bytes<64, true>(q8) : ring_bytes<64, false>(q8));
     const size_t row = (size_t)(hd + 4) * sizeof(float);
-    return (qf32 ? 2 : 1) * (hd / 16) * 32 * qb + qb * (row + 12) + std::max(ring, 4 * qb * row);
+    return (qf32 ? 2 : 1) * (hd / 16) * 32 * qb + qb * (row + sizeof(RowSight) + 4) + std::max(ring, 4 * qb * row);
 }
 
 // Query vectors whose partial states fit.  The row kernel's two parts keep to (ranges) x
@@ -1049,27 +1093,39 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     const size_t fit = m->attend_part_floats / (hd + 2) / TH;      // ranges the workspace holds
     const long long pre_work = pre ? (long long)((span.T * G + 15) / 16) * Hkv * pre->max_ctx : 0;
     const bool rows_do = span.T * G <= kRowVectors || (span.T * G <= kRowVectorsShort && pre_work <= kRowKeysShort);
-    const bool tile = pre && !rows_do && attend_tile_ok(pre);
+    const bool win = kv->window_of(layer) > 0;
+    const bool tile = pre && !win && !rows_do && attend_tile_ok(pre);
     // blocks of 8 query vectors where one holds all of a part's, else of 16
-    const int QB = span.max_rows * G <= 8 && (!pre || tile || span.T * G <= 8) ? 8 : 16;
+    const bool blocks = win && span.max_rows * G > kWindowVectors && attend_window_ok(kv);
+    const int QB = blocks ? attend_window_block(span.max_rows * G) : span.max_rows * G <= 8 && (!pre || win || tile || span.T * G <= 8) ? 8 : 16;
     a.own_qb = (span.max_rows * G + QB - 1) / QB;
-    a.pre_qb = pre && !tile ? (span.T * G + QB - 1) / QB : 0;
-    const long long own_blocks = (long long)span.batch * Hkv * a.own_qb, pre_blocks = (long long)Hkv * a.pre_qb;
-    const long long keys = own_blocks * kv->max_ctx + pre_blocks * (pre ? pre->max_ctx : 0);
+    a.pre_qb = pre && !tile ? ((win ? span.max_rows : span.T) * G + QB - 1) / QB : 0;
+    // the most keys of a part
+    long long own_ctx = kv->max_ctx, pre_ctx = pre ? pre->max_ctx : 0;
+    if (win) {
+        a.window = kv->window_of(layer);
+        a.sinks = kv->sinks[layer];
+        const long long seen = (long long)a.window + a.sinks + 30;       // whole tiles of both
+        own_ctx = std::min(own_ctx, seen + span.max_rows);
+        pre_ctx = std::min(pre_ctx, seen);
+    }
+    const long long own_blocks = (long long)span.batch * Hkv * a.own_qb;
+    const long long pre_blocks = (long long)Hkv * a.pre_qb * (win ? span.batch : 1);
+    const long long keys = own_blocks * own_ctx + pre_blocks * pre_ctx;
     // ranges: as many CTAs as run at a time, by each part's share of the keys; more only add starts and
     // partial states (8 vectors, 32 KV heads, 32768 slots: one wave 72 us in 8 bits and 89 in bf16, two 86
     // and 117)
-    const long long wave = (long long)row_ctas_per_sm(hd, QB) * m->num_sms;
+    const long long wave = (long long)(blocks ? attend_window_ctas(hd) : row_ctas_per_sm(hd, QB)) * m->num_sms;
     const long long per = std::max<long long>(kMinKeys, keys / wave + 1), round = per > kMinKeys ? per / 2 : per - 1;
-    auto splits = [&](long long blocks, long long ctx) {
-        if (blocks == 0) return 0;
+    auto splits = [&](long long n_blocks, long long ctx) {
+        if (n_blocks == 0) return 0;
         long long n = (ctx + round) / per;
         // whole caches that would be among the longest CTAs are halved: sequences differ in length
         if (n == 1 && 2 * ctx > per && ctx > 2 * kMinKeys) n = 2;
-        return (int)std::max<long long>(1, std::min<long long>({n, 64, (16 * 512) / (16 * blocks) + 1}));
+        return (int)std::max<long long>(1, std::min<long long>({n, 64, (16 * 512) / (std::max(16, QB) * n_blocks) + 1}));
     };
-    a.own_splits = splits(own_blocks, kv->max_ctx);
-    a.pre_splits = splits(pre_blocks, pre ? pre->max_ctx : 0);
+    a.own_splits = splits(own_blocks, own_ctx);
+    a.pre_splits = splits(pre_blocks, pre_ctx);
     int tile_ranges = 0;
     if (tile) {
         a.tile_ctas = attend_tile_ctas(m, span, q_f32, pre->max_ctx);
@@ -1083,22 +1139,37 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     a.part_ml = m->attend_part + (size_t)ranges * TH * hd;
     const dim3 grid((unsigned)(a.pre_splits * pre_blocks + a.own_splits * own_blocks));
     const size_t smem = rows_smem(hd, q_f32, QB, a.own.q8 || (a.pre_qb > 0 && a.pre.q8));
-    void (*const kernels[8])(AttendArgs) = {
-        attend_rows_kernel<64, false, 8>, attend_rows_kernel<64, false, 16>, attend_rows_kernel<64, true, 8>, attend_rows_kernel<64, true, 16>,
-        attend_rows_kernel<128, false, 8>, attend_rows_kernel<128, false, 16>, attend_rows_kernel<128, true, 8>, attend_rows_kernel<128, true, 16>};
-    const int which = (hd == 128 ? 4 : 0) + (q_f32 ? 2 : 0) + (QB == 16 ? 1 : 0);
+    void (*const kernels[16])(AttendArgs) = {
+        attend_rows_kernel<64, false, 8, false>, attend_rows_kernel<64, false, 16, false>,
+        attend_rows_kernel<64, true, 8, false>, attend_rows_kernel<64, true, 16, false>,
+        attend_rows_kernel<128, false, 8, false>, attend_rows_kernel<128, false, 16, false>,
+        attend_rows_kernel<128, true, 8, false>, attend_rows_kernel<128, true, 16, false>,
+        attend_rows_kernel<64, false, 8, true>, attend_rows_kernel<64, false, 16, true>,
+        attend_rows_kernel<64, true, 8, true>, attend_rows_kernel<64, true, 16, true>,
+        attend_rows_kernel<128, false, 8, true>, attend_rows_kernel<128, false, 16, true>,
+        attend_rows_kernel<128, true, 8, true>, attend_rows_kernel<128, true, 16, true>};
+    const int which = (win ? 8 : 0) + (hd == 128 ? 4 : 0) + (q_f32 ? 2 : 0) + (QB == 16 ? 1 : 0);
     void (*f)(AttendArgs) = kernels[which];
-    static std::atomic<unsigned long long> set[8] = {};        // devices where a kernel may take more than 48 KB
+    static std::atomic<unsigned long long> set[16] = {};       // devices where a kernel may take more than 48 KB
     const unsigned long long bit = 1ull << (m->device & 63);
     if (smem > 48 * 1024 && !(set[which].load() & bit)) {
         SPEC_TRY(check_cuda(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)rows_smem(hd, true, QB, true)),
                             "attention rows attribute"));
         set[which].fetch_or(bit);
     }
+    a.out = out;
+    a.direct = win && !pre && a.own_splits == 1;
     const int slot = prof_start(m, st);
     if (tile) SPEC_TRY(launch_attend_tile(pre, a, st));
-    cudaError_t e = launch_k(m->pdl, f, grid, dim3(kRowThreads), smem, st, a);
+    cudaError_t e = cudaSuccess;
+    if (blocks) SPEC_TRY(launch_attend_window(kv, a, st));
+    else e = launch_k(m->pdl, f, grid, dim3(kRowThreads), smem, st, a);
     SPEC_TRY(check_cuda(e, "attention rows launch"));
+    ++m->launches;
+    if (a.direct) {
+        prof_stop(m, slot, st, PROF_ATTN, 0.0);
+        return SPEC_OK;
+    }
     JoinArgs j{};
     j.part_o = a.part_o;
     j.part_ml = a.part_ml;
@@ -1118,7 +1189,7 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
     void (*jf)(JoinArgs) = ranges > 12 ? (hd == 128 ? attend_join_kernel<128, 4> : attend_join_kernel<64, 4>)
                                        : (hd == 128 ? attend_join_kernel<128, 1> : attend_join_kernel<64, 1>);
     e = launch_k(m->pdl, jf, dim3(ranges > 12 ? TH : (TH + 3) / 4), dim3(128), 0, st, j);
-    m->launches += 2;
+    ++m->launches;
     prof_stop(m, slot, st, PROF_ATTN, 0.0);
     return check_cuda(e, "attention join launch");
 }
@@ -1147,6 +1218,34 @@ extern "C" int spec_kv_set_prefix(spec_kv* kv, spec_kv* prefix, int32_t seq) {
         }
         kv->prefix = prefix;
         kv->prefix_seq = seq;
+    }
+    return SPEC_OK;
+}
+
+extern "C" int spec_kv_set_window(spec_kv* kv, int32_t layer0, int32_t n_layers, int32_t window, int32_t sinks) {
+    if (!kv) return set_error(SPEC_ERR_ARG, "spec_kv_set_window: null cache");
+    const int N = kv->m->cfg.n_layers;
+    if (layer0 < 0 || n_layers < 1 || layer0 >= N || n_layers > N - layer0)
+        return set_error(SPEC_ERR_ARG, "spec_kv_set_window: layers out of range");
+    if (window < 0 || sinks < 0) return set_error(SPEC_ERR_ARG, "spec_kv_set_window: window and sinks must not be negative");
+    if (!kv->m->bf16) return set_error(SPEC_ERR_UNSUPPORTED, "spec_kv_set_window: bf16 models only");
+    if (kv->window.empty()) {
+        if (window == 0) return SPEC_OK;
+        try {
+            std::vector<int> w(N, 0), s(N, 0);
+            kv->window.swap(w);
+            kv->sinks.swap(s);
+        } catch (...) {
+            return set_error(SPEC_ERR_CAPACITY, "spec_kv_set_window: out of host memory");
+        }
+    }
+    for (int l = layer0; l < layer0 + n_layers; ++l) {
+        kv->window[l] = window;
+        kv->sinks[l] = window ? sinks : 0;
+    }
+    if (*std::max_element(kv->window.begin(), kv->window.end()) == 0) {
+        kv->window.clear();
+        kv->sinks.clear();
     }
     return SPEC_OK;
 }

@@ -42,6 +42,14 @@ CacheView cache_view(const spec_kv* kv, int layer);
 // span of a call with n_rows[b] rows of sequence b
 int make_span(AttendSpan* s, int batch, const int* n_rows, int extra, const int* tree_parent, const int* dev_parent);
 
+// Where the attention's result goes: bf16 rows of the caller, or the model's
+// O-projection input (hi rows, then lo rows at out_lo).
+struct AttendOut { __nv_bfloat16* p; long long stride; size_t lo; };
+SPEC_DEV void put_out(const AttendOut& o, long long at, float v) {
+    if (o.lo) store_act(o.p, (size_t)at, o.lo, v);
+    else o.p[at] = __float2bfloat16_rn(v);
+}
+
 // Parameters of the attention kernels.  Ranges of keys leave partial states:
 // the prompt's ranges first, then each sequence's own.
 struct AttendArgs {
@@ -61,9 +69,54 @@ struct AttendArgs {
     float* part_o;                    // [range][T * H][hd]
     float* part_ml;                   // [range][T * H][2]
     int own_range0;                   // first range of the own part
+    AttendOut out;
+    int direct;                       // one range holds all of a row's keys: its result goes out, no state
+    int window, sinks;                // > 0: rows see the last `window` keys of their sequence and its first `sinks`
     int* err;
 };
 
+// Where a window's keys lie: the tiles of the sinks, then those of the window, one list of keys without the
+// gap between them.  Without a window (WIN false) a key's place in the list is its slot.
+struct KeyMap {
+    int sink_keys;                   // the list's first keys, whole tiles: slots [0, sink_keys)
+    int lo;                          // slot of the next key, a multiple of 16
+    int sinks;                       // slots below it are seen by every row
+    int low_max;                     // no row of the CTA starts to see slots past it
+};
+template <bool WIN>
+SPEC_DEV int key_slot(const KeyMap& km, int kt) { return WIN && kt >= km.sink_keys ? kt - km.sink_keys + km.lo : kt; }
+// What a CTA's row sees of a tile's keys: the slots below n_ctx (with a window those below the sinks' end or
+// from the row's own bound on), and the call's rows of its mask.
+struct RowSight { unsigned long long mask; int low; };
+template <bool WIN>
+SPEC_DEV bool row_sees(const KeyMap& km, const RowSight& rs, int slot, int n_ctx) {
+    if (slot >= n_ctx) return (rs.mask >> ((slot - n_ctx) & 63)) & 1ull;
+    return !WIN || slot < km.sinks || slot >= rs.low;
+}
+
+SPEC_DEV unsigned long long row_mask(const AttendSpan& s, int b, int j) {
+    if (s.tree == 0) return j >= 63 ? ~0ull : (2ull << j) - 1ull;
+    if (s.tree == 1) return s.mask[j];
+    unsigned long long mk = 0ull;
+    const int* par = s.dev_parent + (size_t)b * kMaxSeqRows;
+    for (int x = j, n = 0; x >= 0 && n < kMaxSeqRows; x = par[x], ++n) mk |= 1ull << x;
+    return mk;
+}
+
+// The rows that row j sees under a window: the same, without those too far above it that are no sinks.
+// d: its depth; sinks: those of the call's rows (by depth).
+SPEC_DEV unsigned long long window_mask(const AttendSpan& s, int b, unsigned long long mk, int d, int window, int sinks) {
+    if (d < window) return mk;
+    unsigned long long kept = 0ull;
+    for (unsigned long long left = mk; left; left &= left - 1ull) {
+        const int x = __ffsll((long long)left) - 1, dx = __popcll(row_mask(s, b, x)) - 1;
+        if (d - dx < window || dx < sinks) kept |= 1ull << x;
+    }
+    return kept;
+}
+
+// generic writes to shared memory before asynchronous copies over it, or reads of it by the tensor cores
+SPEC_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 SPEC_DEV float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -112,9 +165,12 @@ SPEC_DEV int tile_range_count(int g, int KB, long long W, int n) {
 }
 int launch_attend_tile(const spec_kv* pre, const AttendArgs& a, cudaStream_t st);
 
-// Where the attention's result goes: bf16 rows of the caller, or the model's
-// O-projection input (hi rows, then lo rows at out_lo).
-struct AttendOut { __nv_bfloat16* p; long long stride; size_t lo; };
+// attend_window.cu: windows under more than kWindowVectors query vectors a sequence and KV head
+constexpr int kWindowVectors = 16;
+bool attend_window_ok(const spec_kv* kv);
+int attend_window_block(int vectors);                 // query vectors of a block
+int attend_window_ctas(int hd);                       // CTAs an SM
+int launch_attend_window(const spec_kv* kv, const AttendArgs& a, cudaStream_t st);
 
 // rows [T][Hkv][hd] (strides in elements) into layer `layer` of kv at their slots
 int launch_append(spec_kv* kv, int layer, const AttendSpan& span, const void* k, long long k_stride, const void* v,

@@ -134,7 +134,6 @@ SPEC_DEV float max3(float x, uint32_t y, uint32_t z) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(__uint_as_float(y)), "f"(__uint_as_float(z)));
     return r;
 }
-SPEC_DEV void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // What a CTA does in one turn: a KV head, its query tiles and a run of its keys.
 struct TileJob {

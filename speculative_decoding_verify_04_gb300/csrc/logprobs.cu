@@ -27,7 +27,7 @@
 #include <climits>
 #include <cooperative_groups.h>
 
-#include "attend.cuh"
+#include "logits.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -35,7 +35,6 @@ namespace spec {
 
 constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpSeg = 256;
 constexpr int kLpMaxTop = 32;
 constexpr int kLpMaxVocab = 1 << 20;
 constexpr int kLpMaxCtas = 4;
@@ -127,53 +126,6 @@ SPEC_DEV int lp_place(const unsigned long long* list, int nc, int n, unsigned lo
     return before;
 }
 
-SPEC_DEV float warp_redux_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
-}
-
-// a 16-byte piece as floats
-template <typename T>
-SPEC_DEV void lp_unpack(const uint4& w, float* x) {
-    const uint32_t a[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (sizeof(T) == 4) {
-            x[i] = __uint_as_float(a[i]);
-        } else {
-            x[2 * i] = __uint_as_float(a[i] << 16);
-            x[2 * i + 1] = __uint_as_float(a[i] & 0xFFFF0000u);
-        }
-    }
-}
-
-// One segment of a row: 8 logits a lane.  Element i of the row sits at position
-// i + mis, mis the elements between a 16-byte boundary and the row's start, so
-// whole pieces are aligned; pieces that the row does not fill are read one by one.
-template <typename T>
-SPEC_DEV void lp_load(const T* row, int V, int mis, int seg, float (&x)[8]) {
-    constexpr int VE = 16 / sizeof(T), NP = 8 / VE;
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int p = 0; p < NP; ++p) {
-        const int i0 = seg * kLpSeg + (p * 32 + lane) * VE - mis;
-        if (i0 >= 0 && i0 + VE <= V) {
-            lp_unpack<T>(__ldg(reinterpret_cast<const uint4*>(row + i0)), &x[p * VE]);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VE; ++i)
-                x[p * VE + i] = i0 + i >= 0 && i0 + i < V ? to_f32<T>(row[i0 + i]) : -INFINITY;
-        }
-    }
-}
-// row index of the lane's element e of a segment
-template <typename T>
-SPEC_DEV int lp_index(int mis, int seg, int e) {
-    constexpr int VE = 16 / sizeof(T);
-    return seg * kLpSeg + ((e / VE) * 32 + (threadIdx.x & 31)) * VE + e % VE - mis;
-}
-
 SPEC_DEV void lp_add(LpState& a, const float (&x)[8], float c, float xm) {
     const float m = fmaxf(a.m, xm);
     if (m == -INFINITY) {
@@ -205,10 +157,6 @@ struct LpSmem {
     float low, least;
     int n_near, n_cand;
 };
-
-// a cluster barrier in two halves
-SPEC_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-SPEC_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 template <typename T, int TOP>
 __global__ void __launch_bounds__(kLpThreads, sizeof(T) == 4 ? 4 : 5)

@@ -205,7 +205,10 @@ struct spec_kv {
     int prefix_seq = 0;
     bool prefix_lost = false;        // the prompt's cache was destroyed while attached
     std::vector<spec_kv*> users;     // caches that continue a sequence of this one
-    bool by_range() const { return q8 || prefix != nullptr; }   // attention in ranges (attend.cu)
+    // by layer (empty: no layer has one): rows see the last window[l] keys and the first sinks[l] (0: every key)
+    std::vector<int> window, sinks;
+    int window_of(int layer) const { return window.empty() ? 0 : window[layer]; }
+    bool by_range() const { return q8 || prefix != nullptr || !window.empty(); }   // attention in ranges (attend.cu)
     spec::KVPages pages() const {
         int sh = -1;
         if (paged) { sh = 0; while ((1 << sh) < page) ++sh; }

@@ -31,6 +31,7 @@ EXPORTS = [
     "spec_schedule_decay", "spec_draft_tree", "spec_kv_create_paged", "spec_kv_free_pages", "spec_kv_page_table",
     "spec_draft_tree_dynamic", "spec_verify_trees", "spec_set_exit_layer", "spec_kv_read_page",
     "spec_test_stall_next_chain", "spec_kv_create_q8", "spec_kv_set_prefix", "spec_attend", "spec_logprobs",
+    "spec_rope", "spec_kv_set_window", "spec_sample_logits",
 ]
 
 
@@ -52,6 +53,16 @@ class KSchedule(ctypes.Structure):
 class AIMDSchedule(ctypes.Structure):
     _fields_ = [("window", c_int32), ("min_k", c_int32), ("max_k", c_int32), ("up_num", c_int32),
                 ("up_den", c_int32), ("down_num", c_int32), ("down_den", c_int32)]
+
+
+class RopeConfig(ctypes.Structure):
+    _fields_ = [(n, c_int32) for n in ("n_heads", "n_kv_heads", "head_dim", "dtype", "axes")] + \
+               [("sections", c_int32 * 4), ("interleaved", c_int32), ("theta", c_double)]
+
+
+class SampleConfig(ctypes.Structure):
+    _fields_ = [(n, c_float) for n in ("temperature", "top_p", "min_p")] + [("top_k", c_int32)] + \
+               [(n, c_void_p) for n in ("temperatures", "top_ps", "min_ps", "top_ks")]
 
 
 _lib = None
@@ -98,8 +109,11 @@ def load(path: str = LIB_PATH):
         "spec_test_stall_next_chain": ([P, I, ctypes.c_int64], I),
         "spec_kv_create_q8": ([P, I, I, I, I, POINTER(P)], I),
         "spec_kv_set_prefix": ([P, P, I], I),
+        "spec_kv_set_window": ([P, I, I, I, I], I),
         "spec_attend": ([P, I, I, P, P, L, P, L, P, L, P, P, L, P], I),
         "spec_logprobs": ([P, I, L, I, I, c_float, P, P, P, I, P, P, P], I),
+        "spec_rope": ([POINTER(RopeConfig), I, P, L, P, L, P, L, P, L, P, L, P, I, P, P, P], I),
+        "spec_sample_logits": ([P, I, L, I, I, P, POINTER(SampleConfig), P, P, P, L, P], I),
         "spec_accept_greedy": ([P, P, POINTER(I), I, I, I, P, P, P, P], I),
         "kv_commit": ([P, I, P, P, I, P], I),
         "spec_row_probs": ([P, I, P, P], I),
@@ -272,6 +286,14 @@ class KVCache:
             raise SpecError("set_prefix: the prefix is closed")
         _check(load().spec_kv_set_prefix(self.handle, None if prefix is None else prefix.handle, int(seq)))
         self.prefix = prefix
+
+    def set_window(self, window, sinks=0, layer0=0, n_layers=None):
+        """Rows of the layers (default: all) see the last ``window`` tokens of their
+        sequence, themselves among them, and its first ``sinks`` (window 0: everything)."""
+        if not self.handle:
+            raise SpecError("set_window: the cache is closed")
+        n = self.model.n_layers - layer0 if n_layers is None else n_layers
+        _check(load().spec_kv_set_window(self.handle, int(layer0), int(n), int(window), int(sinks)))
 
     def free_pages(self, stream=None):
         n = c_int32()
@@ -529,6 +551,58 @@ def spec_attend(kv, layer, n_rows, q, out, k=None, v=None, tree_parent=None, str
         _check(rc)
 
 
+def spec_rope(q, q_out, k=None, k_out=None, theta=10000.0, positions=None, sections=None, interleaved=False, kv=None,
+              n_rows=None, tree_parent=None, stream=None):
+    """``q_out`` [T, H, hd] and ``k_out`` [T, Hkv, hd]: ``q`` and ``k`` (bf16 or f32) with their
+    positions encoded, in place where a result is its input.  ``positions`` is int32 [T] or
+    [axes, T] with ``sections`` frequency pairs an axis (default: one axis, all hd / 2); or the
+    rows are those of a call on the cache ``kv`` with ``n_rows`` and ``tree_parent``."""
+    if q is None or q.dim() != 3 or q.dtype not in (torch.bfloat16, torch.float32):
+        raise SpecError("q: need a CUDA bfloat16 or float32 tensor [T, H, hd]")
+    dt, dev = q.dtype, torch.cuda.current_device()
+    T, H, hd = q.shape
+    qp, qs = _rows3d(q, "q", H, hd, T, dt, dev)
+    qop, qos = _rows3d(q_out, "q_out", H, hd, T, dt, dev)
+    kp = kop = None
+    ks = kos = Hkv = 0
+    if k is not None:
+        if k.dim() != 3:
+            raise SpecError("k: need a tensor [T, Hkv, hd]")
+        Hkv = k.shape[1]
+        kp, ks = _rows3d(k, "k", Hkv, hd, T, dt, dev)
+        kop, kos = _rows3d(k_out, "k_out", Hkv, hd, T, dt, dev)
+    elif k_out is not None:
+        raise SpecError("k_out: given without k")
+    sections = [hd // 2] if sections is None else [int(n) for n in sections]
+    if not 1 <= len(sections) <= 4:
+        raise SpecError("sections: one to four axes")
+    cfg = RopeConfig(H, Hkv, hd, SPEC_DTYPE_BF16 if dt is torch.bfloat16 else SPEC_DTYPE_F32, len(sections),
+                     (c_int32 * 4)(*sections), 1 if interleaved else 0, float(theta))
+    pp = handle = cp = tp = None
+    batch = pos_stride = 0
+    if positions is not None:
+        sh = positions.shape
+        if positions.dtype is not torch.int32 or not positions.is_cuda or len(sh) not in (1, 2) or sh[-1] != T or \
+                (T > 1 and positions.stride(-1) != 1) or (sh[0] if len(sh) == 2 else 1) != len(sections):
+            raise SpecError(f"positions: need a CUDA int32 tensor [{len(sections)}, {T}] with contiguous rows")
+        _on(positions, dev, "positions")
+        pp, pos_stride = positions.data_ptr(), positions.stride(0) if len(sh) == 2 and sh[0] > 1 else T
+    if kv is not None:
+        counts = array("i", n_rows if n_rows is not None else [])
+        handle, batch, cp = kv.handle, len(counts), counts.buffer_info()[0]
+        if tree_parent is not None:
+            tree = array("i", tree_parent)
+            if counts and len(tree) < max(counts):
+                raise SpecError("tree_parent: shorter than the sequences' rows")
+            tp = tree.buffer_info()[0]
+    elif positions is None:
+        raise SpecError("spec_rope: positions or a cache")
+    rc = load().spec_rope(ctypes.byref(cfg), T, qp, qs, qop, qos, kp, ks, kop, kos, pp, pos_stride, handle, batch, cp, tp,
+                          _stream(stream, dev))
+    if rc:
+        _check(rc)
+
+
 def spec_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logprobs=None, temperature=1.0,
                   stream=None):
     """log p of ``tokens`` [rows] under softmax(logits / temperature) of ``logits``
@@ -556,6 +630,45 @@ def spec_logprobs(logits, tokens, logprob, entropy=None, top_ids=None, top_logpr
     rc = load().spec_logprobs(logits.data_ptr(), SPEC_DTYPE_BF16 if dt is torch.bfloat16 else SPEC_DTYPE_F32,
                               logits.stride(0) if rows > 1 else V, rows, V, temperature, tok, lp, ent, n, ids, tlp,
                               _stream(stream, dev))
+    if rc:
+        _check(rc)
+
+
+def spec_sample_logits(logits, u, tokens, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, logprob=None, probs=None,
+                       stream=None):
+    """One token a row of ``logits`` [rows, V] (f32 or bf16) drawn with ``u`` [rows] (f32 in [0, 1)) after
+    temperature, top-k, top-p and min-p, each a number or a tensor [rows] (top_k int32, the others f32).
+    ``logprob`` [rows] gets the tokens' log probabilities, ``probs`` [rows, V] the distributions drawn from."""
+    sh = logits.shape if logits is not None else ()
+    dt = logits.dtype if len(sh) == 2 else None
+    if dt not in (torch.float32, torch.bfloat16) or not logits.is_cuda or (sh[1] > 1 and logits.stride(1) != 1):
+        raise SpecError("logits: need a 2-D CUDA float32 or bfloat16 tensor with contiguous rows")
+    rows, V = sh
+    dev = torch.cuda.current_device()
+    _on(logits, dev, "logits")
+    cfg = SampleConfig()
+    for value, dtype, name, array_ in ((temperature, torch.float32, "temperature", "temperatures"),
+                                       (top_p, torch.float32, "top_p", "top_ps"), (min_p, torch.float32, "min_p", "min_ps"),
+                                       (top_k, torch.int32, "top_k", "top_ks")):
+        if isinstance(value, torch.Tensor):
+            setattr(cfg, array_, _at(value, dtype, name, rows, dev))
+        else:
+            setattr(cfg, name, value)
+    up = _at(u, torch.float32, "u", rows, dev)
+    tok = _at(tokens, torch.int32, "tokens", rows, dev)
+    lp = _at(logprob, torch.float32, "logprob", rows, dev)
+    pp, ps = None, 0
+    if probs is not None:
+        pp, prow, pV, ps = _rows2d(probs, "probs")
+        _on(probs, dev, "probs")
+        if prow < rows or pV != V:
+            raise SpecError("probs: shape does not match logits")
+        ps = ps if prow > 1 else V
+    if rows == 0:
+        return
+    rc = load().spec_sample_logits(logits.data_ptr(), SPEC_DTYPE_BF16 if dt is torch.bfloat16 else SPEC_DTYPE_F32,
+                                   logits.stride(0) if rows > 1 else V, rows, V, up, ctypes.byref(cfg), tok, lp, pp, ps,
+                                   _stream(stream, dev))
     if rc:
         _check(rc)
 
