@@ -12,21 +12,27 @@
 // units of 2^-q of the best token's (q = 62 - log2 V, 45 for 131072 tokens), exact to
 // 2^-38 of itself and half a unit, and sums of integers are exact in any order.
 //
-// A weight: d = x - m with its rounding error, t = 32 c d as a sum of two floats, the
-// nearest integer 32 n + j split off, 2^(j / 32) from a table that lies in the warp's
-// lanes, and 2^r of the rest (|r| <= 1 / 64) as 1 + a polynomial whose first term is
-// taken in two floats; the product and the shift by n are integer arithmetic.
+// A weight, relative to 2^N (N the least integer not below the best token's log2 w): t = 32 c x as a
+// sum of two floats, the nearest integer 32 n + j split off, 2^(j / 32) from a table that lies
+// in the warp's lanes, and 2^r of the rest (|r| <= 1 / 64) as 1 + a polynomial whose first term
+// is taken in two floats; the product and the shift by N - n are integer arithmetic.
 //
 // A row is taken by a cluster of 1 to 8 CTAs, each warp on a contiguous run of spans
 // of 1024 tokens.  One pass finds the maximum and leaves the maximum of every lane's 32
-// tokens of a span in shared memory.  A bound below which no token can be kept follows
+// tokens of a span in shared memory, and where the row's whole mass is asked for (no
+// top-k, and a nucleus or nothing else) the mass of every span, relative to the span's own
+// maximum: N changes a mass by a shift.  A bound below which no token can be kept follows
 // from what is asked: the best lanes' maxima (k tokens are not below the least of k of
-// them), min_p, or the row's mass (tokens below (1 - p) S / V of it add up to less than
+// them), min_p, or the row's mass S (tokens below (1 - p) S / V of it add up to less than
 // what the nucleus leaves out).  The tokens above the bound, by id, go into a list in the
 // first CTA's shared memory (a span whose maxima lie below it is not read again), where
-// the k-th logit and the nucleus' last one are found by bisection over the order of the
-// floats.  A row with more such tokens than the list holds is bisected where it lies (in
-// L2 by then).
+// the k-th logit and the nucleus' last one are found, by counting what ranks before each token
+// (up to 256) or by bisection over the order of the floats.  A row with more such tokens
+// than the list holds is looked through where it lies (in L2 by then): a histogram of
+// 2048 steps of the logit, of counts or of masses in 32 bits, names the few steps in which
+// the border lies, a second look adds up exactly what lies above them, and the tokens in
+// them are listed and searched.  (What defeats that, a row of equal logits, is bisected as
+// a whole.)
 #include <algorithm>
 #include <cfloat>
 #include <climits>
@@ -46,6 +52,8 @@ constexpr int kDrSegs = 4;                             // segments of a span
 constexpr int kDrSpan = kDrSegs * kLpSeg;
 constexpr int kDrEach = 8;                             // listed tokens a thread
 constexpr int kDrList = kDrEach * kDrThreads;
+constexpr int kDrBins = 2048;                          // steps of a histogram; it lies where the list does
+static_assert(kDrBins * 4 <= kDrList * 8, "histogram");
 constexpr int kDrMaxVocab = 1 << 20;
 constexpr int kDrCtaVocab = 1 << 18;                   // a CTA's share at most: its lanes' maxima take 32 KB
 
@@ -113,18 +121,29 @@ struct DrSmem {
     float wmax[kDrWarps], wlow[kDrWarps];
     float cmax[kDrMaxCtas], clow[kDrMaxCtas];
     int cbad[kDrMaxCtas], wbad[kDrWarps];
-    float T, p, mp, u, ch, cl;
-    int k, ok;
-    u64 S;                                             // the list's result for the other CTAs
-    uint32_t cv; int ci;
+    u64 S;                                             // the first CTA's results for the others
+    uint32_t cv; int ci, holds;
+    int bin_lo, bin_hi;
 };
 
 // A weight's arithmetic, the same in every lane but for the lane's entry of the table.
 struct DrExp {
-    float m, xmin, ch, cl;
-    int q;
+    float b, xmin, ch, cl;                             // b: 0, or the maximum where c x has too many digits
+    int N, q;
     uint32_t t_lo, t_hi;                               // 2^(62 + lane / 32)
+    // weights relative to 2^N for logits up to `top`; the logits that lie 2^-q under it have none
+    SPEC_DEV void refer_to(float top) {
+        const float t = (top - b) * ch * 0.03125f;
+        refer_to_n((int)ceilf(t));
+    }
+    SPEC_DEV void refer_to_n(int n) {
+        N = n;
+        xmin = b + (float)(32 * (N - q)) / ch;
+    }
 };
+// c x as the arithmetic takes it: beyond, logits are taken relative to the maximum (exactly: those near it lie within
+// a factor of two of it)
+constexpr float kDrDigits = 131072.f;
 
 // ln 2 / 32 in two floats, its powers over the factorials, all by 2^37
 constexpr double kDrL = 0.69314718055994530942 / 32, kDrUnit = 137438953472.0;
@@ -137,15 +156,12 @@ SPEC_DEV float2 both(float x) { return make_float2(x, x); }
 
 // weights of two logits: w = v * 2^-n with v in units of 2^-62
 SPEC_DEV void dr_weight2(const DrExp& E, float x0, float x1, u64 (&v)[2], int (&n)[2]) {
-    const float2 neg = both(-1.f), x = make_float2(fmaxf(x0, E.xmin), fmaxf(x1, E.xmin)), nm = both(-E.m);
-    // d + dl = x - m exactly
-    const float2 d = add2(x, nm), b = fma2(x, neg, d), a = fma2(b, neg, d);
-    const float2 dl = add2(fma2(a, neg, x), fma2(b, neg, nm));
-    // -p - e = -t
+    const float2 neg = both(-1.f);
+    const float2 d = add2(make_float2(fmaxf(x0, E.xmin), fmaxf(x1, E.xmin)), both(-E.b));
+    // p + e = 32 t; p leaves its nearest integer
     const float2 np = mul2(d, both(-E.ch));
     float2 e = fma2(d, both(E.ch), np);
     e = fma2(d, both(E.cl), e);
-    e = fma2(dl, both(E.ch), e);
     const float2 magic = both(12582912.f);
     const float2 k = fma2(np, neg, magic), nk = fma2(k, neg, magic), r = fma2(np, neg, nk);
     // 2^((r + e) / 32) - 1 in units of 2^-37
@@ -166,12 +182,12 @@ SPEC_DEV void dr_weight2(const DrExp& E, float x0, float x1, u64 (&v)[2], int (&
         const uint32_t lo = __shfl_sync(0xffffffffu, E.t_lo, ki & 31), hi = __shfl_sync(0xffffffffu, E.t_hi, ki & 31);
         const int delta = __float2int_rn(af[i]) - __float2int_rn(nf[i]);
         v[i] = (((u64)hi << 32) | lo) + (u64)(((long long)(int)hi * delta + 16) >> 5);
-        n[i] = -(ki >> 5);
+        n[i] = E.N - (ki >> 5);
     }
 }
 // to units of 2^-q, to the nearest: cut off, the many small weights of a large vocabulary would be missed in the
-// sum by half a unit each; logits below xmin, which lies 2^-q under the maximum, have no weight
-SPEC_DEV int dr_shift(const DrExp& E, float x, int n) { return x >= E.xmin ? 62 - E.q + n : 64; }
+// sum by half a unit each
+SPEC_DEV int dr_shift(const DrExp& E, float x, int n) { return x >= E.xmin ? max(62 - E.q + n, 1) : 64; }
 SPEC_DEV u64 dr_round(u64 v, int shift) { return ((v >> (shift - 1)) + 1) >> 1; }
 SPEC_DEV void dr_weights(const DrExp& E, const float (&x)[8], u64 (&w)[8]) {
 #pragma unroll
@@ -183,13 +199,15 @@ SPEC_DEV void dr_weights(const DrExp& E, const float (&x)[8], u64 (&w)[8]) {
         w[i + 1] = dr_round(v[1], dr_shift(E, x[i + 1], n[1]));
     }
 }
+// a mass relative to 2^n as one relative to 2^N
+SPEC_DEV u64 dr_rescale(u64 w, int by) { return by <= 0 ? w : (by > 63 ? 0 : dr_round(w, by)); }
 
 // a kept logit: above the cut's value, or equal to it with an id not above the cut's
 struct DrCut { uint32_t v; int id; };
 SPEC_DEV bool dr_kept(const DrCut& c, uint32_t o, int id) { return o > c.v || (o == c.v && id <= c.id); }
 
 template <typename T>
-__global__ void __launch_bounds__(kDrThreads, 3)
+__global__ void __launch_bounds__(kDrThreads, 2)
 draw_kernel(const __grid_constant__ DrawArgs a) {
     pdl_wait();
     pdl_trigger();
@@ -197,8 +215,10 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     __shared__ DrSmem sm;
     extern __shared__ __align__(16) u64 dyn[];
     u64* list = dyn;                                   // [kDrList] (value's order, id) by id; the first CTA's
-    u64* span_sum = dyn + kDrList;                     // [kDrWarps][per]
-    float* lane_max = reinterpret_cast<float*>(span_sum + kDrWarps * a.per);   // [kDrWarps][per][32]
+    uint32_t* hist = reinterpret_cast<uint32_t*>(dyn); // [kDrBins] while there is no list
+    u64* span_sum = dyn + kDrList;                     // [kDrWarps][per] masses, relative to 2^N
+    int* span_n = reinterpret_cast<int*>(span_sum + kDrWarps * a.per);         // [kDrWarps][per] ... to 2^span_n at first
+    float* lane_max = reinterpret_cast<float*>(span_n + kDrWarps * a.per);     // [kDrWarps][per][32]
     cg::cluster_group cl = cg::this_cluster();
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const long long row_i = blockIdx.x / C;
@@ -207,8 +227,6 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     const int V = a.V, mis = (int)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
     const int n_span = (V + mis + kDrSpan - 1) / kDrSpan;
     const int s0 = min(n_span, gw * a.per), s1 = min(n_span, s0 + a.per);
-    span_sum += w * a.per;
-    lane_max += w * a.per * 32;
     auto cluster_sync = [&]() {
         if (C > 1) cl.sync();
         else __syncthreads();
@@ -216,23 +234,29 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     auto everywhere = [&](auto* p, auto value) {       // by one warp: the same variable of every CTA
         if (lane < C) *cl.map_shared_rank(p, lane) = value;
     };
-    cluster_sync();                                    // every CTA has started: its shared memory may be written
+    if (C > 1) cluster_arrive();                       // this CTA has started: its shared memory may be written
 
-    if (t == 0) {
-        const float temp = a.Ts ? a.Ts[row_i] : a.T, p = a.ps ? a.ps[row_i] : a.p, mp = a.mps ? a.mps[row_i] : a.mp;
-        const int k = a.ks ? a.ks[row_i] : a.k;
-        const float u = a.u[row_i];
-        sm.ok = (temp == 0.f || (temp >= 1e-30f && temp <= 1e30f)) && p >= 0.f && mp >= 0.f && mp <= 1.f && k >= 0 && u >= 0.f && u < 1.f;
-        // temperature 0: the best token
-        sm.k = temp == 0.f ? 1 : (k >= V ? 0 : k);
-        sm.T = temp == 0.f ? 1.f : temp;
-        sm.p = p;
-        sm.mp = mp;
-        sm.u = u;
-        const double c = 46.166241308446828384 / (double)sm.T;     // 32 log2 e / T
-        sm.ch = (float)c;
-        sm.cl = (float)(c - (double)sm.ch);
+    const float temp = a.Ts ? a.Ts[row_i] : a.T, top_p = a.ps ? a.ps[row_i] : a.p, min_p = a.mps ? a.mps[row_i] : a.mp;
+    const int top_k = a.ks ? a.ks[row_i] : a.k;
+    const float u = a.u[row_i];
+    const bool settings = (temp == 0.f || (temp >= 1e-30f && temp <= 1e30f)) && top_p >= 0.f && min_p >= 0.f && min_p <= 1.f &&
+                          top_k >= 0 && u >= 0.f && u < 1.f;
+    // temperature 0: the best token
+    const int K = temp == 0.f ? 1 : (top_k >= V ? 0 : top_k);
+    const float T_ = temp == 0.f ? 1.f : temp;
+    const bool nucleus = top_p < 1.f;
+    const bool whole = K == 0 && (nucleus || min_p == 0.f);        // the row's mass is asked for
+    DrExp E;
+    {   // 32 log2 e / T in two floats
+        constexpr double c = 46.166241308446828384;
+        constexpr float c_hi = (float)c, c_lo = (float)(c - (double)c_hi);
+        E.ch = c_hi / T_;
+        E.cl = (fmaf(-E.ch, T_, c_hi) + c_lo) / T_;
     }
+    E.b = 0.f;
+    E.q = a.q;
+    E.t_lo = (uint32_t)a.pow[lane];
+    E.t_hi = (uint32_t)(a.pow[lane] >> 32);
 
     // a span's logits, 32 a lane
     auto load_span = [&](int s, float (&x)[kDrSegs][8]) {
@@ -252,34 +276,81 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
             for (int g = 0; g < kDrSegs; ++g) lp_load(row, V, mis, s * kDrSegs + g, x[g]);
         }
     };
+    // this warp's part of an array by span (a span's owner is warp s / per of the cluster)
+    u64* my_sum = span_sum + w * a.per;
+    int* my_n = span_n + w * a.per;
+    float* my_max = lane_max + w * a.per * 32;
 
-    // -------- the maximum, every lane's maxima, and whether the row has a distribution
+    // -------- the maximum, every lane's maxima, the spans' masses, and whether the row has a distribution
     float mx = -INFINITY;
     bool bad = false;
-    for (int s = s0; s < s1; ++s) {
-        float x[kDrSegs][8], g4[kDrSegs];
-        load_span(s, x);
+    if (whole && settings) {
+        float x[8], nx[8];
+        if (s0 < s1) lp_load(row, V, mis, s0 * kDrSegs, nx);
+        for (int s = s0; s < s1; ++s) {
+            float lm = -INFINITY;
+            u64 sum = 0;
+            int N = INT_MIN;
+#pragma unroll 1
+            for (int g = 0; g < kDrSegs; ++g) {
 #pragma unroll
-        for (int g = 0; g < kDrSegs; ++g) {
-            g4[g] = x[g][0];
+                for (int i = 0; i < 8; ++i) x[i] = nx[i];
+                if (s * kDrSegs + g + 1 < s1 * kDrSegs) lp_load(row, V, mis, s * kDrSegs + g + 1, nx);
+                float gm = x[0];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                bad |= !(x[g][i] <= FLT_MAX);          // NaN or +inf
-                g4[g] = fmaxf(g4[g], x[g][i]);
+                for (int i = 0; i < 8; ++i) {
+                    bad |= !(x[i] <= FLT_MAX);         // NaN or +inf
+                    gm = fmaxf(gm, x[i]);
+                }
+                lm = fmaxf(lm, gm);
+                const float top = warp_redux_max(gm);
+                // (logits this large: none of the row's mass, or its maximum is one of them and the pass does not count)
+                if (!(fabsf(top * E.ch) < kDrDigits)) continue;
+                E.refer_to(top);
+                if (E.N > N) {
+                    if (N != INT_MIN) sum = dr_rescale(sum, E.N - N);
+                    N = E.N;
+                } else {
+                    E.refer_to_n(N);
+                }
+                u64 wt[8];
+                dr_weights(E, x, wt);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum += wt[i];
+            }
+            my_max[(s - s0) * 32 + lane] = lm;
+            mx = fmaxf(mx, lm);
+            sum = dr_warp_sum(sum);
+            if (lane == 0) {
+                my_sum[s - s0] = sum;
+                my_n[s - s0] = N;
             }
         }
-        const float g = fmaxf(fmaxf(g4[0], g4[1]), fmaxf(g4[2], g4[3]));
-        lane_max[(s - s0) * 32 + lane] = g;
-        mx = fmaxf(mx, g);
+    } else {
+        for (int s = s0; s < s1; ++s) {
+            float x[kDrSegs][8], g4[kDrSegs];
+            load_span(s, x);
+#pragma unroll
+            for (int g = 0; g < kDrSegs; ++g) {
+                g4[g] = x[g][0];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    bad |= !(x[g][i] <= FLT_MAX);
+                    g4[g] = fmaxf(g4[g], x[g][i]);
+                }
+            }
+            const float g = fmaxf(fmaxf(g4[0], g4[1]), fmaxf(g4[2], g4[3]));
+            my_max[(s - s0) * 32 + lane] = g;
+            mx = fmaxf(mx, g);
+        }
     }
     mx = warp_redux_max(mx);
     bad = __any_sync(0xffffffffu, bad);
-    __syncthreads();                                   // the settings are there
-    const int K = sm.k;
-    // This warp's share of the bound for top-k: of the warps with a full run of spans each gives the value of
+    __syncwarp();
+    // This warp's share of the bound for top-k: of the warps with a full run of whole spans (none: no bound) each gives the value of
     // (about) its r-th largest lane maximum; the least of these has r tokens a warp that are not below it.
     float low = INFINITY;
-    const int full = n_span / a.per, r_low = K > 0 ? (K + full - 1) / full : 0;
+    const int full = (V + mis) / kDrSpan / a.per, r_low = full > 0 ? (K + full - 1) / full : 0;
     if (K > 0 && gw < full) {
         low = mx;
         if (r_low > 32 * a.per) {
@@ -290,7 +361,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                 const uint32_t mid = lo + (hi - lo) / 2;
                 const float v = dr_value(mid);
                 int n = 0;
-                for (int i = 0; i < a.per; ++i) n += lane_max[i * 32 + lane] >= v;
+                for (int i = 0; i < a.per; ++i) n += my_max[i * 32 + lane] >= v;
                 n = __reduce_add_sync(0xffffffffu, n);
                 if (n >= r_low) {
                     lo = mid;
@@ -305,6 +376,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     }
     if (lane == 0) { sm.wmax[w] = mx; sm.wlow[w] = low; sm.wbad[w] = bad; }
     __syncthreads();
+    if (C > 1) cluster_wait();
     if (w == 0) {
         float m = lane < kDrWarps ? sm.wmax[lane] : -INFINITY, l = lane < kDrWarps ? sm.wlow[lane] : INFINITY;
         const bool b = __any_sync(0xffffffffu, lane < kDrWarps && sm.wbad[lane]);
@@ -323,7 +395,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
         bad |= sm.cbad[i] != 0;
     }
     float* probs = a.probs ? a.probs + row_i * a.p_stride : nullptr;
-    if (bad || m == -INFINITY || !sm.ok) {             // no distribution, or settings out of range
+    if (bad || m == -INFINITY || !settings) {          // no distribution, or settings out of range
         const float nan = __int_as_float(0x7fc00000);
         if (rank == 0 && t == 0) {
             a.tok[row_i] = -1;
@@ -333,19 +405,23 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
             for (int i = rank * kDrThreads + t; i < V; i += C * kDrThreads) probs[i] = nan;
         return;
     }
-    DrExp E;
-    E.m = m;
-    E.ch = sm.ch;
-    E.cl = sm.cl;
-    E.xmin = m - (float)(32 * a.q) / E.ch;             // 62 - q + n is 63 at most
-    E.q = a.q;
-    E.t_lo = (uint32_t)a.pow[lane];
-    E.t_hi = (uint32_t)(a.pow[lane] >> 32);
-    const u64 one = 1ull << a.q, w_min = dr_part(sm.mp, one, true);
+    const bool far = !(fabsf(m * E.ch) < kDrDigits);
+    if (far) E.b = m;
+    E.refer_to(m);
+    u64 one;                                           // the best token's weight
+    {
+        float x[8];
+        u64 wt[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = m;
+        dr_weights(E, x, wt);
+        one = wt[0];
+    }
+    const u64 w_min = dr_part(min_p, one, true);
     const uint32_t o_max = dr_ord(m), o_inf = dr_ord(-INFINITY);
 
-    int par = 0;
-    // sums over the CTA, or over the cluster
+    // sums over the CTA, or over the cluster (the first CTA takes more of the former: each kind has its own turns)
+    int par = 0, cpar = 0;
     auto sum_cta = [&](u64 v) {
         v = dr_warp_sum(v);
         if (lane == 0) sm.red[par][w] = v;
@@ -357,43 +433,76 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
         return s;
     };
     auto sum_all = [&](u64 v) {
-        const int p = par;
         u64 s = sum_cta(v);
         if (C > 1) {
-            if (w == 0) everywhere(&sm.redc[p][rank], s);
+            if (w == 0) everywhere(&sm.redc[cpar][rank], s);
             cl.sync();
             s = 0;
-            for (int i = 0; i < C; ++i) s += sm.redc[p][i];
+            for (int i = 0; i < C; ++i) s += sm.redc[cpar][i];
+            cpar ^= 1;
         }
         return s;
     };
-    // every span of this warp that holds a logit not below `least`: f(logits, span)
+    // every segment of this warp's spans that hold a logit not below `least`: f(logits, segment), then done(span) (also
+    // for the others)
+    auto each_segment = [&](float least, auto f, auto done) {
+        for (int s = s0; s < s1; ++s) {
+            if (__any_sync(0xffffffffu, my_max[(s - s0) * 32 + lane] >= least)) {
+                float x[8], nx[8];
+                lp_load(row, V, mis, s * kDrSegs, nx);
+#pragma unroll 1
+                for (int g = 0; g < kDrSegs; ++g) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = nx[i];
+                    if (g + 1 < kDrSegs) lp_load(row, V, mis, s * kDrSegs + g + 1, nx);
+                    f(x, s * kDrSegs + g);
+                }
+            }
+            done(s);
+        }
+    };
+    // the same for whole spans: f(logits, span)
     auto each_span = [&](float least, auto f) {
         for (int s = s0; s < s1; ++s) {
-            if (!__any_sync(0xffffffffu, lane_max[(s - s0) * 32 + lane] >= least)) continue;
+            if (!__any_sync(0xffffffffu, my_max[(s - s0) * 32 + lane] >= least)) continue;
             float x[kDrSegs][8];
             load_span(s, x);
             f(x, s);
         }
     };
+    // weights of a segment by f(logits, segment, weights): every span's sum in my_sum, the warp's returned
+    auto span_masses = [&](float least, auto f) {
+        u64 sum = 0, mine = 0;
+        each_segment(least, [&](const float (&x)[8], int seg) {
+            u64 wt[8];
+            f(x, seg, wt);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += wt[i];
+        }, [&](int s) {
+            sum = dr_warp_sum(sum);
+            if (lane == 0) my_sum[s - s0] = sum;
+            mine += sum;
+            sum = 0;
+        });
+        __syncwarp();
+        return mine;
+    };
+    auto kept_weights = [&](const DrCut& cut, uint32_t least, u64 w_least) {
+        return [&, cut, least, w_least](const float (&x)[8], int seg, u64 (&wt)[8]) {
+            dr_weights(E, x, wt);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t o = dr_ord(x[i]);
+                if (o < least || wt[i] < w_least || !dr_kept(cut, o, lp_index<T>(mis, seg, i))) wt[i] = 0;
+            }
+        };
+    };
     // the sum of the weights of the kept logits not below `least`
     auto row_mass = [&](uint32_t least, const DrCut& cut) {
-        u64 sum = 0;
-        each_span(dr_value(least), [&](const float (&x)[kDrSegs][8], int s) {
-#pragma unroll 1
-            for (int g = 0; g < kDrSegs; ++g) {
-                u64 wt[8];
-                dr_weights(E, x[g], wt);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t o = dr_ord(x[g][i]);
-                    if (o >= least && dr_kept(cut, o, lp_index<T>(mis, s * kDrSegs + g, i))) sum += wt[i];
-                }
-            }
-        });
-        return sum_all(sum);
+        const u64 mine = span_masses(dr_value(least), kept_weights(cut, least, 0));
+        return sum_all(lane == 0 ? mine : 0);
     };
-    auto row_count = [&](uint32_t least) {
+    auto row_count = [&](uint32_t least, const DrCut&) {
         u64 n = 0;
         each_span(dr_value(least), [&](const float (&x)[kDrSegs][8], int) {
 #pragma unroll
@@ -403,28 +512,9 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
         });
         return sum_all(n);
     };
-    // Tokens by id, weighed by f(logits of a segment, segment, weights): the one at which the sum passes `target`.
-    // found(id, logit) is called by one thread of the cluster; returns the sum of all.
-    auto row_locate = [&](float least, auto f, auto target_of, auto found) {
-        u64 mine = 0;
-        for (int s = s0; s < s1; ++s) {
-            u64 sum = 0;
-            if (__any_sync(0xffffffffu, lane_max[(s - s0) * 32 + lane] >= least)) {
-                float x[kDrSegs][8];
-                load_span(s, x);
-#pragma unroll 1
-                for (int g = 0; g < kDrSegs; ++g) {
-                    u64 wt[8];
-                    f(x[g], s * kDrSegs + g, wt);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) sum += wt[i];
-                }
-            }
-            sum = dr_warp_sum(sum);
-            if (lane == 0) span_sum[s - s0] = sum;
-            mine += sum;
-        }
-        __syncwarp();
+    // With every span's sum in my_sum, `mine` a warp's: the token by id, weighed by f, at which the sum passes the
+    // target; found(id, logit, total) is called by one thread of the cluster.
+    auto locate = [&](u64 mine, auto f, auto target_of, auto found) {
         everywhere(&sm.part[gw], mine);
         cluster_sync();
         u64 total = 0, before = 0;
@@ -436,14 +526,33 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
         if (before <= target && target < before + mine) {
             u64 left = target - before;
             int s = s0;
-            while (left >= span_sum[s - s0]) left -= span_sum[s++ - s0];
-            float x[kDrSegs][8];
-            load_span(s, x);
+            while (s + 1 < s1 && left >= my_sum[s - s0]) left -= my_sum[s++ - s0];
+            // (the first pass' masses are rounded on their way to a common unit: a few of 2^-45)
+            bool done = false, ones = false;
+            {
+                u64 exact = 0;
 #pragma unroll 1
-            for (int g = 0; g < kDrSegs; ++g) {
+                for (int g = 0; g < kDrSegs; ++g) {
+                    float x[8];
+                    u64 wt[8];
+                    lp_load(row, V, mis, s * kDrSegs + g, x);
+                    f(x, s * kDrSegs + g, wt);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) exact += wt[i];
+                }
+                exact = dr_warp_sum(exact);
+                ones = exact == 0;
+                left = ones ? 0 : min(left, exact - 1);
+            }
+#pragma unroll 1
+            for (int g = 0; g < kDrSegs && !done; ++g) {
+                float x[8];
                 u64 wt[8];
-                f(x[g], s * kDrSegs + g, wt);
-                bool done = false;
+                lp_load(row, V, mis, s * kDrSegs + g, x);
+                f(x, s * kDrSegs + g, wt);
+                if (ones)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) wt[i] = x[i] >= -FLT_MAX ? 1 : 0;
 #pragma unroll
                 for (int p = 0; p < NP; ++p) {
                     u64 sum = 0, all;
@@ -459,7 +568,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                                 at += wt[p * VE + i];
                                 if (!hit && left < at) {
                                     hit = true;
-                                    found(lp_index<T>(mis, s * kDrSegs + g, p * VE + i), x[g][p * VE + i]);
+                                    found(lp_index<T>(mis, s * kDrSegs + g, p * VE + i), x[p * VE + i], total);
                                 }
                             }
                         }
@@ -467,7 +576,6 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                     }
                     left -= done ? 0 : all;
                 }
-                if (done) break;
             }
         }
         return total;
@@ -477,64 +585,40 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
         if (a.lp) {
             // log S without cancellation where one token holds nearly all of it
             const float ls = S < 2 * one ? log1pf((float)(S - one) / (float)one) : logf((float)S / (float)one);
-            a.lp[row_i] = (x - m) / sm.T - ls;
+            a.lp[row_i] = (x - m) / T_ - ls;
         }
     };
-
-    // -------- a bound below which nothing is kept
-    const float T_ = sm.T, slack = 1e-3f;
-    float low_bound = -FLT_MAX;
-    u64 p_target = 0;
-    const bool nucleus = sm.p < 1.f;
-    bool listed = true;
-    auto below = [&](float z) {                        // safely below m + T z
-        const float v = m + T_ * (z - slack);
-        return fmaxf(v - fabsf(v) * 1e-6f, -FLT_MAX);
-    };
-    if (K == 1) {
-        low_bound = m;
-    } else if (K > 0) {
-        low_bound = fmaxf(k_low, -FLT_MAX);
-    } else if (nucleus) {
-        const u64 S = row_mass(o_inf + 1, DrCut{o_inf, -1});
-        p_target = max(dr_part(sm.p, S, true), 1ull);
-        low_bound = below(logf(fmaxf((1.f - sm.p) * ((float)S / (float)one) / (float)V, 1e-30f)));
-    } else {
-        listed = sm.mp > 0.f;
-    }
-    // (min_p leaves out of top-k's and the nucleus' tokens, whose number and mass count them)
-    if (sm.mp > 0.f && K == 0) low_bound = fmaxf(low_bound, below(logf(sm.mp)));
-
-    // -------- the list
-    int n_list = 0;
-    if (listed) {
+    // Tokens for which in(logit, segment, element) holds, by id, into the first CTA's list; their number, and
+    // whether the list holds them.
+    auto make_list = [&](float least, int& n_list, auto in) {
         int n = 0;
-        each_span(low_bound, [&](const float (&x)[kDrSegs][8], int) {
+        each_span(least, [&](const float (&x)[kDrSegs][8], int s) {
 #pragma unroll
             for (int g = 0; g < kDrSegs; ++g)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) n += x[g][i] >= low_bound ? 1 : 0;
+                for (int i = 0; i < 8; ++i) n += in(x[g][i], s * kDrSegs + g, i) ? 1 : 0;
         });
         n = __reduce_add_sync(0xffffffffu, n);
         everywhere(&sm.part[gw], (u64)n);
         cluster_sync();
         int before = 0;
+        n_list = 0;
         for (int i = 0; i < C * kDrWarps; ++i) {
             if (i == gw) before = n_list;
             n_list += (int)sm.part[i];
         }
-        listed = n_list <= kDrList;
-        if (listed) {
+        if (n_list <= kDrList && n > 0) {
             u64* first = cl.map_shared_rank(list, 0);
-            each_span(low_bound, [&](const float (&x)[kDrSegs][8], int s) {
+            each_span(least, [&](const float (&x)[kDrSegs][8], int s) {
 #pragma unroll
                 for (int g = 0; g < kDrSegs; ++g)
 #pragma unroll
                     for (int p = 0; p < NP; ++p) {
-                        int c = 0;
+                        uint32_t mine = 0;
 #pragma unroll
-                        for (int i = 0; i < VE; ++i) c += x[g][p * VE + i] >= low_bound ? 1 : 0;
-                        if (!__any_sync(0xffffffffu, c > 0)) continue;
+                        for (int i = 0; i < VE; ++i) mine |= in(x[g][p * VE + i], s * kDrSegs + g, p * VE + i) ? 1u << i : 0u;
+                        if (!__any_sync(0xffffffffu, mine != 0)) continue;
+                        const int c = __popc(mine);
                         int upto = c;
 #pragma unroll
                         for (int o = 1; o < 32; o <<= 1) {
@@ -544,114 +628,195 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                         int at = before + upto - c;
 #pragma unroll
                         for (int i = 0; i < VE; ++i)
-                            if (x[g][p * VE + i] >= low_bound)
+                            if ((mine >> i) & 1u)
                                 first[at++] = (u64)dr_ord(x[g][p * VE + i]) << 32 | (uint32_t)lp_index<T>(mis, s * kDrSegs + g, p * VE + i);
                         before += __shfl_sync(0xffffffffu, upto, 31);
                     }
             });
         }
         cluster_sync();
+        return n_list <= kDrList;
+    };
+
+    // -------- a bound below which nothing is kept
+    const float slack = 1e-3f;
+    float low_bound = -FLT_MAX;
+    u64 S = 0, p_target = 0, mine_all = 0;             // the row's mass, this warp's part of it
+    auto below = [&](float z) {                        // safely below m + T z
+        const float v = m + T_ * (z - slack);
+        return fmaxf(v - fabsf(v) * 1e-6f, -FLT_MAX);
+    };
+    if (whole) {
+        const DrCut all{o_inf, -1};
+        if (far) {
+            mine_all = span_masses(-FLT_MAX, kept_weights(all, o_inf + 1, 0));
+        } else {
+            for (int i = lane; i < s1 - s0; i += 32) my_sum[i] = my_n[i] == INT_MIN ? 0 : dr_rescale(my_sum[i], E.N - my_n[i]);
+            __syncwarp();
+            for (int i = 0; i < s1 - s0; ++i) mine_all += my_sum[i];
+        }
+        S = sum_all(lane == 0 ? mine_all : 0);
     }
+    bool listed = true;
+    if (K == 1) {
+        low_bound = m;
+    } else if (K > 0) {
+        low_bound = full > 0 ? fmaxf(k_low, -FLT_MAX) : -FLT_MAX;
+    } else if (nucleus) {
+        p_target = max(dr_part(top_p, S, true), 1ull);
+        low_bound = below(logf(fmaxf((1.f - top_p) * ((float)S / (float)one) / (float)V, 1e-30f)));
+    } else {
+        listed = min_p > 0.f;
+    }
+    // (min_p leaves out of top-k's and the nucleus' tokens, whose number and mass count them)
+    if (min_p > 0.f && K == 0) low_bound = fmaxf(low_bound, below(logf(min_p)));
+    int n_list = 0;
+    if (listed) listed = make_list(low_bound, n_list, [&](float x, int, int) { return x >= low_bound; });
 
     DrCut cut{o_inf, -1};
     u64 S_kept = 0;
-    if (listed) {
-        if (rank == 0) {
-            // every thread holds `each` neighbours of the list
-            const int each = (n_list + kDrThreads - 1) / kDrThreads;
-            uint32_t o[kDrEach];
-            int id[kDrEach];
-            u64 wt[kDrEach];
-            float x[kDrEach];
+    // -------- the first CTA's threads with `each` neighbours of the list
+    uint32_t o[kDrEach];
+    int id[kDrEach];
+    u64 wt[kDrEach];
+    float x[kDrEach];
+    auto take_list = [&](int n) {
+        const int each = (n + kDrThreads - 1) / kDrThreads;
 #pragma unroll
-            for (int e = 0; e < kDrEach; ++e) {
-                const int i = t * each + e;
-                const bool in = e < each && i < n_list;
-                const u64 key = in ? list[i] : 0;
-                o[e] = (uint32_t)(key >> 32);
-                id[e] = (int)(uint32_t)key;
-                x[e] = in ? dr_value(o[e]) : -INFINITY;
-            }
-            dr_weights(E, x, wt);
+        for (int e = 0; e < kDrEach; ++e) {
+            const int i = t * each + e;
+            const bool in = e < each && i < n;
+            const u64 key = in ? list[i] : 0;
+            o[e] = (uint32_t)(key >> 32);
+            id[e] = (int)(uint32_t)key;
+            x[e] = in ? dr_value(o[e]) : -INFINITY;
+        }
+        dr_weights(E, x, wt);
+#pragma unroll
+        for (int e = 0; e < kDrEach; ++e)
+            if (o[e] == 0) wt[e] = 0;
+    };
+    // the first `n` by id of the tokens equal to v, and those above it, stay
+    auto cut_at = [&](uint32_t v, u64 n) {
+        u64 mine = 0;
+#pragma unroll
+        for (int e = 0; e < kDrEach; ++e) mine += o[e] == v ? 1 : 0;
+        u64 all, at = dr_warp_before(mine, all);
+        if (lane == 0) sm.red[par][w] = all;
+        __syncthreads();
+        for (int i = 0; i < w; ++i) at += sm.red[par][i];
+        par ^= 1;
+#pragma unroll
+        for (int e = 0; e < kDrEach; ++e) {
+            if (o[e] == v && at++ >= n) o[e] = 0;
+            if (o[e] < v) o[e] = 0;
+            if (o[e] == 0) wt[e] = 0;
+        }
+    };
+    auto count = [&](int) -> u64 { return 1; };
+    auto mass = [&](int e) -> u64 { return wt[e]; };
+    auto above = [&](uint32_t v, auto of) {
+        u64 s = 0;
+#pragma unroll
+        for (int e = 0; e < kDrEach; ++e) s += o[e] > v ? of(e) : 0;
+        return sum_cta(s);
+    };
+    // the tokens of the list that come first, by decreasing logit, until they weigh (or count) `need`, which all of
+    // them do
+    auto cut_to = [&](u64 need, uint32_t from, bool weighed, auto of) {
+        uint32_t lo = max(o_inf + 1, from), hi = o_max + 1;   // largest lo whose tokens not below it reach `need`
+        while (hi - lo > 1) {
+            const uint32_t mid = lo + (hi - lo) / 2;
+            u64 s = 0;
+#pragma unroll
+            for (int e = 0; e < kDrEach; ++e) s += o[e] >= mid ? of(e) : 0;
+            if (sum_cta(s) >= need) lo = mid;
+            else hi = mid;
+        }
+        u64 rest = need - above(lo, of);
+        if (weighed) {
+            // tokens of one value have one weight
+            u64 w1 = 0;
 #pragma unroll
             for (int e = 0; e < kDrEach; ++e)
-                if (o[e] == 0) wt[e] = 0;
-            // the first `n` by id of the tokens equal to v, and those above it, stay
-            auto cut_at = [&](uint32_t v, u64 n) {
-                u64 mine = 0;
+                if (o[e] == lo) w1 = wt[e];
+            const u64 holders = sum_cta(w1 ? 1 : 0);
+            w1 = sum_cta(w1) / holders;
+            rest = (rest + w1 - 1) / w1;
+        }
+        cut_at(lo, rest);
+    };
+    // the least kept token of the list as (value's order, ~id)
+    auto least_key = [&]() {
+        u64 least = ~0ull;
 #pragma unroll
-                for (int e = 0; e < kDrEach; ++e) mine += o[e] == v ? 1 : 0;
-                u64 all, at = dr_warp_before(mine, all);
-                if (lane == 0) sm.red[par][w] = all;
-                __syncthreads();
-                for (int i = 0; i < w; ++i) at += sm.red[par][i];
-                par ^= 1;
+        for (int e = 0; e < kDrEach; ++e)
+            if (o[e]) least = min(least, (u64)o[e] << 32 | (uint32_t)~id[e]);
 #pragma unroll
-                for (int e = 0; e < kDrEach; ++e) {
-                    if (o[e] == v && at++ >= n) o[e] = 0;
-                    if (o[e] < v) o[e] = 0;
-                    if (o[e] == 0) wt[e] = 0;
+        for (int b = 16; b > 0; b >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, b));
+        if (lane == 0) sm.red[par][w] = least;
+        __syncthreads();
+        for (int i = 0; i < kDrWarps; ++i) least = min(least, sm.red[par][i]);
+        par ^= 1;
+        return least;
+    };
+    if (listed) {
+        if (rank == 0) {
+            take_list(n_list);
+            const uint32_t from = dr_ord(low_bound);
+            if (n_list <= kDrThreads) {
+                // one token a thread: its place is the number of tokens that rank before it
+                const uint32_t mine = o[0];
+                int place = 0;
+                for (int i = 0; i < n_list; ++i) {
+                    const uint32_t other = (uint32_t)(list[i] >> 32);
+                    place += other > mine || (other == mine && i < t) ? 1 : 0;
                 }
-            };
-            // largest v whose tokens not below it weigh (or count) at least `need`
-            auto bisect = [&](u64 need, auto of) {
-                uint32_t lo = o_inf + 1, hi = o_max + 1;
-                const uint32_t from = dr_ord(low_bound);
-                lo = max(lo, from);
-                while (hi - lo > 1) {
-                    const uint32_t mid = lo + (hi - lo) / 2;
-                    u64 s = 0;
-#pragma unroll
-                    for (int e = 0; e < kDrEach; ++e) s += o[e] >= mid ? of(e) : 0;
-                    if (sum_cta(s) >= need) lo = mid;
-                    else hi = mid;
+                if (K > 0 && place >= K) o[0] = 0;
+                if (o[0] == 0) wt[0] = 0;
+                if (nucleus) {
+                    // masses by place, and what comes before each
+                    u64* by_place = list + kDrThreads;
+                    if (t < n_list) by_place[place] = wt[0];
+                    __syncthreads();
+                    u64 all, at = dr_warp_before(t < n_list ? by_place[t] : 0, all);
+                    if (lane == 0) sm.red[par][w] = all;
+                    __syncthreads();
+                    all = 0;
+                    for (int i = 0; i < kDrWarps; ++i) {
+                        if (i == w) at += all;
+                        all += sm.red[par][i];
+                    }
+                    par ^= 1;
+                    by_place[kDrThreads + t] = at;
+                    __syncthreads();
+                    const u64 target = K > 0 ? max(dr_part(top_p, all, true), 1ull) : p_target;
+                    if (t < n_list && by_place[kDrThreads + place] >= target) o[0] = 0;
+                    if (o[0] == 0) wt[0] = 0;
                 }
-                return lo;
-            };
-            auto above = [&](uint32_t v, auto of) {
-                u64 s = 0;
-#pragma unroll
-                for (int e = 0; e < kDrEach; ++e) s += o[e] > v ? of(e) : 0;
-                return sum_cta(s);
-            };
-            auto count = [&](int) -> u64 { return 1; };
-            auto mass = [&](int e) -> u64 { return wt[e]; };
-            if (K > 0 && n_list > K) {
-                const uint32_t v = bisect((u64)K, count);
-                cut_at(v, (u64)K - above(v, count));
+            } else {
+                if (K > 0 && n_list > K) cut_to((u64)K, from, false, count);
+                if (nucleus) {
+                    const u64 all = above(0, mass), target = K > 0 ? max(dr_part(top_p, all, true), 1ull) : p_target;
+                    if (all >= target) cut_to(target, from, true, mass);
+                }
             }
-            if (nucleus) {
-                const u64 all = above(0, mass), target = K > 0 ? max(dr_part(sm.p, all, true), 1ull) : p_target;
-                if (all >= target) {
-                    const uint32_t v = bisect(target, mass);
-                    const u64 rest = target - above(v, mass);
-                    // tokens of one value have one weight
-                    u64 one_w = 0;
-#pragma unroll
-                    for (int e = 0; e < kDrEach; ++e)
-                        if (o[e] == v) one_w = wt[e];
-                    const u64 holders = sum_cta(one_w ? 1 : 0), sum_w = sum_cta(one_w);
-                    const u64 w1 = sum_w / holders;
-                    cut_at(v, (rest + w1 - 1) / w1);
-                }
-            }
-            u64 mine = 0, least = ~0ull;
+            u64 mine = 0;
 #pragma unroll
             for (int e = 0; e < kDrEach; ++e) {
-                if (o[e]) least = min(least, (u64)o[e] << 32 | (uint32_t)~id[e]);
                 if (wt[e] < w_min) wt[e] = 0;
                 mine += wt[e];
             }
             u64 all, at = dr_warp_before(mine, all);
             if (lane == 0) sm.red[par][w] = all;
             __syncthreads();
-            u64 S = 0;
+            u64 sum = 0;
             for (int i = 0; i < kDrWarps; ++i) {
-                if (i == w) at += S;
-                S += sm.red[par][i];
+                if (i == w) at += sum;
+                sum += sm.red[par][i];
             }
             par ^= 1;
-            const u64 target = dr_part(sm.u, S, false);
+            const u64 target = dr_part(u, sum, false);
             if (at <= target && target < at + mine) {
                 bool hit = false;
 #pragma unroll
@@ -659,18 +824,14 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                     at += wt[e];
                     if (!hit && target < at) {
                         hit = true;
-                        finish(id[e], x[e], S);
+                        finish(id[e], x[e], sum);
                     }
                 }
             }
             if (probs) {
-#pragma unroll
-                for (int o2 = 16; o2 > 0; o2 >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o2));
-                if (lane == 0) sm.red[par][w] = least;
-                __syncthreads();
-                for (int i = 0; i < kDrWarps; ++i) least = min(least, sm.red[par][i]);
+                const u64 least = least_key();
                 if (w == 0) {
-                    everywhere(&sm.S, S);
+                    everywhere(&sm.S, sum);
                     everywhere(&sm.cv, (uint32_t)(least >> 32));
                     everywhere(&sm.ci, (int)~(uint32_t)least);
                 }
@@ -682,61 +843,191 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
         cut = DrCut{sm.cv, sm.ci};
     } else {
         // -------- the row where it lies
-        // the id of the n-th (from 0) of the tokens that equal v
-        auto tie_cut = [&](uint32_t v, u64 n, const DrCut& old) {
-            row_locate(dr_value(v), [&](const float (&x)[8], int seg, u64 (&wt)[8]) {
+        bool masses = whole;                           // my_sum holds the spans' masses of what is kept
+        u64 mine = mine_all;
+        // The cut at which the kept tokens, by decreasing logit, reach `need`, counted or weighed (`all` in all).
+        auto select = [&](u64 need, bool weighed, u64 all) {
+            const DrCut old = cut;
+            auto kept = [&](float v, int seg, int i) { return dr_kept(old, dr_ord(v), lp_index<T>(mis, seg, i)); };
+            float from = low_bound, to = INFINITY;     // the border lies in [from, to)
+            bool found = false, none = false;
+            int n = 0;
+            for (int round = 0; round < 4 && !found; ++round) {
+                // 1. a histogram of [from, to) by the logit, from the top down, in units of 2^-30 of the whole mass, and
+                // what lies above.  (Without a bound the steps are steps of the floats' order.)
+                const float top = fminf(to, m), step = (float)(kDrBins - 1) / fmaxf(top - from, 1e-30f);
+                const bool by_order = from == -FLT_MAX;
+                const float per_one = weighed ? 1073741824.f / ((float)all / (float)one) : 1.f, c2 = E.ch * 0.03125f;
+                for (int i = t; i < kDrBins; i += kDrThreads) hist[i] = 0;
+                __syncthreads();
+                u64 over = 0;
+                each_span(from, [&](const float (&v)[kDrSegs][8], int s) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int id = lp_index<T>(mis, seg, i);
-                    wt[i] = dr_ord(x[i]) == v && id >= 0 && id < V && dr_kept(old, v, id) ? 1 : 0;
+                    for (int g = 0; g < kDrSegs; ++g)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            if (!(v[g][i] >= from) || !kept(v[g][i], s * kDrSegs + g, i)) continue;
+                            const uint32_t c = weighed ? __float2uint_rn(ex2((v[g][i] - m) * c2) * per_one) : 1u;
+                            if (v[g][i] >= to) over += c;
+                            else atomicAdd(&hist[by_order ? (o_max - dr_ord(v[g][i])) >> 21 : min(kDrBins - 1, (int)((top - v[g][i]) * step))], c);
+                        }
+                });
+                over = sum_all(over);                  // (and the histograms are there)
+                // 2. the whole row's histogram, 8 steps a thread, and the steps that may hold the border
+                constexpr int kEachBin = kDrBins / kDrThreads;
+                u64 h[kEachBin], sum = 0;
+#pragma unroll
+                for (int e = 0; e < kEachBin; ++e) {
+                    h[e] = 0;
+                    for (int i = 0; i < C; ++i) h[e] += *cl.map_shared_rank(&hist[t * kEachBin + e], i);
+                    sum += h[e];
                 }
-            }, [&](u64) { return n; }, [&](int id, float) {
-                for (int i = 0; i < C; ++i) *cl.map_shared_rank(&sm.ci, i) = id;
-            });
-            cluster_sync();
-            return DrCut{v, sm.ci};
-        };
-        auto bisect = [&](u64 need, auto of) {
+                u64 wall, at = dr_warp_before(sum, wall);
+                if (lane == 0) sm.red[par][w] = wall;
+                if (t == 0) { sm.bin_lo = kDrBins; sm.bin_hi = 0; }
+                __syncthreads();
+                u64 whole_sum = over;
+                at += over;
+                for (int i = 0; i < kDrWarps; ++i) {
+                    if (i < w) at += sm.red[par][i];
+                    whole_sum += sm.red[par][i];
+                }
+                par ^= 1;
+                // (masses are rounded and a little off; a border outside these steps is noticed below)
+                const u64 goal = weighed ? (u64)((float)need / (float)all * 1073741824.f) : need, err = weighed ? 8192 : 0;
+#pragma unroll
+                for (int e = 0; e < kEachBin; ++e) {
+                    at += h[e];
+                    if (at + err >= goal) atomicMin(&sm.bin_lo, t * kEachBin + e);      // first that may hold the border
+                    if (at < goal + err) atomicMax(&sm.bin_hi, t * kEachBin + e + 1);   // past it: the last that may
+                }
+                cluster_sync();                        // (the histograms are read; the list may be written)
+                if (whole_sum + err < goal) {          // min_p's bound lies above the border
+                    none = true;
+                    break;
+                }
+                const int b_lo = min(sm.bin_lo, kDrBins - 1), b_hi = min(sm.bin_hi, kDrBins - 1);
+                __syncthreads();                       // (before they are set again)
+                if (by_order) {
+                    const uint32_t up = (uint32_t)b_lo << 21, down = ((uint32_t)b_hi + 1) << 21;
+                    if (b_lo > 0) to = dr_value(o_max - up + 1);
+                    from = b_hi + 1 < 2048 && down < o_max - o_inf ? dr_value(o_max - down) : -FLT_MAX;
+                } else {
+                    // a step more on either side: what the steps' rounding may move
+                    if (b_lo > 1) to = top - (float)(b_lo - 1) / step;
+                    from = fmaxf(from, top - (float)(b_hi + 2) / step);
+                }
+                // 3. the tokens of these steps, if the list holds them; else the steps are taken apart
+                found = make_list(from, n, [&](float v, int seg, int i) { return v >= from && v < to && kept(v, seg, i); });
+            }
+            if (none) {
+                masses = false;
+                return;
+            }
+            if (found) {
+                // 4. what lies above them, exactly, and the border among the listed
+                u64 over = 0;
+                if (weighed) {
+                    mine = span_masses(to, [&](const float (&v)[8], int seg, u64 (&wt8)[8]) {
+                        bool any = false;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) any |= v[i] >= to;
+                        if (__any_sync(0xffffffffu, any)) dr_weights(E, v, wt8);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (!(v[i] >= to) || !kept(v[i], seg, i)) wt8[i] = 0;
+                    });
+                    over = sum_all(lane == 0 ? mine : 0);
+                } else {
+                    each_span(to, [&](const float (&v)[kDrSegs][8], int s) {
+#pragma unroll
+                        for (int g = 0; g < kDrSegs; ++g)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) over += v[g][i] >= to && kept(v[g][i], s * kDrSegs + g, i) ? 1 : 0;
+                    });
+                    over = sum_all(over);
+                }
+                masses = weighed;
+                if (rank == 0) {
+                    take_list(n);
+                    const u64 in = weighed ? above(0, mass) : above(0, count);
+                    const bool holds = over < need && need <= over + in;
+                    if (holds) {
+                        if (weighed) cut_to(need - over, o_inf + 1, true, mass);
+                        else cut_to(need - over, o_inf + 1, false, count);
+                        const u64 least = least_key();
+                        if (weighed) {
+                            // the listed tokens that stay, to the masses of their spans
+#pragma unroll
+                            for (int e = 0; e < kDrEach; ++e)
+                                if (o[e]) {
+                                    const int s = (id[e] + mis) / kDrSpan, owner = s / a.per;
+                                    atomicAdd(cl.map_shared_rank(&span_sum[(owner % kDrWarps) * a.per + s - owner * a.per], owner / kDrWarps), wt[e]);
+                                }
+                        }
+                        if (w == 0) {
+                            everywhere(&sm.cv, (uint32_t)(least >> 32));
+                            everywhere(&sm.ci, (int)~(uint32_t)least);
+                        }
+                    }
+                    if (w == 0) everywhere(&sm.holds, (int)holds);
+                }
+                cluster_sync();
+                if (sm.holds) {
+                    cut = DrCut{sm.cv, sm.ci};
+                    if (weighed) {
+                        mine = 0;
+                        for (int i = 0; i < s1 - s0; ++i) mine += my_sum[i];
+                    }
+                    return;
+                }
+            }
+            // the whole row by bisection (more equal logits than the list holds)
+            masses = false;
             uint32_t lo = max(o_inf + 1, dr_ord(low_bound)), hi = o_max + 1;
+            auto of = [&](uint32_t v) { return weighed ? row_mass(v, old) : row_count(v, old); };
             while (hi - lo > 1) {
                 const uint32_t mid = lo + (hi - lo) / 2;
                 if (of(mid) >= need) lo = mid;
                 else hi = mid;
             }
-            return lo;
+            if (of(lo) < need) return;
+            u64 rest = need - (lo < o_max ? of(lo + 1) : 0);
+            if (weighed) {
+                float v[8];
+                u64 wt8[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = dr_value(lo);
+                dr_weights(E, v, wt8);
+                rest = (rest + wt8[0] - 1) / wt8[0];
+            }
+            // the id of the last of the equal tokens that stay
+            auto tie = [&](const float (&v)[8], int seg, u64 (&wt8)[8]) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int d = lp_index<T>(mis, seg, i);
+                    wt8[i] = dr_ord(v[i]) == lo && d >= 0 && d < V && dr_kept(old, lo, d) ? 1 : 0;
+                }
+            };
+            const u64 ties = span_masses(dr_value(lo), tie);
+            locate(ties, tie, [&](u64) { return rest - 1; }, [&](int d, float, u64) {
+                for (int i = 0; i < C; ++i) *cl.map_shared_rank(&sm.ci, i) = d;
+            });
+            cluster_sync();
+            cut = DrCut{lo, sm.ci};
         };
         if (K > 0) {
             // (at least K tokens are finite, or every finite one stays)
-            if (row_count(o_inf + 1) > (u64)K) {
-                const uint32_t v = bisect((u64)K, row_count);
-                const u64 over = v < o_max ? row_count(v + 1) : 0;
-                cut = tie_cut(v, (u64)K - over - 1, cut);
+            if (row_count(o_inf + 1, cut) > (u64)K) select((u64)K, false, 0);
+            if (nucleus) {
+                S = row_mass(o_inf + 1, cut);
+                p_target = max(dr_part(top_p, S, true), 1ull);
             }
         }
-        if (nucleus) {
-            if (K > 0) p_target = max(dr_part(sm.p, row_mass(o_inf + 1, cut), true), 1ull);
-            auto mass = [&](uint32_t v) { return row_mass(v, cut); };
-            const uint32_t v = bisect(p_target, mass);
-            if (mass(v) >= p_target) {
-                const u64 rest = p_target - (v < o_max ? mass(v + 1) : 0);
-                float x[8];
-                u64 wt[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = dr_value(v);
-                dr_weights(E, x, wt);
-                cut = tie_cut(v, (rest + wt[0] - 1) / wt[0] - 1, cut);
-            }
-        }
-        S_kept = row_locate(dr_value(max(cut.v, o_inf + 1)), [&](const float (&x)[8], int seg, u64 (&wt)[8]) {
-            dr_weights(E, x, wt);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (wt[i] < w_min || !dr_kept(cut, dr_ord(x[i]), lp_index<T>(mis, seg, i))) wt[i] = 0;
-        }, [&](u64 total) { return dr_part(sm.u, total, false); }, [&](int id, float x) {
-            u64 total = 0;
-            for (int i = 0; i < C * kDrWarps; ++i) total += sm.part[i];
-            finish(id, x, total);
-        });
+        if (nucleus) select(p_target, true, S);
+        const auto f = kept_weights(cut, o_inf + 1, w_min);
+        if (!masses || w_min > 1) mine = span_masses(dr_value(max(cut.v, o_inf + 1)), f);
+        S_kept = locate(mine, f, [&](u64 total) { return dr_part(u, total, false); }, finish);
     }
     if (!probs) {
         cluster_sync();                                // (a CTA's shared memory stays while others read it)
@@ -744,41 +1035,41 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     }
 
     // -------- the distribution
-    const float inv = (float)one / (float)S_kept;
+    const float inv = (float)(1ull << a.q) / (float)S_kept;
     const float least = dr_value(max(cut.v, o_inf + 1));
+#pragma unroll 1
     for (int s = s0; s < s1; ++s) {
-        const bool any = __any_sync(0xffffffffu, lane_max[(s - s0) * 32 + lane] >= least);
-        float x[kDrSegs][8];
-        if (any) load_span(s, x);
+        const bool any = __any_sync(0xffffffffu, my_max[(s - s0) * 32 + lane] >= least);
 #pragma unroll 1
         for (int g = 0; g < kDrSegs; ++g) {
-            float y[8];
+            float v[8], y[8];
+            if (any) lp_load(row, V, mis, s * kDrSegs + g, v);
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
                 y[i] = y[i + 1] = 0.f;
                 if (!any) continue;
-                u64 v[2];
+                u64 vv[2];
                 int n[2];
-                dr_weight2(E, x[g][i], x[g][i + 1], v, n);
+                dr_weight2(E, v[i], v[i + 1], vv, n);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float l = x[g][i + j];
+                    const float l = v[i + j];
                     const bool in = l >= E.xmin && dr_kept(cut, dr_ord(l), lp_index<T>(mis, s * kDrSegs + g, i + j)) &&
-                                    dr_round(v[j], dr_shift(E, l, n[j])) >= w_min;
-                    if (in) y[i + j] = (float)v[j] * __uint_as_float((uint32_t)(127 - 62 - n[j]) << 23) * inv;
+                                    dr_round(vv[j], dr_shift(E, l, n[j])) >= w_min;
+                    if (in) y[i + j] = (float)vv[j] * __uint_as_float((uint32_t)(127 - 62 - n[j]) << 23) * inv;
                 }
             }
 #pragma unroll
             for (int p = 0; p < NP; ++p) {
-                const int id = lp_index<T>(mis, s * kDrSegs + g, p * VE);
-                if (a.p_vec && id >= 0 && id + VE <= V) {
+                const int d = lp_index<T>(mis, s * kDrSegs + g, p * VE);
+                if (a.p_vec && d >= 0 && d + VE <= V) {
 #pragma unroll
                     for (int i = 0; i < VE; i += 4)
-                        *reinterpret_cast<float4*>(probs + id + i) = make_float4(y[p * VE + i], y[p * VE + i + 1], y[p * VE + i + 2], y[p * VE + i + 3]);
+                        *reinterpret_cast<float4*>(probs + d + i) = make_float4(y[p * VE + i], y[p * VE + i + 1], y[p * VE + i + 2], y[p * VE + i + 3]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < VE; ++i)
-                        if (id + i >= 0 && id + i < V) probs[id + i] = y[p * VE + i];
+                        if (d + i >= 0 && d + i < V) probs[d + i] = y[p * VE + i];
                 }
             }
         }
@@ -786,7 +1077,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     cluster_sync();
 }
 
-static size_t dr_smem(int per) { return (size_t)kDrList * 8 + (size_t)kDrWarps * per * (8 + 32 * 4); }
+static size_t dr_smem(int per) { return (size_t)kDrList * 8 + (size_t)kDrWarps * per * (8 + 4 + 32 * 4); }
 
 }  // namespace spec
 
