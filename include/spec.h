@@ -595,9 +595,10 @@ int spec_logprobs(const void* logits, int32_t dtype, int64_t lg_stride, int32_t 
  *            those that stay
  *   probs    device f32 out, nullable, row r at probs + r * p_stride: that
  *            distribution, zeros elsewhere (the p or q of spec_accept)
- * A weight is exact to 2^-38 of itself and to half of 2^-q of the best token's
- * (q = 62 - ceil log2 vocab, 45 for 131072 tokens), and sums are exact: the token is that
- * of the exact weights unless u or a cut lies that close to a border.  Calls of any number of rows give the same bits.  A row without
+ * A weight is exact to 2^-35 of itself and to 2^-49 of the best token's (to
+ * 2^(log2 vocab - 61) of it where the row's weights add up to more than 2^12 of them), and
+ * sums are exact: the token is that of the exact weights unless u or a cut lies that
+ * close to a border.  A row without
  * a distribution (NaN or +inf in it, or every token masked), and one whose settings
  * by row or u are out of range, gets token -1 and NaN.  vocab <= 1048576.  async. */
 int spec_sample_logits(const void* logits, int32_t dtype, int64_t lg_stride, int32_t rows, int32_t vocab,

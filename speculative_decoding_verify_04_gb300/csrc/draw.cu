@@ -9,13 +9,16 @@
 // their sum.  Which token's interval u meets, and which token ends the nucleus, are
 // matters of the last bits: sums of 32-bit floats over a large vocabulary would give
 // another token once in a few dozen rows.  So a weight is held as a 64-bit integer in
-// units of 2^-q of the best token's (q = 62 - log2 V, 45 for 131072 tokens), exact to
-// 2^-38 of itself and half a unit, and sums of integers are exact in any order.
+// units of 2^-q of about the best token's (q = 50, less where the row's mass takes more bits: 45
+// for 131072 equal tokens), exact to 2^-35 of itself and a unit, and sums of integers are
+// exact in any order.
 //
-// A weight, relative to 2^N (N the least integer not below the best token's log2 w): t = 32 c x as a
-// sum of two floats, the nearest integer 32 n + j split off, 2^(j / 32) from a table that lies
-// in the warp's lanes, and 2^r of the rest (|r| <= 1 / 64) as 1 + a polynomial whose first term
-// is taken in two floats; the product and the shift by N - n are integer arithmetic.
+// A weight, relative to 2^N (N the least integer not below the best token's log2 w): t = 2048 c x
+// as a sum of two floats, the nearest integer 2048 n + j split off, 2^(j / 2048) from a table in
+// shared memory (made by each CTA, products of two small ones), and 2^r of the rest
+// (|r| <= 1 / 4096) as 1 + two terms; the product and the shift by N - n are integer
+// arithmetic.  About 20 instructions a logit.  (A table of 32 steps in the warp's lanes and six terms,
+// the first in two floats: 30, and 622 us a call for 512 rows of 131072 to their nuclei.)
 //
 // A row is taken by a cluster of 1 to 8 CTAs, each warp on a contiguous run of spans
 // of 1024 tokens.  One pass finds the maximum and leaves the maximum of every lane's 32
@@ -46,12 +49,15 @@ namespace cg = cooperative_groups;
 namespace spec {
 
 constexpr int kDrThreads = 256;
+constexpr int kDrCtasWanted = 3;                       // CTAs an SM up to which rows are cut into more of them
 constexpr int kDrWarps = kDrThreads / 32;
 constexpr int kDrMaxCtas = 8;
 constexpr int kDrSegs = 4;                             // segments of a span
 constexpr int kDrSpan = kDrSegs * kLpSeg;
 constexpr int kDrEach = 8;                             // listed tokens a thread
 constexpr int kDrList = kDrEach * kDrThreads;
+constexpr int kDrSpanUnit = 51;                        // 1024 weights in units of 2^-51 fit 64 bits, and so does a listed token's
+constexpr int kDrListUnit = 50;
 constexpr int kDrBins = 2048;                          // steps of a histogram; it lies where the list does
 static_assert(kDrBins * 4 <= kDrList * 8, "histogram");
 constexpr int kDrMaxVocab = 1 << 20;
@@ -59,13 +65,14 @@ constexpr int kDrCtaVocab = 1 << 18;                   // a CTA's share at most:
 
 struct DrawArgs {
     const void* x; long long stride;
-    int V, per, q;                                     // per: spans a warp; q: a weight of 1 is 2^q
+    int V, per, q;                                     // per: spans a warp; q: the whole row's weights fit 64 bits as integers
+                                                       // in units of 2^-q, whatever they are
     const float* u;
     float T, p, mp; int k;
     const float* Ts; const float* ps; const float* mps; const int* ks;   // settings by row; null: the ones above
     int* tok; float* lp;
     float* probs; long long p_stride; int p_vec;
-    unsigned long long pow[32];                        // 2^(62 + j / 32)
+    unsigned long long coarse[32], fine[64];           // 2^(62 + j / 32), 2^(63 + j / 2048)
 };
 
 typedef unsigned long long u64;
@@ -117,7 +124,8 @@ SPEC_DEV u64 dr_warp_before(u64 v, u64& total) {
 struct DrSmem {
     u64 red[2][kDrWarps];
     u64 redc[2][kDrMaxCtas];
-    u64 part[kDrMaxCtas * kDrWarps];                   // every warp's sum, in every CTA
+    u64 part[kDrMaxCtas * kDrWarps];                   // every warp's sum, in every CTA; a barrier lies between its uses
+    u64 mass[kDrMaxCtas * kDrWarps];                   // every warp's share of the row's mass
     float wmax[kDrWarps], wlow[kDrWarps];
     float cmax[kDrMaxCtas], clow[kDrMaxCtas];
     int cbad[kDrMaxCtas], wbad[kDrWarps];
@@ -126,81 +134,72 @@ struct DrSmem {
     int bin_lo, bin_hi;
 };
 
-// A weight's arithmetic, the same in every lane but for the lane's entry of the table.
+// A weight's arithmetic.
+constexpr int kDrSteps = 2048;                         // of the table, an octave
 struct DrExp {
-    float b, xmin, ch, cl;                             // b: 0, or the maximum where c x has too many digits
+    float b, ch, cl;                                   // b: 0, or the maximum where c x has too many digits
+    float most;                                        // -2048 t of a logit without a weight
     int N, q;
-    uint32_t t_lo, t_hi;                               // 2^(62 + lane / 32)
-    // weights relative to 2^N for logits up to `top`; the logits that lie 2^-q under it have none
-    SPEC_DEV void refer_to(float top) {
-        const float t = (top - b) * ch * 0.03125f;
-        refer_to_n((int)ceilf(t));
-    }
+    const u64* table;                                  // 2^(62 + j / 2048), in shared memory
+    // weights relative to 2^N for logits up to `top`
+    SPEC_DEV void refer_to(float top) { refer_to_n((int)ceilf((top - b) * ch * (1.f / kDrSteps))); }
     SPEC_DEV void refer_to_n(int n) {
         N = n;
-        xmin = b + (float)(32 * (N - q)) / ch;
+        most = (float)(-kDrSteps * (N - q - 4));       // well below 2^-q
     }
 };
 // c x as the arithmetic takes it: beyond, logits are taken relative to the maximum (exactly: those near it lie within
 // a factor of two of it)
-constexpr float kDrDigits = 131072.f;
+constexpr float kDrDigits = 2097152.f;
 
-// ln 2 / 32 in two floats, its powers over the factorials, all by 2^37
-constexpr double kDrL = 0.69314718055994530942 / 32, kDrUnit = 137438953472.0;
-constexpr float kDrL1h = (float)(kDrL * kDrUnit), kDrL1l = (float)(kDrL * kDrUnit - (double)kDrL1h);
-constexpr float kDrL2 = (float)(kDrL * kDrL / 2 * kDrUnit), kDrL3 = (float)(kDrL * kDrL * kDrL / 6 * kDrUnit),
-                kDrL4 = (float)(kDrL * kDrL * kDrL * kDrL / 24 * kDrUnit),
-                kDrL5 = (float)(kDrL * kDrL * kDrL * kDrL * kDrL / 120 * kDrUnit);
+// ln 2 / 2048 and half its square, by 2^36
+constexpr double kDrL = 0.69314718055994530942 / kDrSteps;
+constexpr float kDrL1 = (float)(kDrL * 68719476736.0), kDrL2 = (float)(kDrL * kDrL / 2 * 68719476736.0);
 
 SPEC_DEV float2 both(float x) { return make_float2(x, x); }
 
 // weights of two logits: w = v * 2^-n with v in units of 2^-62
 SPEC_DEV void dr_weight2(const DrExp& E, float x0, float x1, u64 (&v)[2], int (&n)[2]) {
     const float2 neg = both(-1.f);
-    const float2 d = add2(make_float2(fmaxf(x0, E.xmin), fmaxf(x1, E.xmin)), both(-E.b));
-    // p + e = 32 t; p leaves its nearest integer
-    const float2 np = mul2(d, both(-E.ch));
+    const float2 d = add2(make_float2(x0, x1), both(-E.b));
+    // p + e = 2048 t; p leaves its nearest integer.  (Where p is cut short, e, NaN for a masked logit, is
+    // anything: what comes of it is shifted out.)
+    float2 np = mul2(d, both(-E.ch));
     float2 e = fma2(d, both(E.ch), np);
     e = fma2(d, both(E.cl), e);
+    np = make_float2(fminf(np.x, E.most), fminf(np.y, E.most));
     const float2 magic = both(12582912.f);
     const float2 k = fma2(np, neg, magic), nk = fma2(k, neg, magic), r = fma2(np, neg, nk);
-    // 2^((r + e) / 32) - 1 in units of 2^-37
-    const float2 s = add2(r, e);
-    float2 g = fma2(both(kDrL5), s, both(kDrL4));
-    g = fma2(g, s, both(kDrL3));
-    g = fma2(g, s, both(kDrL2));
-    g = mul2(g, s);
-    const float2 na = mul2(r, both(-kDrL1h));
-    float2 ae = fma2(r, both(kDrL1h), na);
-    ae = fma2(r, both(kDrL1l), ae);
-    ae = fma2(e, both(kDrL1h), ae);
-    ae = fma2(g, s, ae);
-    const float kf[2] = {k.x, k.y}, nf[2] = {na.x, na.y}, af[2] = {ae.x, ae.y};
+    // 2^((r + e) / 2048) - 1 in units of 2^-36: off by 2^-36 of a weight, its f32 sums; the table's value to 26 bits
+    // is enough for the product
+    const float2 s = add2(r, e), f = mul2(fma2(both(kDrL2), s, both(kDrL1)), s);
+    const float kf[2] = {k.x, k.y}, ff[2] = {f.x, f.y};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int ki = __float_as_int(kf[i]) - 0x4B400000;
-        const uint32_t lo = __shfl_sync(0xffffffffu, E.t_lo, ki & 31), hi = __shfl_sync(0xffffffffu, E.t_hi, ki & 31);
-        const int delta = __float2int_rn(af[i]) - __float2int_rn(nf[i]);
-        v[i] = (((u64)hi << 32) | lo) + (u64)(((long long)(int)hi * delta + 16) >> 5);
-        n[i] = E.N - (ki >> 5);
+        const u64 T = E.table[ki & (kDrSteps - 1)];
+        v[i] = T + (u64)((long long)((int)(T >> 32) >> 4) * __float2int_rn(ff[i]));
+        n[i] = E.N - (ki >> 11);
     }
 }
-// to units of 2^-q, to the nearest: cut off, the many small weights of a large vocabulary would be missed in the
-// sum by half a unit each
-SPEC_DEV int dr_shift(const DrExp& E, float x, int n) { return x >= E.xmin ? max(62 - E.q + n, 1) : 64; }
-SPEC_DEV u64 dr_round(u64 v, int shift) { return ((v >> (shift - 1)) + 1) >> 1; }
+// v * 2^-n in units of 2^-q, cut off (shifts of 64 and more give zero)
+SPEC_DEV u64 dr_units(const DrExp& E, u64 v, int n) {
+    u64 r;
+    asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(v), "r"(62 - E.q + n));
+    return r;
+}
 SPEC_DEV void dr_weights(const DrExp& E, const float (&x)[8], u64 (&w)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
         u64 v[2];
         int n[2];
         dr_weight2(E, x[i], x[i + 1], v, n);
-        w[i] = dr_round(v[0], dr_shift(E, x[i], n[0]));
-        w[i + 1] = dr_round(v[1], dr_shift(E, x[i + 1], n[1]));
+        w[i] = dr_units(E, v[0], n[0]);
+        w[i + 1] = dr_units(E, v[1], n[1]);
     }
 }
-// a mass relative to 2^n as one relative to 2^N
-SPEC_DEV u64 dr_rescale(u64 w, int by) { return by <= 0 ? w : (by > 63 ? 0 : dr_round(w, by)); }
+// a mass in units of 2^-by, to the nearest
+SPEC_DEV u64 dr_rescale(u64 w, int by) { return by <= 0 ? w << -by : (by > 63 ? 0 : ((w >> (by - 1)) + 1) >> 1); }
 
 // a kept logit: above the cut's value, or equal to it with an id not above the cut's
 struct DrCut { uint32_t v; int id; };
@@ -219,6 +218,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     u64* span_sum = dyn + kDrList;                     // [kDrWarps][per] masses, relative to 2^N
     int* span_n = reinterpret_cast<int*>(span_sum + kDrWarps * a.per);         // [kDrWarps][per] ... to 2^span_n at first
     float* lane_max = reinterpret_cast<float*>(span_n + kDrWarps * a.per);     // [kDrWarps][per][32]
+    u64* table = reinterpret_cast<u64*>(lane_max + kDrWarps * a.per * 32);     // [kDrSteps]
     cg::cluster_group cl = cg::this_cluster();
     const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const long long row_i = blockIdx.x / C;
@@ -247,16 +247,17 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     const bool nucleus = top_p < 1.f;
     const bool whole = K == 0 && (nucleus || min_p == 0.f);        // the row's mass is asked for
     DrExp E;
-    {   // 32 log2 e / T in two floats
-        constexpr double c = 46.166241308446828384;
+    {   // 2048 log2 e / T in two floats
+        constexpr double c = 1.4426950408889634074 * kDrSteps;
         constexpr float c_hi = (float)c, c_lo = (float)(c - (double)c_hi);
         E.ch = c_hi / T_;
         E.cl = (fmaf(-E.ch, T_, c_hi) + c_lo) / T_;
     }
     E.b = 0.f;
-    E.q = a.q;
-    E.t_lo = (uint32_t)a.pow[lane];
-    E.t_hi = (uint32_t)(a.pow[lane] >> 32);
+    E.q = kDrSpanUnit;
+    E.table = table;
+    for (int i = t; i < kDrSteps; i += kDrThreads) table[i] = __umul64hi(a.coarse[i >> 6], a.fine[i & 63]) << 1;
+    __syncthreads();
 
     // a span's logits, 32 a lane
     auto load_span = [&](int s, float (&x)[kDrSegs][8]) {
@@ -276,6 +277,32 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
             for (int g = 0; g < kDrSegs; ++g) lp_load(row, V, mis, s * kDrSegs + g, x[g]);
         }
     };
+    // a span's logits, 8 a lane at a time: f(logits, segment), the next ones on their way
+    auto walk_span = [&](int s, auto f) {
+        float x[8];
+        if (s * kDrSpan >= mis && (s + 1) * kDrSpan - mis <= V) {
+            uint4 nx[NP];
+            const T* at = row + (s * kDrSpan - mis + lane * VE);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) nx[i] = __ldg(reinterpret_cast<const uint4*>(at + i * 32 * VE));
+#pragma unroll 1
+            for (int g = 0; g < kDrSegs; ++g) {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) lp_unpack<T>(nx[i], &x[i * VE]);
+                at += kLpSeg;
+                if (g + 1 < kDrSegs)
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) nx[i] = __ldg(reinterpret_cast<const uint4*>(at + i * 32 * VE));
+                f(x, s * kDrSegs + g);
+            }
+        } else {
+#pragma unroll 1
+            for (int g = 0; g < kDrSegs; ++g) {
+                lp_load(row, V, mis, s * kDrSegs + g, x);
+                f(x, s * kDrSegs + g);
+            }
+        }
+    };
     // this warp's part of an array by span (a span's owner is warp s / per of the cluster)
     u64* my_sum = span_sum + w * a.per;
     int* my_n = span_n + w * a.per;
@@ -285,17 +312,11 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     float mx = -INFINITY;
     bool bad = false;
     if (whole && settings) {
-        float x[8], nx[8];
-        if (s0 < s1) lp_load(row, V, mis, s0 * kDrSegs, nx);
         for (int s = s0; s < s1; ++s) {
             float lm = -INFINITY;
             u64 sum = 0;
             int N = INT_MIN;
-#pragma unroll 1
-            for (int g = 0; g < kDrSegs; ++g) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = nx[i];
-                if (s * kDrSegs + g + 1 < s1 * kDrSegs) lp_load(row, V, mis, s * kDrSegs + g + 1, nx);
+            walk_span(s, [&](const float (&x)[8], int) {
                 float gm = x[0];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -305,19 +326,18 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                 lm = fmaxf(lm, gm);
                 const float top = warp_redux_max(gm);
                 // (logits this large: none of the row's mass, or its maximum is one of them and the pass does not count)
-                if (!(fabsf(top * E.ch) < kDrDigits)) continue;
-                E.refer_to(top);
-                if (E.N > N) {
-                    if (N != INT_MIN) sum = dr_rescale(sum, E.N - N);
-                    N = E.N;
-                } else {
+                if (!(fabsf(top * E.ch) < kDrDigits)) return;
+                const int n = (int)ceilf(top * E.ch * (1.f / kDrSteps));
+                if (n > N) {
+                    if (N != INT_MIN) sum = dr_rescale(sum, n - N);
+                    N = n;
                     E.refer_to_n(N);
                 }
                 u64 wt[8];
                 dr_weights(E, x, wt);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum += wt[i];
-            }
+            });
             my_max[(s - s0) * 32 + lane] = lm;
             mx = fmaxf(mx, lm);
             sum = dr_warp_sum(sum);
@@ -407,17 +427,16 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     }
     const bool far = !(fabsf(m * E.ch) < kDrDigits);
     if (far) E.b = m;
-    E.refer_to(m);
-    u64 one;                                           // the best token's weight
-    {
-        float x[8];
-        u64 wt[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = m;
-        dr_weights(E, x, wt);
-        one = wt[0];
-    }
-    const u64 w_min = dr_part(min_p, one, true);
+    u64 one, w_min;                                    // the best token's weight, the least that min_p leaves
+    auto set_unit = [&](int q) {
+        E.q = q;
+        E.refer_to(m);
+        u64 v[2];
+        int n[2];
+        dr_weight2(E, m, m, v, n);
+        one = dr_units(E, v[0], n[0]);
+        w_min = dr_part(min_p, one, true);
+    };
     const uint32_t o_max = dr_ord(m), o_inf = dr_ord(-INFINITY);
 
     // sums over the CTA, or over the cluster (the first CTA takes more of the former: each kind has its own turns)
@@ -447,17 +466,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     // for the others)
     auto each_segment = [&](float least, auto f, auto done) {
         for (int s = s0; s < s1; ++s) {
-            if (__any_sync(0xffffffffu, my_max[(s - s0) * 32 + lane] >= least)) {
-                float x[8], nx[8];
-                lp_load(row, V, mis, s * kDrSegs, nx);
-#pragma unroll 1
-                for (int g = 0; g < kDrSegs; ++g) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = nx[i];
-                    if (g + 1 < kDrSegs) lp_load(row, V, mis, s * kDrSegs + g + 1, nx);
-                    f(x, s * kDrSegs + g);
-                }
-            }
+            if (__any_sync(0xffffffffu, my_max[(s - s0) * 32 + lane] >= least)) walk_span(s, f);
             done(s);
         }
     };
@@ -488,13 +497,13 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
         return mine;
     };
     auto kept_weights = [&](const DrCut& cut, uint32_t least, u64 w_least) {
-        return [&, cut, least, w_least](const float (&x)[8], int seg, u64 (&wt)[8]) {
+        const float at_least = dr_value(least), cut_v = dr_value(cut.v);
+        const int cut_id = cut.id;
+        return [&, at_least, cut_v, cut_id, w_least](const float (&x)[8], int seg, u64 (&wt)[8]) {
             dr_weights(E, x, wt);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t o = dr_ord(x[i]);
-                if (o < least || wt[i] < w_least || !dr_kept(cut, o, lp_index<T>(mis, seg, i))) wt[i] = 0;
-            }
+            for (int i = 0; i < 8; ++i)
+                if (!(x[i] >= at_least) || wt[i] < w_least || !(x[i] > cut_v || (x[i] == cut_v && lp_index<T>(mis, seg, i) <= cut_id))) wt[i] = 0;
         };
     };
     // the sum of the weights of the kept logits not below `least`
@@ -647,15 +656,33 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
         return fmaxf(v - fabsf(v) * 1e-6f, -FLT_MAX);
     };
     if (whole) {
+        // the warps' masses in units of 2^-46 (33 spans at most), their sum S 2^46 in 128 bits: what unit the row's have
+        constexpr int kWarpUnit = 46;
         const DrCut all{o_inf, -1};
+        set_unit(kWarpUnit);
         if (far) {
             mine_all = span_masses(-FLT_MAX, kept_weights(all, o_inf + 1, 0));
         } else {
-            for (int i = lane; i < s1 - s0; i += 32) my_sum[i] = my_n[i] == INT_MIN ? 0 : dr_rescale(my_sum[i], E.N - my_n[i]);
-            __syncwarp();
-            for (int i = 0; i < s1 - s0; ++i) mine_all += my_sum[i];
+            for (int i = 0; i < s1 - s0; ++i) mine_all += my_n[i] == INT_MIN ? 0 : dr_rescale(my_sum[i], E.N - my_n[i] + kDrSpanUnit - kWarpUnit);
         }
-        S = sum_all(lane == 0 ? mine_all : 0);
+        everywhere(&sm.mass[gw], mine_all);
+        cluster_sync();
+        unsigned __int128 sum = 0;
+        for (int i = 0; i < C * kDrWarps; ++i) sum += sm.mass[i];
+        const int bits = (u64)(sum >> 64) ? 128 - __clzll((u64)(sum >> 64)) : 64 - __clzll((u64)sum);   // S < 2^(bits - 46)
+        const int q = min(kDrListUnit, 62 + kWarpUnit - bits);
+        set_unit(q);
+        S = q >= kWarpUnit ? (u64)sum << (q - kWarpUnit) : (u64)(sum >> (kWarpUnit - q));
+        if (far) {
+            for (int i = lane; i < s1 - s0; i += 32) my_sum[i] = dr_rescale(my_sum[i], kWarpUnit - q);
+        } else {
+            for (int i = lane; i < s1 - s0; i += 32) my_sum[i] = my_n[i] == INT_MIN ? 0 : dr_rescale(my_sum[i], E.N - my_n[i] + kDrSpanUnit - q);
+        }
+        __syncwarp();
+        mine_all = 0;
+        for (int i = 0; i < s1 - s0; ++i) mine_all += my_sum[i];
+    } else {
+        set_unit(kDrListUnit);
     }
     bool listed = true;
     if (K == 1) {
@@ -843,6 +870,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
         cut = DrCut{sm.cv, sm.ci};
     } else {
         // -------- the row where it lies
+        if (!whole) set_unit(a.q);
         bool masses = whole;                           // my_sum holds the spans' masses of what is kept
         u64 mine = mine_all;
         // The cut at which the kept tokens, by decreasing logit, reach `need`, counted or weighed (`all` in all).
@@ -850,14 +878,14 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
             const DrCut old = cut;
             auto kept = [&](float v, int seg, int i) { return dr_kept(old, dr_ord(v), lp_index<T>(mis, seg, i)); };
             float from = low_bound, to = INFINITY;     // the border lies in [from, to)
-            bool found = false, none = false;
+            bool found = false;
             int n = 0;
             for (int round = 0; round < 4 && !found; ++round) {
                 // 1. a histogram of [from, to) by the logit, from the top down, in units of 2^-30 of the whole mass, and
                 // what lies above.  (Without a bound the steps are steps of the floats' order.)
                 const float top = fminf(to, m), step = (float)(kDrBins - 1) / fmaxf(top - from, 1e-30f);
                 const bool by_order = from == -FLT_MAX;
-                const float per_one = weighed ? 1073741824.f / ((float)all / (float)one) : 1.f, c2 = E.ch * 0.03125f;
+                const float per_one = weighed ? 1073741824.f / ((float)all / (float)one) : 1.f, c2 = E.ch * (1.f / kDrSteps);
                 for (int i = t; i < kDrBins; i += kDrThreads) hist[i] = 0;
                 __syncthreads();
                 u64 over = 0;
@@ -902,10 +930,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                     if (at < goal + err) atomicMax(&sm.bin_hi, t * kEachBin + e + 1);   // past it: the last that may
                 }
                 cluster_sync();                        // (the histograms are read; the list may be written)
-                if (whole_sum + err < goal) {          // min_p's bound lies above the border
-                    none = true;
-                    break;
-                }
+                if (whole_sum + err < goal) break;     // the border lies below the bound (min_p's), as far as this sum goes
                 const int b_lo = min(sm.bin_lo, kDrBins - 1), b_hi = min(sm.bin_hi, kDrBins - 1);
                 __syncthreads();                       // (before they are set again)
                 if (by_order) {
@@ -919,10 +944,6 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                 }
                 // 3. the tokens of these steps, if the list holds them; else the steps are taken apart
                 found = make_list(from, n, [&](float v, int seg, int i) { return v >= from && v < to && kept(v, seg, i); });
-            }
-            if (none) {
-                masses = false;
-                return;
             }
             if (found) {
                 // 4. what lies above them, exactly, and the border among the listed
@@ -982,16 +1003,16 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                     return;
                 }
             }
-            // the whole row by bisection (more equal logits than the list holds)
+            // the whole row by bisection (more equal logits than the list holds), where the border lies above the bound
             masses = false;
             uint32_t lo = max(o_inf + 1, dr_ord(low_bound)), hi = o_max + 1;
             auto of = [&](uint32_t v) { return weighed ? row_mass(v, old) : row_count(v, old); };
+            if (of(lo) < need) return;
             while (hi - lo > 1) {
                 const uint32_t mid = lo + (hi - lo) / 2;
                 if (of(mid) >= need) lo = mid;
                 else hi = mid;
             }
-            if (of(lo) < need) return;
             u64 rest = need - (lo < o_max ? of(lo + 1) : 0);
             if (weighed) {
                 float v[8];
@@ -1035,7 +1056,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     }
 
     // -------- the distribution
-    const float inv = (float)(1ull << a.q) / (float)S_kept;
+    const float inv = (float)(1ull << E.q) / (float)S_kept;
     const float least = dr_value(max(cut.v, o_inf + 1));
 #pragma unroll 1
     for (int s = s0; s < s1; ++s) {
@@ -1054,8 +1075,8 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const float l = v[i + j];
-                    const bool in = l >= E.xmin && dr_kept(cut, dr_ord(l), lp_index<T>(mis, s * kDrSegs + g, i + j)) &&
-                                    dr_round(vv[j], dr_shift(E, l, n[j])) >= w_min;
+                    const bool in = dr_kept(cut, dr_ord(l), lp_index<T>(mis, s * kDrSegs + g, i + j)) &&
+                                    dr_units(E, vv[j], n[j]) >= max(w_min, 1ull);
                     if (in) y[i + j] = (float)vv[j] * __uint_as_float((uint32_t)(127 - 62 - n[j]) << 23) * inv;
                 }
             }
@@ -1077,7 +1098,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     cluster_sync();
 }
 
-static size_t dr_smem(int per) { return (size_t)kDrList * 8 + (size_t)kDrWarps * per * (8 + 4 + 32 * 4); }
+static size_t dr_smem(int per) { return (size_t)kDrList * 8 + (size_t)kDrSteps * 8 + (size_t)kDrWarps * per * (8 + 4 + 32 * 4); }
 
 }  // namespace spec
 
@@ -1127,13 +1148,17 @@ extern "C" int spec_sample_logits(const void* logits, int32_t dtype, int64_t lg_
     a.q = 61;
     while ((1ll << (62 - a.q)) < vocab) --a.q;
     static const struct Table {
-        unsigned long long t[32];
-        Table() { for (int j = 0; j < 32; ++j) t[j] = (unsigned long long)std::ldexp(std::exp2((long double)j / 32), 62); }
+        unsigned long long coarse[32], fine[64];
+        Table() {
+            for (int j = 0; j < 32; ++j) coarse[j] = (unsigned long long)std::ldexp(std::exp2((long double)j / 32), 62);
+            for (int j = 0; j < 64; ++j) fine[j] = (unsigned long long)std::ldexp(std::exp2((long double)j / kDrSteps), 63);
+        }
     } table;
-    std::copy(table.t, table.t + 32, a.pow);
+    std::copy(table.coarse, table.coarse + 32, a.coarse);
+    std::copy(table.fine, table.fine + 64, a.fine);
     const int n_span = (vocab + 7 + kDrSpan - 1) / kDrSpan;
     int C = 1;
-    while (C < kDrMaxCtas && ((long long)vocab > (long long)C * kDrCtaVocab || ((long long)rows * C < 3 * sms && n_span > C * kDrWarps))) C *= 2;
+    while (C < kDrMaxCtas && ((long long)vocab > (long long)C * kDrCtaVocab || ((long long)rows * C < kDrCtasWanted * sms && n_span > C * kDrWarps))) C *= 2;
     a.per = (n_span + C * kDrWarps - 1) / (C * kDrWarps);
     const size_t smem = dr_smem(a.per);
     void (*f)(DrawArgs) = dtype == SPEC_DTYPE_BF16 ? draw_kernel<__nv_bfloat16> : draw_kernel<float>;

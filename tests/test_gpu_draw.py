@@ -16,10 +16,10 @@ def _lib():
 
 def draw64(x, u, T, k, p, mp):
     """(token, log probability, kept ids, their probabilities, ids at the nucleus' border) of one row x (float64 numpy) for
-    float32 settings.  Weights are exact to 2^-38 of themselves and to half a unit, 2^-46 and more of the best token's 1 for
-    up to 2^16 tokens (a unit is V 2^-62, rounded up to a power of two): the mass before a token and p of the whole are each
-    off by 2^-38 of the whole and n half units at most, so a token may count to either side of the border only where the two
-    lie within twice that."""
+    float32 settings.  Weights are exact to 2^-35 of themselves and to a unit, 2^-49 of the best token's 1 or, in rows whose
+    weights add up to much, V 2^-61 rounded up to a power of two: the mass before a token and p of the whole are each off by
+    2^-35 of the whole and n units at most, so a token may count to either side of the border only where the two lie within
+    twice that."""
     T, p, mp, u = (float(np.float32(v)) for v in (T, p, mp, u))
     if T == 0:
         return int(np.argmax(x)), 0.0, np.array([np.argmax(x)]), np.ones(1), []
@@ -32,8 +32,8 @@ def draw64(x, u, T, k, p, mp):
     if p < 1:
         before, all_ = np.concatenate([[0.0], np.cumsum(w)[:-1]]), math.fsum(w)
         keep = before < p * all_
-        half_unit = 2.0 ** (math.ceil(math.log2(max(2, x.size))) - 63)
-        border = order[np.abs(before - p * all_) <= 2 * (2.0 ** -38 * all_ + w.size * half_unit)]
+        unit = max(2.0 ** -49, 2.0 ** (math.ceil(math.log2(max(2, x.size))) - 61))
+        border = order[np.abs(before - p * all_) <= 2 * (2.0 ** -35 * all_ + w.size * unit)]
         keep[0] = True
         order, w = order[keep], w[keep]
     order, w = order[w >= mp], w[w >= mp]
@@ -84,7 +84,7 @@ def check(x, u, T=1.0, k=0, p=1.0, mp=0.0, probs=True, strided=None):
             full = np.zeros(V)
             full[ids] = q
             got[border] = full[border] = 0.0
-            # 2^-38 of a weight, two roundings of it, the sum's and the quotient's; weights below 2^-42 of the best are zero
+            # 2^-35 of a weight, two roundings of it, the sum's and the quotient's; weights below 2^-41 of the best are zero
             assert np.abs(got - full).max() <= 1e-12 + 2.0 ** -21 * full.max()
             assert (np.abs(got - full) <= 2.0 ** -21 * full + 2.0 ** -41).all()
             assert not got[np.setdiff1d(np.arange(V), ids)].any()
