@@ -58,8 +58,11 @@ constexpr int kDrEach = 8;                             // listed tokens a thread
 constexpr int kDrList = kDrEach * kDrThreads;
 constexpr int kDrSpanUnit = 51;                        // 1024 weights in units of 2^-51 fit 64 bits, and so does a listed token's
 constexpr int kDrListUnit = 50;
-constexpr int kDrBins = 2048;                          // steps of a histogram; it lies where the list does
-static_assert(kDrBins * 4 <= kDrList * 8, "histogram");
+constexpr int kDrStage = 384;                          // tokens a warp holds before they go to the list (one CTA's eight: 256 on average)
+constexpr int kDrBins = 2048;                          // steps of a histogram; it lies where the stages do
+static_assert(kDrBins * 4 <= kDrWarps * kDrStage * 8 && kDrList <= kDrWarps * kDrStage, "histogram, masses by place");
+constexpr int kDrRing = 4;                             // segments a warp has room for
+constexpr int kDrCtasSm = 2;
 constexpr int kDrMaxVocab = 1 << 20;
 constexpr int kDrCtaVocab = 1 << 18;                   // a CTA's share at most: its lanes' maxima take 32 KB
 
@@ -123,15 +126,15 @@ SPEC_DEV u64 dr_warp_before(u64 v, u64& total) {
 
 struct DrSmem {
     u64 red[2][kDrWarps];
-    u64 redc[2][kDrMaxCtas];
-    u64 part[kDrMaxCtas * kDrWarps];                   // every warp's sum, in every CTA; a barrier lies between its uses
-    u64 mass[kDrMaxCtas * kDrWarps];                   // every warp's share of the row's mass
-    float wmax[kDrWarps], wlow[kDrWarps];
-    float cmax[kDrMaxCtas], clow[kDrMaxCtas];
-    int cbad[kDrMaxCtas], wbad[kDrWarps];
+    u64 part[2][kDrMaxCtas * kDrWarps];                // every warp's number, in every CTA
+    float offer[kDrMaxCtas * kDrWarps];                // every warp's bound for top-k, and how many lanes' maxima reach it
+    int reach[kDrMaxCtas * kDrWarps];
+    float wmax[kDrWarps], cmax[kDrMaxCtas];
+    int wbad[kDrWarps], cbad[kDrMaxCtas];
     u64 S;                                             // the first CTA's results for the others
-    uint32_t cv; int ci, holds;
-    int bin_lo, bin_hi;
+    float cv;
+    int ci, holds;
+    int bin_lo, bin_hi, bin_at, stop;
 };
 
 // A weight's arithmetic.
@@ -202,11 +205,11 @@ SPEC_DEV void dr_weights(const DrExp& E, const float (&x)[8], u64 (&w)[8]) {
 SPEC_DEV u64 dr_rescale(u64 w, int by) { return by <= 0 ? w << -by : (by > 63 ? 0 : ((w >> (by - 1)) + 1) >> 1); }
 
 // a kept logit: above the cut's value, or equal to it with an id not above the cut's
-struct DrCut { uint32_t v; int id; };
-SPEC_DEV bool dr_kept(const DrCut& c, uint32_t o, int id) { return o > c.v || (o == c.v && id <= c.id); }
+struct DrCut { float v; int id; };
+SPEC_DEV bool dr_kept(const DrCut& c, float x, int id) { return x > c.v || (x == c.v && id <= c.id); }
 
 template <typename T>
-__global__ void __launch_bounds__(kDrThreads, 2)
+__global__ void __launch_bounds__(kDrThreads, kDrCtasSm)
 draw_kernel(const __grid_constant__ DrawArgs a) {
     pdl_wait();
     pdl_trigger();
@@ -214,13 +217,15 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     __shared__ DrSmem sm;
     extern __shared__ __align__(16) u64 dyn[];
     u64* list = dyn;                                   // [kDrList] (value's order, id) by id; the first CTA's
-    uint32_t* hist = reinterpret_cast<uint32_t*>(dyn); // [kDrBins] while there is no list
-    u64* span_sum = dyn + kDrList;                     // [kDrWarps][per] masses, relative to 2^N
+    u64* staged = dyn + kDrList;                       // [kDrWarps][kDrStage] what each warp has for it
+    uint32_t* hist = reinterpret_cast<uint32_t*>(staged);       // [kDrBins] at other times
+    u64* table = staged + kDrWarps * kDrStage;         // [kDrSteps]
+    char* ring = reinterpret_cast<char*>(table + kDrSteps);     // [kDrWarps][kDrRing][NP][32] pieces
+    u64* span_sum = reinterpret_cast<u64*>(ring + kDrWarps * kDrRing * NP * 512);       // [kDrWarps][per] masses, relative to 2^N
     int* span_n = reinterpret_cast<int*>(span_sum + kDrWarps * a.per);         // [kDrWarps][per] ... to 2^span_n at first
     float* lane_max = reinterpret_cast<float*>(span_n + kDrWarps * a.per);     // [kDrWarps][per][32]
-    u64* table = reinterpret_cast<u64*>(lane_max + kDrWarps * a.per * 32);     // [kDrSteps]
     cg::cluster_group cl = cg::this_cluster();
-    const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+    const int C = (int)cl.num_blocks(), rank = (int)cl.block_rank(), NW = C * kDrWarps;
     const long long row_i = blockIdx.x / C;
     const int t = threadIdx.x, lane = t & 31, w = t >> 5, gw = rank * kDrWarps + w;
     const T* row = static_cast<const T*>(a.x) + row_i * a.stride;
@@ -259,85 +264,131 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     for (int i = t; i < kDrSteps; i += kDrThreads) table[i] = __umul64hi(a.coarse[i >> 6], a.fine[i & 63]) << 1;
     __syncthreads();
 
-    // a span's logits, 32 a lane
-    auto load_span = [&](int s, float (&x)[kDrSegs][8]) {
-        if (s * kDrSpan >= mis && (s + 1) * kDrSpan - mis <= V) {
-            uint4 p[kDrSegs][NP];
-            const T* at = row + (s * kDrSpan - mis + lane * VE);
-#pragma unroll
-            for (int g = 0; g < kDrSegs; ++g)
-#pragma unroll
-                for (int i = 0; i < NP; ++i) p[g][i] = __ldg(reinterpret_cast<const uint4*>(at + g * kLpSeg + i * 32 * VE));
-#pragma unroll
-            for (int g = 0; g < kDrSegs; ++g)
-#pragma unroll
-                for (int i = 0; i < NP; ++i) lp_unpack<T>(p[g][i], &x[g][i * VE]);
-        } else {
-#pragma unroll
-            for (int g = 0; g < kDrSegs; ++g) lp_load(row, V, mis, s * kDrSegs + g, x[g]);
-        }
-    };
-    // a span's logits, 8 a lane at a time: f(logits, segment), the next ones on their way
-    auto walk_span = [&](int s, auto f) {
-        float x[8];
-        if (s * kDrSpan >= mis && (s + 1) * kDrSpan - mis <= V) {
-            uint4 nx[NP];
-            const T* at = row + (s * kDrSpan - mis + lane * VE);
-#pragma unroll
-            for (int i = 0; i < NP; ++i) nx[i] = __ldg(reinterpret_cast<const uint4*>(at + i * 32 * VE));
-#pragma unroll 1
-            for (int g = 0; g < kDrSegs; ++g) {
-#pragma unroll
-                for (int i = 0; i < NP; ++i) lp_unpack<T>(nx[i], &x[i * VE]);
-                at += kLpSeg;
-                if (g + 1 < kDrSegs)
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) nx[i] = __ldg(reinterpret_cast<const uint4*>(at + i * 32 * VE));
-                f(x, s * kDrSegs + g);
-            }
-        } else {
-#pragma unroll 1
-            for (int g = 0; g < kDrSegs; ++g) {
-                lp_load(row, V, mis, s * kDrSegs + g, x);
-                f(x, s * kDrSegs + g);
-            }
-        }
-    };
     // this warp's part of an array by span (a span's owner is warp s / per of the cluster)
     u64* my_sum = span_sum + w * a.per;
     int* my_n = span_n + w * a.per;
     float* my_max = lane_max + w * a.per * 32;
 
+    // the piece at row index i0, which the row does not fill: masked where it does not
+    auto edge_piece = [&](int i0) {
+        uint32_t u4[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (sizeof(T) == 4) {
+                u4[j] = i0 + j >= 0 && i0 + j < V ? __float_as_uint(to_f32<T>(row[i0 + j])) : 0xFF800000u;
+            } else {
+                u4[j] = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int d = i0 + 2 * j + h;
+                    u4[j] |= (d >= 0 && d < V ? __float_as_uint(to_f32<T>(row[d])) >> 16 : 0xFF80u) << (16 * h);
+                }
+            }
+        }
+        return make_uint4(u4[0], u4[1], u4[2], u4[3]);
+    };
+    // a segment's pieces of this lane, as they lie in memory
+    auto load_raw = [&](int seg, uint4 (&p)[NP]) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            const int i0 = seg * kLpSeg + (i * 32 + lane) * VE - mis;
+            p[i] = i0 >= 0 && i0 + VE <= V ? __ldg(reinterpret_cast<const uint4*>(row + i0)) : edge_piece(i0);
+        }
+    };
+    auto unpack = [&](const uint4 (&p)[NP], float (&x)[8]) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) lp_unpack<T>(p[i], &x[i * VE]);
+    };
+    // every span of this warp from s on that `wanted` names
+    auto next_span = [&](int s, auto wanted) {
+        while (s < s1 && !wanted(s)) ++s;
+        return s;
+    };
+    // The segments of the spans that `wanted` names, in order (of each span all four, or one), f(logits, segment); then
+    // done(span).  Three segments are copied ahead into the warp's ring, a lane's pieces into slots of its own, so
+    // that a lane waits for its own copies only.
+    const uint32_t slots = smem_u32(ring) + (w * kDrRing * NP * 32 + lane) * 16;
+    auto stream = [&](auto wanted, bool one_of_four, auto f, auto done) {
+        float x[8];
+        int ls = next_span(s0, wanted), lg = one_of_four ? ls & 3 : 0, to = 0;      // the next segment to copy
+        auto copy_next = [&]() {
+            if (ls < s1) {
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    const int i0 = (ls * kDrSegs + lg) * kLpSeg + (i * 32 + lane) * VE - mis;
+                    const uint32_t dst = slots + (to * NP + i) * 512;
+                    if (i0 >= 0 && i0 + VE <= V) {
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(row + i0) : "memory");
+                    } else {
+                        const uint4 v = edge_piece(i0);
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" :: "r"(dst), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+                    }
+                }
+                if (one_of_four || ++lg == kDrSegs) {
+                    ls = next_span(ls + 1, wanted);
+                    lg = one_of_four ? ls & 3 : 0;
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            to = (to + 1) % kDrRing;
+        };
+        int s = ls, at = 0;
+#pragma unroll
+        for (int i = 0; i < kDrRing - 1; ++i) copy_next();
+        while (s < s1) {
+#pragma unroll 1
+            for (int g = one_of_four ? s & 3 : 0; g < kDrSegs; ++g) {
+                asm volatile("cp.async.wait_group %0;" :: "n"(kDrRing - 2) : "memory");
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    uint4 v;
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(slots + (at * NP + i) * 512) : "memory");
+                    lp_unpack<T>(v, &x[i * VE]);
+                }
+                at = (at + 1) % kDrRing;
+                copy_next();
+                f(x, s * kDrSegs + g);
+                if (one_of_four) break;
+            }
+            done(s);
+            s = next_span(s + 1, wanted);
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+    };
+    auto every = [&](int) { return true; };
+    // spans that hold a logit not below `least`
+    auto reaching = [&](float least) {
+        return [&, least](int s) { return __any_sync(0xffffffffu, my_max[(s - s0) * 32 + lane] >= least); };
+    };
+
     // -------- the maximum, every lane's maxima, the spans' masses, and whether the row has a distribution
-    float mx = -INFINITY;
+    float mx = -INFINITY, lm = -INFINITY;
     bool bad = false;
     if (whole && settings) {
-        for (int s = s0; s < s1; ++s) {
-            float lm = -INFINITY;
-            u64 sum = 0;
-            int N = INT_MIN;
-            walk_span(s, [&](const float (&x)[8], int) {
-                float gm = x[0];
+        u64 sum = 0;
+        int N = INT_MIN;
+        stream(every, false, [&](const float (&x)[8], int) {
+            float gm = x[0];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    bad |= !(x[i] <= FLT_MAX);         // NaN or +inf
-                    gm = fmaxf(gm, x[i]);
-                }
-                lm = fmaxf(lm, gm);
-                const float top = warp_redux_max(gm);
-                // (logits this large: none of the row's mass, or its maximum is one of them and the pass does not count)
-                if (!(fabsf(top * E.ch) < kDrDigits)) return;
-                const int n = (int)ceilf(top * E.ch * (1.f / kDrSteps));
-                if (n > N) {
-                    if (N != INT_MIN) sum = dr_rescale(sum, n - N);
-                    N = n;
-                    E.refer_to_n(N);
-                }
-                u64 wt[8];
-                dr_weights(E, x, wt);
+            for (int i = 0; i < 8; ++i) {
+                bad |= !(x[i] <= FLT_MAX);             // NaN or +inf
+                gm = fmaxf(gm, x[i]);
+            }
+            lm = fmaxf(lm, gm);
+            const float top = warp_redux_max(gm);
+            // (logits this large: none of the row's mass, or its maximum is one of them and the pass does not count)
+            if (!(fabsf(top * E.ch) < kDrDigits)) return;
+            const int n = (int)ceilf(top * E.ch * (1.f / kDrSteps));
+            if (n > N) {
+                if (N != INT_MIN) sum = dr_rescale(sum, n - N);
+                N = n;
+                E.refer_to_n(N);
+            }
+            u64 wt[8];
+            dr_weights(E, x, wt);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum += wt[i];
-            });
+            for (int i = 0; i < 8; ++i) sum += wt[i];
+        }, [&](int s) {
             my_max[(s - s0) * 32 + lane] = lm;
             mx = fmaxf(mx, lm);
             sum = dr_warp_sum(sum);
@@ -345,37 +396,36 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                 my_sum[s - s0] = sum;
                 my_n[s - s0] = N;
             }
-        }
+            lm = -INFINITY;
+            sum = 0;
+            N = INT_MIN;
+        });
     } else {
-        for (int s = s0; s < s1; ++s) {
-            float x[kDrSegs][8], g4[kDrSegs];
-            load_span(s, x);
+        stream(every, false, [&](const float (&x)[8], int) {
 #pragma unroll
-            for (int g = 0; g < kDrSegs; ++g) {
-                g4[g] = x[g][0];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    bad |= !(x[g][i] <= FLT_MAX);
-                    g4[g] = fmaxf(g4[g], x[g][i]);
-                }
+            for (int i = 0; i < 8; ++i) {
+                bad |= !(x[i] <= FLT_MAX);
+                lm = fmaxf(lm, x[i]);
             }
-            const float g = fmaxf(fmaxf(g4[0], g4[1]), fmaxf(g4[2], g4[3]));
-            my_max[(s - s0) * 32 + lane] = g;
-            mx = fmaxf(mx, g);
-        }
+        }, [&](int s) {
+            my_max[(s - s0) * 32 + lane] = lm;
+            mx = fmaxf(mx, lm);
+            lm = -INFINITY;
+        });
     }
     mx = warp_redux_max(mx);
     bad = __any_sync(0xffffffffu, bad);
     __syncwarp();
-    // This warp's share of the bound for top-k: of the warps with a full run of whole spans (none: no bound) each gives the value of
-    // (about) its r-th largest lane maximum; the least of these has r tokens a warp that are not below it.
+    // This warp's share of the bound for top-k: of the warps with a full run of whole spans (none: no bound) each
+    // offers the value of (about) its r-th largest lane maximum.  The least of these has r tokens a warp that are not
+    // below it; below, a larger one is taken that has k all the same.
     float low = INFINITY;
-    const int full = (V + mis) / kDrSpan / a.per, r_low = full > 0 ? (K + full - 1) / full : 0;
-    if (K > 0 && gw < full) {
-        low = mx;
-        if (r_low > 32 * a.per) {
-            low = -INFINITY;
-        } else if (r_low > 1) {
+    const int full = (V + mis) / kDrSpan / a.per, r_low = K > 1 && full > 0 ? (K + full - 1) / full : 0;
+    if (r_low > 0 && gw < full) {
+        low = -INFINITY;
+        if (r_low == 1) {
+            low = mx;
+        } else if (r_low <= 32 * a.per) {
             uint32_t lo = 0, hi = dr_ord(mx);          // at least r not below lo; hi: fewer (or not looked at)
             while (hi - lo > 1) {
                 const uint32_t mid = lo + (hi - lo) / 2;
@@ -385,7 +435,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                 n = __reduce_add_sync(0xffffffffu, n);
                 if (n >= r_low) {
                     lo = mid;
-                    if (n <= r_low + r_low / 8) break;
+                    if (n <= r_low + r_low / 16) break;
                 } else {
                     hi = mid;
                 }
@@ -394,26 +444,19 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
             if (!(low >= -FLT_MAX)) low = -INFINITY;
         }
     }
-    if (lane == 0) { sm.wmax[w] = mx; sm.wlow[w] = low; sm.wbad[w] = bad; }
+    if (lane == 0) { sm.wmax[w] = mx; sm.wbad[w] = bad; }
     __syncthreads();
     if (C > 1) cluster_wait();
+    everywhere(&sm.offer[gw], low);
     if (w == 0) {
-        float m = lane < kDrWarps ? sm.wmax[lane] : -INFINITY, l = lane < kDrWarps ? sm.wlow[lane] : INFINITY;
+        const float m = warp_redux_max(lane < kDrWarps ? sm.wmax[lane] : -INFINITY);
         const bool b = __any_sync(0xffffffffu, lane < kDrWarps && sm.wbad[lane]);
-        m = warp_redux_max(m);
-        l = -warp_redux_max(-l);
         everywhere(&sm.cmax[rank], m);
-        everywhere(&sm.clow[rank], l);
         everywhere(&sm.cbad[rank], (int)b);
     }
     cluster_sync();
-    float m = -INFINITY, k_low = INFINITY;
-    bad = false;
-    for (int i = 0; i < C; ++i) {
-        m = fmaxf(m, sm.cmax[i]);
-        k_low = fminf(k_low, sm.clow[i]);
-        bad |= sm.cbad[i] != 0;
-    }
+    const float m = warp_redux_max(lane < C ? sm.cmax[lane] : -INFINITY);
+    bad = __any_sync(0xffffffffu, lane < C && sm.cbad[lane]);
     float* probs = a.probs ? a.probs + row_i * a.p_stride : nullptr;
     if (bad || m == -INFINITY || !settings) {          // no distribution, or settings out of range
         const float nan = __int_as_float(0x7fc00000);
@@ -437,10 +480,26 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
         one = dr_units(E, v[0], n[0]);
         w_min = dr_part(min_p, one, true);
     };
-    const uint32_t o_max = dr_ord(m), o_inf = dr_ord(-INFINITY);
 
-    // sums over the CTA, or over the cluster (the first CTA takes more of the former: each kind has its own turns)
-    int par = 0, cpar = 0;
+    // Every warp's number in every CTA (two buffers in turn: whoever writes one has passed the barrier of the other,
+    // which comes after everybody's reading of this one): their sum, and the sum of the warps before this one.
+    int turn = 0;
+    auto exchange = [&](u64 mine, u64& before) {
+        everywhere(&sm.part[turn][gw], mine);
+        cluster_sync();
+        const u64 x = 2 * lane < NW ? sm.part[turn][2 * lane] : 0, y = 2 * lane < NW ? sm.part[turn][2 * lane + 1] : 0;
+        turn ^= 1;
+        u64 all;
+        const u64 at = dr_warp_before(x + y, all) + (gw & 1 ? x : 0);
+        before = __shfl_sync(0xffffffffu, at, gw >> 1);
+        return all;
+    };
+    auto sum_all = [&](u64 v) {                        // of what the warps hold (in every lane)
+        u64 before;
+        return exchange(v, before);
+    };
+    // sums over the CTA
+    int par = 0;
     auto sum_cta = [&](u64 v) {
         v = dr_warp_sum(v);
         if (lane == 0) sm.red[par][w] = v;
@@ -451,38 +510,27 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
         par ^= 1;
         return s;
     };
-    auto sum_all = [&](u64 v) {
-        u64 s = sum_cta(v);
-        if (C > 1) {
-            if (w == 0) everywhere(&sm.redc[cpar][rank], s);
-            cl.sync();
-            s = 0;
-            for (int i = 0; i < C; ++i) s += sm.redc[cpar][i];
-            cpar ^= 1;
+    // what the threads before this one hold, and all
+    auto before_cta = [&](u64 v, u64& all) {
+        u64 in_warp, at = dr_warp_before(v, in_warp);
+        if (lane == 0) sm.red[par][w] = in_warp;
+        __syncthreads();
+        all = 0;
+#pragma unroll
+        for (int i = 0; i < kDrWarps; ++i) {
+            if (i == w) at += all;
+            all += sm.red[par][i];
         }
-        return s;
+        par ^= 1;
+        return at;
     };
-    // every segment of this warp's spans that hold a logit not below `least`: f(logits, segment), then done(span) (also
-    // for the others)
-    auto each_segment = [&](float least, auto f, auto done) {
-        for (int s = s0; s < s1; ++s) {
-            if (__any_sync(0xffffffffu, my_max[(s - s0) * 32 + lane] >= least)) walk_span(s, f);
-            done(s);
-        }
-    };
-    // the same for whole spans: f(logits, span)
-    auto each_span = [&](float least, auto f) {
-        for (int s = s0; s < s1; ++s) {
-            if (!__any_sync(0xffffffffu, my_max[(s - s0) * 32 + lane] >= least)) continue;
-            float x[kDrSegs][8];
-            load_span(s, x);
-            f(x, s);
-        }
-    };
-    // weights of a segment by f(logits, segment, weights): every span's sum in my_sum, the warp's returned
+    // Weights of the segments that reach `least` by f(logits, segment, weights): every span's sum in my_sum, the warp's
+    // returned.
     auto span_masses = [&](float least, auto f) {
         u64 sum = 0, mine = 0;
-        each_segment(least, [&](const float (&x)[8], int seg) {
+        for (int i = lane; i < s1 - s0; i += 32) my_sum[i] = 0;
+        __syncwarp();
+        stream(reaching(least), false, [&](const float (&x)[8], int seg) {
             u64 wt[8];
             f(x, seg, wt);
 #pragma unroll
@@ -496,77 +544,53 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
         __syncwarp();
         return mine;
     };
-    auto kept_weights = [&](const DrCut& cut, uint32_t least, u64 w_least) {
-        const float at_least = dr_value(least), cut_v = dr_value(cut.v);
-        const int cut_id = cut.id;
-        return [&, at_least, cut_v, cut_id, w_least](const float (&x)[8], int seg, u64 (&wt)[8]) {
+    auto kept_weights = [&](const DrCut& cut, float least, u64 w_least) {
+        return [&, cut, least, w_least](const float (&x)[8], int seg, u64 (&wt)[8]) {
             dr_weights(E, x, wt);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (!(x[i] >= at_least) || wt[i] < w_least || !(x[i] > cut_v || (x[i] == cut_v && lp_index<T>(mis, seg, i) <= cut_id))) wt[i] = 0;
+                if (!(x[i] >= least) || wt[i] < w_least || !dr_kept(cut, x[i], lp_index<T>(mis, seg, i))) wt[i] = 0;
         };
-    };
-    // the sum of the weights of the kept logits not below `least`
-    auto row_mass = [&](uint32_t least, const DrCut& cut) {
-        const u64 mine = span_masses(dr_value(least), kept_weights(cut, least, 0));
-        return sum_all(lane == 0 ? mine : 0);
-    };
-    auto row_count = [&](uint32_t least, const DrCut&) {
-        u64 n = 0;
-        each_span(dr_value(least), [&](const float (&x)[kDrSegs][8], int) {
-#pragma unroll
-            for (int g = 0; g < kDrSegs; ++g)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) n += dr_ord(x[g][i]) >= least ? 1 : 0;
-        });
-        return sum_all(n);
     };
     // With every span's sum in my_sum, `mine` a warp's: the token by id, weighed by f, at which the sum passes the
     // target; found(id, logit, total) is called by one thread of the cluster.
     auto locate = [&](u64 mine, auto f, auto target_of, auto found) {
-        everywhere(&sm.part[gw], mine);
-        cluster_sync();
-        u64 total = 0, before = 0;
-        for (int i = 0; i < C * kDrWarps; ++i) {
-            if (i == gw) before = total;
-            total += sm.part[i];
-        }
-        const u64 target = target_of(total);
+        u64 before;
+        const u64 total = exchange(mine, before), target = target_of(total);
         if (before <= target && target < before + mine) {
             u64 left = target - before;
             int s = s0;
             while (s + 1 < s1 && left >= my_sum[s - s0]) left -= my_sum[s++ - s0];
-            // (the first pass' masses are rounded on their way to a common unit: a few of 2^-45)
-            bool done = false, ones = false;
-            {
-                u64 exact = 0;
+            // (the first pass' masses are rounded on their way to a common unit: the span's own, once more)
+            u64 exact = 0;
+            uint4 p[NP];
+            float x[8];
+            u64 wt[8];
 #pragma unroll 1
-                for (int g = 0; g < kDrSegs; ++g) {
-                    float x[8];
-                    u64 wt[8];
-                    lp_load(row, V, mis, s * kDrSegs + g, x);
-                    f(x, s * kDrSegs + g, wt);
+            for (int g = 0; g < kDrSegs; ++g) {
+                load_raw(s * kDrSegs + g, p);
+                unpack(p, x);
+                f(x, s * kDrSegs + g, wt);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) exact += wt[i];
-                }
-                exact = dr_warp_sum(exact);
-                ones = exact == 0;
-                left = ones ? 0 : min(left, exact - 1);
+                for (int i = 0; i < 8; ++i) exact += wt[i];
             }
+            exact = dr_warp_sum(exact);
+            const bool ones = exact == 0;
+            left = ones ? 0 : min(left, exact - 1);
+            bool done = false;
 #pragma unroll 1
             for (int g = 0; g < kDrSegs && !done; ++g) {
-                float x[8];
-                u64 wt[8];
-                lp_load(row, V, mis, s * kDrSegs + g, x);
+                load_raw(s * kDrSegs + g, p);
+                unpack(p, x);
                 f(x, s * kDrSegs + g, wt);
                 if (ones)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) wt[i] = x[i] >= -FLT_MAX ? 1 : 0;
 #pragma unroll
-                for (int p = 0; p < NP; ++p) {
+                for (int k = 0; k < NP; ++k) {
                     u64 sum = 0, all;
 #pragma unroll
-                    for (int i = 0; i < VE; ++i) sum += wt[p * VE + i];
+                    for (int i = 0; i < VE; ++i) sum += wt[k * VE + i];
                     const u64 pre = dr_warp_before(sum, all);
                     if (!done && left < all) {
                         if (pre <= left && left < pre + sum) {
@@ -574,10 +598,10 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                             bool hit = false;
 #pragma unroll
                             for (int i = 0; i < VE; ++i) {
-                                at += wt[p * VE + i];
+                                at += wt[k * VE + i];
                                 if (!hit && left < at) {
                                     hit = true;
-                                    found(lp_index<T>(mis, s * kDrSegs + g, p * VE + i), x[p * VE + i], total);
+                                    found(lp_index<T>(mis, s * kDrSegs + g, k * VE + i), x[k * VE + i], total);
                                 }
                             }
                         }
@@ -597,58 +621,97 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
             a.lp[row_i] = (x - m) / T_ - ls;
         }
     };
-    // Tokens for which in(logit, segment, element) holds, by id, into the first CTA's list; their number, and
-    // whether the list holds them.
-    auto make_list = [&](float least, int& n_list, auto in) {
+    // The kept tokens in [from, to), by id, into the first CTA's list if it holds them (their number, or more than
+    // the list's length); weighed: and the mass of the kept tokens from `to` on, the spans' in my_sum.
+    u64 over_mass = 0;                                 // this warp's
+    auto make_list = [&](float from, float to, const DrCut& old, bool cut_some, bool weighed) {
+        u64* mine = staged + w * kDrStage;
         int n = 0;
-        each_span(least, [&](const float (&x)[kDrSegs][8], int s) {
+        u64 sum = 0;
+        over_mass = 0;
+        if (t == 0) sm.stop = 0;
+        if (weighed)
+            for (int i = lane; i < s1 - s0; i += 32) my_sum[i] = 0;
+        __syncthreads();
+        const auto reach = reaching(from);
+        stream([&](int s) { return (weighed || !__any_sync(0xffffffffu, *(volatile int*)&sm.stop)) && reach(s); }, false, [&](const float (&x)[8], int seg) {
+            uint32_t in = 0, above = 0;
 #pragma unroll
-            for (int g = 0; g < kDrSegs; ++g)
+            for (int i = 0; i < 8; ++i) in |= x[i] >= from ? 1u << i : 0u;
+            if (to < INFINITY) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) n += in(x[g][i], s * kDrSegs + g, i) ? 1 : 0;
+                for (int i = 0; i < 8; ++i) above |= x[i] >= to ? 1u << i : 0u;
+                in &= ~above;
+            }
+            if (cut_some)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (!dr_kept(old, x[i], lp_index<T>(mis, seg, i))) in &= ~(1u << i);
+            if (weighed && __any_sync(0xffffffffu, above != 0)) {
+                u64 wt[8];
+                dr_weights(E, x, wt);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if ((above >> i) & 1u && (!cut_some || dr_kept(old, x[i], lp_index<T>(mis, seg, i)))) sum += wt[i];
+            }
+            if (!__any_sync(0xffffffffu, in != 0)) return;
+            // places by piece, lane, element: two pieces' counts in one scan
+            const uint32_t c = NP == 1 ? __popc(in) : __popc(in & 0xFu) | (uint32_t)__popc(in >> 4) << 16;
+            uint32_t upto = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+            int at = n + (int)((upto - c) & 0xFFFFu), at2 = n + (int)(all & 0xFFFFu) + (int)((upto - c) >> 16);
+            for (; in; in &= in - 1u) {                // (most lanes have none)
+                const int i = __ffs(in) - 1, k = i < VE ? at++ : at2++;
+                float v = x[0];
+#pragma unroll
+                for (int j = 1; j < 8; ++j) v = i == j ? x[j] : v;
+                if (k < kDrStage) mine[k] = (u64)dr_ord(v) << 32 | (uint32_t)lp_index<T>(mis, seg, i);
+            }
+            __syncwarp();
+            n += (int)(all & 0xFFFFu) + (int)(all >> 16);
+            if (n > kDrList && lane == 0) *(volatile int*)&sm.stop = 1;        // (it will not hold them)
+        }, [&](int s) {
+            if (!weighed) return;
+            sum = dr_warp_sum(sum);
+            if (lane == 0) my_sum[s - s0] = sum;
+            over_mass += sum;
+            sum = 0;
         });
-        n = __reduce_add_sync(0xffffffffu, n);
-        everywhere(&sm.part[gw], (u64)n);
-        cluster_sync();
-        int before = 0;
-        n_list = 0;
-        for (int i = 0; i < C * kDrWarps; ++i) {
-            if (i == gw) before = n_list;
-            n_list += (int)sm.part[i];
-        }
-        if (n_list <= kDrList && n > 0) {
-            u64* first = cl.map_shared_rank(list, 0);
-            each_span(least, [&](const float (&x)[kDrSegs][8], int s) {
-#pragma unroll
-                for (int g = 0; g < kDrSegs; ++g)
-#pragma unroll
-                    for (int p = 0; p < NP; ++p) {
-                        uint32_t mine = 0;
-#pragma unroll
-                        for (int i = 0; i < VE; ++i) mine |= in(x[g][p * VE + i], s * kDrSegs + g, p * VE + i) ? 1u << i : 0u;
-                        if (!__any_sync(0xffffffffu, mine != 0)) continue;
-                        const int c = __popc(mine);
-                        int upto = c;
-#pragma unroll
-                        for (int o = 1; o < 32; o <<= 1) {
-                            const int v = __shfl_up_sync(0xffffffffu, upto, o);
-                            if (lane >= o) upto += v;
-                        }
-                        int at = before + upto - c;
-#pragma unroll
-                        for (int i = 0; i < VE; ++i)
-                            if ((mine >> i) & 1u)
-                                first[at++] = (u64)dr_ord(x[g][p * VE + i]) << 32 | (uint32_t)lp_index<T>(mis, s * kDrSegs + g, p * VE + i);
-                        before += __shfl_sync(0xffffffffu, upto, 31);
+        __syncwarp();
+        // a warp with more than its stage holds takes another look (order unlike chance's), if the list takes them
+        u64 before;
+        const u64 total = exchange((u64)n, before);
+        if (total <= kDrList && n > 0) {
+            u64* first = cl.map_shared_rank(list, 0) + before;
+            if (n <= kDrStage) {
+                for (int i = lane; i < n; i += 32) first[i] = mine[i];
+            } else {
+                int at = 0;
+                for (int s = s0; s < s1; ++s) {
+                    if (!reach(s)) continue;
+                    for (int i0 = s * kDrSpan - mis; i0 < (s + 1) * kDrSpan - mis; i0 += 32) {
+                        const int id = i0 + lane;
+                        const float x = id >= 0 && id < V ? to_f32<T>(row[id]) : -INFINITY;
+                        const bool in = x >= from && x < to && dr_kept(old, x, id);
+                        const uint32_t b = __ballot_sync(0xffffffffu, in);
+                        if (in) first[at + __popc(b & ((1u << lane) - 1u))] = (u64)dr_ord(x) << 32 | (uint32_t)id;
+                        at += __popc(b);
                     }
-            });
+                }
+            }
         }
         cluster_sync();
-        return n_list <= kDrList;
+        return total;
     };
 
     // -------- a bound below which nothing is kept
     const float slack = 1e-3f;
+    const DrCut nothing{-INFINITY, -1};                // (every finite logit is kept)
     float low_bound = -FLT_MAX;
     u64 S = 0, p_target = 0, mine_all = 0;             // the row's mass, this warp's part of it
     auto below = [&](float z) {                        // safely below m + T z
@@ -656,31 +719,23 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
         return fmaxf(v - fabsf(v) * 1e-6f, -FLT_MAX);
     };
     if (whole) {
-        // the warps' masses in units of 2^-46 (33 spans at most), their sum S 2^46 in 128 bits: what unit the row's have
-        constexpr int kWarpUnit = 46;
-        const DrCut all{o_inf, -1};
-        set_unit(kWarpUnit);
+        // the row's mass in units of 2^-43 (2^20 tokens at most), and with it the unit for the rest
+        constexpr int kRowUnit = 43;
+        set_unit(kRowUnit);
         if (far) {
-            mine_all = span_masses(-FLT_MAX, kept_weights(all, o_inf + 1, 0));
+            mine_all = span_masses(-FLT_MAX, kept_weights(nothing, -FLT_MAX, 0));
         } else {
-            for (int i = 0; i < s1 - s0; ++i) mine_all += my_n[i] == INT_MIN ? 0 : dr_rescale(my_sum[i], E.N - my_n[i] + kDrSpanUnit - kWarpUnit);
+            for (int i = 0; i < s1 - s0; ++i) mine_all += my_n[i] == INT_MIN ? 0 : dr_rescale(my_sum[i], E.N - my_n[i] + kDrSpanUnit - kRowUnit);
         }
-        everywhere(&sm.mass[gw], mine_all);
-        cluster_sync();
-        unsigned __int128 sum = 0;
-        for (int i = 0; i < C * kDrWarps; ++i) sum += sm.mass[i];
-        const int bits = (u64)(sum >> 64) ? 128 - __clzll((u64)(sum >> 64)) : 64 - __clzll((u64)sum);   // S < 2^(bits - 46)
-        const int q = min(kDrListUnit, 62 + kWarpUnit - bits);
+        S = sum_all(mine_all);
+        const int q = min(kDrListUnit, kRowUnit + __clzll(S) - 2);      // S < 2^62 of them
         set_unit(q);
-        S = q >= kWarpUnit ? (u64)sum << (q - kWarpUnit) : (u64)(sum >> (kWarpUnit - q));
-        if (far) {
-            for (int i = lane; i < s1 - s0; i += 32) my_sum[i] = dr_rescale(my_sum[i], kWarpUnit - q);
-        } else {
-            for (int i = lane; i < s1 - s0; i += 32) my_sum[i] = my_n[i] == INT_MIN ? 0 : dr_rescale(my_sum[i], E.N - my_n[i] + kDrSpanUnit - q);
-        }
+        for (int i = lane; i < s1 - s0; i += 32)
+            my_sum[i] = far ? dr_rescale(my_sum[i], kRowUnit - q) : (my_n[i] == INT_MIN ? 0 : dr_rescale(my_sum[i], E.N - my_n[i] + kDrSpanUnit - q));
         __syncwarp();
         mine_all = 0;
         for (int i = 0; i < s1 - s0; ++i) mine_all += my_sum[i];
+        S = dr_rescale(S, kRowUnit - q);
     } else {
         set_unit(kDrListUnit);
     }
@@ -688,7 +743,30 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     if (K == 1) {
         low_bound = m;
     } else if (K > 0) {
-        low_bound = full > 0 ? fmaxf(k_low, -FLT_MAX) : -FLT_MAX;
+        if (full > 0) {
+            // Of the warps' offers the largest that K lanes' maxima reach: every warp counts its own for each of the
+            // offers (two a lane), and the counts add up in every CTA.
+            const float a0 = lane < NW ? sm.offer[lane] : INFINITY, a1 = lane + 32 < NW ? sm.offer[lane + 32] : INFINITY;
+            int n0 = 0, n1 = 0;
+            for (int s = s0; s < s1; ++s)
+                for (int i = 0; i < 32; ++i) {
+                    const float v = my_max[(s - s0) * 32 + i];
+                    n0 += v >= a0;
+                    n1 += v >= a1;
+                }
+            if (t < kDrMaxCtas * kDrWarps) sm.reach[t] = 0;
+            cluster_sync();
+            for (int i = 0; i < C; ++i) {
+                int* r = cl.map_shared_rank(sm.reach, i);
+                if (n0) atomicAdd(r + lane, n0);
+                if (n1) atomicAdd(r + lane + 32, n1);
+            }
+            cluster_sync();
+            float best = -FLT_MAX;
+            if (lane < NW && a0 < INFINITY && sm.reach[lane] >= K) best = fmaxf(best, a0);
+            if (lane + 32 < NW && a1 < INFINITY && sm.reach[lane + 32] >= K) best = fmaxf(best, a1);
+            low_bound = warp_redux_max(best);
+        }
     } else if (nucleus) {
         p_target = max(dr_part(top_p, S, true), 1ull);
         low_bound = below(logf(fmaxf((1.f - top_p) * ((float)S / (float)one) / (float)V, 1e-30f)));
@@ -697,18 +775,21 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     }
     // (min_p leaves out of top-k's and the nucleus' tokens, whose number and mass count them)
     if (min_p > 0.f && K == 0) low_bound = fmaxf(low_bound, below(logf(min_p)));
-    int n_list = 0;
-    if (listed) listed = make_list(low_bound, n_list, [&](float x, int, int) { return x >= low_bound; });
+    u64 n_list = 0;
+    if (listed) {
+        n_list = make_list(low_bound, INFINITY, nothing, false, false);
+        listed = n_list <= kDrList;
+    }
 
-    DrCut cut{o_inf, -1};
+    DrCut cut = nothing;
     u64 S_kept = 0;
     // -------- the first CTA's threads with `each` neighbours of the list
     uint32_t o[kDrEach];
     int id[kDrEach];
     u64 wt[kDrEach];
-    float x[kDrEach];
     auto take_list = [&](int n) {
         const int each = (n + kDrThreads - 1) / kDrThreads;
+        float x[kDrEach];
 #pragma unroll
         for (int e = 0; e < kDrEach; ++e) {
             const int i = t * each + e;
@@ -723,55 +804,130 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
         for (int e = 0; e < kDrEach; ++e)
             if (o[e] == 0) wt[e] = 0;
     };
-    // the first `n` by id of the tokens equal to v, and those above it, stay
-    auto cut_at = [&](uint32_t v, u64 n) {
-        u64 mine = 0;
+    // Keeps the tokens of the list that come first, by decreasing logit (equal ones by id), until they number `first`
+    // and, of these, until they weigh need(weight of all of these) (no more than what stays where they do not).
+    // A token's place: 2048 steps of the logit from `top` down to `from`, counted, and inside its step by comparing.
+    auto cut_list = [&](int n, float from, float top, u64 first, bool weighed, auto need) {
+        u64* sorted = list;
+        u64* by_place = staged;
+        const float step = (float)(kDrBins - 1) / fmaxf(top - from, 1e-30f);
+        auto bin_of = [&](uint32_t ord) { return max(0, min(kDrBins - 1, (int)((top - dr_value(ord)) * step))); };
+        for (int i = t; i < kDrBins; i += kDrThreads) hist[i] = 0;
+        __syncthreads();                               // (and the list has been taken)
+        int in_bin[kDrEach];
 #pragma unroll
-        for (int e = 0; e < kDrEach; ++e) mine += o[e] == v ? 1 : 0;
-        u64 all, at = dr_warp_before(mine, all);
-        if (lane == 0) sm.red[par][w] = all;
+        for (int e = 0; e < kDrEach; ++e)
+            if (o[e]) in_bin[e] = (int)atomicAdd(&hist[bin_of(o[e])], 1u);
         __syncthreads();
-        for (int i = 0; i < w; ++i) at += sm.red[par][i];
-        par ^= 1;
+        constexpr int kEachBin = kDrBins / kDrThreads;
+        uint32_t h[kEachBin];
+        u64 sum = 0, all;
+        bool crowd = false;
+#pragma unroll
+        for (int e = 0; e < kEachBin; ++e) {
+            h[e] = hist[t * kEachBin + e];
+            sum += h[e];
+            crowd |= h[e] > 64;
+        }
+        crowd = __syncthreads_or(crowd);
+        u64 at = before_cta(sum, all);
+        if (crowd) {
+            // many equal or nearly equal logits: by bisection over the order of the floats
+            const uint32_t o_from = max(dr_ord(-INFINITY) + 1, dr_ord(from)), o_to = dr_ord(m) + 1;
+            auto cut_at = [&](uint32_t v, u64 k) {     // the first k by id of the tokens equal to v stay, and those above
+                u64 mine = 0, every;
+#pragma unroll
+                for (int e = 0; e < kDrEach; ++e) mine += o[e] == v ? 1 : 0;
+                u64 place = before_cta(mine, every);
+#pragma unroll
+                for (int e = 0; e < kDrEach; ++e) {
+                    if (o[e] == v && place++ >= k) o[e] = 0;
+                    if (o[e] < v) o[e] = 0;
+                    if (o[e] == 0) wt[e] = 0;
+                }
+            };
+            auto reach = [&](uint32_t v, bool weigh) {
+                u64 s = 0;
+#pragma unroll
+                for (int e = 0; e < kDrEach; ++e) s += o[e] >= v && o[e] ? (weigh ? wt[e] : 1) : 0;
+                return sum_cta(s);
+            };
+            auto bisect = [&](u64 goal, bool weigh) {
+                uint32_t lo = o_from, hi = o_to;
+                while (hi - lo > 1) {
+                    const uint32_t mid = lo + (hi - lo) / 2;
+                    if (reach(mid, weigh) >= goal) lo = mid;
+                    else hi = mid;
+                }
+                return lo;
+            };
+            if (first < (u64)n) {
+                const uint32_t v = bisect(first, false);
+                cut_at(v, first - reach(v + 1, false));
+            }
+            if (weighed) {
+                const u64 mass = reach(1, true), goal = need(mass);
+                if (mass >= goal) {
+                    const uint32_t v = bisect(goal, true);
+                    const u64 rest = goal - reach(v + 1, true);
+                    u64 w1 = 0;                        // tokens of one value have one weight
+#pragma unroll
+                    for (int e = 0; e < kDrEach; ++e)
+                        if (o[e] == v) w1 = wt[e];
+                    const u64 holders = sum_cta(w1 ? 1 : 0);
+                    w1 = sum_cta(w1) / holders;
+                    cut_at(v, (rest + w1 - 1) / w1);
+                }
+            }
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < kEachBin; ++e) {
+            hist[t * kEachBin + e] = (uint32_t)at;     // the tokens of the steps before
+            at += h[e];
+        }
+        __syncthreads();
+        const int each = (n + kDrThreads - 1) / kDrThreads;
+#pragma unroll
+        for (int e = 0; e < kDrEach; ++e)
+            if (o[e]) sorted[hist[bin_of(o[e])] + in_bin[e]] = (u64)o[e] << 32 | (uint32_t)~(t * each + e);
+        __syncthreads();
+        int place[kDrEach];
 #pragma unroll
         for (int e = 0; e < kDrEach; ++e) {
-            if (o[e] == v && at++ >= n) o[e] = 0;
-            if (o[e] < v) o[e] = 0;
-            if (o[e] == 0) wt[e] = 0;
+            if (!o[e]) continue;
+            const int b = bin_of(o[e]), b0 = hist[b], b1 = b + 1 < kDrBins ? (int)hist[b + 1] : n;
+            const u64 key = (u64)o[e] << 32 | (uint32_t)~(t * each + e);
+            place[e] = b0;
+            for (int j = b0; j < b1; ++j) place[e] += sorted[j] > key;
         }
-    };
-    auto count = [&](int) -> u64 { return 1; };
-    auto mass = [&](int e) -> u64 { return wt[e]; };
-    auto above = [&](uint32_t v, auto of) {
-        u64 s = 0;
+        __syncthreads();
 #pragma unroll
-        for (int e = 0; e < kDrEach; ++e) s += o[e] > v ? of(e) : 0;
-        return sum_cta(s);
-    };
-    // the tokens of the list that come first, by decreasing logit, until they weigh (or count) `need`, which all of
-    // them do
-    auto cut_to = [&](u64 need, uint32_t from, bool weighed, auto of) {
-        uint32_t lo = max(o_inf + 1, from), hi = o_max + 1;   // largest lo whose tokens not below it reach `need`
-        while (hi - lo > 1) {
-            const uint32_t mid = lo + (hi - lo) / 2;
-            u64 s = 0;
-#pragma unroll
-            for (int e = 0; e < kDrEach; ++e) s += o[e] >= mid ? of(e) : 0;
-            if (sum_cta(s) >= need) lo = mid;
-            else hi = mid;
+        for (int e = 0; e < kDrEach; ++e) {
+            if (!o[e]) continue;
+            if ((u64)place[e] >= first) { o[e] = 0; wt[e] = 0; }
+            if (weighed) by_place[place[e]] = wt[e];
         }
-        u64 rest = need - above(lo, of);
-        if (weighed) {
-            // tokens of one value have one weight
-            u64 w1 = 0;
+        if (!weighed) return;
+        __syncthreads();
+        u64 mine[kDrEach], mass = 0;
 #pragma unroll
-            for (int e = 0; e < kDrEach; ++e)
-                if (o[e] == lo) w1 = wt[e];
-            const u64 holders = sum_cta(w1 ? 1 : 0);
-            w1 = sum_cta(w1) / holders;
-            rest = (rest + w1 - 1) / w1;
+        for (int e = 0; e < kDrEach; ++e) {
+            const int i = t * kDrEach + e;
+            mine[e] = i < n ? by_place[i] : 0;
+            mass += mine[e];
         }
-        cut_at(lo, rest);
+        at = before_cta(mass, all);
+#pragma unroll
+        for (int e = 0; e < kDrEach; ++e) {
+            by_place[t * kDrEach + e] = at;            // the mass before the place
+            at += mine[e];
+        }
+        __syncthreads();
+        const u64 goal = need(all);
+#pragma unroll
+        for (int e = 0; e < kDrEach; ++e)
+            if (o[e] && by_place[place[e]] >= goal) { o[e] = 0; wt[e] = 0; }
     };
     // the least kept token of the list as (value's order, ~id)
     auto least_key = [&]() {
@@ -789,60 +945,19 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     };
     if (listed) {
         if (rank == 0) {
-            take_list(n_list);
-            const uint32_t from = dr_ord(low_bound);
-            if (n_list <= kDrThreads) {
-                // one token a thread: its place is the number of tokens that rank before it
-                const uint32_t mine = o[0];
-                int place = 0;
-                for (int i = 0; i < n_list; ++i) {
-                    const uint32_t other = (uint32_t)(list[i] >> 32);
-                    place += other > mine || (other == mine && i < t) ? 1 : 0;
-                }
-                if (K > 0 && place >= K) o[0] = 0;
-                if (o[0] == 0) wt[0] = 0;
-                if (nucleus) {
-                    // masses by place, and what comes before each
-                    u64* by_place = list + kDrThreads;
-                    if (t < n_list) by_place[place] = wt[0];
-                    __syncthreads();
-                    u64 all, at = dr_warp_before(t < n_list ? by_place[t] : 0, all);
-                    if (lane == 0) sm.red[par][w] = all;
-                    __syncthreads();
-                    all = 0;
-                    for (int i = 0; i < kDrWarps; ++i) {
-                        if (i == w) at += all;
-                        all += sm.red[par][i];
-                    }
-                    par ^= 1;
-                    by_place[kDrThreads + t] = at;
-                    __syncthreads();
-                    const u64 target = K > 0 ? max(dr_part(top_p, all, true), 1ull) : p_target;
-                    if (t < n_list && by_place[kDrThreads + place] >= target) o[0] = 0;
-                    if (o[0] == 0) wt[0] = 0;
-                }
-            } else {
-                if (K > 0 && n_list > K) cut_to((u64)K, from, false, count);
-                if (nucleus) {
-                    const u64 all = above(0, mass), target = K > 0 ? max(dr_part(top_p, all, true), 1ull) : p_target;
-                    if (all >= target) cut_to(target, from, true, mass);
-                }
-            }
-            u64 mine = 0;
+            const int n = (int)n_list;
+            take_list(n);
+            if ((K > 0 && n > K) || nucleus)
+                cut_list(n, low_bound, m, K > 0 ? (u64)K : ~0ull, nucleus, [&](u64 all) {
+                    return K > 0 ? max(dr_part(top_p, all, true), 1ull) : p_target;
+                });
+            u64 mine = 0, sum;
 #pragma unroll
             for (int e = 0; e < kDrEach; ++e) {
                 if (wt[e] < w_min) wt[e] = 0;
                 mine += wt[e];
             }
-            u64 all, at = dr_warp_before(mine, all);
-            if (lane == 0) sm.red[par][w] = all;
-            __syncthreads();
-            u64 sum = 0;
-            for (int i = 0; i < kDrWarps; ++i) {
-                if (i == w) at += sum;
-                sum += sm.red[par][i];
-            }
-            par ^= 1;
+            u64 at = before_cta(mine, sum);
             const u64 target = dr_part(u, sum, false);
             if (at <= target && target < at + mine) {
                 bool hit = false;
@@ -851,7 +966,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                     at += wt[e];
                     if (!hit && target < at) {
                         hit = true;
-                        finish(id[e], x[e], sum);
+                        finish(id[e], dr_value(o[e]), sum);
                     }
                 }
             }
@@ -859,7 +974,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                 const u64 least = least_key();
                 if (w == 0) {
                     everywhere(&sm.S, sum);
-                    everywhere(&sm.cv, (uint32_t)(least >> 32));
+                    everywhere(&sm.cv, dr_value((uint32_t)(least >> 32)));
                     everywhere(&sm.ci, (int)~(uint32_t)least);
                 }
             }
@@ -876,61 +991,81 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
         // The cut at which the kept tokens, by decreasing logit, reach `need`, counted or weighed (`all` in all).
         auto select = [&](u64 need, bool weighed, u64 all) {
             const DrCut old = cut;
-            auto kept = [&](float v, int seg, int i) { return dr_kept(old, dr_ord(v), lp_index<T>(mis, seg, i)); };
-            float from = low_bound, to = INFINITY;     // the border lies in [from, to)
-            bool found = false;
-            int n = 0;
-            for (int round = 0; round < 4 && !found; ++round) {
-                // 1. a histogram of [from, to) by the logit, from the top down, in units of 2^-30 of the whole mass, and
-                // what lies above.  (Without a bound the steps are steps of the floats' order.)
+            const bool cut_some = old.v > -INFINITY;
+            constexpr int kEachBin = kDrBins / kDrThreads;
+            constexpr float kWholeUnits = 1073741824.f;                        // the whole mass in a histogram's units
+            const float per_one = weighed ? kWholeUnits / ((float)all / (float)one) : 1.f, c2 = E.ch * (1.f / kDrSteps);
+            const long long goal = weighed ? (long long)((float)need / (float)all * kWholeUnits) : (long long)need;
+            // A histogram of the kept tokens in [from, to) by the logit, from the top down, and from it the steps that may
+            // hold the border: [from, to) shrinks to them.  A look at every fourth segment (masses only) is filled up
+            // to the whole mass from the top, so that what it errs by is its error of the mass below the border.
+            auto narrow = [&](float& from, float& to, bool quarter) {
                 const float top = fminf(to, m), step = (float)(kDrBins - 1) / fmaxf(top - from, 1e-30f);
-                const bool by_order = from == -FLT_MAX;
-                const float per_one = weighed ? 1073741824.f / ((float)all / (float)one) : 1.f, c2 = E.ch * (1.f / kDrSteps);
+                const bool by_order = from == -FLT_MAX;        // (without a bound the steps are steps of the floats' order)
+                const uint32_t o_max = dr_ord(m), o_inf = dr_ord(-INFINITY);
                 for (int i = t; i < kDrBins; i += kDrThreads) hist[i] = 0;
                 __syncthreads();
-                u64 over = 0;
-                each_span(from, [&](const float (&v)[kDrSegs][8], int s) {
+                u64 outside = 0, under = 0;            // what lies above, and below
+                auto look = [&](const float (&x)[8], int seg) {
 #pragma unroll
-                    for (int g = 0; g < kDrSegs; ++g)
+                    for (int i = 0; i < 8; ++i) {
+                        const bool in = x[i] >= -FLT_MAX && (!cut_some || dr_kept(old, x[i], lp_index<T>(mis, seg, i)));
+                        const uint32_t c = !in ? 0u : weighed ? __float2uint_rn(ex2((x[i] - m) * c2) * per_one) : 1u;
+                        const bool inside = x[i] >= from && x[i] < to;
+                        if (inside && c) atomicAdd(&hist[by_order ? (o_max - dr_ord(x[i])) >> 21 : min(kDrBins - 1, (int)((top - x[i]) * step))], c);
+                        if (to < INFINITY) outside += x[i] >= to ? c : 0u;
+                        if (quarter) under += x[i] < from ? c : 0u;
+                    }
+                };
+                if (quarter) stream(every, true, look, [](int) {});
+                else stream(reaching(from), false, look, [](int) {});
+                under = sum_all(dr_warp_sum(under));
+                const u64 over = sum_all(dr_warp_sum(outside));                // (and the histograms are there)
+                u64 h[kEachBin], sum = 0, inside;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            if (!(v[g][i] >= from) || !kept(v[g][i], s * kDrSegs + g, i)) continue;
-                            const uint32_t c = weighed ? __float2uint_rn(ex2((v[g][i] - m) * c2) * per_one) : 1u;
-                            if (v[g][i] >= to) over += c;
-                            else atomicAdd(&hist[by_order ? (o_max - dr_ord(v[g][i])) >> 21 : min(kDrBins - 1, (int)((top - v[g][i]) * step))], c);
-                        }
-                });
-                over = sum_all(over);                  // (and the histograms are there)
-                // 2. the whole row's histogram, 8 steps a thread, and the steps that may hold the border
-                constexpr int kEachBin = kDrBins / kDrThreads;
-                u64 h[kEachBin], sum = 0;
+                for (int e = 0; e < kEachBin; ++e) h[e] = 0;
+#pragma unroll
+                for (int i = 0; i < kDrMaxCtas; ++i) {
+                    const uint4* r = reinterpret_cast<const uint4*>(cl.map_shared_rank(hist, min(i, C - 1))) + t * (kEachBin / 4);
+#pragma unroll
+                    for (int e = 0; e < kEachBin / 4; ++e) {
+                        const uint4 v = i < C ? r[e] : make_uint4(0, 0, 0, 0);
+                        h[4 * e] += v.x;
+                        h[4 * e + 1] += v.y;
+                        h[4 * e + 2] += v.z;
+                        h[4 * e + 3] += v.w;
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < kEachBin; ++e) sum += h[e];
+                if (t == 0) { sm.bin_lo = kDrBins; sm.bin_hi = sm.bin_at = 0; }
+                long long at = (long long)before_cta(sum, inside), err = weighed ? 8192 : 0;    // (masses are rounded and a little off)
+                at += (long long)over;
+                const int scale = quarter ? 4 : 1;
+                if (quarter) {
+                    at += ((long long)kWholeUnits - 4 * (long long)(over + inside + under)) / 4;   // in quarters of the units
+                    // the mass below the border is off by a few parts of a hundred: as many tokens on either side as the
+                    // list may hold, but 1 / 48 of that mass at least and 1 / 8 at most
+                    long long sum_to = at;
+                    int b_at = 0;
+#pragma unroll
+                    for (int e = 0; e < kEachBin; ++e) {
+                        sum_to += (long long)h[e];
+                        if (4 * sum_to < goal) b_at = t * kEachBin + e + 1;
+                    }
+                    atomicMax(&sm.bin_at, b_at);
+                    __syncthreads();
+                    const float w_at = ex2((top - (float)sm.bin_at / step - m) * c2) * per_one;
+                    const long long rest = (long long)kWholeUnits - goal;
+                    err += min(max(rest / 48, (long long)(800.f * w_at)), rest / 8);
+                }
 #pragma unroll
                 for (int e = 0; e < kEachBin; ++e) {
-                    h[e] = 0;
-                    for (int i = 0; i < C; ++i) h[e] += *cl.map_shared_rank(&hist[t * kEachBin + e], i);
-                    sum += h[e];
+                    at += (long long)h[e];
+                    if (scale * at + err >= goal) atomicMin(&sm.bin_lo, t * kEachBin + e);      // first that may hold the border
+                    if (scale * at < goal + err) atomicMax(&sm.bin_hi, t * kEachBin + e + 1);   // past it: the last that may
                 }
-                u64 wall, at = dr_warp_before(sum, wall);
-                if (lane == 0) sm.red[par][w] = wall;
-                if (t == 0) { sm.bin_lo = kDrBins; sm.bin_hi = 0; }
-                __syncthreads();
-                u64 whole_sum = over;
-                at += over;
-                for (int i = 0; i < kDrWarps; ++i) {
-                    if (i < w) at += sm.red[par][i];
-                    whole_sum += sm.red[par][i];
-                }
-                par ^= 1;
-                // (masses are rounded and a little off; a border outside these steps is noticed below)
-                const u64 goal = weighed ? (u64)((float)need / (float)all * 1073741824.f) : need, err = weighed ? 8192 : 0;
-#pragma unroll
-                for (int e = 0; e < kEachBin; ++e) {
-                    at += h[e];
-                    if (at + err >= goal) atomicMin(&sm.bin_lo, t * kEachBin + e);      // first that may hold the border
-                    if (at < goal + err) atomicMax(&sm.bin_hi, t * kEachBin + e + 1);   // past it: the last that may
-                }
-                cluster_sync();                        // (the histograms are read; the list may be written)
-                if (whole_sum + err < goal) break;     // the border lies below the bound (min_p's), as far as this sum goes
+                cluster_sync();                        // (the histograms are read; their memory may be written)
                 const int b_lo = min(sm.bin_lo, kDrBins - 1), b_hi = min(sm.bin_hi, kDrBins - 1);
                 __syncthreads();                       // (before they are set again)
                 if (by_order) {
@@ -942,40 +1077,32 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                     if (b_lo > 1) to = top - (float)(b_lo - 1) / step;
                     from = fmaxf(from, top - (float)(b_hi + 2) / step);
                 }
-                // 3. the tokens of these steps, if the list holds them; else the steps are taken apart
-                found = make_list(from, n, [&](float v, int seg, int i) { return v >= from && v < to && kept(v, seg, i); });
-            }
-            if (found) {
-                // 4. what lies above them, exactly, and the border among the listed
+            };
+            // The border among the tokens of [from, to), if the list holds them and it lies there.
+            auto settle = [&](float from, float to) {
+                const u64 n = make_list(from, to, old, cut_some, weighed);
+                if (n > kDrList) return false;
                 u64 over = 0;
                 if (weighed) {
-                    mine = span_masses(to, [&](const float (&v)[8], int seg, u64 (&wt8)[8]) {
-                        bool any = false;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) any |= v[i] >= to;
-                        if (__any_sync(0xffffffffu, any)) dr_weights(E, v, wt8);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (!(v[i] >= to) || !kept(v[i], seg, i)) wt8[i] = 0;
-                    });
-                    over = sum_all(lane == 0 ? mine : 0);
+                    over = over_mass;
                 } else {
-                    each_span(to, [&](const float (&v)[kDrSegs][8], int s) {
+                    stream(reaching(to), false, [&](const float (&x)[8], int seg) {
 #pragma unroll
-                        for (int g = 0; g < kDrSegs; ++g)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) over += v[g][i] >= to && kept(v[g][i], s * kDrSegs + g, i) ? 1 : 0;
-                    });
-                    over = sum_all(over);
+                        for (int i = 0; i < 8; ++i) over += x[i] >= to && dr_kept(old, x[i], lp_index<T>(mis, seg, i)) ? 1 : 0;
+                    }, [](int) {});
+                    over = dr_warp_sum(over);
                 }
+                over = sum_all(over);
                 masses = weighed;
                 if (rank == 0) {
-                    take_list(n);
-                    const u64 in = weighed ? above(0, mass) : above(0, count);
+                    take_list((int)n);
+                    u64 in = 0;
+#pragma unroll
+                    for (int e = 0; e < kDrEach; ++e) in += o[e] ? (weighed ? wt[e] : 1) : 0;
+                    in = sum_cta(in);
                     const bool holds = over < need && need <= over + in;
                     if (holds) {
-                        if (weighed) cut_to(need - over, o_inf + 1, true, mass);
-                        else cut_to(need - over, o_inf + 1, false, count);
+                        cut_list((int)n, from, fminf(to, m), weighed ? ~0ull : need - over, weighed, [&](u64) { return need - over; });
                         const u64 least = least_key();
                         if (weighed) {
                             // the listed tokens that stay, to the masses of their spans
@@ -987,67 +1114,92 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                                 }
                         }
                         if (w == 0) {
-                            everywhere(&sm.cv, (uint32_t)(least >> 32));
+                            everywhere(&sm.cv, dr_value((uint32_t)(least >> 32)));
                             everywhere(&sm.ci, (int)~(uint32_t)least);
                         }
                     }
                     if (w == 0) everywhere(&sm.holds, (int)holds);
                 }
                 cluster_sync();
-                if (sm.holds) {
-                    cut = DrCut{sm.cv, sm.ci};
-                    if (weighed) {
-                        mine = 0;
-                        for (int i = 0; i < s1 - s0; ++i) mine += my_sum[i];
-                    }
-                    return;
+                if (!sm.holds) return false;
+                cut = DrCut{sm.cv, sm.ci};
+                if (weighed) {
+                    mine = 0;
+                    for (int i = 0; i < s1 - s0; ++i) mine += my_sum[i];
                 }
+                return true;
+            };
+            float from = low_bound, to = INFINITY;
+            if (weighed && !cut_some && from > -FLT_MAX) {
+                narrow(from, to, true);
+                if (settle(from, to)) return;
+                from = low_bound;
+                to = INFINITY;
             }
-            // the whole row by bisection (more equal logits than the list holds), where the border lies above the bound
+            for (int round = 0; round < 3; ++round) {
+                narrow(from, to, false);
+                if (settle(from, to)) return;
+            }
+            // the whole row by bisection: more equal logits than the list holds, or a border below the bound
             masses = false;
-            uint32_t lo = max(o_inf + 1, dr_ord(low_bound)), hi = o_max + 1;
-            auto of = [&](uint32_t v) { return weighed ? row_mass(v, old) : row_count(v, old); };
+            uint32_t lo = max(dr_ord(-INFINITY) + 1, dr_ord(low_bound)), hi = dr_ord(m) + 1;
+            auto of = [&](uint32_t v) {
+                if (weighed) return sum_all(span_masses(dr_value(v), kept_weights(old, dr_value(v), 0)));
+                u64 n = 0;
+                const float least = dr_value(v);
+                stream(reaching(least), false, [&](const float (&x)[8], int seg) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) n += x[i] >= least && dr_kept(old, x[i], lp_index<T>(mis, seg, i)) ? 1 : 0;
+                }, [](int) {});
+                return sum_all(dr_warp_sum(n));
+            };
             if (of(lo) < need) return;
             while (hi - lo > 1) {
                 const uint32_t mid = lo + (hi - lo) / 2;
                 if (of(mid) >= need) lo = mid;
                 else hi = mid;
             }
-            u64 rest = need - (lo < o_max ? of(lo + 1) : 0);
+            const float v = dr_value(lo);
+            u64 rest = need - (v < m ? of(lo + 1) : 0);
             if (weighed) {
-                float v[8];
-                u64 wt8[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = dr_value(lo);
-                dr_weights(E, v, wt8);
-                rest = (rest + wt8[0] - 1) / wt8[0];
+                u64 vv[2];
+                int n[2];
+                dr_weight2(E, v, v, vv, n);
+                const u64 w1 = dr_units(E, vv[0], n[0]);
+                rest = (rest + w1 - 1) / w1;
             }
             // the id of the last of the equal tokens that stay
-            auto tie = [&](const float (&v)[8], int seg, u64 (&wt8)[8]) {
+            auto tie = [&](const float (&x)[8], int seg, u64 (&wt8)[8]) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int d = lp_index<T>(mis, seg, i);
-                    wt8[i] = dr_ord(v[i]) == lo && d >= 0 && d < V && dr_kept(old, lo, d) ? 1 : 0;
+                    wt8[i] = x[i] == v && d >= 0 && d < V && dr_kept(old, v, d) ? 1 : 0;
                 }
             };
-            const u64 ties = span_masses(dr_value(lo), tie);
+            const u64 ties = span_masses(v, tie);
             locate(ties, tie, [&](u64) { return rest - 1; }, [&](int d, float, u64) {
                 for (int i = 0; i < C; ++i) *cl.map_shared_rank(&sm.ci, i) = d;
             });
             cluster_sync();
-            cut = DrCut{lo, sm.ci};
+            cut = DrCut{v, sm.ci};
         };
         if (K > 0) {
             // (at least K tokens are finite, or every finite one stays)
-            if (row_count(o_inf + 1, cut) > (u64)K) select((u64)K, false, 0);
+            u64 n = 0;
+            stream(reaching(-FLT_MAX), false, [&](const float (&x)[8], int) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) n += x[i] >= -FLT_MAX ? 1 : 0;
+            }, [](int) {});
+            if (sum_all(dr_warp_sum(n)) > (u64)K) select((u64)K, false, 0);
             if (nucleus) {
-                S = row_mass(o_inf + 1, cut);
+                S = sum_all(span_masses(fmaxf(cut.v, -FLT_MAX), kept_weights(cut, -FLT_MAX, 0)));
                 p_target = max(dr_part(top_p, S, true), 1ull);
+                low_bound = fmaxf(low_bound, cut.v);
             }
         }
         if (nucleus) select(p_target, true, S);
-        const auto f = kept_weights(cut, o_inf + 1, w_min);
-        if (!masses || w_min > 1) mine = span_masses(dr_value(max(cut.v, o_inf + 1)), f);
+        const auto f = kept_weights(cut, -FLT_MAX, w_min);
+        if (!masses || w_min > 1) mine = span_masses(fmaxf(cut.v, -FLT_MAX), f);
         S_kept = locate(mine, f, [&](u64 total) { return dr_part(u, total, false); }, finish);
     }
     if (!probs) {
@@ -1057,40 +1209,42 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
 
     // -------- the distribution
     const float inv = (float)(1ull << E.q) / (float)S_kept;
-    const float least = dr_value(max(cut.v, o_inf + 1));
+    const float least = fmaxf(cut.v, -FLT_MAX);
+    const u64 w_some = max(w_min, 1ull);
 #pragma unroll 1
     for (int s = s0; s < s1; ++s) {
         const bool any = __any_sync(0xffffffffu, my_max[(s - s0) * 32 + lane] >= least);
 #pragma unroll 1
         for (int g = 0; g < kDrSegs; ++g) {
-            float v[8], y[8];
-            if (any) lp_load(row, V, mis, s * kDrSegs + g, v);
+            uint4 p[NP];
+            float x[8], y[8];
+            if (any) {
+                load_raw(s * kDrSegs + g, p);
+                unpack(p, x);
+            }
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
                 y[i] = y[i + 1] = 0.f;
                 if (!any) continue;
-                u64 vv[2];
+                u64 v[2];
                 int n[2];
-                dr_weight2(E, v[i], v[i + 1], vv, n);
+                dr_weight2(E, x[i], x[i + 1], v, n);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float l = v[i + j];
-                    const bool in = dr_kept(cut, dr_ord(l), lp_index<T>(mis, s * kDrSegs + g, i + j)) &&
-                                    dr_units(E, vv[j], n[j]) >= max(w_min, 1ull);
-                    if (in) y[i + j] = (float)vv[j] * __uint_as_float((uint32_t)(127 - 62 - n[j]) << 23) * inv;
-                }
+                for (int j = 0; j < 2; ++j)
+                    if (x[i + j] >= least && dr_kept(cut, x[i + j], lp_index<T>(mis, s * kDrSegs + g, i + j)) && dr_units(E, v[j], n[j]) >= w_some)
+                        y[i + j] = (float)v[j] * __uint_as_float((uint32_t)(127 - 62 - n[j]) << 23) * inv;
             }
 #pragma unroll
-            for (int p = 0; p < NP; ++p) {
-                const int d = lp_index<T>(mis, s * kDrSegs + g, p * VE);
+            for (int k = 0; k < NP; ++k) {
+                const int d = lp_index<T>(mis, s * kDrSegs + g, k * VE);
                 if (a.p_vec && d >= 0 && d + VE <= V) {
 #pragma unroll
                     for (int i = 0; i < VE; i += 4)
-                        *reinterpret_cast<float4*>(probs + d + i) = make_float4(y[p * VE + i], y[p * VE + i + 1], y[p * VE + i + 2], y[p * VE + i + 3]);
+                        *reinterpret_cast<float4*>(probs + d + i) = make_float4(y[k * VE + i], y[k * VE + i + 1], y[k * VE + i + 2], y[k * VE + i + 3]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < VE; ++i)
-                        if (d + i >= 0 && d + i < V) probs[d + i] = y[p * VE + i];
+                        if (d + i >= 0 && d + i < V) probs[d + i] = y[k * VE + i];
                 }
             }
         }
@@ -1098,7 +1252,10 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     cluster_sync();
 }
 
-static size_t dr_smem(int per) { return (size_t)kDrList * 8 + (size_t)kDrSteps * 8 + (size_t)kDrWarps * per * (8 + 4 + 32 * 4); }
+static size_t dr_smem(int per, size_t elem) {
+    return (size_t)(kDrList + kDrWarps * kDrStage + kDrSteps) * 8 + (size_t)kDrWarps * kDrRing * (elem / 2) * 512 +
+           (size_t)kDrWarps * per * (8 + 4 + 32 * 4);
+}
 
 }  // namespace spec
 
@@ -1160,12 +1317,12 @@ extern "C" int spec_sample_logits(const void* logits, int32_t dtype, int64_t lg_
     int C = 1;
     while (C < kDrMaxCtas && ((long long)vocab > (long long)C * kDrCtaVocab || ((long long)rows * C < kDrCtasWanted * sms && n_span > C * kDrWarps))) C *= 2;
     a.per = (n_span + C * kDrWarps - 1) / (C * kDrWarps);
-    const size_t smem = dr_smem(a.per);
+    const size_t smem = dr_smem(a.per, elem);
     void (*f)(DrawArgs) = dtype == SPEC_DTYPE_BF16 ? draw_kernel<__nv_bfloat16> : draw_kernel<float>;
     if (smem > 48 * 1024) {
         // the most that any call takes: another thread's call may come between this one's two steps
         constexpr int most_per = (kDrCtaVocab / kDrSpan + 1 + kDrWarps) / kDrWarps;
-        SPEC_TRY(check_cuda(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dr_smem(most_per)), "spec_sample_logits attribute"));
+        SPEC_TRY(check_cuda(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dr_smem(most_per, elem)), "spec_sample_logits attribute"));
     }
     cudaLaunchConfig_t cfg_l = {};
     cfg_l.gridDim = dim3((unsigned)(rows * C));

@@ -9,6 +9,7 @@ the loader raises -- there is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from array import array
 from ctypes import POINTER, c_double, c_float, c_int32, c_void_p
@@ -517,10 +518,12 @@ def _rows3d(t, name, heads, dim, rows, dtype, dev):
     """[rows][heads][dim] rows with their heads in one piece: (pointer, row stride)."""
     sh = t.shape if t is not None else ()
     st = t.stride() if len(sh) == 3 else ()
-    if (len(sh) != 3 or t.dtype is not dtype or not t.is_cuda or sh[0] < rows or sh[1] != heads or sh[2] != dim
-            or st[2] != 1 or (heads > 1 and st[1] != dim)):
+    # (a tensor of the current device is a CUDA tensor: one look instead of two)
+    if (len(sh) != 3 or t.dtype is not dtype or sh[0] < rows or sh[1] != heads or sh[2] != dim
+            or st[2] != 1 or (heads > 1 and st[1] != dim) or t.get_device() != dev):
+        if len(sh) == 3 and t.is_cuda and t.get_device() != dev:
+            _on(t, dev, name)
         raise SpecError(f"{name}: need a CUDA {dtype} tensor [{rows}, {heads}, {dim}] with contiguous rows")
-    _on(t, dev, name)
     return t.data_ptr(), st[0] if sh[0] > 1 else heads * dim
 
 
@@ -551,16 +554,27 @@ def spec_attend(kv, layer, n_rows, q, out, k=None, v=None, tree_parent=None, str
         _check(rc)
 
 
+@functools.lru_cache(maxsize=64)
+def _rope_config(heads, kv_heads, dim, bf16, sections, interleaved, theta):
+    """The call's settings as the library takes them (made once for each set of values)."""
+    if not 1 <= len(sections) <= 4:
+        raise SpecError("sections: one to four axes")
+    return RopeConfig(heads, kv_heads, dim, SPEC_DTYPE_BF16 if bf16 else SPEC_DTYPE_F32, len(sections),
+                      (c_int32 * 4)(*sections), 1 if interleaved else 0, theta)
+
+
 def spec_rope(q, q_out, k=None, k_out=None, theta=10000.0, positions=None, sections=None, interleaved=False, kv=None,
               n_rows=None, tree_parent=None, stream=None):
     """``q_out`` [T, H, hd] and ``k_out`` [T, Hkv, hd]: ``q`` and ``k`` (bf16 or f32) with their
     positions encoded, in place where a result is its input.  ``positions`` is int32 [T] or
     [axes, T] with ``sections`` frequency pairs an axis (default: one axis, all hd / 2); or the
     rows are those of a call on the cache ``kv`` with ``n_rows`` and ``tree_parent``."""
-    if q is None or q.dim() != 3 or q.dtype not in (torch.bfloat16, torch.float32):
+    sh = q.shape if q is not None else ()
+    dt = q.dtype if len(sh) == 3 else None
+    if dt is not torch.bfloat16 and dt is not torch.float32:
         raise SpecError("q: need a CUDA bfloat16 or float32 tensor [T, H, hd]")
-    dt, dev = q.dtype, torch.cuda.current_device()
-    T, H, hd = q.shape
+    dev = torch.cuda.current_device()
+    T, H, hd = sh
     qp, qs = _rows3d(q, "q", H, hd, T, dt, dev)
     qop, qos = _rows3d(q_out, "q_out", H, hd, T, dt, dev)
     kp = kop = None
@@ -573,20 +587,16 @@ def spec_rope(q, q_out, k=None, k_out=None, theta=10000.0, positions=None, secti
         kop, kos = _rows3d(k_out, "k_out", Hkv, hd, T, dt, dev)
     elif k_out is not None:
         raise SpecError("k_out: given without k")
-    sections = [hd // 2] if sections is None else [int(n) for n in sections]
-    if not 1 <= len(sections) <= 4:
-        raise SpecError("sections: one to four axes")
-    cfg = RopeConfig(H, Hkv, hd, SPEC_DTYPE_BF16 if dt is torch.bfloat16 else SPEC_DTYPE_F32, len(sections),
-                     (c_int32 * 4)(*sections), 1 if interleaved else 0, float(theta))
+    sections = (hd // 2,) if sections is None else tuple(sections)
+    cfg = _rope_config(H, Hkv, hd, dt is torch.bfloat16, sections, bool(interleaved), float(theta))
     pp = handle = cp = tp = None
     batch = pos_stride = 0
     if positions is not None:
-        sh = positions.shape
-        if positions.dtype is not torch.int32 or not positions.is_cuda or len(sh) not in (1, 2) or sh[-1] != T or \
-                (T > 1 and positions.stride(-1) != 1) or (sh[0] if len(sh) == 2 else 1) != len(sections):
-            raise SpecError(f"positions: need a CUDA int32 tensor [{len(sections)}, {T}] with contiguous rows")
-        _on(positions, dev, "positions")
-        pp, pos_stride = positions.data_ptr(), positions.stride(0) if len(sh) == 2 and sh[0] > 1 else T
+        psh, pst, axes = positions.shape, positions.stride(), len(sections)
+        if positions.dtype is not torch.int32 or (psh != (axes, T) and (axes > 1 or psh != (T,))) or \
+                (T > 1 and pst[-1] != 1) or positions.get_device() != dev:
+            raise SpecError(f"positions: need a CUDA int32 tensor [{axes}, {T}] with contiguous rows, on the current device")
+        pp, pos_stride = positions.data_ptr(), pst[0] if axes > 1 else T
     if kv is not None:
         counts = array("i", n_rows if n_rows is not None else [])
         handle, batch, cp = kv.handle, len(counts), counts.buffer_info()[0]
@@ -597,7 +607,7 @@ def spec_rope(q, q_out, k=None, k_out=None, theta=10000.0, positions=None, secti
             tp = tree.buffer_info()[0]
     elif positions is None:
         raise SpecError("spec_rope: positions or a cache")
-    rc = load().spec_rope(ctypes.byref(cfg), T, qp, qs, qop, qos, kp, ks, kop, kos, pp, pos_stride, handle, batch, cp, tp,
+    rc = load().spec_rope(cfg, T, qp, qs, qop, qos, kp, ks, kop, kos, pp, pos_stride, handle, batch, cp, tp,
                           _stream(stream, dev))
     if rc:
         _check(rc)
