@@ -1122,7 +1122,9 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
         long long n = (ctx + round) / per;
         // whole caches that would be among the longest CTAs are halved: sequences differ in length
         if (n == 1 && 2 * ctx > per && ctx > 2 * kMinKeys) n = 2;
-        return (int)std::max<long long>(1, std::min<long long>({n, 64, (16 * 512) / (std::max(16, QB) * n_blocks) + 1}));
+        // (windows: all that the workspace holds; it is shared by the two parts)
+        const long long most = win ? (long long)fit / (pre ? 2 : 1) : (16 * 512) / (16 * n_blocks) + 1;
+        return (int)std::max<long long>(1, std::min<long long>({n, 64, most}));
     };
     a.own_splits = splits(own_blocks, own_ctx);
     a.pre_splits = splits(pre_blocks, pre_ctx);

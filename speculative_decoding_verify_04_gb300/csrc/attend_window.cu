@@ -6,14 +6,18 @@
 // softmax's running maximum and sum in registers, S = Q K^T and O += P V by mma.sync
 // m16n8k16, four warps that share every tile.  Each warp holds 16 query vectors; in a
 // block of 32 two warps share them and take half of a tile's keys each, and join at the
-// end.  A fifth warp copies the tiles ahead: bf16 caches by tensor boxes (128-byte
-// swizzle, a tile of K and one of V a stage), 8-bit ones as they are held, which the four
-// warps turn into bf16 tiles first, y 2^e, exactly.  The window's bounds cost masks only in
-// the tiles where not every row sees every key; there a value that is not finite is taken
-// out of the product (zero times it is not zero) and reaches the rows that see it as NaN.
+// end.  A fifth warp copies the tiles ahead by tensor boxes (128-byte swizzle, a tile of K
+// and one of V a stage).  The window's bounds cost masks only in the tiles where not every
+// row sees every key; there a value that is not finite is taken out of the product (zero
+// times it is not zero) and reaches the rows that see it as NaN.
 //
 // mma.sync and not tcgen05: a block of the latter has 128 rows, and a list of 32 query
 // vectors is bound by reading its keys once (32 flops a byte) long before that.
+//
+// bf16 caches only: 8-bit tiles turned into bf16 ones in shared memory made a call slower than
+// the row kernel's products in f16 (32 sequences, 2048 keys, 8 KV heads of 128: 24 vectors 95 us
+// against 76, 32 97 / 78, 64 122 / 118, 116 223 / 229).  In bf16 the row kernel is the faster one up to
+// 16 vectors (16: 55 against 61 us; 24: 85 / 63; 32: 88 / 65; 64: 137 / 91; 116: 253 / 160).
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -39,22 +43,20 @@ struct WinShape {
     static constexpr int kStage = 2 * kTile;
     static constexpr int kQ = RB * 16 * HD * 2;        // the block's query vectors
     static constexpr int kQBytes = (QF32 ? 2 : 1) * kQ;
-    static constexpr int kStages = HD == 64 ? 4 : (kQBytes > 16384 ? 2 : 3);
-    static constexpr int kRaw = 2 * kWinKeys * (HD + 1);   // an 8-bit tile of K and V, exponents behind the values
-    static constexpr int kRawStages = HD == 64 ? 3 : (kQBytes >= 16384 ? 1 : 2);
-    // 8-bit caches: two tiles in bf16 and the raw ones behind them
-    static constexpr int kRing = kStages * kStage > 2 * kStage + kRawStages * kRaw ? kStages * kStage : 2 * kStage + kRawStages * kRaw;
+    static constexpr int kStages = HD == 64 ? (kQBytes > 8192 ? 3 : 4) : (kQBytes > 16384 ? 2 : 3);
+    static constexpr int kRing = kStages * kStage;
     static constexpr int kJoin = RB == 2 ? 32 * (HD + 2) * 4 : 0;
     static_assert(kRing >= kJoin, "the second half's states");
     static constexpr int kSmem = kRing + kQBytes + QR * 12 + (int)sizeof(WinBars);
-    static_assert(kSmem <= (233472 - 2048) / 2, "two CTAs an SM");
+    static constexpr int kCtas = HD == 64 ? 3 : 2;     // an SM
+    static_assert(kSmem <= 233472 / kCtas - 1024, "CTAs an SM");
 };
 
 // row r, 16-byte piece c of a tile of [64 dims][rows] halves with 128-byte rows
 SPEC_DEV uint32_t swz(int half_bytes, int r, int c) { return (c >> 3) * half_bytes + r * 128 + (((c & 7) ^ (r & 7)) << 4); }
 
 template <int HD, bool QF32, int RB>
-__global__ void __launch_bounds__(kWinThreads, 2)
+__global__ void __launch_bounds__(kWinThreads, WinShape<HD, QF32, RB>::kCtas)
 attend_window_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap own_k,
                      const __grid_constant__ CUtensorMap own_v, const __grid_constant__ CUtensorMap pre_k,
                      const __grid_constant__ CUtensorMap pre_v) {
@@ -171,8 +173,7 @@ attend_window_kernel(const __grid_constant__ AttendArgs a, const __grid_constant
     }
     __syncthreads();
     volatile int* ab = &B.abort;
-    const int n_stages = cv.q8 ? S::kRawStages : S::kStages;
-    char* raw = ring + 2 * S::kStage;                  // 8-bit caches
+    constexpr int n_stages = S::kStages;
 
     if (warp == kWinWarps) {
         // -------- copies
@@ -187,21 +188,12 @@ attend_window_kernel(const __grid_constant__ AttendArgs a, const __grid_constant
                 // 64 slots from a multiple of 64 on: no page is crossed
                 long long row = kv_row_in_layer(cv.pages, a.Hkv, seq, g, key_slot<true>(km, (t0 + i) * kWinKeys));
                 if (row < 0) { dev_error(a.err, SPEC_DEVERR_CAPACITY); row = 0; }
-                if (cv.q8) {
-                    mbar_arrive_expect_tx(&B.full[s], S::kRaw);
-                    char* dst = raw + s * S::kRaw;
-                    bulk_load(dst, static_cast<const uint8_t*>(cv.k) + row * HD, kWinKeys * HD, &B.full[s], keep);
-                    bulk_load(dst + kWinKeys * HD, static_cast<const uint8_t*>(cv.v) + row * HD, kWinKeys * HD, &B.full[s], keep);
-                    bulk_load(dst + 2 * kWinKeys * HD, cv.ke + row, kWinKeys, &B.full[s], keep);
-                    bulk_load(dst + 2 * kWinKeys * HD + kWinKeys, cv.ve + row, kWinKeys, &B.full[s], keep);
-                } else {
-                    mbar_arrive_expect_tx(&B.full[s], S::kStage);
-                    char* dst = ring + s * S::kStage;
+                mbar_arrive_expect_tx(&B.full[s], S::kStage);
+                char* dst = ring + s * S::kStage;
 #pragma unroll
-                    for (int h = 0; h < HD / 64; ++h) {
-                        tma_load_3d(dst + h * kKHalf, mk, 64 * h, (int)row, a.layer, &B.full[s], keep);
-                        tma_load_3d(dst + S::kTile + h * kKHalf, mv, 64 * h, (int)row, a.layer, &B.full[s], keep);
-                    }
+                for (int h = 0; h < HD / 64; ++h) {
+                    tma_load_3d(dst + h * kKHalf, mk, 64 * h, (int)row, a.layer, &B.full[s], keep);
+                    tma_load_3d(dst + S::kTile + h * kKHalf, mv, 64 * h, (int)row, a.layer, &B.full[s], keep);
                 }
                 ++issued;
             }
@@ -230,34 +222,7 @@ attend_window_kernel(const __grid_constant__ AttendArgs a, const __grid_constant
     for (int i = 0; i < n_tiles && ok; ++i) {
         const int s = i % n_stages;
         ok = __all_sync(0xffffffffu, mbar_wait(&B.full[s], (i / n_stages) & 1, ab, a.err));
-        if (cv.q8) {
-            // every warp a quarter of the tile's rows; all of it is there behind the barrier.  (Two tiles in turn: whoever
-            // writes this one has passed the last barrier, so every warp is done with the tile before the last.)
-            if (ok) {
-                const char* src = raw + s * S::kRaw;
-                char* dst = ring + (i & 1) * S::kStage;
-                for (int x = t; x < 2 * kWinKeys * (HD / 16); x += 32 * kWinWarps) {
-                    const int which = x / (kWinKeys * (HD / 16)), y = x % (kWinKeys * (HD / 16)), key = y / (HD / 16), ch = y % (HD / 16);
-                    const uint4 w = *reinterpret_cast<const uint4*>(src + which * kWinKeys * HD + y * 16);
-                    const float sc = kv8_scale(static_cast<uint8_t>(src[2 * kWinKeys * HD + which * kWinKeys + key]));
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                    uint32_t p[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 f = e4m3x2_f32(u[e]), h = e4m3x2_f32(u[e] >> 16);
-                        p[2 * e] = bf16x2(f.x * sc, f.y * sc);
-                        p[2 * e + 1] = bf16x2(h.x * sc, h.y * sc);
-                    }
-                    char* d = dst + which * S::kTile;
-                    *reinterpret_cast<uint4*>(d + swz(kKHalf, key, 2 * ch)) = make_uint4(p[0], p[1], p[2], p[3]);
-                    *reinterpret_cast<uint4*>(d + swz(kKHalf, key, 2 * ch + 1)) = make_uint4(p[4], p[5], p[6], p[7]);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&B.empty[s]);
-            }
-            named_bar(1, 32 * kWinWarps);
-        }
-        char* tile = ring + (cv.q8 ? i & 1 : s) * S::kStage;
+        char* tile = ring + s * S::kStage;
         const int kt = (t0 + i) * kWinKeys, slot = key_slot<true>(km, kt), valid = n_keys - kt;
         const bool edge = slot + kWinKeys > n_ctx || slot < km.low_max || valid < kWinKeys;
         unsigned long long bad = 0ull;                 // bit k: key k's values are not finite
@@ -374,10 +339,8 @@ attend_window_kernel(const __grid_constant__ AttendArgs a, const __grid_constant
                 }
             }
         }
-        if (!cv.q8) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&B.empty[s]);
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.empty[s]);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -438,9 +401,9 @@ attend_window_kernel(const __grid_constant__ AttendArgs a, const __grid_constant
 }
 
 // ---------------------------------------------------------------------------
-bool attend_window_ok(const spec_kv* kv) { return (kv->q8 || kv->tmaps) && (!kv->prefix || kv->prefix->q8 || kv->prefix->tmaps); }
+bool attend_window_ok(const spec_kv* kv) { return !kv->q8 && kv->tmaps && (!kv->prefix || (!kv->prefix->q8 && kv->prefix->tmaps)); }
 int attend_window_block(int vectors) { return vectors <= 32 ? 32 : 64; }
-int attend_window_ctas(int) { return 2; }
+int attend_window_ctas(int hd) { return hd == 64 ? 3 : 2; }
 
 template <int HD, bool QF32, int RB>
 static int launch_window(const spec_kv* kv, const AttendArgs& a, cudaStream_t st) {

@@ -12,6 +12,7 @@
 // A CTA takes `group` rows: their angles once, in shared memory, for all heads, while the
 // rows' own loads are on their way; then 16 bytes of each half of a head a thread at a time.
 // Bound by memory (three operations a value).
+#include <algorithm>
 #include <cmath>
 
 #include "attend.cuh"
@@ -22,6 +23,7 @@ constexpr int kRopeThreads = 256;
 constexpr int kRopeMaxPairs = 128;           // head_dim <= 256
 constexpr int kRopeMaxAxes = 4;
 constexpr int kRopeMaxGroup = 4;
+constexpr int kRopeAhead = 4;                // pieces of each half that a thread has on their way
 
 struct RopeArgs {
     const void* src[2];                      // queries, keys
@@ -58,16 +60,19 @@ SPEC_DEV float2 cos_sin(uint64_t turns) {
     return q & 2 ? make_float2(-x, -y) : make_float2(x, y);
 }
 
-// VE elements of each half of a head (VE * sizeof(T) = 16 bytes, or one element)
+// VE elements of a head as they lie in memory (VE * sizeof(T) = 16 bytes, or one element)
 template <typename T, int VE>
 struct RopePiece {
-    float x[VE];
+    uint4 raw;
     SPEC_DEV void load(const T* p) {
+        if constexpr (VE == 1) raw.x = sizeof(T) == 4 ? *reinterpret_cast<const uint32_t*>(p) : (uint32_t)*reinterpret_cast<const uint16_t*>(p) << 16;
+        else raw = *reinterpret_cast<const uint4*>(p);      // (a plain load: results may lie over their inputs)
+    }
+    SPEC_DEV void get(float (&x)[VE]) const {
         if constexpr (VE == 1) {
-            x[0] = to_f32<T>(*p);
+            x[0] = __uint_as_float(raw.x);
         } else {
-            const uint4 w = *reinterpret_cast<const uint4*>(p);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+            const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if constexpr (sizeof(T) == 4) {
@@ -79,7 +84,7 @@ struct RopePiece {
             }
         }
     }
-    SPEC_DEV void store(T* p) const {
+    SPEC_DEV static void store(T* p, const float (&x)[VE]) {
         if constexpr (VE == 1) {
             if constexpr (sizeof(T) == 4) *p = x[0];
             else *p = __float2bfloat16_rn(x[0]);
@@ -97,7 +102,7 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ AttendSp
     pdl_wait();
     pdl_trigger();
     __shared__ __align__(16) float cs[kRopeMaxGroup][2][kRopeMaxPairs];
-    constexpr int U = VE == 1 ? 4 : 2;
+    constexpr int U = kRopeAhead;
     const int t = threadIdx.x, row0 = blockIdx.x * a.group, rows = min(a.group, a.rows - row0);
     const int chunks = a.n / VE, per = (a.heads[0] + a.heads[1]) * chunks, items = rows * per;
     RopePiece<T, VE> lo[U], hi[U];
@@ -137,15 +142,18 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ AttendSp
             if (i >= items) break;
             int r, c, which, h;
             at(i, r, c, which, h);
+            float x[VE], y[VE];
+            lo[u].get(x);
+            hi[u].get(y);
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                const float x = lo[u].x[e], y = hi[u].x[e], co = cs[r][0][c + e], si = cs[r][1][c + e];
-                lo[u].x[e] = x * co - y * si;
-                hi[u].x[e] = y * co + x * si;
+                const float v = x[e], z = y[e], co = cs[r][0][c + e], si = cs[r][1][c + e];
+                x[e] = v * co - z * si;
+                y[e] = z * co + v * si;
             }
             T* p = static_cast<T*>(a.dst[which]) + (row0 + r) * a.dst_stride[which] + h * a.hd + c;
-            lo[u].store(p);
-            hi[u].store(p + a.n);
+            RopePiece<T, VE>::store(p, x);
+            RopePiece<T, VE>::store(p + a.n, y);
         }
         i0 += U * kRopeThreads;
         fetch(i0);
@@ -157,9 +165,11 @@ rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ AttendSp
             int h = hr - r * (a.heads[0] + a.heads[1]);
             const int which = h >= a.heads[0];
             h -= which ? a.heads[0] : 0;
-            RopePiece<T, VE> x;
-            x.load(static_cast<const T*>(a.src[which]) + (row0 + r) * a.src_stride[which] + h * a.hd + c);
-            x.store(static_cast<T*>(a.dst[which]) + (row0 + r) * a.dst_stride[which] + h * a.hd + c);
+            RopePiece<T, VE> p;
+            float x[VE];
+            p.load(static_cast<const T*>(a.src[which]) + (row0 + r) * a.src_stride[which] + h * a.hd + c);
+            p.get(x);
+            RopePiece<T, VE>::store(static_cast<T*>(a.dst[which]) + (row0 + r) * a.dst_stride[which] + h * a.hd + c, x);
         }
     }
 }
@@ -261,7 +271,9 @@ extern "C" int spec_rope(const spec_rope_config* cfg, int32_t rows, const void* 
         in_place &= a.src[w] == a.dst[w] && a.src_stride[w] == a.dst_stride[w];
     }
     a.rest = 2 * n < c.head_dim && !in_place;
-    a.group = rows >= 4096 ? 4 : (rows >= 1024 ? 2 : 1);
+    // rows a CTA: one, or as many as its threads hold at once where there are enough
+    const int pieces = (c.n_heads + c.n_kv_heads) * (int)(vec ? n / ve : n);
+    a.group = rows < 2048 ? 1 : std::max(1, std::min(kRopeMaxGroup, kRopeAhead * kRopeThreads / pieces));
     void (*f)(RopeArgs, AttendSpan) = elem == 2 ? (vec ? rope_kernel<__nv_bfloat16, 8> : rope_kernel<__nv_bfloat16, 1>)
                                                 : (vec ? rope_kernel<float, 4> : rope_kernel<float, 1>);
     return check_cuda(launch_k(true, f, dim3((unsigned)((rows + a.group - 1) / a.group)), dim3(kRopeThreads), 0,
