@@ -1121,7 +1121,7 @@ int launch_attend(spec_kv* kv, int layer, const AttendSpan& span, const void* q,
         if (n_blocks == 0) return 0;
         long long n = (ctx + round) / per;
         // whole caches that would be among the longest CTAs are halved: sequences differ in length
-        if (n == 1 && 2 * ctx > per && ctx > 2 * kMinKeys) n = 2;
+        if (!blocks && n == 1 && 2 * ctx > per && ctx > 2 * kMinKeys) n = 2;
         // (windows: all that the workspace holds; it is shared by the two parts)
         const long long most = win ? (long long)fit / (pre ? 2 : 1) : (16 * 512) / (16 * n_blocks) + 1;
         return (int)std::max<long long>(1, std::min<long long>({n, 64, most}));
