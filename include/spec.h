@@ -594,7 +594,8 @@ int spec_logprobs(const void* logits, int32_t dtype, int64_t lg_stride, int32_t 
  *   logprob  device f32 [rows] out, nullable: log of the token's probability among
  *            those that stay
  *   probs    device f32 out, nullable, row r at probs + r * p_stride: that
- *            distribution, zeros elsewhere (the p or q of spec_accept)
+ *            distribution, zeros elsewhere (the p or q of spec_accept); not over
+ *            the logits
  * A weight is exact to 2^-35 of itself and to 2^-49 of the best token's (to
  * 2^(log2 vocab - 61) of it where the row's weights add up to more than 2^12 of them), and
  * sums are exact: the token is that of the exact weights unless u or a cut lies that

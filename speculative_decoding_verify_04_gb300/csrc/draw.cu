@@ -18,7 +18,7 @@
 // shared memory (made by each CTA, products of two small ones), and 2^r of the rest
 // (|r| <= 1 / 4096) as 1 + two terms; the product and the shift by N - n are integer
 // arithmetic.  About 20 instructions a logit.  (A table of 32 steps in the warp's lanes and six terms,
-// the first in two floats: 30, and 622 us a call for 512 rows of 131072 to their nuclei.)
+// the first in two floats, takes 30: 512 rows of 131072 to their nuclei in 622 us against 547 then.)
 //
 // A row is taken by a cluster of 1 to 8 CTAs, each warp on a contiguous run of spans
 // of 1024 tokens.  One pass finds the maximum and leaves the maximum of every lane's 32
@@ -36,7 +36,16 @@
 // the border lies, a second look adds up exactly what lies above them, and the tokens in
 // them are listed and searched.  (What defeats that, a row of equal logits, is bisected as
 // a whole.)
+//
+// Bound by instructions and latency, not by the row's bytes: 512 rows of 131072 bf16 logits
+// to their nuclei (p 0.95) 530 us, 0.5 TB/s; 100 rows of 50257 with mixed settings 100 us;
+// one greedy row of 32000 17 us a call.  Of a long row's time 45 to 55 us go to the
+// masses, 20 to 50 to the list, 20 to the histogram and 30 to 90 to the mass above the border.
+// Not faster: a launch of its own for the rows without a list, which gives the others three CTAs
+// an SM (754), three CTAs an SM for all in 80 registers (spills), blocks of 128 or 512 threads
+// (892 and 181, 537 and 111), logits through registers instead of the ring of copies.
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <climits>
 #include <cmath>
@@ -139,16 +148,19 @@ struct DrSmem {
 
 // A weight's arithmetic.
 constexpr int kDrSteps = 2048;                         // of the table, an octave
+constexpr int kDrMagic = 0x4B400000;                   // 1.5 * 2^23: adding it leaves a float's nearest integer in the low bits
 struct DrExp {
     float b, ch, cl;                                   // b: 0, or the maximum where c x has too many digits
-    float most;                                        // -2048 t of a logit without a weight
+    float most;                                        // -2048 t of a logit whose weight is below a unit
     int N, q;
-    const u64* table;                                  // 2^(62 + j / 2048), in shared memory
+    int shift;                                         // a weight's shift is this less its integer's upper bits
+    uint32_t table;                                    // 2^(62 + j / 2048), in shared memory
     // weights relative to 2^N for logits up to `top`
     SPEC_DEV void refer_to(float top) { refer_to_n((int)ceilf((top - b) * ch * (1.f / kDrSteps))); }
     SPEC_DEV void refer_to_n(int n) {
         N = n;
-        most = (float)(-kDrSteps * (N - q - 4));       // well below 2^-q
+        most = (float)(-kDrSteps * (N - q - 1));       // there the shift is 63, and leaves nothing
+        shift = 62 - q + N + (kDrMagic >> 11);
     }
 };
 // c x as the arithmetic takes it: beyond, logits are taken relative to the maximum (exactly: those near it lie within
@@ -161,8 +173,8 @@ constexpr float kDrL1 = (float)(kDrL * 68719476736.0), kDrL2 = (float)(kDrL * kD
 
 SPEC_DEV float2 both(float x) { return make_float2(x, x); }
 
-// weights of two logits: w = v * 2^-n with v in units of 2^-62
-SPEC_DEV void dr_weight2(const DrExp& E, float x0, float x1, u64 (&v)[2], int (&n)[2]) {
+// weights of two logits: w = v * 2^-s in units of 2^-q, s in [0, 63], v in [2^62, 2^63)
+SPEC_DEV void dr_weight2(const DrExp& E, float x0, float x1, u64 (&v)[2], int (&s)[2]) {
     const float2 neg = both(-1.f);
     const float2 d = add2(make_float2(x0, x1), both(-E.b));
     // p + e = 2048 t; p leaves its nearest integer.  (Where p is cut short, e, NaN for a masked logit, is
@@ -171,34 +183,29 @@ SPEC_DEV void dr_weight2(const DrExp& E, float x0, float x1, u64 (&v)[2], int (&
     float2 e = fma2(d, both(E.ch), np);
     e = fma2(d, both(E.cl), e);
     np = make_float2(fminf(np.x, E.most), fminf(np.y, E.most));
-    const float2 magic = both(12582912.f);
+    const float2 magic = both(__int_as_float(kDrMagic));
     const float2 k = fma2(np, neg, magic), nk = fma2(k, neg, magic), r = fma2(np, neg, nk);
     // 2^((r + e) / 2048) - 1 in units of 2^-36: off by 2^-36 of a weight, its f32 sums; the table's value to 26 bits
     // is enough for the product
-    const float2 s = add2(r, e), f = mul2(fma2(both(kDrL2), s, both(kDrL1)), s);
+    const float2 t = add2(r, e), f = mul2(fma2(both(kDrL2), t, both(kDrL1)), t);
     const float kf[2] = {k.x, k.y}, ff[2] = {f.x, f.y};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int ki = __float_as_int(kf[i]) - 0x4B400000;
-        const u64 T = E.table[ki & (kDrSteps - 1)];
+        const int ki = __float_as_int(kf[i]);
+        u64 T;
+        asm("ld.shared.u64 %0, [%1];" : "=l"(T) : "r"(E.table + (ki & (kDrSteps - 1)) * 8));
         v[i] = T + (u64)((long long)((int)(T >> 32) >> 4) * __float2int_rn(ff[i]));
-        n[i] = E.N - (ki >> 11);
+        s[i] = E.shift - (ki >> 11);
     }
-}
-// v * 2^-n in units of 2^-q, cut off (shifts of 64 and more give zero)
-SPEC_DEV u64 dr_units(const DrExp& E, u64 v, int n) {
-    u64 r;
-    asm("shr.u64 %0, %1, %2;" : "=l"(r) : "l"(v), "r"(62 - E.q + n));
-    return r;
 }
 SPEC_DEV void dr_weights(const DrExp& E, const float (&x)[8], u64 (&w)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
         u64 v[2];
-        int n[2];
-        dr_weight2(E, x[i], x[i + 1], v, n);
-        w[i] = dr_units(E, v[0], n[0]);
-        w[i + 1] = dr_units(E, v[1], n[1]);
+        int s[2];
+        dr_weight2(E, x[i], x[i + 1], v, s);
+        w[i] = v[0] >> s[0];
+        w[i + 1] = v[1] >> s[1];
     }
 }
 // a mass in units of 2^-by, to the nearest
@@ -260,7 +267,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     }
     E.b = 0.f;
     E.q = kDrSpanUnit;
-    E.table = table;
+    E.table = smem_u32(table);
     for (int i = t; i < kDrSteps; i += kDrThreads) table[i] = __umul64hi(a.coarse[i >> 6], a.fine[i & 63]) << 1;
     __syncthreads();
 
@@ -475,9 +482,9 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
         E.q = q;
         E.refer_to(m);
         u64 v[2];
-        int n[2];
-        dr_weight2(E, m, m, v, n);
-        one = dr_units(E, v[0], n[0]);
+        int s[2];
+        dr_weight2(E, m, m, v, s);
+        one = v[0] >> s[0];
         w_min = dr_part(min_p, one, true);
     };
 
@@ -1163,9 +1170,9 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
             u64 rest = need - (v < m ? of(lo + 1) : 0);
             if (weighed) {
                 u64 vv[2];
-                int n[2];
-                dr_weight2(E, v, v, vv, n);
-                const u64 w1 = dr_units(E, vv[0], n[0]);
+                int sh[2];
+                dr_weight2(E, v, v, vv, sh);
+                const u64 w1 = vv[0] >> sh[0];
                 rest = (rest + w1 - 1) / w1;
             }
             // the id of the last of the equal tokens that stay
@@ -1208,7 +1215,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     }
 
     // -------- the distribution
-    const float inv = (float)(1ull << E.q) / (float)S_kept;
+    const float inv = 1.f / (float)S_kept;
     const float least = fmaxf(cut.v, -FLT_MAX);
     const u64 w_some = max(w_min, 1ull);
 #pragma unroll 1
@@ -1227,12 +1234,12 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
                 y[i] = y[i + 1] = 0.f;
                 if (!any) continue;
                 u64 v[2];
-                int n[2];
-                dr_weight2(E, x[i], x[i + 1], v, n);
+                int sh[2];
+                dr_weight2(E, x[i], x[i + 1], v, sh);
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    if (x[i + j] >= least && dr_kept(cut, x[i + j], lp_index<T>(mis, s * kDrSegs + g, i + j)) && dr_units(E, v[j], n[j]) >= w_some)
-                        y[i + j] = (float)v[j] * __uint_as_float((uint32_t)(127 - 62 - n[j]) << 23) * inv;
+                    if (x[i + j] >= least && dr_kept(cut, x[i + j], lp_index<T>(mis, s * kDrSegs + g, i + j)) && v[j] >> sh[j] >= w_some)
+                        y[i + j] = (float)v[j] * __uint_as_float((uint32_t)(127 - sh[j]) << 23) * inv;
             }
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
@@ -1318,11 +1325,15 @@ extern "C" int spec_sample_logits(const void* logits, int32_t dtype, int64_t lg_
     while (C < kDrMaxCtas && ((long long)vocab > (long long)C * kDrCtaVocab || ((long long)rows * C < kDrCtasWanted * sms && n_span > C * kDrWarps))) C *= 2;
     a.per = (n_span + C * kDrWarps - 1) / (C * kDrWarps);
     const size_t smem = dr_smem(a.per, elem);
-    void (*f)(DrawArgs) = dtype == SPEC_DTYPE_BF16 ? draw_kernel<__nv_bfloat16> : draw_kernel<float>;
-    if (smem > 48 * 1024) {
-        // the most that any call takes: another thread's call may come between this one's two steps
+    const bool half = dtype == SPEC_DTYPE_BF16;
+    void (*f)(DrawArgs) = half ? draw_kernel<__nv_bfloat16> : draw_kernel<float>;
+    static std::atomic<unsigned long long> set[2] = {};        // devices where a kernel may take more than 48 KB
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (smem > 48 * 1024 && !(set[half].load() & bit)) {
+        // (the most that any call takes)
         constexpr int most_per = (kDrCtaVocab / kDrSpan + 1 + kDrWarps) / kDrWarps;
         SPEC_TRY(check_cuda(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dr_smem(most_per, elem)), "spec_sample_logits attribute"));
+        set[half].fetch_or(bit);
     }
     cudaLaunchConfig_t cfg_l = {};
     cfg_l.gridDim = dim3((unsigned)(rows * C));
@@ -1330,13 +1341,13 @@ extern "C" int spec_sample_logits(const void* logits, int32_t dtype, int64_t lg_
     cfg_l.dynamicSmemBytes = smem;
     cfg_l.stream = (cudaStream_t)stream;
     cudaLaunchAttribute at[2];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = C;
-    at[0].val.clusterDim.y = 1;
-    at[0].val.clusterDim.z = 1;
-    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[1].val.programmaticStreamSerializationAllowed = 1;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = C;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
     cfg_l.attrs = at;
-    cfg_l.numAttrs = 2;
+    cfg_l.numAttrs = C > 1 ? 2 : 1;
     return check_cuda(cudaLaunchKernelEx(&cfg_l, f, a), "spec_sample_logits launch");
 }

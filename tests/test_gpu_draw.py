@@ -285,3 +285,52 @@ def test_refusals():
                 (x, u.double(), tok), (x, u, tok[:1]), (x, u, tok.long()), (x, None, tok), (x, u, None)):
         with pytest.raises(spec.SpecError):
             spec.spec_sample_logits(*bad)
+
+
+@pytest.mark.parametrize("order", ["down", "up", "blocks"])
+@pytest.mark.parametrize("kw", [dict(), dict(k=700), dict(k=1900), dict(k=6000), dict(p=0.9), dict(p=0.99), dict(k=3000, p=0.8),
+                                dict(mp=0.001), dict(p=0.999, mp=1e-4)])
+def test_rows_whose_order_is_unlike_chance(order, kw):
+    """Sorted rows, and rows whose likely tokens all lie in one segment of four: what holds on average does not."""
+    R, V = 4, 60000
+    x = rows_of(33, R, V, fall=(0.7, 1.4))
+    if order == "blocks":
+        away = (torch.arange(V) // 256) % 4 != (torch.arange(V) // 1024) % 4
+        x = torch.where(away, x - 6.0, x)
+    else:
+        x = torch.sort(x, 1, descending=order == "down")[0]
+    check(x, uniforms(34, R), **kw)
+
+
+@pytest.mark.parametrize("kw", [dict(), dict(k=5000), dict(k=69999), dict(p=0.5), dict(p=0.25, k=20000), dict(mp=0.5), dict(p=0.7, mp=1.0)])
+@pytest.mark.parametrize("values", [1, 2, 3])
+def test_large_rows_of_few_values(kw, values):
+    R, V = 3, 70001
+    x = torch.randint(0, values, (R, V), generator=torch.Generator().manual_seed(values)).float() * 0.3
+    check(x, uniforms(35, R), **kw)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kw", [dict(p=0.95), dict(k=1500, p=0.9), dict()])
+def test_two_calls_at_once(dtype, kw):
+    """Calls on two streams at a time, many times over: the tokens of the calls on their own."""
+    from speculative_decoding_verify_04_gb300 import spec
+    R, V = 60, 50257
+    x = [rows_of(36 + i, R, V, dtype).cuda() for i in range(2)]
+    u = [uniforms(38 + i, R).cuda() for i in range(2)]
+    args = dict(top_k=kw.get("k", 0), top_p=kw.get("p", 1.0))
+    want = []
+    for a, b in zip(x, u):
+        t = torch.empty(R, dtype=torch.int32, device="cuda")
+        spec.spec_sample_logits(a, b, t, **args)
+        want.append(t)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[torch.empty(R, dtype=torch.int32, device="cuda") for _ in range(20)] for _ in range(2)]
+    for n in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                spec.spec_sample_logits(x[i], u[i], got[i][n], **args)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(t, want[i]) for t in got[i])
