@@ -53,6 +53,11 @@ SPEC_DEV void mma16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
 //     hd / 8 consecutive dims of V rows 4c .. 4c+3.
 //
 // bf16 caches: P is split into bf16 hi + lo, so its rounding does not show.
+// Windows (WIN): the list of keys leaves out what lies between the sinks and the
+// first row's window, and only tiles that not every row sees whole take masks.  64
+// sequences of one row over windows of 4096, 8 KV heads of 128: 144 us a call, 6.5 TB/s,
+// 96 % of a copy's rate.
+//
 // 8-bit caches: products in f16, which holds every e4m3 value (one conversion
 // for two values; to bf16 it takes four).  The queries are scaled by a power of
 // two a row to a magnitude of 2^13 .. 2^14 (bf16 queries stay exact down to

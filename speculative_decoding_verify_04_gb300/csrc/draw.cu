@@ -37,7 +37,7 @@
 // them are listed and searched.  (What defeats that, a row of equal logits, is bisected as
 // a whole.)
 //
-// Bound by instructions and latency, not by the row's bytes: 512 rows of 131072 bf16 logits
+// Bound by instructions and latency, not by the row's bytes: 512 rows of 131072 f32 logits
 // to their nuclei (p 0.95) 530 us, 0.5 TB/s; 100 rows of 50257 with mixed settings 100 us;
 // one greedy row of 32000 17 us a call.  Of a long row's time 45 to 55 us go to the
 // masses, 20 to 50 to the list, 20 to the histogram and 30 to 90 to the mass above the border.
@@ -58,7 +58,10 @@ namespace cg = cooperative_groups;
 namespace spec {
 
 constexpr int kDrThreads = 256;
-constexpr int kDrCtasWanted = 3;                       // CTAs an SM up to which rows are cut into more of them
+// CTAs an SM up to which rows are cut into more of them: a single row's time counts where rows are few.  (100 mixed
+// rows of 50257 take 117 us with one CTA a row, 101 with two and 99.5 with eight; a row of 32000 20.7 with one, 17 with
+// eight; 512 rows of 131072 537 with one, 534 with two.)
+constexpr int kDrCtasWanted = 3;
 constexpr int kDrWarps = kDrThreads / 32;
 constexpr int kDrMaxCtas = 8;
 constexpr int kDrSegs = 4;                             // segments of a span

@@ -11,7 +11,9 @@
 //
 // A CTA takes `group` rows: their angles once, in shared memory, for all heads, while the
 // rows' own loads are on their way; then 16 bytes of each half of a head a thread at a time.
-// Bound by memory (three operations a value).
+// Bound by memory (three operations a value): 16384 bf16 rows of 32 + 8 heads of 128 with three axes
+// take 58 us a call, 5.8 TB/s of reads and writes, 85 % of a copy's rate; without the loads ahead
+// of the angles 67.6.  One row: 9.1 us, a call's own time.
 #include <algorithm>
 #include <cmath>
 

@@ -663,7 +663,8 @@ def spec_sample_logits(logits, u, tokens, temperature=1.0, top_k=0, top_p=1.0, m
         if isinstance(value, torch.Tensor):
             setattr(cfg, array_, _at(value, dtype, name, rows, dev))
         else:
-            setattr(cfg, name, value)
+            # (a k past 32 bits, which ctypes would cut, is every token like any past the vocabulary)
+            setattr(cfg, name, max(-1, min(value, 0x7FFFFFFF)) if name == "top_k" else value)
     up = _at(u, torch.float32, "u", rows, dev)
     tok = _at(tokens, torch.int32, "tokens", rows, dev)
     lp = _at(logprob, torch.float32, "logprob", rows, dev)

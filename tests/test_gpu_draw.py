@@ -334,3 +334,14 @@ def test_two_calls_at_once(dtype, kw):
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(t, want[i]) for t in got[i])
+
+
+def test_a_k_past_32_bits_is_every_token():
+    from speculative_decoding_verify_04_gb300 import spec
+    x, u = rows_of(44, 4, 5000, torch.float32).cuda(), uniforms(44, 4).cuda()
+    got = [torch.empty(4, dtype=torch.int32, device="cuda") for _ in range(3)]
+    for t, k in zip(got, (0, 2 ** 31 - 1, 2 ** 32 + 1)):
+        spec.spec_sample_logits(x, u, t, top_k=k)
+    assert torch.equal(got[1], got[0]) and torch.equal(got[2], got[0])
+    with pytest.raises(spec.SpecError):
+        spec.spec_sample_logits(x, u, got[0], top_k=1 - 2 ** 32)
