@@ -636,7 +636,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
     u64 over_mass = 0;                                 // this warp's
     auto make_list = [&](float from, float to, const DrCut& old, bool cut_some, bool weighed) {
         u64* mine = staged + w * kDrStage;
-        int n = 0;
+        int n = 0, told = 0;
         u64 sum = 0;
         over_mass = 0;
         if (t == 0) sm.stop = 0;
@@ -644,7 +644,7 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
             for (int i = lane; i < s1 - s0; i += 32) my_sum[i] = 0;
         __syncthreads();
         const auto reach = reaching(from);
-        stream([&](int s) { return (weighed || !__any_sync(0xffffffffu, *(volatile int*)&sm.stop)) && reach(s); }, false, [&](const float (&x)[8], int seg) {
+        stream([&](int s) { return (weighed || !__any_sync(0xffffffffu, *(volatile int*)&sm.stop > kDrList)) && reach(s); }, false, [&](const float (&x)[8], int seg) {
             uint32_t in = 0, above = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) in |= x[i] >= from ? 1u << i : 0u;
@@ -684,9 +684,13 @@ draw_kernel(const __grid_constant__ DrawArgs a) {
             }
             __syncwarp();
             n += (int)(all & 0xFFFFu) + (int)(all >> 16);
-            if (n > kDrList && lane == 0) *(volatile int*)&sm.stop = 1;        // (it will not hold them)
         }, [&](int s) {
-            if (!weighed) return;
+            if (!weighed) {
+                // what the CTA's warps have found: once the list will not hold it, they stop
+                if (lane == 0) atomicAdd(&sm.stop, n - told);
+                told = n;
+                return;
+            }
             sum = dr_warp_sum(sum);
             if (lane == 0) my_sum[s - s0] = sum;
             over_mass += sum;
