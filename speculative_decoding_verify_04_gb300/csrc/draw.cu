@@ -20,7 +20,7 @@
 // arithmetic.  About 20 instructions a logit.  (A table of 32 steps in the warp's lanes and six terms,
 // the first in two floats, takes 30: 512 rows of 131072 to their nuclei in 622 us against 547 then.)
 //
-// A row is taken by a cluster of 1 to 8 CTAs, each warp on a contiguous run of spans
+// A row is taken by a cluster of 1 to 4 CTAs, each warp on a contiguous run of spans
 // of 1024 tokens.  One pass finds the maximum and leaves the maximum of every lane's 32
 // tokens of a span in shared memory, and where the row's whole mass is asked for (no
 // top-k, and a nucleus or nothing else) the mass of every span, relative to the span's own
@@ -38,12 +38,11 @@
 // a whole.)
 //
 // Bound by instructions and latency, not by the row's bytes: 512 rows of 131072 f32 logits
-// to their nuclei (p 0.95) 530 us, 0.5 TB/s; 100 rows of 50257 with mixed settings 100 us;
-// one greedy row of 32000 17 us a call.  Of a long row's time 45 to 55 us go to the
-// masses, 20 to 50 to the list, 20 to the histogram and 30 to 90 to the mass above the border.
-// Not faster: a launch of its own for the rows without a list, which gives the others three CTAs
-// an SM (754), three CTAs an SM for all in 80 registers (spills), blocks of 128 or 512 threads
-// (892 and 181, 537 and 111), logits through registers instead of the ring of copies.
+// to their nuclei (p 0.95) 400 us, 0.7 TB/s; 100 rows of 50257 with mixed settings 79 us;
+// one row of 32000 18 us a call.  One block of 512 threads an SM: its rows take less of a wave
+// each and its list holds twice the tokens (two blocks of 256: 502 and 100 us; a launch of its own for
+// the rows without a list, which gives the others three blocks of 256 an SM, 754).  Not faster either:
+// 80 registers a thread (spills), logits through registers instead of the ring of copies.
 #include <algorithm>
 #include <atomic>
 #include <cfloat>
@@ -57,24 +56,25 @@ namespace cg = cooperative_groups;
 
 namespace spec {
 
-constexpr int kDrThreads = 256;
+constexpr int kDrThreads = 512;
 // CTAs an SM up to which rows are cut into more of them: a single row's time counts where rows are few.  (100 mixed
-// rows of 50257 take 117 us with one CTA a row, 101 with two and 99.5 with eight; a row of 32000 20.7 with one, 17 with
-// eight; 512 rows of 131072 537 with one, 534 with two.)
-constexpr int kDrCtasWanted = 3;
+// rows of 50257 take 82 us with one CTA a row, 79 with two, 95 with four; a row of 32000 19.6 with one, 18.1 with
+// two or four; 512 rows of 131072 397 with one, 520 with four.)
+constexpr int kDrCtasWanted = 1;
 constexpr int kDrWarps = kDrThreads / 32;
-constexpr int kDrMaxCtas = 8;
+constexpr int kDrMaxCtas = 4;
+static_assert(kDrMaxCtas * kDrWarps <= 64, "two warps' numbers a lane");
 constexpr int kDrSegs = 4;                             // segments of a span
 constexpr int kDrSpan = kDrSegs * kLpSeg;
 constexpr int kDrEach = 8;                             // listed tokens a thread
 constexpr int kDrList = kDrEach * kDrThreads;
 constexpr int kDrSpanUnit = 51;                        // 1024 weights in units of 2^-51 fit 64 bits, and so does a listed token's
 constexpr int kDrListUnit = 50;
-constexpr int kDrStage = 384;                          // tokens a warp holds before they go to the list (one CTA's eight: 256 on average)
+constexpr int kDrStage = 384;                          // tokens a warp holds before they go to the list (one CTA's sixteen: 256 on average)
 constexpr int kDrBins = 2048;                          // steps of a histogram; it lies where the stages do
 static_assert(kDrBins * 4 <= kDrWarps * kDrStage * 8 && kDrList <= kDrWarps * kDrStage, "histogram, masses by place");
 constexpr int kDrRing = 4;                             // segments a warp has room for
-constexpr int kDrCtasSm = 2;
+constexpr int kDrCtasSm = 1;
 constexpr int kDrMaxVocab = 1 << 20;
 constexpr int kDrCtaVocab = 1 << 18;                   // a CTA's share at most: its lanes' maxima take 32 KB
 
